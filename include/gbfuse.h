@@ -79,6 +79,16 @@ typedef int gbf_status_t;
 #define GBF_OP_MLP 3 /* gbf_workspace_size(GBF_OP_MLP, M, D, F, fused) */
 #define GBF_OP_W8A16_FP8 4
 #define GBF_OP_W4A16_NVFP4 5
+#define GBF_OP_EMBEDDING_GRAD 6 /* gbf_workspace_size(op, M, V, D, 1) */
+#define GBF_OP_CLIP_GRAD_NORM 7 /* gbf_workspace_size(op, tensors, 0, 0, 1) */
+
+/* Type of an array of ids (`ids`, `targets`). */
+#define GBF_INDEX_I64 0
+#define GBF_INDEX_I32 1
+
+/* Type of a gradient tensor. */
+#define GBF_TYPE_BF16 0
+#define GBF_TYPE_F32 1
 
 /*
  * gemm_epilogue -- out[M][N] = bf16( act(alpha * A*B~ + beta*C + bias) + residual )
@@ -294,6 +304,56 @@ GBF_API gbf_status_t gemm_epilogue_unfused_noalloc(const void *A, const void *B,
                                                    const void *residual, void *out, int64_t M,
                                                    int64_t N, int64_t K, float alpha, float beta,
                                                    int act, gbf_stream_t stream);
+
+/*
+ * gbf_embedding_lookup -- out[m][D] = bf16( scale * table[ids[m]][D] ), one rounding.
+ *   ids    [M] of index_type (aligned to its size, not to 16 bytes).  An id
+ *          outside [0, V) reads nothing and its row of out is zero (use -1
+ *          for padding).
+ *   table  [V][D] bf16; out [M][D] bf16.  D % 8 == 0; M < 2^31; V <= 2^31 - 2.
+ *   HBM-bound: reads each row asked for once, writes out once.
+ * gbf_embedding_grad -- the gradient of the table:
+ *   dtable[v] = bf16( scale * sum_{m : ids[m] == v} dout[m] )              accumulate == 0
+ *   dtable[v] = bf16( dtable[v] + scale * sum_{m : ids[m] == v} dout[m] )  accumulate == 1
+ *   Without accumulate every row of dtable is written (zeros where no id
+ *   occurs); with it only the rows whose id occurs are read and written (the
+ *   gradient of a tied table is added to what the loss left there).  Sums in
+ *   fp32 over the positions in ascending order, cut at fixed places of the
+ *   list sorted by id: the same bits on every run.  Positions whose id is
+ *   outside [0, V) are left out, whatever dout holds there.
+ *   dout [M][D], dtable [V][D] bf16.  M <= 2^30.  Workspace:
+ *   gbf_workspace_size(GBF_OP_EMBEDDING_GRAD, M, V, D, 1) bytes.
+ */
+GBF_API gbf_status_t gbf_embedding_lookup(const void *ids, int index_type, const void *table,
+                                      void *out, int64_t M, int64_t V, int64_t D, float scale,
+                                      gbf_stream_t stream);
+GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const void *dout,
+                                    void *dtable, int64_t M, int64_t V, int64_t D, float scale,
+                                    int accumulate, void *workspace, size_t workspace_bytes,
+                                    gbf_stream_t stream);
+
+/*
+ * gbf_clip_grad_norm -- the 2-norm over all values of `tensors` gradients, and
+ *   the gradients scaled so that it is at most max_norm:
+ *     norm   = sqrt( sum x^2 )                     written to norm[0], fp32
+ *     factor = min(1, max_norm / (norm + eps))     (1 where norm is 0 or max_norm infinite)
+ *     out    = factor * x, rounded once to the tensor's type
+ *   grads, out, counts, types are HOST arrays of `tensors` entries, read
+ *   before the call returns: device pointers (aligned to their element's size
+ *   only: views into flat buffers are fine), element counts >= 0 and
+ *   GBF_TYPE_*.  out == NULL: in place, and nothing is written when the factor
+ *   is 1.  Otherwise every out[i] is written, and may equal grads[i] but not
+ *   overlap it otherwise.  A pointer may be NULL where its count is 0.
+ *   A NaN among the values makes norm and factor NaN; an infinite one makes
+ *   norm infinite and the factor 0.  No value that fp32 holds overflows or is
+ *   lost in the squares.  The same bits on every run.
+ *   max_norm >= 0 (INFINITY: the norm only), eps >= 0.  norm 4-byte aligned.
+ *   Workspace: gbf_workspace_size(GBF_OP_CLIP_GRAD_NORM, tensors, 0, 0, 1) bytes.
+ */
+GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *out,
+                                    const int64_t *counts, const int *types, int tensors,
+                                    float max_norm, float eps, float *norm, void *workspace,
+                                    size_t workspace_bytes, gbf_stream_t stream);
 
 /* Workspace bytes an entry point needs (0 for the fused ones).  `op` is a
  * GBF_OP_* id; `fused` selects the fused (1) or unfused (0) entry point. */

@@ -14,6 +14,12 @@ there is no CPU fallback, and a missing library is an error.
   mlp_swiglu_down    gate/up GEMM -> bf16 h -> down GEMM + residual
   add_rmsnorm        fused residual add + RMSNorm
   *_unfused          the same results as GEMM -> HBM -> pointwise kernel
+
+The operators at a model's two ends carry the prefix gbf_ in the C ABI only:
+
+  embedding_lookup   out = scale * table[ids]
+  embedding_grad     the table's gradient, by sorted ids
+  clip_grad_norm     global 2-norm over many gradients, and clipping
 """
 from __future__ import annotations
 
@@ -25,7 +31,10 @@ from . import build as _build
 
 ACT = {"identity": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 LAYOUT = {"kn": 0, "nk": 1}
-OP = {"gemm_epilogue": 0, "swiglu": 1, "w4a16": 2, "mlp": 3, "w8a16_fp8": 4, "w4a16_nvfp4": 5}
+OP = {"gemm_epilogue": 0, "swiglu": 1, "w4a16": 2, "mlp": 3, "w8a16_fp8": 4, "w4a16_nvfp4": 5,
+      "embedding_grad": 6, "clip_grad_norm": 7}
+INDEX = {"i64": 0, "i32": 1}
+TYPE = {"bf16": 0, "f32": 1}
 STATUS = {0: "GBF_OK", 1: "GBF_ERR_INVALID_ARG", 2: "GBF_ERR_MISALIGNED",
           3: "GBF_ERR_UNSUPPORTED_SHAPE", 4: "GBF_ERR_WORKSPACE", 5: "GBF_ERR_CUDA",
           6: "GBF_ERR_TIMEOUT", 7: "GBF_ERR_NO_DEVICE"}
@@ -39,7 +48,8 @@ EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unf
            "gemm_epilogue_unfused_noalloc", "gbf_debug_force_splits", "gbf_debug_force_path", "gbf_debug_set_profile",
            "swiglu_pointwise", "add_rmsnorm", "add_rmsnorm_unfused", "mlp_swiglu_down",
            "mlp_swiglu_down_unfused", "w8a16_fp8_gemm", "w8a16_fp8_gemm_unfused",
-           "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused")
+           "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused", "gbf_embedding_lookup",
+           "gbf_embedding_grad", "gbf_clip_grad_norm")
 
 _lock = threading.Lock()
 _lib = None
@@ -89,6 +99,12 @@ def load(path: str | None = None):
             fn = getattr(lib, name)
             fn.argtypes = [V, V, V, V, V, I64, I64, F, V]
             fn.restype = I
+        lib.gbf_embedding_lookup.argtypes = [V, I, V, V, I64, I64, I64, F, V]
+        lib.gbf_embedding_lookup.restype = I
+        lib.gbf_embedding_grad.argtypes = [V, I, V, V, I64, I64, I64, F, I, V, SZ, V]
+        lib.gbf_embedding_grad.restype = I
+        lib.gbf_clip_grad_norm.argtypes = [V, V, V, V, I, F, F, V, V, SZ, V]
+        lib.gbf_clip_grad_norm.restype = I
         lib.swiglu_pointwise.argtypes = [V, V, V, V, I64, I64, F, F, I, V]
         lib.swiglu_pointwise.restype = I
         lib.gemm_epilogue_unfused_noalloc.argtypes = [V, V, I, V, V, V, V, I64, I64, I64, F, F,
@@ -284,6 +300,59 @@ def w4a16_nvfp4_gemm_unfused(A, Wq, scales, C, bias, residual, out, M, N, K, alp
                                          _code(act, ACT), _p(workspace), workspace_bytes,
                                          _s(stream))
     return _check(st, "w4a16_nvfp4_gemm_unfused", raise_on_error)
+
+
+def embedding_lookup(ids, table, out, M, V, D, scale=1.0, index_type="i64", stream=None,
+                     raise_on_error=True):
+    st = load().gbf_embedding_lookup(_p(ids), _code(index_type, INDEX), _p(table), _p(out), M, V, D,
+                                 scale, _s(stream))
+    return _check(st, "embedding_lookup", raise_on_error)
+
+
+def embedding_grad(ids, dout, dtable, M, V, D, scale=1.0, accumulate=False, index_type="i64",
+                   workspace=None, workspace_bytes=0, stream=None, raise_on_error=True):
+    st = load().gbf_embedding_grad(_p(ids), _code(index_type, INDEX), _p(dout), _p(dtable), M, V, D,
+                               scale, int(accumulate), _p(workspace), workspace_bytes,
+                               _s(stream))
+    return _check(st, "embedding_grad", raise_on_error)
+
+
+class TensorList:
+    """The host arrays (addresses, element counts, types) that
+    ``clip_grad_norm`` takes, laid out once for a list of contiguous bf16 or
+    fp32 tensors, which it keeps alive."""
+
+    def __init__(self, tensors):
+        import torch
+        kinds = {torch.bfloat16: TYPE["bf16"], torch.float32: TYPE["f32"]}
+        self.tensors = list(tensors)
+        for t in self.tensors:
+            if t.dtype not in kinds:
+                raise TypeError(f"clip_grad_norm takes bf16 and fp32 tensors, not {t.dtype}")
+            if not t.is_contiguous():
+                raise ValueError("clip_grad_norm takes contiguous tensors")
+        n = len(self.tensors)
+        self.pointers = (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in self.tensors])
+        self.counts = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in self.tensors])
+        self.types = (ctypes.c_int * max(n, 1))(*[kinds[t.dtype] for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def clip_grad_norm(grads, out, max_norm, norm, eps=1e-6, workspace=None, workspace_bytes=0,
+                   stream=None, raise_on_error=True):
+    """``grads`` and ``out``: lists of tensors, or ``TensorList``s made once;
+    ``out`` None clips in place."""
+    grads = grads if isinstance(grads, TensorList) else TensorList(grads)
+    if out is not None:
+        out = out if isinstance(out, TensorList) else TensorList(out)
+        if list(out.counts) != list(grads.counts) or list(out.types) != list(grads.types):
+            raise ValueError("out must match grads in number, sizes and types")
+    st = load().gbf_clip_grad_norm(grads.pointers, None if out is None else out.pointers,
+                               grads.counts, grads.types, len(grads), max_norm, eps, _p(norm),
+                               _p(workspace), workspace_bytes, _s(stream))
+    return _check(st, "clip_grad_norm", raise_on_error)
 
 
 def gbf_workspace_size(op, M, N, K, fused) -> int:

@@ -444,6 +444,16 @@ double plan_time(const GemmPlan& p, bool dual, const DeviceInfo& dev) {
 
 }  // namespace
 
+int lib_device(const DeviceInfo** info, unsigned** err) { return current_device(info, err); }
+
+bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
+                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                 CUtensorMapSwizzle swz) {
+  return tmap_2d(m, base, dt, inner, outer, row_bytes, box_inner, box_outer, swz);
+}
+
+KernelCtl lib_ctl(unsigned* err, int64_t ctas) { return make_ctl(err, ctas); }
+
 int check_gemm_call(const void* A, const void* B, int b_layout, const void* C, const void* bias,
                     const void* residual, const void* out, int64_t M, int64_t N, int64_t K,
                     int act) {
@@ -669,6 +679,7 @@ size_t gbf_workspace_size(int op, int64_t M, int64_t N, int64_t K, int fused) {
     if (fused) return h;
     return 4 * h + align256(static_cast<size_t>(M * N) * 2);  // g, u (2h), h, D
   }
+  if (op >= GBF_OP_EMBEDDING_GRAD) return heads_workspace_size(op, M, N, K);
   if (fused) return 0;
   switch (op) {
     case GBF_OP_GEMM_EPILOGUE: return align256(static_cast<size_t>(M * N) * 2);

@@ -1,0 +1,467 @@
+// embedding.cu -- the embedding lookup with scaling and its gradient.
+//
+// Lookup: out[m] = bf16(scale * table[id_m]), zeros for an id outside [0, V).
+// HBM-bound: a warp moves 1024 columns of one row, four 16-byte vectors per
+// lane in flight.
+//
+// Gradient: dtable[v] (+)= scale * sum over {m : id_m = v} of dout[m], in
+// fp32, in the order of m.  Summing with atomics would add in an order that
+// changes from run to run, so the positions are sorted by id first (a stable
+// radix sort inside one cluster of CTAs) and the sorted list is cut into
+// pieces of equal length, however the ids repeat:
+//   1. embed_sort_kernel: (id, m) sorted by id, and a bit per table row that
+//      occurs;
+//   2. embed_sum_kernel: one piece of the list x 1024 columns per CTA.  A run
+//      of equal ids inside the piece is summed and written; the part of a run
+//      that continues from the previous piece or into the next one goes to the
+//      workspace in fp32.  Without accumulation further CTAs write the zero
+//      rows of the ids that do not occur;
+//   3. embed_join_kernel: the runs over several pieces, their parts added in
+//      order, written once.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gbf {
+
+namespace {
+
+constexpr int kLookThreads = 128;
+constexpr int kSegCols = 1024;  // columns per warp (lookup) or CTA (gradient)
+
+template <typename Id>
+__global__ void __launch_bounds__(kLookThreads)
+    embed_lookup_kernel(const Id* __restrict__ ids, const __nv_bfloat16* __restrict__ table,
+                        __nv_bfloat16* __restrict__ out, int64_t M, int64_t V, int D, int segs,
+                        float scale) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t task =
+      static_cast<int64_t>(blockIdx.x) * (kLookThreads / 32) + (threadIdx.x >> 5);
+  const int64_t m = task / segs;
+  if (m >= M) return;
+  const int col0 = static_cast<int>(task - m * segs) * kSegCols + lane * 8;
+  const int64_t id = static_cast<int64_t>(ids[m]);
+  const bool known = id >= 0 && id < V;
+  const __nv_bfloat16* src = table + (known ? id : 0) * D;
+  __nv_bfloat16* dst = out + m * D;
+  uint4 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = col0 + i * 256;
+    v[i] = (known && col < D) ? ldg_u4(src + col) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int col = col0 + i * 256;
+    if (col < D) {
+      float f[8];
+      unpack8(v[i], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] *= scale;
+      // 0 * inf must not reach the row of an unknown id
+      st_u4(dst + col, known ? pack8(f) : make_uint4(0u, 0u, 0u, 0u));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sort
+//
+// Stable least-significant-digit radix sort of (id, m) by one cluster: CTA c
+// holds the c-th contiguous share of the list, warp w the w-th of the CTA's.
+// Per pass: every warp counts its digits, the counts are summed over warps
+// and CTAs (one CTA's totals are read by the others from its shared memory),
+// and every warp writes its items to their places, 32 at a time, ranked among
+// equal digits by lane.  Ids outside [0, V) get the key V and end the list.
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kMaxDigitBits = 9;
+constexpr int kMaxDigits = 1 << kMaxDigitBits;
+constexpr int kSortCluster = 8;
+constexpr size_t kSortSmem = (kSortWarps + 2) * kMaxDigits * sizeof(int);
+
+__device__ __forceinline__ int ld_cg(const int* p) { return __ldcg(p); }
+
+__device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(kSortThreads)
+    embed_sort_kernel(const Id* __restrict__ ids, int M, int V, int passes, int digit_bits,
+                      int* key0, int* idx0, int* key1, int* idx1, unsigned* present) {
+  extern __shared__ int sort_smem[];
+  int* hist = sort_smem;                            // [warps][digits]
+  int* total = sort_smem + kSortWarps * kMaxDigits;  // this CTA's digit counts
+  int* base = total + kMaxDigits;                    // where this CTA's digits begin
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int ctas = static_cast<int>(gridDim.x);  // one cluster
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int digits = 1 << digit_bits;
+  griddep_launch_dependents();
+  griddep_wait();
+  if (present) {
+    const int words = (V + 31) / 32;
+    for (int i = rank * kSortThreads + threadIdx.x; i < words; i += ctas * kSortThreads)
+      present[i] = 0u;
+  }
+  // contiguous shares, multiples of 32 so that a warp's steps are full but the last
+  const int64_t share =
+      ((static_cast<int64_t>(M) + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
+  const int64_t lo64 = (static_cast<int64_t>(rank) * kSortWarps + warp) * share;
+  const int lo = static_cast<int>(min(lo64, static_cast<int64_t>(M)));
+  const int hi = static_cast<int>(min(lo64 + share, static_cast<int64_t>(M)));
+  int* const my_hist = hist + warp * kMaxDigits;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int shift = pass * digit_bits;
+    const int* ksrc = (pass & 1) ? key0 : key1;
+    const int* isrc = (pass & 1) ? idx0 : idx1;
+    int* kdst = (pass & 1) ? key1 : key0;
+    int* idst = (pass & 1) ? idx1 : idx0;
+    auto key_at = [&](int i) -> int {
+      if (pass > 0) return ld_cg(ksrc + i);
+      const int64_t id = static_cast<int64_t>(ids[i]);
+      return (id >= 0 && id < V) ? static_cast<int>(id) : V;
+    };
+    for (int d = lane; d < digits; d += 32) my_hist[d] = 0;
+    __syncwarp();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      // lanes past the end form a group of their own
+      const int d = in ? ((key_at(i) >> shift) & (digits - 1)) : -1;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      if (in && lane == __ffs(same) - 1) my_hist[d] += __popc(same);
+      __syncwarp();
+    }
+    __syncthreads();
+    // per digit: this CTA's count, and each warp's offset within it
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+      int sum = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int n = hist[w * kMaxDigits + d];
+        hist[w * kMaxDigits + d] = sum;
+        sum += n;
+      }
+      total[d] = sum;
+    }
+    cluster_sync_all();  // every CTA's counts are written
+    // per digit: the count over all CTAs and that of the CTAs before this one
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+      int all = 0, before = 0;
+      for (int c = 0; c < ctas; ++c) {
+        const int n = ld_dsmem_s32(mapa_shared(smem_u32(&total[d]), c));
+        if (c < rank) before += n;
+        all += n;
+      }
+      base[d] = all;
+      // parked until the scan below: where equal digits of this CTA begin
+      for (int w = 0; w < kSortWarps; ++w) hist[w * kMaxDigits + d] += before;
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive scan of the digits' counts
+      int run = 0;
+      for (int d0 = 0; d0 < digits; d0 += 32) {
+        const int d = d0 + lane;
+        const int n = d < digits ? base[d] : 0;
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (d < digits) base[d] = run + x - n;
+        run += __shfl_sync(0xFFFFFFFFu, x, 31);
+      }
+    }
+    __syncthreads();
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const int key = in ? key_at(i) : 0;
+      const int d = in ? ((key >> shift) & (digits - 1)) : -1;
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+      int at = 0;
+      if (in) at = base[d] + my_hist[d] + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (in && lane == __ffs(same) - 1) my_hist[d] += __popc(same);
+      __syncwarp();
+      if (in) {
+        kdst[at] = key;
+        idst[at] = pass > 0 ? ld_cg(isrc + i) : i;
+        if (pass == 0 && present && key < V) atomicOr(&present[key >> 5], 1u << (key & 31));
+      }
+    }
+    cluster_sync_all();  // the pass is written before the next one reads it
+  }
+}
+
+// ---------------------------------------------------------------- sums
+
+constexpr int kSumThreads = 128;
+constexpr int kMaxPiece = 32;  // sorted positions per piece at most
+
+struct SumArgs {
+  const int* key;   // sorted ids, V for the unknown ones
+  const int* idx;   // their positions
+  const __nv_bfloat16* dout;
+  __nv_bfloat16* dtable;
+  float* head;      // [pieces][D]: the part of a run that began in an earlier piece
+  float* tail;      // [pieces][D]: the part of a run that goes on in the next piece
+  const unsigned* present;
+  int M, V, D;
+  int piece;        // positions per piece
+  int pieces;
+  int segs;         // column segments
+  float scale;
+  int accumulate;
+};
+
+__device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int col,
+                                          const float (&sum)[8]) {
+  __nv_bfloat16* p = a.dtable + v * a.D + col;
+  float f[8];
+  if (a.accumulate) {
+    unpack8(ld_u4(p), f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = fmaf(a.scale, sum[j], f[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = a.scale * sum[j];
+  }
+  st_u4(p, pack8(f));
+}
+
+__device__ __forceinline__ void store_part(float* p, const float (&sum)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+}
+
+// CTAs [0, pieces * segs): sums; the rest: zero rows, one warp per 1024
+// columns of a row.
+__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a) {
+  __shared__ int skey[kMaxPiece + 2];
+  __shared__ int sidx[kMaxPiece];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
+  if (static_cast<int64_t>(blockIdx.x) >= sums) {
+    const int64_t step = (static_cast<int64_t>(gridDim.x) - sums) * (kSumThreads / 32);
+    const int lane = threadIdx.x & 31;
+    for (int64_t t = (blockIdx.x - sums) * (kSumThreads / 32) + (threadIdx.x >> 5);
+         t < static_cast<int64_t>(a.V) * a.segs; t += step) {
+      const int64_t v = t / a.segs;
+      if ((a.present[v >> 5] >> (v & 31)) & 1u) continue;
+      const int col0 = static_cast<int>(t - v * a.segs) * kSegCols + lane * 8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (col0 + i * 256 < a.D)
+          st_u4(a.dtable + v * a.D + col0 + i * 256, make_uint4(0u, 0u, 0u, 0u));
+    }
+    return;
+  }
+  const int p = static_cast<int>(blockIdx.x / a.segs);
+  const int seg = static_cast<int>(blockIdx.x - static_cast<int64_t>(p) * a.segs);
+  const int64_t first = static_cast<int64_t>(p) * a.piece;
+  const int n = static_cast<int>(min(static_cast<int64_t>(a.piece), a.M - first));
+  // the keys before and after the piece tell whether its runs go on
+  for (int i = threadIdx.x; i < n + 2; i += kSumThreads) {
+    const int64_t at = first + i - 1;
+    skey[i] = (at >= 0 && at < a.M) ? a.key[at] : -1;
+  }
+  for (int i = threadIdx.x; i < n; i += kSumThreads) sidx[i] = a.idx[first + i];
+  __syncthreads();
+  const int col = seg * kSegCols + threadIdx.x * 8;
+  if (col >= a.D) return;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  bool began = skey[0] != skey[1];  // the current run began in this piece
+  constexpr int kAhead = 8;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u < n && skey[i0 + u + 1] < a.V)
+        v[u] = ldg_u4(a.dout + static_cast<int64_t>(sidx[i0 + u]) * a.D + col);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= n) break;
+      const int key = skey[i + 1];
+      if (key >= a.V) return;  // the unknown ids end the list
+      float f[8];
+      unpack8(v[u], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+      const bool ends = skey[i + 2] != key;
+      if (ends || i + 1 == n) {
+        if (began && ends)
+          write_row(a, key, col, sum);
+        else
+          store_part((began ? a.tail : a.head) + static_cast<int64_t>(p) * a.D + col, sum);
+        began = true;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+      }
+    }
+  }
+}
+
+// One CTA per piece x segment: where the piece's last run began in it and goes
+// on, adds the run's parts in order and writes the row.
+__global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int p = static_cast<int>(blockIdx.x / a.segs);
+  const int seg = static_cast<int>(blockIdx.x - static_cast<int64_t>(p) * a.segs);
+  const int64_t next = static_cast<int64_t>(p + 1) * a.piece;  // first position after the piece
+  if (next >= a.M) return;
+  const int key = a.key[next - 1];
+  if (key >= a.V || a.key[next] != key) return;                     // the last run ends here
+  const int64_t first = static_cast<int64_t>(p) * a.piece;
+  if (a.key[first] == key && first > 0 && a.key[first - 1] == key) return;  // began earlier
+  const int col = seg * kSegCols + threadIdx.x * 8;
+  if (col >= a.D) return;
+  float sum[8];
+  {
+    const float4* t = reinterpret_cast<const float4*>(a.tail + static_cast<int64_t>(p) * a.D + col);
+    const float4 x = t[0], y = t[1];
+    sum[0] = x.x; sum[1] = x.y; sum[2] = x.z; sum[3] = x.w;
+    sum[4] = y.x; sum[5] = y.y; sum[6] = y.z; sum[7] = y.w;
+  }
+  for (int q = p + 1; q < a.pieces; ++q) {
+    const float4* t = reinterpret_cast<const float4*>(a.head + static_cast<int64_t>(q) * a.D + col);
+    const float4 x = t[0], y = t[1];
+    sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
+    sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
+    const int64_t end = static_cast<int64_t>(q + 1) * a.piece;
+    if (end >= a.M || a.key[end] != key) break;
+  }
+  write_row(a, key, col, sum);
+}
+
+// A launch that may begin while the previous kernel of the stream finishes:
+// every kernel here waits for it before it reads or writes memory.
+cudaLaunchConfig_t overlapped(int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                              cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+int bit_length(int64_t x) {
+  int n = 0;
+  while (x > 0) {
+    ++n;
+    x >>= 1;
+  }
+  return n;
+}
+
+template <typename Id>
+cudaError_t launch_sort(const Id* ids, int M, int V, const EmbedGradWs& ws, int* passes_out,
+                        unsigned* present, cudaStream_t stream) {
+  auto kernel = embed_sort_kernel<Id>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(kSortSmem));
+  if (e != cudaSuccess) return e;
+  const int bits = bit_length(V);  // keys 0 .. V
+  const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
+  const int digit_bits = (bits + passes - 1) / passes;
+  // one CTA up to 2048 ids (two per thread), then as many as keep that, 8 at most
+  int ctas = 1;
+  while (ctas < kSortCluster && static_cast<int64_t>(ctas) * 2048 < M) ctas *= 2;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = overlapped(ctas, kSortThreads, kSortSmem, stream, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  *passes_out = passes;
+  return cudaLaunchKernelEx(&cfg, kernel, ids, M, V, passes, digit_bits, ws.key0, ws.idx0,
+                            ws.key1, ws.idx1, present);
+}
+
+}  // namespace
+
+cudaError_t launch_embedding_lookup(const void* ids, bool ids64, const __nv_bfloat16* table,
+                                    __nv_bfloat16* out, int64_t M, int64_t V, int D, float scale,
+                                    cudaStream_t stream) {
+  const int segs = (D + kSegCols - 1) / kSegCols;
+  const int64_t warps = M * segs;
+  const int64_t per = kLookThreads / 32;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped((warps + per - 1) / per, kLookThreads, 0, stream, attr);
+  return ids64 ? cudaLaunchKernelEx(&cfg, embed_lookup_kernel<int64_t>,
+                                    static_cast<const int64_t*>(ids), table, out, M, V, D, segs,
+                                    scale)
+               : cudaLaunchKernelEx(&cfg, embed_lookup_kernel<int>, static_cast<const int*>(ids),
+                                    table, out, M, V, D, segs, scale);
+}
+
+// Positions per piece: 32, fewer while that leaves under eight CTAs per SM.
+int embed_piece(int64_t M, int D) {
+  const int segs = (D + kSegCols - 1) / kSegCols;
+  int piece = kMaxPiece;
+  while (piece > 4 && (M + piece - 1) / piece * segs < 152 * 8) piece /= 2;
+  return piece;
+}
+
+cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat16* dout,
+                                  __nv_bfloat16* dtable, int M, int V, int D, float scale,
+                                  bool accumulate, const EmbedGradWs& ws, int sms,
+                                  cudaStream_t stream) {
+  cudaError_t e;
+  int passes = 0;
+  unsigned* present = accumulate ? nullptr : ws.present;
+  e = ids64 ? launch_sort(static_cast<const int64_t*>(ids), M, V, ws, &passes, present, stream)
+            : launch_sort(static_cast<const int*>(ids), M, V, ws, &passes, present, stream);
+  if (e != cudaSuccess) return e;
+  SumArgs a{};
+  a.key = (passes & 1) ? ws.key0 : ws.key1;
+  a.idx = (passes & 1) ? ws.idx0 : ws.idx1;
+  a.dout = dout;
+  a.dtable = dtable;
+  a.head = ws.head;
+  a.tail = ws.tail;
+  a.present = present;
+  a.M = M;
+  a.V = V;
+  a.D = D;
+  a.piece = embed_piece(M, D);
+  a.pieces = (M + a.piece - 1) / a.piece;
+  a.segs = (D + kSegCols - 1) / kSegCols;
+  a.scale = scale;
+  a.accumulate = accumulate ? 1 : 0;
+  const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
+  int64_t zeros = 0;
+  if (!accumulate) {
+    const int64_t warps = static_cast<int64_t>(V) * a.segs;
+    zeros = std::min<int64_t>((warps + 3) / 4, static_cast<int64_t>(sms) * 16);
+  }
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped(sums + zeros, kSumThreads, 0, stream, attr);
+  if ((e = cudaLaunchKernelEx(&cfg, embed_sum_kernel, a)) != cudaSuccess) return e;
+  cudaLaunchAttribute attr2[1];
+  cudaLaunchConfig_t cfg2 = overlapped(sums, kSumThreads, 0, stream, attr2);
+  return cudaLaunchKernelEx(&cfg2, embed_join_kernel, a);
+}
+
+}  // namespace gbf

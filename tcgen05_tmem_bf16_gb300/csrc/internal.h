@@ -129,6 +129,42 @@ cudaError_t launch_add_rmsnorm(const __nv_bfloat16* a, const __nv_bfloat16* x,
                                cudaStream_t stream);
 constexpr int kRmsMaxN = 16384;
 
+// Embedding lookup and its gradient (embedding.cu).  ids: int64 or int32;
+// one outside [0, V) reads zeros and gets no gradient.
+cudaError_t launch_embedding_lookup(const void* ids, bool ids64, const __nv_bfloat16* table,
+                                    __nv_bfloat16* out, int64_t M, int64_t V, int D, float scale,
+                                    cudaStream_t stream);
+struct EmbedGradWs {
+  int *key0, *idx0, *key1, *idx1;  // [M] each: the sorted list, twice
+  unsigned* present;               // one bit per table row that occurs
+  float *head, *tail;              // [pieces][D]: parts of runs over several pieces
+};
+int embed_piece(int64_t M, int D);  // sorted positions per piece
+cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat16* dout,
+                                  __nv_bfloat16* dtable, int M, int V, int D, float scale,
+                                  bool accumulate, const EmbedGradWs& ws, int sms,
+                                  cudaStream_t stream);
+
+// Global norm and clipping (clip.cu).  out == null: in place.  partial: three
+// doubles for each of clip_ctas() CTAs of each of clip_launches() launches.
+int clip_ctas(int sms);
+int clip_launches(int n);
+cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* counts,
+                                  const int* types, int n, float max_norm, float eps, float* norm,
+                                  double* partial, int sms, cudaStream_t stream);
+
+// ---- shared with the other entry-point files (api.cu) ---------------------------
+// The current device and the address of its error word (a GBF_* status).
+int lib_device(const DeviceInfo** info, unsigned** err);
+// Row-major 2-D tensor map; false if the driver refuses it.
+bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
+                 uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+                 CUtensorMapSwizzle swz);
+// Launch control of a grid of `ctas`.
+KernelCtl lib_ctl(unsigned* err, int64_t ctas);
+// gbf_workspace_size() of the operators in heads.cu.
+size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K);
+
 // Tile geometry shared by the planner and the kernels.
 constexpr int kBM = 128;        // MMA M: rows of TMEM / output tile height
 constexpr int kBK = 64;         // K per pipeline stage (one 128-byte swizzle row of bf16)
