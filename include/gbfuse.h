@@ -81,10 +81,17 @@ typedef int gbf_status_t;
 #define GBF_OP_W4A16_NVFP4 5
 #define GBF_OP_EMBEDDING_GRAD 6 /* gbf_workspace_size(op, M, V, D, 1) */
 #define GBF_OP_CLIP_GRAD_NORM 7 /* gbf_workspace_size(op, tensors, 0, 0, 1) */
+#define GBF_OP_LINEAR_CE 8        /* gbf_workspace_size(op, M, V, D, 1) */
+#define GBF_OP_LINEAR_CE_GRAD 9   /* gbf_workspace_size(op, M, V, D, 1) */
 
 /* Type of an array of ids (`ids`, `targets`). */
 #define GBF_INDEX_I64 0
 #define GBF_INDEX_I32 1
+
+/* What a gradient is taken of: the sum of the losses, or their mean over the
+ * rows with a target. */
+#define GBF_REDUCE_SUM 0
+#define GBF_REDUCE_MEAN 1
 
 /* Type of a gradient tensor. */
 #define GBF_TYPE_BF16 0
@@ -331,6 +338,42 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
                                     void *dtable, int64_t M, int64_t V, int64_t D, float scale,
                                     int accumulate, void *workspace, size_t workspace_bytes,
                                     gbf_stream_t stream);
+
+/*
+ * gbf_linear_ce -- softmax cross entropy of a linear head, row by row, the
+ *   logits never in memory (they end inside the product as running sums):
+ *     l = alpha * x w^T,  lse[m] = log sum_v exp(l[m][v]),
+ *     loss[m] = lse[m] - l[m][targets[m]],  mean[0] = mean of loss over the scored rows.
+ *   x [M][D], w [V][D] bf16; targets [M] of index_type.  A row whose target is
+ *   outside [0, V) (-100, -1, ...) is not scored: its loss and lse are 0, it
+ *   costs no products, and whatever its row of x holds reaches no result.
+ *   loss, lse [M] fp32, 4-byte aligned; mean (may be NULL) one fp32, 0 where
+ *   no row is scored.
+ *   D % 8 == 0, D >= 8, V >= 1; M <= 2^24, V <= 2^26, D <= 2^20; alpha finite.
+ *   Products accumulated in fp32 on the tensor cores, sums of exponentials in
+ *   fp32 relative to their maximum.  Workspace:
+ *   gbf_workspace_size(GBF_OP_LINEAR_CE, M, V, D, 1) bytes.
+ * gbf_linear_ce_grad -- its gradients, from the lse that gbf_linear_ce wrote:
+ *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - [v == targets[m]])
+ *     dx = f * G w (rows that are not scored: zero),   dw = f * G^T x,
+ *     f = alpha * scale, divided by the number of scored rows (at least 1)
+ *         with GBF_REDUCE_MEAN.
+ *   dloss [M] fp32 or NULL (1 for every row); dx [M][D], dw [V][D] bf16, either
+ *   may be NULL (not computed), every row of the others is written.  The
+ *   logits are computed again, a piece of the vocabulary at a time; G of the
+ *   piece is rounded to bf16 (before f), the sums are fp32, dx and dw are
+ *   rounded once.  The same bits on every run.  Workspace:
+ *   gbf_workspace_size(GBF_OP_LINEAR_CE_GRAD, M, V, D, 1) bytes.
+ */
+GBF_API gbf_status_t gbf_linear_ce(const void *x, const void *w, const void *targets,
+                                   int index_type, float *loss, float *lse, float *mean,
+                                   int64_t M, int64_t V, int64_t D, float alpha, void *workspace,
+                                   size_t workspace_bytes, gbf_stream_t stream);
+GBF_API gbf_status_t gbf_linear_ce_grad(const void *x, const void *w, const void *targets,
+                                        int index_type, const float *lse, const float *dloss,
+                                        void *dx, void *dw, int64_t M, int64_t V, int64_t D,
+                                        float alpha, float scale, int reduction, void *workspace,
+                                        size_t workspace_bytes, gbf_stream_t stream);
 
 /*
  * gbf_clip_grad_norm -- the 2-norm over all values of `tensors` gradients, and

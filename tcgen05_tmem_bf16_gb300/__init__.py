@@ -19,6 +19,8 @@ The operators at a model's two ends carry the prefix gbf_ in the C ABI only:
 
   embedding_lookup   out = scale * table[ids]
   embedding_grad     the table's gradient, by sorted ids
+  linear_ce          softmax cross entropy of a linear head, the logits never stored
+  linear_ce_grad     its gradients by the head's input and weight
   clip_grad_norm     global 2-norm over many gradients, and clipping
 """
 from __future__ import annotations
@@ -32,8 +34,9 @@ from . import build as _build
 ACT = {"identity": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 LAYOUT = {"kn": 0, "nk": 1}
 OP = {"gemm_epilogue": 0, "swiglu": 1, "w4a16": 2, "mlp": 3, "w8a16_fp8": 4, "w4a16_nvfp4": 5,
-      "embedding_grad": 6, "clip_grad_norm": 7}
+      "embedding_grad": 6, "clip_grad_norm": 7, "linear_ce": 8, "linear_ce_grad": 9}
 INDEX = {"i64": 0, "i32": 1}
+REDUCTION = {"sum": 0, "mean": 1}
 TYPE = {"bf16": 0, "f32": 1}
 STATUS = {0: "GBF_OK", 1: "GBF_ERR_INVALID_ARG", 2: "GBF_ERR_MISALIGNED",
           3: "GBF_ERR_UNSUPPORTED_SHAPE", 4: "GBF_ERR_WORKSPACE", 5: "GBF_ERR_CUDA",
@@ -49,7 +52,7 @@ EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unf
            "swiglu_pointwise", "add_rmsnorm", "add_rmsnorm_unfused", "mlp_swiglu_down",
            "mlp_swiglu_down_unfused", "w8a16_fp8_gemm", "w8a16_fp8_gemm_unfused",
            "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused", "gbf_embedding_lookup",
-           "gbf_embedding_grad", "gbf_clip_grad_norm")
+           "gbf_embedding_grad", "gbf_clip_grad_norm", "gbf_linear_ce", "gbf_linear_ce_grad")
 
 _lock = threading.Lock()
 _lib = None
@@ -103,6 +106,11 @@ def load(path: str | None = None):
         lib.gbf_embedding_lookup.restype = I
         lib.gbf_embedding_grad.argtypes = [V, I, V, V, I64, I64, I64, F, I, V, SZ, V]
         lib.gbf_embedding_grad.restype = I
+        lib.gbf_linear_ce.argtypes = [V, V, V, I, V, V, V, I64, I64, I64, F, V, SZ, V]
+        lib.gbf_linear_ce.restype = I
+        lib.gbf_linear_ce_grad.argtypes = [V, V, V, I, V, V, V, V, I64, I64, I64, F, F, I, V, SZ,
+                                           V]
+        lib.gbf_linear_ce_grad.restype = I
         lib.gbf_clip_grad_norm.argtypes = [V, V, V, V, I, F, F, V, V, SZ, V]
         lib.gbf_clip_grad_norm.restype = I
         lib.swiglu_pointwise.argtypes = [V, V, V, V, I64, I64, F, F, I, V]
@@ -315,6 +323,24 @@ def embedding_grad(ids, dout, dtable, M, V, D, scale=1.0, accumulate=False, inde
                                scale, int(accumulate), _p(workspace), workspace_bytes,
                                _s(stream))
     return _check(st, "embedding_grad", raise_on_error)
+
+
+def linear_ce(x, w, targets, loss, lse, mean, M, V, D, alpha=1.0, index_type="i64",
+              workspace=None, workspace_bytes=0, stream=None, raise_on_error=True):
+    st = load().gbf_linear_ce(_p(x), _p(w), _p(targets), _code(index_type, INDEX), _p(loss),
+                              _p(lse), _p(mean), M, V, D, alpha, _p(workspace), workspace_bytes,
+                              _s(stream))
+    return _check(st, "linear_ce", raise_on_error)
+
+
+def linear_ce_grad(x, w, targets, lse, dloss, dx, dw, M, V, D, alpha=1.0, scale=1.0,
+                   reduction="mean", index_type="i64", workspace=None, workspace_bytes=0,
+                   stream=None, raise_on_error=True):
+    st = load().gbf_linear_ce_grad(_p(x), _p(w), _p(targets), _code(index_type, INDEX), _p(lse),
+                                   _p(dloss), _p(dx), _p(dw), M, V, D, alpha, scale,
+                                   _code(reduction, REDUCTION), _p(workspace), workspace_bytes,
+                                   _s(stream))
+    return _check(st, "linear_ce_grad", raise_on_error)
 
 
 class TensorList:

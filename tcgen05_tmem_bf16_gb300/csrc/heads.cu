@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -58,6 +59,115 @@ size_t embed_grad_sections(void* base, int64_t M, int64_t V, int64_t D, EmbedGra
   return s.at;
 }
 
+// ---- linear cross entropy
+
+constexpr int kCePairs = 76;  // CTA pairs that run at once
+constexpr int kCeTileRows = 256;
+
+// Columns of the vocabulary per piece of the backward pass: as many whole
+// tiles as keep G of the piece within 256 MB, at least 512.
+constexpr int64_t kPieceBytes = int64_t(256) << 20;
+int64_t ce_piece(int64_t M, int64_t V) {
+  const int64_t cols = std::max<int64_t>(512, kPieceBytes / 2 / std::max<int64_t>(M, 1) / 512 * 512);
+  return std::min(cols, V);
+}
+
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles per unit of work: two (one B tile for two MMA streams) or one,
+// whichever fills the rounds of units over the CTA pairs better; one stream
+// runs at about 0.9 of the rate of two.
+int ce_streams(int64_t rows, int64_t n) {
+  const int64_t n_tiles = ceil_div64(n, kCeTileRows);
+  const int64_t one = ceil_div64(ceil_div64(rows, kCeTileRows) * n_tiles, kCePairs);
+  const int64_t two = ceil_div64(ceil_div64(rows, 2 * kCeTileRows) * n_tiles, kCePairs);
+  return static_cast<double>(two) * 2.0 <= static_cast<double>(one) / 0.9 ? 2 : 1;
+}
+
+// Parts of K of the product for dx, where its tiles are fewer than the pairs:
+// each at least 8 K blocks long.
+int ce_splits(int64_t M, int64_t D, int64_t cols) {
+  const int64_t tiles = ceil_div64(M, kCeTileRows) * ceil_div64(D, kCeTileRows);
+  const int64_t most = std::max<int64_t>(1, ceil_div64(cols, 64) / 8);
+  return static_cast<int>(std::min<int64_t>({kCePairs / std::max<int64_t>(tiles, 1) + (tiles > kCePairs ? 1 : 0),
+                                             most, 16}));
+}
+
+struct CeWs {
+  int *count, *rows, *tgt;
+  unsigned* ticket;
+  float *lse2, *dl, *tlog, *dxacc;
+  float2* part;
+  double* sums;
+  __nv_bfloat16 *xc, *g;
+};
+
+size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs* w) {
+  Sections s{static_cast<uint8_t*>(base)};
+  *w = CeWs{};
+  w->count = s.take<int>(1);
+  w->ticket = s.take<unsigned>(1);
+  w->rows = s.take<int>(M);
+  w->tgt = s.take<int>(M);
+  w->xc = s.take<__nv_bfloat16>(static_cast<size_t>(M) * D);
+  if (!grad) {
+    w->part = s.take<float2>(static_cast<size_t>(2 * ceil_div64(V, kCeTileRows)) * M);
+    w->tlog = s.take<float>(M);
+    w->sums = s.take<double>(ceil_div64(M, 32));
+  } else {
+    const int64_t cols = ce_piece(M, V);
+    const int64_t m_pad = ceil_div64(M, 512) * 512;
+    w->lse2 = s.take<float>(M);
+    w->dl = s.take<float>(M);
+    w->g = s.take<__nv_bfloat16>(static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8));
+    w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
+  }
+  return s.at;
+}
+
+// Sizes that the kernels' 32-bit coordinates and unit counts hold.
+gbf_status_t check_ce(const void* x, const void* w, const void* targets, int index_type,
+                      int64_t M, int64_t V, int64_t D, float alpha) {
+  gbf_status_t st = check_ids(targets, index_type, M, V, D);
+  if (st != GBF_OK) return st;
+  if (!x || !w || !std::isfinite(alpha)) return GBF_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16)) return GBF_ERR_MISALIGNED;
+  if (V < 1 || D < 8 || M > (int64_t(1) << 24) || V > (int64_t(1) << 26) || D > (int64_t(1) << 20))
+    return GBF_ERR_UNSUPPORTED_SHAPE;
+  const int64_t m = ceil_div64(M, 256), v = ceil_div64(V, 256), d = ceil_div64(D, 256);
+  if (m * v > kMaxInt / 2 || m * d * 16 > kMaxInt / 2 || v * d > kMaxInt / 2)
+    return GBF_ERR_UNSUPPORTED_SHAPE;
+  return GBF_OK;
+}
+
+// K-major operand: rows of D values, 64 x 128 boxes.
+bool ce_map_k(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, kBK, 128,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Operand with one row per k: 64 x 64 boxes.
+bool ce_map_mn(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, 64, kBK,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool ce_map_out(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, 32, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool ce_map_out_f32(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, inner, outer, inner * 4, 16, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// One product over at most M rows: as many CTAs as units of work, or all pairs.
+gbf_status_t run_ce_gemm(const CeJob& job, const CeEnd& end, int64_t rows, int64_t n,
+                         const DeviceInfo& dev, unsigned* err, cudaStream_t s) {
+  const int streams = job.splits > 1 ? 1 : ce_streams(rows, n);
+  const int64_t units = ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, kCeTileRows) * job.splits;
+  const int grid = 2 * static_cast<int>(std::min<int64_t>(units, dev.pairs));
+  return cuda_status(launch_ce_gemm(job, end, streams, grid, lib_ctl(err, grid), s));
+}
+
 }  // namespace
 
 size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
@@ -71,6 +181,12 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
       if (M > kMaxInt) return 0;
       return align256(static_cast<size_t>(clip_launches(static_cast<int>(M))) *
                       clip_ctas(kMaxSms) * 3 * sizeof(double));
+    case GBF_OP_LINEAR_CE:
+    case GBF_OP_LINEAR_CE_GRAD: {
+      if (M > (int64_t(1) << 24) || N > (int64_t(1) << 26) || K > (int64_t(1) << 20)) return 0;
+      CeWs w;
+      return ce_sections(nullptr, M, N, K, op == GBF_OP_LINEAR_CE_GRAD, &w);
+    }
     default: return 0;
   }
 }
@@ -152,6 +268,167 @@ gbf_status_t gbf_clip_grad_norm(const void* const* grads, void* const* out, cons
                                            static_cast<double*>(workspace),
                                            dev->sms < kMaxSms ? dev->sms : kMaxSms,
                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, int index_type,
+                           float* loss, float* lse, float* mean, int64_t M, int64_t V, int64_t D,
+                           float alpha, void* workspace, size_t workspace_bytes,
+                           gbf_stream_t stream) {
+  gbf_status_t st = check_ce(x, w, targets, index_type, M, V, D, alpha);
+  if (st != GBF_OK) return st;
+  if (!loss || !lse) return GBF_ERR_INVALID_ARG;
+  if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(mean, 4) || !aligned(workspace, 16))
+    return GBF_ERR_MISALIGNED;
+  CeWs ws;
+  const size_t need = ce_sections(workspace, M, V, D, false, &ws);
+  if (!workspace || workspace_bytes < need) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) return mean ? cuda_status(cudaMemsetAsync(mean, 0, 4, s)) : GBF_OK;
+  CePrep p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.xc = ws.xc;
+  p.loss = loss;
+  p.lse_out = lse;
+  p.count = ws.count;
+  p.rows = ws.rows;
+  p.tgt = ws.tgt;
+  p.ticket = ws.ticket;
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.D = static_cast<int>(D);
+  CeJob job{};
+  if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+      !ce_map_k(&job.b[0], w, D, V, D))
+    return GBF_ERR_CUDA;
+  job.o = job.a[0];  // not used: the ending's results are not a tile
+  job.mode = kCeLse;
+  job.cols = p.V;
+  job.d = p.D;
+  job.splits = 1;
+  CeEnd end{};
+  end.count = ws.count;
+  end.tgt = ws.tgt;
+  end.part = ws.part;
+  end.tlog = ws.tlog;
+  end.c2 = alpha * 1.4426950408889634f;
+  end.M = p.M;
+  CeJoin join{};
+  join.count = ws.count;
+  join.rows = ws.rows;
+  join.part = ws.part;
+  join.tlog = ws.tlog;
+  join.ticket = ws.ticket;
+  join.sums = ws.sums;
+  join.loss = loss;
+  join.lse = lse;
+  join.mean = mean;
+  join.alpha = alpha;
+  join.M = p.M;
+  join.parts = static_cast<int>(2 * ceil_div64(V, kCeTileRows));
+  if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
+      GBF_OK)
+    return st;
+  if ((st = run_ce_gemm(job, end, M, V, *dev, err, s)) != GBF_OK) return st;
+  return cuda_status(launch_ce_join(join, s));
+}
+
+gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* targets, int index_type,
+                                const float* lse, const float* dloss, void* dx, void* dw,
+                                int64_t M, int64_t V, int64_t D, float alpha, float scale,
+                                int reduction, void* workspace, size_t workspace_bytes,
+                                gbf_stream_t stream) {
+  gbf_status_t st = check_ce(x, w, targets, index_type, M, V, D, alpha);
+  if (st != GBF_OK) return st;
+  if (!lse || (!dx && !dw) || (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
+    return GBF_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16) ||
+      !aligned(workspace, 16))
+    return GBF_ERR_MISALIGNED;
+  CeWs ws;
+  const size_t need = ce_sections(workspace, M, V, D, true, &ws);
+  if (!workspace || workspace_bytes < need) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return dw ? cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, s)) : GBF_OK;
+  CePrep p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.xc = ws.xc;
+  p.lse_in = lse;
+  p.dloss = dloss;
+  p.dx = static_cast<__nv_bfloat16*>(dx);
+  p.count = ws.count;
+  p.rows = ws.rows;
+  p.tgt = ws.tgt;
+  p.lse2 = ws.lse2;
+  p.dl = ws.dl;
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.D = static_cast<int>(D);
+  if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
+      GBF_OK)
+    return st;
+  const int64_t piece = ce_piece(M, V);
+  const int64_t ld = ceil_div64(piece, 8) * 8;
+  const int64_t m_pad = ceil_div64(M, 512) * 512;
+  const int splits = ce_splits(M, D, piece);
+  CeEnd end{};
+  end.count = ws.count;
+  end.tgt = ws.tgt;
+  end.lse2 = ws.lse2;
+  end.dl = ws.dl;
+  end.c2 = alpha * 1.4426950408889634f;
+  end.scale = alpha * scale;
+  end.mean = reduction == GBF_REDUCE_MEAN;
+  end.M = p.M;
+  end.m_pad = static_cast<int>(m_pad);
+  for (int64_t v0 = 0; v0 < V; v0 += piece) {
+    const int64_t cols = std::min(piece, V - v0);
+    CeJob job{};
+    job.cols = static_cast<int>(cols);
+    job.v0 = static_cast<int>(v0);
+    job.d = p.D;
+    job.splits = 1;
+    job.mode = kCeGrad;
+    if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+        !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g, cols, M, ld))
+      return GBF_ERR_CUDA;
+    if ((st = run_ce_gemm(job, end, M, cols, *dev, err, s)) != GBF_OK) return st;
+    if (dx) {
+      job.mode = kCeDx;
+      job.splits = splits;
+      job.add = v0 > 0;
+      if (!ce_map_k(&job.a[0], ws.g, cols, M, ld) || !ce_map_mn(&job.b[0], w, D, V, D) ||
+          !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
+        return GBF_ERR_CUDA;
+      if ((st = run_ce_gemm(job, end, M, D, *dev, err, s)) != GBF_OK) return st;
+    }
+    if (dw) {
+      job.mode = kCeDw;
+      job.splits = 1;
+      if (!ce_map_mn(&job.a[0], ws.g, cols, M, ld) || !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
+          !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_out(&job.o, dw, D, V, D))
+        return GBF_ERR_CUDA;
+      if ((st = run_ce_gemm(job, end, cols, D, *dev, err, s)) != GBF_OK) return st;
+    }
+  }
+  if (!dx) return GBF_OK;
+  CeDxOut out{};
+  out.count = ws.count;
+  out.rows = ws.rows;
+  out.acc = ws.dxacc;
+  out.dx = p.dx;
+  out.scale = end.scale;
+  out.mean = end.mean;
+  out.m_pad = end.m_pad;
+  out.splits = splits;
+  out.D = p.D;
+  return cuda_status(launch_ce_dx(out, p.M, dev->sms, s));
 }
 
 }  // extern "C"

@@ -153,6 +153,71 @@ cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const
                                   const int* types, int n, float max_norm, float eps, float* norm,
                                   double* partial, int sms, cudaStream_t stream);
 
+// Linear cross entropy (linear_ce.cu).  One product of the kernel with its
+// ending; the scored rows are numbered 0 .. count-1 in their order.
+enum CeMode { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
+struct CeJob {
+  // a[1] / b[1]: x itself, where it is an operand, for when every row is
+  // scored; [0] the gathered rows (or the operand's only map)
+  CUtensorMap a[2], b[2], o;
+  int mode;
+  int cols;    // columns of the vocabulary: all (kCeLse) or the piece's
+  int v0;      // first column of the piece
+  int d;       // hidden width
+  int splits;  // parts of K (kCeDx), each with its own fp32 buffer
+  int add;     // kCeDx: add to the buffer (a later piece)
+};
+struct CeEnd {
+  const int* count;   // scored rows
+  const int* tgt;     // [count] targets
+  const float* lse2;  // [count] lse / ln 2
+  const float* dl;    // [count] gradient of each loss
+  float2* part;       // [2 per column tile][M] (maximum, sum), powers of two
+  float* tlog;        // [count] the targets' products
+  float c2;           // alpha / ln 2
+  float scale;        // of dw
+  int mean;           // divide by the number of scored rows
+  int M;
+  int m_pad;          // rows between the splits' fp32 buffers
+};
+struct CePrep {
+  const __nv_bfloat16* x;
+  __nv_bfloat16* xc;      // gathered rows
+  const float* lse_in;    // gradient: the forward's lse
+  const float* dloss;     // gradient, may be null (1)
+  float *loss, *lse_out;  // forward
+  __nv_bfloat16* dx;      // gradient: zero rows where not scored
+  int *count, *rows, *tgt;
+  unsigned* ticket;
+  float *lse2, *dl;
+  int M, V, D, rows_per;
+};
+struct CeJoin {
+  const int* count;
+  const int* rows;
+  const float2* part;
+  const float* tlog;
+  unsigned* ticket;
+  double* sums;  // per 32 rows
+  float *loss, *lse, *mean;
+  float alpha;
+  int M, parts;
+};
+struct CeDxOut {
+  const int* count;
+  const int* rows;
+  const float* acc;
+  __nv_bfloat16* dx;
+  float scale;
+  int mean, m_pad, splits, D;
+};
+cudaError_t launch_ce_gemm(const CeJob& job, const CeEnd& end, int streams, int grid,
+                           const KernelCtl& ctl, cudaStream_t stream);
+cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
+                           cudaStream_t stream);
+cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream);
+cudaError_t launch_ce_dx(const CeDxOut& p, int M, int sms, cudaStream_t stream);
+
 // ---- shared with the other entry-point files (api.cu) ---------------------------
 // The current device and the address of its error word (a GBF_* status).
 int lib_device(const DeviceInfo** info, unsigned** err);

@@ -1,0 +1,674 @@
+// linear_ce.cu -- softmax cross entropy of a linear head over a large
+// vocabulary, without the logits in memory, and its gradients.
+//
+//   l[m][v] = alpha * sum_d x[m][d] w[v][d]
+//   lse[m] = log sum_v exp(l[m][v]),   loss[m] = lse[m] - l[m][t_m]
+//   G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - [v = t_m])
+//   dx = alpha * scale * G W,   dw = alpha * scale * G^T X
+//
+// One matrix-product kernel (ce_gemm_kernel) with four endings does the work.
+// Its main loop is the CTA-pair form of gemm_pair.cu: 256 x 256 tiles on two
+// SMs (tcgen05.mma.cta_group::2), TMA-fed, one or two MMA streams.
+//   kLse    the logits' tile ends as one (maximum, sum of powers) per row and
+//           128 columns, and the target's logit: 8 bytes for 128 logits;
+//   kGrad   the logits again, ending as G in bf16 for a piece of the
+//           vocabulary;
+//   kDx     G W over the piece, added to an fp32 buffer;
+//   kDw     G^T X, the rows of dw of the piece, complete: written once.
+// Rows whose target is outside [0, V) are not scored: they take part in
+// nothing.  ce_prep_kernel gathers the scored rows' x when there are others,
+// so masked prompts cost no products, and whatever their rows of x hold (NaN
+// included) reaches no result.
+//
+// G is rounded to bf16 without the mean's factor: the factor multiplies the
+// fp32 sums, so it adds no rounding of its own.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gbf {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLn2 = 0.69314718055994531;
+
+__device__ __forceinline__ float pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kCeThreads = 384;        // warps 0-3 roles, 4-11 ending
+constexpr int kCeTile = 256;           // rows and columns of a pair's tile
+constexpr int kCeABytes = kBM * kBK * 2;   // 16 KB: this CTA's 128 rows of A
+constexpr int kCeBBytes = 128 * kBK * 2;   // 16 KB: this CTA's half of B
+constexpr int kCeGroup = 8;            // raster group (units of rows)
+
+template <int STREAMS>
+struct CeCfg {
+  static constexpr int kStageBytes = STREAMS * kCeABytes + kCeBBytes;
+  static constexpr int kStages = STREAMS == 2 ? 4 : 6;
+  static constexpr int kBarBytes = 1024;
+  static constexpr int kStagingBytes = 8 * 2 * kStageChunkBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+// A unit of work: STREAMS row tiles x one column tile x a range of K blocks.
+struct CeUnit {
+  int mp, nb, split, kb0, kb1;
+};
+
+struct CeShape {
+  int m_units, n_tiles, splits, num_kb, total;
+};
+
+__device__ __forceinline__ CeShape ce_shape(const CeJob& j, int count, int streams) {
+  CeShape s;
+  const int rows = j.mode == kCeDw ? j.cols : count;
+  const int n = (j.mode == kCeLse || j.mode == kCeGrad) ? j.cols : j.d;
+  const int k = j.mode == kCeDw ? count : (j.mode == kCeDx ? j.cols : j.d);
+  s.m_units = (rows + kCeTile * streams - 1) / (kCeTile * streams);
+  s.n_tiles = (n + kCeTile - 1) / kCeTile;
+  s.splits = j.splits;
+  s.num_kb = (k + kBK - 1) / kBK;
+  s.total = s.m_units * s.n_tiles * s.splits;
+  return s;
+}
+
+__device__ __forceinline__ CeUnit ce_unit(const CeShape& s, int t) {
+  CeUnit u;
+  const int tiles = s.m_units * s.n_tiles;
+  u.split = t / tiles;
+  tile_coords(t - u.split * tiles, s.m_units, s.n_tiles, u.mp, u.nb, kCeGroup);
+  u.kb0 = static_cast<int>(static_cast<int64_t>(u.split) * s.num_kb / s.splits);
+  u.kb1 = static_cast<int>(static_cast<int64_t>(u.split + 1) * s.num_kb / s.splits);
+  return u;
+}
+
+// One warp's 32 rows x 32 columns of fp32 to the map's tensor, stored or added
+// there by the TMA engine, through the warp's two staging buffers (16 columns
+// each).  Every element is added to by one warp of one launch, so the sums do
+// not depend on timing.
+__device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int& flip, const uint32_t (&v)[32],
+                                              const CUtensorMap* map, int row0, int col0, int n,
+                                              bool add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint8_t* buf = bufs + flip * kStageChunkBytes;
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = v[16 * h + j];
+    stage_row32(buf, lane, w);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (col0 + 16 * h < n) {
+        if (add) tma_add_2d(map, buf, col0 + 16 * h, row0);
+        else tma_store_2d(map, buf, col0 + 16 * h, row0, policy_evict_last());
+      }
+      bulk_commit();
+    }
+    flip ^= 1;
+  }
+}
+
+template <int STREAMS>
+__global__ void __launch_bounds__(kCeThreads, 1)
+    ce_gemm_kernel(const __grid_constant__ CeJob j, const CeEnd e, const KernelCtl kctl) {
+  using Cfg = CeCfg<STREAMS>;
+  constexpr int kStages = Cfg::kStages;
+  constexpr int kLoadBytes = STREAMS * kCeABytes + kCeBBytes;  // into one CTA's stage
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* stages = smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * Cfg::kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+  uint8_t* staging = smem + kStages * Cfg::kStageBytes + Cfg::kBarBytes;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: the even CTA, which issues the MMAs
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int npairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], STREAMS);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
+    }
+    mbar_init(done, STREAMS);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&j.a[0]);
+    tma_prefetch_desc(&j.b[0]);
+    tma_prefetch_desc(&j.o);
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, nullptr};
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  // the number of scored rows is an output of the kernel before
+  griddep_wait();
+  const int count = *e.count;
+  const int all = count == e.M ? 1 : 0;  // every row is scored: x itself, not the gathered rows
+  const CeShape sh = ce_shape(j, count, STREAMS);
+  const bool a_mn = j.mode == kCeDw;                      // A is read along its columns
+  const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;   // B holds one row per k
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");  // the gathered rows: plain stores
+      const CUtensorMap* ma = &j.a[(j.mode == kCeLse || j.mode == kCeGrad) ? all : 0];
+      const CUtensorMap* mb = &j.b[j.mode == kCeDw ? all : 0];
+      uint32_t fills[kStages];
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) fills[i] = 0;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int t = pair; t < sh.total && ok; t += npairs) {
+        const CeUnit u = ce_unit(sh, t);
+        const int n0 = u.nb * kCeTile + static_cast<int>(rank) * 128;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!wait_bar(&empty[s], ph ^ 1, ctl, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = stages + s * Cfg::kStageBytes;
+          uint8_t* sb = sa + STREAMS * kCeABytes;
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * kLoadBytes);
+#pragma unroll
+          for (int i = 0; i < STREAMS; ++i) {
+            const int m0 = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM;
+            if (a_mn) {
+              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, m0, kb * kBK);
+              tma_load_2d_pair(sa + i * kCeABytes + 8192, ma, bar, m0 + 64, kb * kBK);
+            } else {
+              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, kb * kBK, m0);
+            }
+          }
+          if (b_mn) {
+            const int k0 = (j.mode == kCeDx ? j.v0 : 0) + kb * kBK;
+            tma_load_2d_pair(sb, mb, bar, n0, k0);
+            tma_load_2d_pair(sb + 8192, mb, bar, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sb, mb, bar, kb * kBK, j.v0 + n0);
+          }
+          fills[s]++;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (ok) {
+        for (int i = 0; i < kStages; ++i)
+          if (fills[i]) wait_bar(&empty[i], (fills[i] - 1) & 1, ctl, kSiteDrain, false);
+      } else {
+        const uint64_t t0 = globaltimer_ns();  // let the copies in flight land (bounded)
+        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers (even CTA)
+    // Two streams: warp 1 the first, warp 2 the second row tile of every unit,
+    // each in its own accumulator.  One stream: warp 1, accumulators in turn.
+    const int st = warp - 1;
+    if (lane == 0 && leader && st < STREAMS) {
+      const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int l = 0;
+      for (int t = pair; t < sh.total && ok; t += npairs, ++l) {
+        const CeUnit u = ce_unit(sh, t);
+        const int acc = STREAMS == 2 ? st : (l & 1);
+        const int use = STREAMS == 2 ? l : (l >> 1);
+        const uint32_t d = tmem_base + acc * 256;
+        if (!wait_bar(&tempty[acc], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
+        tc_fence_after();
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
+          const uint32_t a0 = s0 + st * kCeABytes;
+          const uint32_t b0 = s0 + STREAMS * kCeABytes;
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            const uint64_t ad = a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(a0 + k * 32, 16, 1024);
+            const uint64_t bd = b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(b0 + k * 32, 16, 1024);
+            mma_ss_pair(d, ad, bd, idesc, (kb != u.kb0 || k != 0) ? 1u : 0u);
+          }
+          mma_commit_pair(&empty[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (!(kctl.inject && l == 0)) mma_commit_pair(&tfull[acc], 0x3);
+      }
+      mma_commit_pair(done, 1);
+      wait_bar(done, 0, ctl, kSiteDrain, false);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ ending (both CTAs)
+    const int q = warp & 3;
+    const int half = (warp - 4) >> 2;  // columns 128 * half .. of the tile
+    const uint64_t pol = l2_evict_first_policy();
+    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
+                                       mapa_shared(smem_u32(&tempty[1]), 0)};
+    uint8_t* my_staging = staging + (warp - 4) * 2 * kStageChunkBytes;
+    int flip = 0;
+    const float out_scale = e.mean ? e.scale / static_cast<float>(max(count, 1)) : e.scale;
+    int local = 0;
+    for (int t = pair; t < sh.total; t += npairs) {
+      const CeUnit u = ce_unit(sh, t);
+      bool ok = true;
+#pragma unroll 1
+      for (int i = 0; i < STREAMS && ok; ++i, ++local) {
+        const int acc_i = local & 1;
+        const uint32_t aph = (local >> 1) & 1;
+        const int row = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM + q * 32 + lane;
+        const bool row_ok = row < count;
+        int tgt = -1;
+        float lse2 = 0.0f, dl = 0.0f;
+        if ((j.mode == kCeLse || j.mode == kCeGrad) && row_ok) {
+          tgt = e.tgt[row] - j.v0 - u.nb * kCeTile - half * 128;  // column of the target here
+          if (j.mode == kCeGrad) {
+            lse2 = e.lse2[row];
+            dl = e.dl[row];
+          }
+        }
+        if (!wait_bar(&tfull[acc_i], aph, ctl, kSiteEpiAccFull)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tb =
+            tmem_base + acc_i * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+        const int tile_col = u.nb * kCeTile + half * 128;
+        float m = -INFINITY, sum = 0.0f;  // kLse
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          const int col0 = tile_col + c * 32;
+          uint32_t v[32];
+          tmem_ld32(tb + c * 32, v);
+          tmem_wait_ld();
+          if (c == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (leader) mbar_arrive(&tempty[acc_i]);
+              else mbar_arrive_cluster(tempty_leader[acc_i]);
+            }
+          }
+          if (j.mode == kCeLse) {
+            if (col0 < j.cols) {
+              float x[32];
+              float top = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) {
+                x[k] = __uint_as_float(v[k]) * e.c2;
+                if (col0 + k >= j.cols) x[k] = -INFINITY;
+                top = fmaxf(top, x[k]);
+              }
+              if (static_cast<unsigned>(tgt - c * 32) < 32u) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (tgt - c * 32 == k) e.tlog[row] = __uint_as_float(v[k]);
+              }
+              const float m2 = fmaxf(m, top);
+              const float ref = m2 == -INFINITY ? 0.0f : m2;  // no -inf - -inf
+              float add = 0.0f;
+#pragma unroll
+              for (int k = 0; k < 32; ++k) add += pow2(x[k] - ref);
+              sum = fmaf(sum, pow2(m - ref), add);
+              m = m2;
+            }
+          } else if (j.mode == kCeGrad) {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float g[2];
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const float p = pow2(fmaf(__uint_as_float(v[2 * k + h]), e.c2, -lse2));
+                g[h] = dl * (tgt - c * 32 == 2 * k + h ? p - 1.0f : p);
+                if (!row_ok) g[h] = 0.0f;  // the rows up to a full K block of kDw
+              }
+              w[k] = pack_bf16x2(g[0], g[1]);
+            }
+            store_chunk32(my_staging, flip, w, &j.o, row - lane, col0, e.M, j.cols, pol);
+          } else if (j.mode == kCeDx) {
+            if (u.kb0 == u.kb1) {  // a split without a K block of a short piece
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] = 0u;
+            }
+            put_chunk_f32(my_staging, flip, v, &j.o, u.split * e.m_pad + row - lane, col0, j.d,
+                          j.add != 0);
+          } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float lo = __uint_as_float(v[2 * k]) * out_scale;
+              const float hi = __uint_as_float(v[2 * k + 1]) * out_scale;
+              w[k] = u.kb0 < u.kb1 ? pack_bf16x2(lo, hi) : 0u;  // no rows: an empty sum
+            }
+            store_chunk32(my_staging, flip, w, &j.o, j.v0 + row - lane, col0, j.v0 + j.cols, j.d,
+                          pol);
+          }
+        }
+        if (j.mode == kCeLse && row_ok)
+          e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + row] = make_float2(m, sum);
+      }
+      if (!ok) break;
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal it or read its memory
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// ---------------------------------------------------------------- before and after
+
+constexpr int kPrepThreads = 256;
+
+// Sum over the CTA of a pair of counts.
+__device__ __forceinline__ int2 block_sum2(int a, int b) {
+  __shared__ int part[2][kPrepThreads / 32];
+  a = __reduce_add_sync(0xFFFFFFFFu, a);
+  b = __reduce_add_sync(0xFFFFFFFFu, b);
+  if ((threadIdx.x & 31) == 0) {
+    part[0][threadIdx.x >> 5] = a;
+    part[1][threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  int2 s = make_int2(0, 0);
+  for (int w = 0; w < kPrepThreads / 32; ++w) {
+    s.x += part[0][w];
+    s.y += part[1][w];
+  }
+  return s;
+}
+
+// CTA b takes the rows [b * rows_per, ...): it counts the scored rows before
+// them itself (all targets are a few KB in L2), so one launch lists the scored
+// rows in order, gathers their x where not all are scored, and writes the
+// results of the others (loss and lse 0, or a zero row of dx).
+template <typename Id>
+__global__ void __launch_bounds__(kPrepThreads)
+    ce_prep_kernel(const Id* __restrict__ targets, const CePrep p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per;
+  const int64_t r1 = min(r0 + p.rows_per, static_cast<int64_t>(p.M));
+  int total = 0, before = 0;
+  for (int64_t i = threadIdx.x; i < p.M; i += kPrepThreads) {
+    const int64_t t = static_cast<int64_t>(targets[i]);
+    const int scored = t >= 0 && t < p.V;
+    total += scored;
+    before += scored && i < r0;
+  }
+  const int2 sums = block_sum2(total, before);
+  total = sums.x;
+  int slot = sums.y;
+  const bool gather = total < p.M;
+  const int zero_to = (total + kBK - 1) / kBK * kBK;  // the last K block of kDw
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *p.count = total;
+    if (p.ticket) *p.ticket = 0u;
+  }
+  for (int64_t r = r0; r < r1; ++r) {
+    const int64_t t = static_cast<int64_t>(targets[r]);
+    if (t >= 0 && t < p.V) {
+      if (threadIdx.x == 0) {
+        p.rows[slot] = static_cast<int>(r);
+        p.tgt[slot] = static_cast<int>(t);
+        if (p.lse2) {
+          p.lse2[slot] = p.lse_in[r] * kLog2e;
+          p.dl[slot] = p.dloss ? p.dloss[r] : 1.0f;
+        }
+      }
+      if (gather)
+        for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
+          st_u4(p.xc + static_cast<int64_t>(slot) * p.D + c, ldg_u4(p.x + r * p.D + c));
+      ++slot;
+    } else if (p.dx) {
+      for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
+        st_u4(p.dx + r * p.D + c, make_uint4(0u, 0u, 0u, 0u));
+    } else if (p.loss && threadIdx.x == 0) {
+      p.loss[r] = 0.0f;
+      p.lse_out[r] = 0.0f;
+    }
+    if (gather && r >= total && r < zero_to)  // slots past the scored rows
+      for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
+        st_u4(p.xc + r * p.D + c, make_uint4(0u, 0u, 0u, 0u));
+  }
+}
+
+constexpr int kJoinThreads = 256;
+
+// (m, s) stands for s * 2^m.
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float ref = m == -INFINITY ? 0.0f : m;
+  return make_float2(m, fmaf(a.y, pow2(a.x - ref), b.y * pow2(b.x - ref)));
+}
+
+// 32 scored rows per CTA: adds up each row's partial sums, writes its loss and
+// lse; the last CTA adds the CTAs' sums of losses in order for the mean.
+__global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
+  __shared__ float2 part[kJoinThreads / 32][32];
+  __shared__ double sums[kJoinThreads / 32];
+  __shared__ bool last;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int count = *p.count;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 32 + lane;
+  float2 a = make_float2(-INFINITY, 0.0f);
+  if (row < count) {
+    const float2* src = p.part + row;
+    int n = warp;
+    constexpr int kAhead = 8, kStep = kJoinThreads / 32;
+    for (; n + (kAhead - 1) * kStep < p.parts; n += kAhead * kStep) {
+      float2 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) v[i] = src[static_cast<int64_t>(n + i * kStep) * p.M];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) a = join(a, v[i]);
+    }
+    for (; n < p.parts; n += kStep) a = join(a, src[static_cast<int64_t>(n) * p.M]);
+  }
+  part[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0) {
+    double loss = 0.0;
+    if (row < count) {
+#pragma unroll
+      for (int w = 1; w < kJoinThreads / 32; ++w) a = join(a, part[w][lane]);
+      // log2 of the sum in 64 bits: a confident row's loss is a small difference
+      const double lse = (static_cast<double>(a.x) + log2(static_cast<double>(a.y))) * kLn2;
+      loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
+      const int r = p.rows[row];
+      p.loss[r] = static_cast<float>(loss);
+      p.lse[r] = static_cast<float>(lse);
+    }
+    if (p.mean) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+      if (lane == 0) {
+        p.sums[blockIdx.x] = loss;
+        __threadfence();
+        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+      }
+    }
+  }
+  if (!p.mean) return;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double s = 0.0;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) s += __ldcg(p.sums + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) sums[warp] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) s += sums[w];
+    *p.mean = static_cast<float>(s / max(count, 1));
+  }
+}
+
+constexpr int kOutThreads = 128;
+
+// dx of the scored rows: the splits' sums added in order, scaled, rounded once.
+// A warp per 256 columns of a row.
+__global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int count = *p.count;
+  const float scale = p.mean ? p.scale / static_cast<float>(max(count, 1)) : p.scale;
+  const int segs = (p.D + 255) / 256;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kOutThreads / 32);
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kOutThreads / 32) + (threadIdx.x >> 5);
+       t < static_cast<int64_t>(count) * segs; t += step) {
+    const int64_t row = t / segs;
+    const int col = static_cast<int>(t - row * segs) * 256 + (threadIdx.x & 31) * 8;
+    if (col >= p.D) continue;
+    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < p.splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(
+          p.acc + (static_cast<int64_t>(s) * p.m_pad + row) * p.D + col);
+      const float4 x = __ldcs(src), y = __ldcs(src + 1);
+      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] *= scale;
+    st_u4(p.dx + static_cast<int64_t>(p.rows[row]) * p.D + col, pack8(f));
+  }
+}
+
+cudaLaunchConfig_t overlapped(int64_t grid, int threads, size_t smem, cudaStream_t stream,
+                              cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <int STREAMS>
+cudaError_t run_ce(const CeJob& job, const CeEnd& end, const KernelCtl& ctl, int grid,
+                   cudaStream_t stream) {
+  static std::atomic<uint64_t> mask{0};
+  auto kernel = ce_gemm_kernel<STREAMS>;
+  constexpr int smem = CeCfg<STREAMS>::kSmem;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = overlapped(grid, kCeThreads, smem, stream, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, job, end, ctl);
+}
+
+}  // namespace
+
+cudaError_t launch_ce_gemm(const CeJob& job, const CeEnd& end, int streams, int grid,
+                           const KernelCtl& ctl, cudaStream_t stream) {
+  return streams == 2 ? run_ce<2>(job, end, ctl, grid, stream)
+                      : run_ce<1>(job, end, ctl, grid, stream);
+}
+
+cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
+                           cudaStream_t stream) {
+  // eight CTAs per SM; one row each up to that
+  const int64_t most = static_cast<int64_t>(sms) * 8;
+  p.rows_per = static_cast<int>((p.M + most - 1) / most);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg =
+      overlapped((p.M + p.rows_per - 1) / p.rows_per, kPrepThreads, 0, stream, attr);
+  return ids64 ? cudaLaunchKernelEx(&cfg, ce_prep_kernel<int64_t>,
+                                    static_cast<const int64_t*>(targets), p)
+               : cudaLaunchKernelEx(&cfg, ce_prep_kernel<int>, static_cast<const int*>(targets), p);
+}
+
+cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped((p.M + 31) / 32, kJoinThreads, 0, stream, attr);
+  return cudaLaunchKernelEx(&cfg, ce_join_kernel, p);
+}
+
+cudaError_t launch_ce_dx(const CeDxOut& p, int M, int sms, cudaStream_t stream) {
+  const int64_t warps = static_cast<int64_t>(M) * ((p.D + 255) / 256);
+  const int64_t ctas = std::min<int64_t>((warps + 3) / 4, static_cast<int64_t>(sms) * 16);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped(ctas, kOutThreads, 0, stream, attr);
+  return cudaLaunchKernelEx(&cfg, ce_dx_kernel, p);
+}
+
+}  // namespace gbf

@@ -78,3 +78,33 @@ def test_workspace_sizes():
     assert 0 < small < gbf.gbf_workspace_size("embedding_grad", 65536, 32000, 1024, True)
     assert gbf.gbf_workspace_size("clip_grad_norm", 1, 0, 0, True) == 152 * 8 * 24
     assert gbf.gbf_workspace_size("clip_grad_norm", 513, 0, 0, True) == 2 * 152 * 8 * 24
+
+
+def ce_args(**change):
+    need = gbf.gbf_workspace_size("linear_ce", 4, 10, 16, True)
+    return {**dict(x=P, w=P, targets=P, loss=P, lse=P, mean=None, M=4, V=10, D=16, workspace=P, workspace_bytes=need),
+            **change}
+
+
+BAD_HEADS = [
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(targets=None), INVALID), (dict(M=-1), INVALID),
+    (dict(alpha=math.inf), INVALID), (dict(alpha=math.nan), INVALID), (dict(index_type=2), INVALID),
+    (dict(x=P + 8), MISALIGNED), (dict(w=P + 8), MISALIGNED), (dict(targets=P + 4), MISALIGNED),
+    (dict(lse=P + 2), MISALIGNED), (dict(workspace=P + 8), MISALIGNED), (dict(D=12), SHAPE), (dict(D=0), SHAPE),
+    (dict(V=0), SHAPE), (dict(M=2 ** 24 + 1), SHAPE), (dict(V=2 ** 26 + 1), SHAPE), (dict(D=2 ** 20 + 8), SHAPE),
+    (dict(M=2 ** 24, V=2 ** 26), SHAPE), (dict(workspace=None), WORKSPACE), (dict(workspace_bytes=64), WORKSPACE)]
+
+
+@pytest.mark.parametrize("change,want", BAD_HEADS + [
+    (dict(loss=None), INVALID), (dict(lse=None), INVALID), (dict(loss=P + 1), MISALIGNED), (dict(mean=P + 1), MISALIGNED)])
+def test_linear_ce_refuses(change, want):
+    assert gbf.linear_ce(**ce_args(**change), stream=0, raise_on_error=False) == want
+
+
+@pytest.mark.parametrize("change,want", BAD_HEADS + [
+    (dict(lse=None), INVALID), (dict(dx=None, dw=None), INVALID), (dict(reduction=2), INVALID),
+    (dict(dx=P + 8), MISALIGNED), (dict(dw=P + 8), MISALIGNED), (dict(dloss=P + 2), MISALIGNED)])
+def test_linear_ce_grad_refuses(change, want):
+    need = gbf.gbf_workspace_size("linear_ce_grad", 4, 10, 16, True)
+    args = dict(x=P, w=P, targets=P, lse=P, dloss=None, dx=P, dw=P, M=4, V=10, D=16, workspace=P, workspace_bytes=need)
+    assert gbf.linear_ce_grad(**{**args, **change}, stream=0, raise_on_error=False) == want
