@@ -6,22 +6,23 @@
 //
 // Gradient: dtable[v] (+)= scale * sum over {m : id_m = v} of dout[m], in
 // fp32, in the order of m.  Summing with atomics would add in an order that
-// changes from run to run, so the positions are sorted by id first (a stable
-// radix sort inside one cluster of CTAs) and the sorted list is cut into
-// pieces of equal length, however the ids repeat:
-//   1. embed_sort_kernel: (id, m) sorted by id, and a bit per table row that
-//      occurs;
+// changes from run to run, so the positions are sorted by id first and the
+// sorted list is cut into pieces of equal length, however the ids repeat:
+//   1. embed_rank_kernel (up to 8192 positions: each placed by comparison with
+//      all others) or embed_sort_kernel (a stable radix sort inside one
+//      cluster of CTAs): the positions in the order of (id, m);
 //   2. embed_sum_kernel: one piece of the list x 1024 columns per CTA.  A run
 //      of equal ids inside the piece is summed and written; the part of a run
 //      that continues from the previous piece or into the next one goes to the
-//      workspace in fp32.  Without accumulation further CTAs write the zero
-//      rows of the ids that do not occur;
+//      workspace in fp32.  Without accumulation further CTAs of kernel 1 or 2
+//      write the zero rows of the ids that do not occur;
 //   3. embed_join_kernel: the runs over several pieces, their parts added in
 //      order, written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -98,6 +99,7 @@ __global__ void __launch_bounds__(kSortThreads)
     embed_sort_kernel(const Id* __restrict__ ids, int M, int V, int passes, int digit_bits,
                       int* key0, int* idx0, int* key1, int* idx1, unsigned* present) {
   extern __shared__ int sort_smem[];
+  __shared__ int warp_sum[kSortWarps];
   int* hist = sort_smem;                            // [warps][digits]
   int* total = sort_smem + kSortWarps * kMaxDigits;  // this CTA's digit counts
   int* base = total + kMaxDigits;                    // where this CTA's digits begin
@@ -145,42 +147,47 @@ __global__ void __launch_bounds__(kSortThreads)
     __syncthreads();
     // per digit: this CTA's count, and each warp's offset within it
     for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+      int n[kSortWarps];
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) n[w] = hist[w * kMaxDigits + d];
       int sum = 0;
+#pragma unroll
       for (int w = 0; w < kSortWarps; ++w) {
-        const int n = hist[w * kMaxDigits + d];
         hist[w * kMaxDigits + d] = sum;
-        sum += n;
+        sum += n[w];
       }
       total[d] = sum;
     }
     cluster_sync_all();  // every CTA's counts are written
-    // per digit: the count over all CTAs and that of the CTAs before this one
-    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+    // per digit: the count over all CTAs and that of the CTAs before this one;
+    // then where the digit begins: a scan over the digits of each warp's 32 and
+    // over the warps
+    {
+      const int d = threadIdx.x;  // digits <= kSortThreads
       int all = 0, before = 0;
-      for (int c = 0; c < ctas; ++c) {
-        const int n = ld_dsmem_s32(mapa_shared(smem_u32(&total[d]), c));
-        if (c < rank) before += n;
-        all += n;
-      }
-      base[d] = all;
-      // parked until the scan below: where equal digits of this CTA begin
-      for (int w = 0; w < kSortWarps; ++w) hist[w * kMaxDigits + d] += before;
-    }
-    __syncthreads();
-    if (warp == 0) {  // exclusive scan of the digits' counts
-      int run = 0;
-      for (int d0 = 0; d0 < digits; d0 += 32) {
-        const int d = d0 + lane;
-        const int n = d < digits ? base[d] : 0;
-        int x = n;
+      if (d < digits) {
+        const uint32_t at = smem_u32(&total[d]);
+        int n[kSortCluster];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-          if (lane >= o) x += y;
+        for (int c = 0; c < kSortCluster; ++c)
+          n[c] = c < ctas ? ld_dsmem_s32(mapa_shared(at, c)) : 0;
+#pragma unroll
+        for (int c = 0; c < kSortCluster; ++c) {
+          if (c < rank) before += n[c];
+          all += n[c];
         }
-        if (d < digits) base[d] = run + x - n;
-        run += __shfl_sync(0xFFFFFFFFu, x, 31);
       }
+      int x = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) warp_sum[warp] = x;
+      __syncthreads();
+      int earlier = lane < warp ? warp_sum[lane] : 0;
+      earlier = __reduce_add_sync(0xFFFFFFFFu, earlier);
+      if (d < digits) base[d] = earlier + x - all + before;
     }
     __syncthreads();
     for (int i0 = lo; i0 < hi; i0 += 32) {
@@ -201,6 +208,75 @@ __global__ void __launch_bounds__(kSortThreads)
       }
     }
     cluster_sync_all();  // the pass is written before the next one reads it
+  }
+}
+
+// Up to 8192 positions: the place of each in the sorted list by comparing it
+// with all others, eight positions per warp (1021 positions: 2 us against 14 of
+// the radix sort, whose passes wait on one another; 8192: 5 against 17).  The
+// CTAs from `rank_ctas` on write the zero rows of dtable meanwhile: each looks
+// through the ids for those of its rows.
+constexpr int kRankThreads = 128;
+constexpr int kRankMax = 8192;
+constexpr int kRankEach = 8;
+constexpr int kZeroRows = 1024;  // rows looked for at a time
+
+template <typename Id>
+__global__ void __launch_bounds__(kRankThreads)
+    embed_rank_kernel(const Id* __restrict__ ids, int M, int V, int D, int rank_ctas, int* key_out,
+                      int* idx_out, __nv_bfloat16* __restrict__ dtable) {
+  __shared__ int keys[kRankMax];
+  griddep_launch_dependents();
+  griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= rank_ctas) {
+    unsigned* found = reinterpret_cast<unsigned*>(keys);
+    const int64_t ctas = gridDim.x - rank_ctas;
+    const int64_t me = blockIdx.x - rank_ctas;
+    const int64_t v0 = V * me / ctas, v1 = V * (me + 1) / ctas;
+    for (int64_t first = v0; first < v1; first += kZeroRows) {
+      const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), v1 - first));
+      for (int i = threadIdx.x; i < kZeroRows / 32; i += kRankThreads) found[i] = 0u;
+      __syncthreads();
+      for (int i = threadIdx.x; i < M; i += kRankThreads) {
+        const int64_t r = static_cast<int64_t>(ids[i]) - first;
+        if (r >= 0 && r < rows) atomicOr(&found[r >> 5], 1u << (r & 31));
+      }
+      __syncthreads();
+      for (int r = 0; r < rows; ++r) {
+        if ((found[r >> 5] >> (r & 31)) & 1u) continue;
+        for (int c = threadIdx.x * 8; c < D; c += kRankThreads * 8)
+          st_u4(dtable + (first + r) * D + c, make_uint4(0u, 0u, 0u, 0u));
+      }
+      __syncthreads();
+    }
+    return;
+  }
+  for (int i = threadIdx.x; i < M; i += kRankThreads) {
+    const int64_t id = static_cast<int64_t>(ids[i]);
+    keys[i] = (id >= 0 && id < V) ? static_cast<int>(id) : V;
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  const int e0 = (blockIdx.x * (kRankThreads / 32) + (threadIdx.x >> 5)) * kRankEach;
+  int k[kRankEach], before[kRankEach];
+#pragma unroll
+  for (int e = 0; e < kRankEach; ++e) {
+    k[e] = e0 + e < M ? keys[e0 + e] : 0;
+    before[e] = 0;
+  }
+  for (int j = lane; j < M; j += 32) {
+    const int kj = keys[j];
+#pragma unroll
+    for (int e = 0; e < kRankEach; ++e)
+      before[e] += kj < k[e] || (kj == k[e] && j < e0 + e) ? 1 : 0;
+  }
+#pragma unroll
+  for (int e = 0; e < kRankEach; ++e) {
+    const int at = __reduce_add_sync(0xFFFFFFFFu, before[e]);
+    if (lane == e && e0 + e < M) {
+      key_out[at] = k[e];
+      idx_out[at] = e0 + e;
+    }
   }
 }
 
@@ -225,12 +301,13 @@ struct SumArgs {
   int accumulate;
 };
 
+// `old`: the row's present values, where they are added to.
 __device__ __forceinline__ void write_row(const SumArgs& a, int64_t v, int col,
-                                          const float (&sum)[8]) {
+                                          const float (&sum)[8], const uint4& old) {
   __nv_bfloat16* p = a.dtable + v * a.D + col;
   float f[8];
   if (a.accumulate) {
-    unpack8(ld_u4(p), f);
+    unpack8(old, f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = fmaf(a.scale, sum[j], f[j]);
   } else {
@@ -285,13 +362,20 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   bool began = skey[0] != skey[1];  // the current run began in this piece
+  // eight positions' rows, and the table's rows that end a run among them, are
+  // loaded before the first is added
   constexpr int kAhead = 8;
   for (int i0 = 0; i0 < n; i0 += kAhead) {
-    uint4 v[kAhead];
+    uint4 v[kAhead], old[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (i0 + u < n && skey[i0 + u + 1] < a.V)
+    for (int u = 0; u < kAhead; ++u) {
+      if (i0 + u < n && skey[i0 + u + 1] < a.V) {
+        const int key = skey[i0 + u + 1];
         v[u] = ldg_u4(a.dout + static_cast<int64_t>(sidx[i0 + u]) * a.D + col);
+        if (a.accumulate && skey[i0 + u + 2] != key)
+          old[u] = ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u;
@@ -305,7 +389,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
       const bool ends = skey[i + 2] != key;
       if (ends || i + 1 == n) {
         if (began && ends)
-          write_row(a, key, col, sum);
+          write_row(a, key, col, sum, old[u]);
         else
           store_part((began ? a.tail : a.head) + static_cast<int64_t>(p) * a.D + col, sum);
         began = true;
@@ -329,24 +413,42 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a
   if (key >= a.V || a.key[next] != key) return;                     // the last run ends here
   const int64_t first = static_cast<int64_t>(p) * a.piece;
   if (a.key[first] == key && first > 0 && a.key[first - 1] == key) return;  // began earlier
+  // how many of the next pieces begin with the run: 128 looked at together
+  int more = 0;
+  for (;;) {
+    const int64_t at = next + (more + static_cast<int64_t>(threadIdx.x)) * a.piece;
+    const int here = __syncthreads_count(at < a.M && a.key[at] == key);
+    more += here;
+    if (here < kSumThreads) break;
+  }
   const int col = seg * kSegCols + threadIdx.x * 8;
   if (col >= a.D) return;
+  const uint4 old = a.accumulate ? ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col)
+                                 : make_uint4(0u, 0u, 0u, 0u);
   float sum[8];
-  {
-    const float4* t = reinterpret_cast<const float4*>(a.tail + static_cast<int64_t>(p) * a.D + col);
-    const float4 x = t[0], y = t[1];
-    sum[0] = x.x; sum[1] = x.y; sum[2] = x.z; sum[3] = x.w;
-    sum[4] = y.x; sum[5] = y.y; sum[6] = y.z; sum[7] = y.w;
+  auto part = [&](const float* base, int q, float4 (&f)[2]) {
+    const float4* t = reinterpret_cast<const float4*>(base + static_cast<int64_t>(q) * a.D + col);
+    f[0] = t[0];
+    f[1] = t[1];
+  };
+  float4 f[2];
+  part(a.tail, p, f);
+  sum[0] = f[0].x; sum[1] = f[0].y; sum[2] = f[0].z; sum[3] = f[0].w;
+  sum[4] = f[1].x; sum[5] = f[1].y; sum[6] = f[1].z; sum[7] = f[1].w;
+  constexpr int kAhead = 8;
+  for (int q0 = p + 1; q0 <= p + more; q0 += kAhead) {
+    float4 g[kAhead][2];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (q0 + u <= p + more) part(a.head, q0 + u, g[u]);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (q0 + u > p + more) break;
+      sum[0] += g[u][0].x; sum[1] += g[u][0].y; sum[2] += g[u][0].z; sum[3] += g[u][0].w;
+      sum[4] += g[u][1].x; sum[5] += g[u][1].y; sum[6] += g[u][1].z; sum[7] += g[u][1].w;
+    }
   }
-  for (int q = p + 1; q < a.pieces; ++q) {
-    const float4* t = reinterpret_cast<const float4*>(a.head + static_cast<int64_t>(q) * a.D + col);
-    const float4 x = t[0], y = t[1];
-    sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
-    sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
-    const int64_t end = static_cast<int64_t>(q + 1) * a.piece;
-    if (end >= a.M || a.key[end] != key) break;
-  }
-  write_row(a, key, col, sum);
+  write_row(a, key, col, sum, old);
 }
 
 // A launch that may begin while the previous kernel of the stream finishes:
@@ -375,18 +477,36 @@ int bit_length(int64_t x) {
 }
 
 template <typename Id>
+cudaError_t launch_rank(const Id* ids, int M, int V, int D, const EmbedGradWs& ws,
+                        __nv_bfloat16* zeros, int sms, cudaStream_t stream) {
+  constexpr int kPer = kRankThreads / 32 * kRankEach;
+  const int ranks = (M + kPer - 1) / kPer;
+  const int more = zeros ? std::min(V, sms * 8) : 0;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = overlapped(ranks + more, kRankThreads, 0, stream, attr);
+  return cudaLaunchKernelEx(&cfg, embed_rank_kernel<Id>, ids, M, V, D, ranks, ws.key0, ws.idx0,
+                            zeros);
+}
+
+template <typename Id>
 cudaError_t launch_sort(const Id* ids, int M, int V, const EmbedGradWs& ws, int* passes_out,
                         unsigned* present, cudaStream_t stream) {
+  static std::atomic<uint64_t> mask{0};  // devices on which the kernel's attribute is set
   auto kernel = embed_sort_kernel<Id>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kSortSmem));
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSortSmem));
+    if (e != cudaSuccess) return e;
+    mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
   const int bits = bit_length(V);  // keys 0 .. V
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   const int digit_bits = (bits + passes - 1) / passes;
-  // one CTA up to 2048 ids (two per thread), then as many as keep that, 8 at most
-  int ctas = 1;
-  while (ctas < kSortCluster && static_cast<int64_t>(ctas) * 2048 < M) ctas *= 2;
+  const int ctas = kSortCluster;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = overlapped(ctas, kSortThreads, kSortSmem, stream, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -429,10 +549,17 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
                                   bool accumulate, const EmbedGradWs& ws, int sms,
                                   cudaStream_t stream) {
   cudaError_t e;
-  int passes = 0;
-  unsigned* present = accumulate ? nullptr : ws.present;
-  e = ids64 ? launch_sort(static_cast<const int64_t*>(ids), M, V, ws, &passes, present, stream)
-            : launch_sort(static_cast<const int*>(ids), M, V, ws, &passes, present, stream);
+  int passes = 1;
+  const bool ranked = M <= kRankMax;
+  unsigned* present = accumulate || ranked ? nullptr : ws.present;
+  if (ranked) {
+    __nv_bfloat16* zeros = accumulate ? nullptr : dtable;
+    e = ids64 ? launch_rank(static_cast<const int64_t*>(ids), M, V, D, ws, zeros, sms, stream)
+              : launch_rank(static_cast<const int*>(ids), M, V, D, ws, zeros, sms, stream);
+  } else {
+    e = ids64 ? launch_sort(static_cast<const int64_t*>(ids), M, V, ws, &passes, present, stream)
+              : launch_sort(static_cast<const int*>(ids), M, V, ws, &passes, present, stream);
+  }
   if (e != cudaSuccess) return e;
   SumArgs a{};
   a.key = (passes & 1) ? ws.key0 : ws.key1;
@@ -452,7 +579,7 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
   a.accumulate = accumulate ? 1 : 0;
   const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
   int64_t zeros = 0;
-  if (!accumulate) {
+  if (present) {
     const int64_t warps = static_cast<int64_t>(V) * a.segs;
     zeros = std::min<int64_t>((warps + 3) / 4, static_cast<int64_t>(sms) * 16);
   }

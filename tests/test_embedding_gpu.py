@@ -161,3 +161,9 @@ def test_on_another_stream_and_in_a_graph(cuda_lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(first * 2, dtable)
+
+
+@pytest.mark.parametrize("M", [4097, 8191, 8192, 8193])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_where_the_way_of_sorting_changes(cuda_lib, M, accumulate):
+    test_gradient(cuda_lib, M, 1500, 64, "mixed", accumulate)
