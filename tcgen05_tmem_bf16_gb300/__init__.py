@@ -71,6 +71,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load the shared library (build it first with ``build.build()``)."""
     global _lib
+    if _lib is not None:  # every call comes through here
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -154,7 +156,8 @@ def _p(x):
 def _s(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
