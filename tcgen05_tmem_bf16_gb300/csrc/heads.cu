@@ -74,23 +74,21 @@ int64_t ce_piece(int64_t M, int64_t V) {
 
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row tiles per unit of work: two (one B tile for two MMA streams) or one,
-// whichever fills the rounds of units over the CTA pairs better; one stream
-// runs at about 0.9 of the rate of two.
-int ce_streams(int64_t rows, int64_t n) {
-  const int64_t n_tiles = ceil_div64(n, kCeTileRows);
-  const int64_t one = ceil_div64(ceil_div64(rows, kCeTileRows) * n_tiles, kCePairs);
-  const int64_t two = ceil_div64(ceil_div64(rows, 2 * kCeTileRows) * n_tiles, kCePairs);
-  return static_cast<double>(two) * 2.0 <= static_cast<double>(one) / 0.9 ? 2 : 1;
-}
+// Row tiles per unit of work: two that share a column tile, or a lone one where
+// there is no second.
+int ce_streams(int64_t M) { return M > kCeTileRows ? 2 : 1; }
 
-// Parts of K of the product for dx, where its tiles are fewer than the pairs:
-// each at least 8 K blocks long.
+// Parts of K of the product for dx, where its units of work are long next to
+// all work that its launch has for a pair: no part is longer than half of that,
+// or shorter than 8 K blocks.
 int ce_splits(int64_t M, int64_t D, int64_t cols) {
-  const int64_t tiles = ceil_div64(M, kCeTileRows) * ceil_div64(D, kCeTileRows);
-  const int64_t most = std::max<int64_t>(1, ceil_div64(cols, 64) / 8);
-  return static_cast<int>(std::min<int64_t>({kCePairs / std::max<int64_t>(tiles, 1) + (tiles > kCePairs ? 1 : 0),
-                                             most, 16}));
+  const int64_t rows = kCeTileRows * ce_streams(M);
+  const int64_t m = ceil_div64(M, rows), v = ceil_div64(cols, kCeTileRows);
+  const int64_t d = ceil_div64(D, kCeTileRows), k = ceil_div64(cols, 64);
+  const int64_t all = m * d * k + m * v * ceil_div64(D, 64) + ceil_div64(cols, rows) * d * ceil_div64(M, 64);
+  const int64_t half = std::max<int64_t>(1, all / kCePairs / 2);
+  return static_cast<int>(
+      std::max<int64_t>(1, std::min<int64_t>({ceil_div64(k, half), k / 8, 16})));
 }
 
 struct CeWs {
@@ -99,7 +97,7 @@ struct CeWs {
   float *lse2, *dl, *tlog, *dxacc;
   float2* part;
   double* sums;
-  __nv_bfloat16 *xc, *g;
+  __nv_bfloat16 *xc, *g[2];
 };
 
 size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs* w) {
@@ -113,13 +111,16 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
   if (!grad) {
     w->part = s.take<float2>(static_cast<size_t>(2 * ceil_div64(V, kCeTileRows)) * M);
     w->tlog = s.take<float>(M);
-    w->sums = s.take<double>(ceil_div64(M, 32));
+    w->sums = s.take<double>(ceil_div64(M, 8));  // one per CTA of the join
   } else {
     const int64_t cols = ce_piece(M, V);
     const int64_t m_pad = ceil_div64(M, 512) * 512;
     w->lse2 = s.take<float>(M);
     w->dl = s.take<float>(M);
-    w->g = s.take<__nv_bfloat16>(static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8));
+    // G of two pieces: one is written while the other's products run
+    const size_t g = static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8);
+    w->g[0] = s.take<__nv_bfloat16>(g);
+    w->g[1] = cols < V ? s.take<__nv_bfloat16>(g) : w->g[0];
     w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
   }
   return s.at;
@@ -159,13 +160,19 @@ bool ce_map_out_f32(CUtensorMap* m, const void* p, int64_t inner, int64_t outer)
                      CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// One product over at most M rows: as many CTAs as units of work, or all pairs.
-gbf_status_t run_ce_gemm(const CeJob& job, const CeEnd& end, int64_t rows, int64_t n,
+// One launch: a CTA pair per unit of work at most, with M rows scored.
+gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M,
                          const DeviceInfo& dev, unsigned* err, cudaStream_t s) {
-  const int streams = job.splits > 1 ? 1 : ce_streams(rows, n);
-  const int64_t units = ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, kCeTileRows) * job.splits;
+  const int streams = ce_streams(M);
+  int64_t units = 0;
+  for (const CeJob& j : launch.job) {
+    if (j.mode == kCeNone) continue;
+    const int64_t rows = j.mode == kCeDw ? j.cols : M;
+    const int64_t n = j.mode == kCeLse || j.mode == kCeGrad ? j.cols : launch.d;
+    units += ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, kCeTileRows) * j.splits;
+  }
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, dev.pairs));
-  return cuda_status(launch_ce_gemm(job, end, streams, grid, lib_ctl(err, grid), s));
+  return cuda_status(launch_ce_gemm(launch, end, streams, grid, lib_ctl(err, grid), s));
 }
 
 }  // namespace
@@ -299,14 +306,14 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   p.M = static_cast<int>(M);
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);
-  CeJob job{};
+  CeLaunch launch{};
+  launch.d = p.D;
+  CeJob& job = launch.job[1];
   if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
       !ce_map_k(&job.b[0], w, D, V, D))
     return GBF_ERR_CUDA;
-  job.o = job.a[0];  // not used: the ending's results are not a tile
   job.mode = kCeLse;
   job.cols = p.V;
-  job.d = p.D;
   job.splits = 1;
   CeEnd end{};
   end.count = ws.count;
@@ -331,7 +338,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
       GBF_OK)
     return st;
-  if ((st = run_ce_gemm(job, end, M, V, *dev, err, s)) != GBF_OK) return st;
+  if ((st = run_ce_gemm(launch, end, M, *dev, err, s)) != GBF_OK) return st;
   return cuda_status(launch_ce_join(join, s));
 }
 
@@ -387,35 +394,48 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   end.mean = reduction == GBF_REDUCE_MEAN;
   end.M = p.M;
   end.m_pad = static_cast<int>(m_pad);
-  for (int64_t v0 = 0; v0 < V; v0 += piece) {
-    const int64_t cols = std::min(piece, V - v0);
-    CeJob job{};
-    job.cols = static_cast<int>(cols);
-    job.v0 = static_cast<int>(v0);
-    job.d = p.D;
-    job.splits = 1;
-    job.mode = kCeGrad;
-    if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
-        !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g, cols, M, ld))
-      return GBF_ERR_CUDA;
-    if ((st = run_ce_gemm(job, end, M, cols, *dev, err, s)) != GBF_OK) return st;
-    if (dx) {
-      job.mode = kCeDx;
-      job.splits = splits;
-      job.add = v0 > 0;
-      if (!ce_map_k(&job.a[0], ws.g, cols, M, ld) || !ce_map_mn(&job.b[0], w, D, V, D) ||
-          !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
-        return GBF_ERR_CUDA;
-      if ((st = run_ce_gemm(job, end, M, D, *dev, err, s)) != GBF_OK) return st;
-    }
-    if (dw) {
-      job.mode = kCeDw;
+  // Launch n: G of piece n, and the products of piece n - 1's G.
+  const int64_t pieces = ceil_div64(V, piece);
+  for (int64_t n = 0; n <= pieces; ++n) {
+    CeLaunch launch{};
+    launch.d = p.D;
+    if (n < pieces) {
+      CeJob& job = launch.job[1];
+      const int64_t v0 = n * piece, cols = std::min(piece, V - v0);
+      job.mode = kCeGrad;
+      job.cols = static_cast<int>(cols);
+      job.v0 = static_cast<int>(v0);
       job.splits = 1;
-      if (!ce_map_mn(&job.a[0], ws.g, cols, M, ld) || !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
-          !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_out(&job.o, dw, D, V, D))
+      if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+          !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g[n & 1], cols, M, ld))
         return GBF_ERR_CUDA;
-      if ((st = run_ce_gemm(job, end, cols, D, *dev, err, s)) != GBF_OK) return st;
     }
+    if (n > 0) {
+      const int64_t v0 = (n - 1) * piece, cols = std::min(piece, V - v0);
+      const __nv_bfloat16* g = ws.g[(n - 1) & 1];
+      if (dx) {
+        CeJob& job = launch.job[0];
+        job.mode = kCeDx;
+        job.cols = static_cast<int>(cols);
+        job.v0 = static_cast<int>(v0);
+        job.splits = splits;
+        job.add = n > 1;
+        if (!ce_map_k(&job.a[0], g, cols, M, ld) || !ce_map_mn(&job.b[0], w, D, V, D) ||
+            !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
+          return GBF_ERR_CUDA;
+      }
+      if (dw) {
+        CeJob& job = launch.job[2];
+        job.mode = kCeDw;
+        job.cols = static_cast<int>(cols);
+        job.v0 = static_cast<int>(v0);
+        job.splits = 1;
+        if (!ce_map_mn(&job.a[0], g, cols, M, ld) || !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
+            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_out(&job.o, dw, D, V, D))
+          return GBF_ERR_CUDA;
+      }
+    }
+    if ((st = run_ce_gemm(launch, end, M, *dev, err, s)) != GBF_OK) return st;
   }
   if (!dx) return GBF_OK;
   CeDxOut out{};

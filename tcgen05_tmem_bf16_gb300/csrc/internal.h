@@ -155,7 +155,7 @@ cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const
 
 // Linear cross entropy (linear_ce.cu).  One product of the kernel with its
 // ending; the scored rows are numbered 0 .. count-1 in their order.
-enum CeMode { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
+enum CeMode { kCeNone = 0, kCeLse = 1, kCeGrad = 2, kCeDx = 3, kCeDw = 4 };
 struct CeJob {
   // a[1] / b[1]: x itself, where it is an operand, for when every row is
   // scored; [0] the gathered rows (or the operand's only map)
@@ -163,9 +163,15 @@ struct CeJob {
   int mode;
   int cols;    // columns of the vocabulary: all (kCeLse) or the piece's
   int v0;      // first column of the piece
-  int d;       // hidden width
   int splits;  // parts of K (kCeDx), each with its own fp32 buffer
   int add;     // kCeDx: add to the buffer (a later piece)
+};
+// The products of one launch, none of which reads what another writes.  Job 0:
+// the one with the longest units, if any.
+constexpr int kCeJobs = 3;
+struct CeLaunch {
+  CeJob job[kCeJobs];
+  int d;  // hidden width
 };
 struct CeEnd {
   const int* count;   // scored rows
@@ -198,7 +204,7 @@ struct CeJoin {
   const float2* part;
   const float* tlog;
   unsigned* ticket;
-  double* sums;  // per 32 rows
+  double* sums;  // per 8 rows
   float *loss, *lse, *mean;
   float alpha;
   int M, parts;
@@ -211,7 +217,7 @@ struct CeDxOut {
   float scale;
   int mean, m_pad, splits, D;
 };
-cudaError_t launch_ce_gemm(const CeJob& job, const CeEnd& end, int streams, int grid,
+cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, int grid,
                            const KernelCtl& ctl, cudaStream_t stream);
 cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
                            cudaStream_t stream);

@@ -52,6 +52,8 @@ constexpr int kCeTile = 256;           // rows and columns of a pair's tile
 constexpr int kCeABytes = kBM * kBK * 2;   // 16 KB: this CTA's 128 rows of A
 constexpr int kCeBBytes = 128 * kBK * 2;   // 16 KB: this CTA's half of B
 constexpr int kCeGroup = 8;            // raster group (units of rows)
+constexpr int kCeUnitCost = 4;         // a unit's ending, in K blocks of its main loop
+constexpr int kCeTwoK = 16;            // K blocks from which a lone row tile gets both issuers
 
 template <int STREAMS>
 struct CeCfg {
@@ -63,37 +65,91 @@ struct CeCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
-// A unit of work: STREAMS row tiles x one column tile x a range of K blocks.
+// A unit of work: STREAMS row tiles x one column tile x a range of K blocks of
+// one of the launch's products.
 struct CeUnit {
-  int mp, nb, split, kb0, kb1;
+  int job, mp, nb, split, kb0, kb1;
 };
 
-struct CeShape {
-  int m_units, n_tiles, splits, num_kb, total;
+// What a launch's products come to on the device, where the number of scored
+// rows is known, and which units a CTA pair works through, in order.
+//
+// The products for dx (job 0) have few, long units, the others many short
+// ones.  The long units are dealt out first, one per pair and round; the pairs
+// that got one more than the others (the first `extra`) then sit out `skip`
+// rounds of short units, about as many as the long one takes.  Every role of a
+// pair computes the same sequence for itself: no shared queue.
+struct CeWork {
+  int units[kCeJobs], m_units[kCeJobs], n_tiles[kCeJobs], num_kb[kCeJobs];
+  int longs, extra, skip, shorts, npairs;
 };
 
-__device__ __forceinline__ CeShape ce_shape(const CeJob& j, int count, int streams) {
-  CeShape s;
-  const int rows = j.mode == kCeDw ? j.cols : count;
-  const int n = (j.mode == kCeLse || j.mode == kCeGrad) ? j.cols : j.d;
-  const int k = j.mode == kCeDw ? count : (j.mode == kCeDx ? j.cols : j.d);
-  s.m_units = (rows + kCeTile * streams - 1) / (kCeTile * streams);
-  s.n_tiles = (n + kCeTile - 1) / kCeTile;
-  s.splits = j.splits;
-  s.num_kb = (k + kBK - 1) / kBK;
-  s.total = s.m_units * s.n_tiles * s.splits;
-  return s;
+__device__ __forceinline__ CeWork ce_work(const CeLaunch& a, int count, int streams, int npairs) {
+  CeWork w;
+  int64_t blocks = 0;
+#pragma unroll
+  for (int i = 0; i < kCeJobs; ++i) {
+    w.units[i] = w.m_units[i] = w.n_tiles[i] = w.num_kb[i] = 0;
+    if (a.job[i].mode == kCeNone) continue;
+    const CeJob& j = a.job[i];
+    const int rows = j.mode == kCeDw ? j.cols : count;
+    const int n = (j.mode == kCeLse || j.mode == kCeGrad) ? j.cols : a.d;
+    const int k = j.mode == kCeDw ? count : (j.mode == kCeDx ? j.cols : a.d);
+    w.m_units[i] = (rows + kCeTile * streams - 1) / (kCeTile * streams);
+    w.n_tiles[i] = (n + kCeTile - 1) / kCeTile;
+    w.num_kb[i] = (k + kBK - 1) / kBK;
+    w.units[i] = w.m_units[i] * w.n_tiles[i] * j.splits;
+    if (i > 0) blocks += static_cast<int64_t>(w.units[i]) * (w.num_kb[i] + kCeUnitCost);
+  }
+  w.npairs = npairs;
+  w.longs = w.units[0];
+  w.shorts = w.units[1] + w.units[2];
+  w.extra = w.longs % npairs;
+  w.skip = 0;
+  if (w.extra > 0 && w.shorts > 0) {
+    const int64_t len = w.num_kb[0] / a.job[0].splits + kCeUnitCost;
+    const int64_t fit = static_cast<int64_t>(w.shorts) / (npairs - w.extra) + 1;
+    w.skip = static_cast<int>(min(len * w.shorts / max(blocks, static_cast<int64_t>(1)), fit));
+  }
+  return w;
 }
 
-__device__ __forceinline__ CeUnit ce_unit(const CeShape& s, int t) {
-  CeUnit u;
-  const int tiles = s.m_units * s.n_tiles;
+// The n-th unit of a pair; false after its last.
+__device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int pair, int n,
+                                        CeUnit& u) {
+  const int mine = w.longs / w.npairs + (pair < w.extra ? 1 : 0);
+  int t;
+  if (n < mine) {
+    t = n * w.npairs + pair;
+    u.job = 0;
+  } else {
+    const int round = n - mine + (pair < w.extra ? w.skip : 0);
+    if (round < w.skip)
+      t = round * (w.npairs - w.extra) + pair - w.extra;
+    else
+      t = w.skip * (w.npairs - w.extra) + (round - w.skip) * w.npairs + pair;
+    if (t >= w.shorts) return false;
+    u.job = 1;
+    if (t >= w.units[1]) {
+      u.job = 2;
+      t -= w.units[1];
+    }
+  }
+  const int m_units = u.job == 0 ? w.m_units[0] : u.job == 1 ? w.m_units[1] : w.m_units[2];
+  const int n_tiles = u.job == 0 ? w.n_tiles[0] : u.job == 1 ? w.n_tiles[1] : w.n_tiles[2];
+  const int num_kb = u.job == 0 ? w.num_kb[0] : u.job == 1 ? w.num_kb[1] : w.num_kb[2];
+  const int splits = a.job[u.job].splits;
+  const int tiles = m_units * n_tiles;
   u.split = t / tiles;
-  tile_coords(t - u.split * tiles, s.m_units, s.n_tiles, u.mp, u.nb, kCeGroup);
-  u.kb0 = static_cast<int>(static_cast<int64_t>(u.split) * s.num_kb / s.splits);
-  u.kb1 = static_cast<int>(static_cast<int64_t>(u.split + 1) * s.num_kb / s.splits);
-  return u;
+  tile_coords(t - u.split * tiles, m_units, n_tiles, u.mp, u.nb, kCeGroup);
+  u.kb0 = static_cast<int>(static_cast<int64_t>(u.split) * num_kb / splits);
+  u.kb1 = static_cast<int>(static_cast<int64_t>(u.split + 1) * num_kb / splits);
+  return true;
 }
+
+// One row tile per unit: whether both MMA issuers share the tile, each over
+// every other K block into its own accumulator.
+__device__ __forceinline__ bool ce_two_k(const CeUnit& u) { return u.kb1 - u.kb0 >= kCeTwoK; }
 
 // One warp's 32 rows x 32 columns of fp32 to the map's tensor, stored or added
 // there by the TMA engine, through the warp's two staging buffers (16 columns
@@ -125,9 +181,22 @@ __device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int& flip, const ui
   }
 }
 
+// v[k] += the accumulator's column k of this thread's lane at taddr.
+__device__ __forceinline__ void add_acc32(uint32_t taddr, uint32_t (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t o[16];
+    tmem_ld16(taddr + 16 * h, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      v[16 * h + k] = __float_as_uint(__uint_as_float(v[16 * h + k]) + __uint_as_float(o[k]));
+  }
+}
+
 template <int STREAMS>
 __global__ void __launch_bounds__(kCeThreads, 1)
-    ce_gemm_kernel(const __grid_constant__ CeJob j, const CeEnd e, const KernelCtl kctl) {
+    ce_gemm_kernel(const __grid_constant__ CeLaunch a, const CeEnd e, const KernelCtl kctl) {
   using Cfg = CeCfg<STREAMS>;
   constexpr int kStages = Cfg::kStages;
   constexpr int kLoadBytes = STREAMS * kCeABytes + kCeBBytes;  // into one CTA's stage
@@ -153,18 +222,21 @@ __global__ void __launch_bounds__(kCeThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], STREAMS);
+      mbar_init(&empty[i], STREAMS);  // two streams: both issuers; else the block's one
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
     }
-    mbar_init(done, STREAMS);
+    mbar_init(done, 2);
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&j.a[0]);
-    tma_prefetch_desc(&j.b[0]);
-    tma_prefetch_desc(&j.o);
+    for (int i = 0; i < kCeJobs; ++i) {
+      if (a.job[i].mode == kCeNone) continue;
+      tma_prefetch_desc(&a.job[i].a[0]);
+      tma_prefetch_desc(&a.job[i].b[0]);
+      if (a.job[i].mode != kCeLse) tma_prefetch_desc(&a.job[i].o);
+    }
   }
   if (warp == 2) {
     tmem_alloc_pair(tmem_holder, 512);
@@ -180,24 +252,25 @@ __global__ void __launch_bounds__(kCeThreads, 1)
   griddep_wait();
   const int count = *e.count;
   const int all = count == e.M ? 1 : 0;  // every row is scored: x itself, not the gathered rows
-  const CeShape sh = ce_shape(j, count, STREAMS);
-  const bool a_mn = j.mode == kCeDw;                      // A is read along its columns
-  const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;   // B holds one row per k
+  const CeWork work = ce_work(a, count, STREAMS, npairs);
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (both CTAs)
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");  // the gathered rows: plain stores
-      const CUtensorMap* ma = &j.a[(j.mode == kCeLse || j.mode == kCeGrad) ? all : 0];
-      const CUtensorMap* mb = &j.b[j.mode == kCeDw ? all : 0];
       uint32_t fills[kStages];
 #pragma unroll
       for (int i = 0; i < kStages; ++i) fills[i] = 0;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (int t = pair; t < sh.total && ok; t += npairs) {
-        const CeUnit u = ce_unit(sh, t);
+      CeUnit u;
+      for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+        const CeJob& j = a.job[u.job];
+        const bool a_mn = j.mode == kCeDw;                     // A is read along its columns
+        const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;  // B holds one row per k
+        const CUtensorMap* ma = &j.a[(j.mode == kCeLse || j.mode == kCeGrad) ? all : 0];
+        const CUtensorMap* mb = &j.b[j.mode == kCeDw ? all : 0];
         const int n0 = u.nb * kCeTile + static_cast<int>(rank) * 128;
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!wait_bar(&empty[s], ph ^ 1, ctl, kSiteProducerEmpty)) {
@@ -243,47 +316,67 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers (even CTA)
-    // Two streams: warp 1 the first, warp 2 the second row tile of every unit,
-    // each in its own accumulator.  One stream: warp 1, accumulators in turn.
+    // Two row tiles per unit: warp 1 the first, warp 2 the second, each in its
+    // own accumulator.  One row tile: both on it, warp 1 the even and warp 2 the
+    // odd K blocks (the ending adds the accumulators), or for a short K one of
+    // them, in turn, so that a tile's ending overlaps the next one's products.
+    // (One thread's MMAs complete one after another, about 150 cycles each.)
     const int st = warp - 1;
-    if (lane == 0 && leader && st < STREAMS) {
-      const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
+    if (lane == 0 && leader) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int l = 0;
-      for (int t = pair; t < sh.total && ok; t += npairs, ++l) {
-        const CeUnit u = ce_unit(sh, t);
-        const int acc = STREAMS == 2 ? st : (l & 1);
-        const int use = STREAMS == 2 ? l : (l >> 1);
-        const uint32_t d = tmem_base + acc * 256;
-        if (!wait_bar(&tempty[acc], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
-        tc_fence_after();
-        for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
-            ok = false;
-            break;
-          }
+      bool first = true;
+      int use = 0;   // of this issuer's accumulator
+      int turn = 0;  // whose turn a short unit is
+      const uint32_t d = tmem_base + st * 256;
+      CeUnit u;
+      for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+        const CeJob& j = a.job[u.job];
+        const bool a_mn = j.mode == kCeDw;
+        const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
+        const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
+        const bool two = STREAMS == 1 && ce_two_k(u);
+        bool mine = true;
+        if (STREAMS == 1 && !two) {
+          mine = turn == st;
+          turn ^= 1;
+        }
+        if (mine) {
+          if (!wait_bar(&tempty[st], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
           tc_fence_after();
-          const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
-          const uint32_t a0 = s0 + st * kCeABytes;
-          const uint32_t b0 = s0 + STREAMS * kCeABytes;
+          ++use;
+        }
+        uint32_t accumulate = 0;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (mine && !(two && ((kb - u.kb0) & 1) != st)) {
+            if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
+            const uint32_t a0 = s0 + (STREAMS == 2 ? st : 0) * kCeABytes;
+            const uint32_t b0 = s0 + STREAMS * kCeABytes;
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k) {
-            const uint64_t ad = a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
-                                     : sdesc_sw128(a0 + k * 32, 16, 1024);
-            const uint64_t bd = b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
-                                     : sdesc_sw128(b0 + k * 32, 16, 1024);
-            mma_ss_pair(d, ad, bd, idesc, (kb != u.kb0 || k != 0) ? 1u : 0u);
+            for (int k = 0; k < kBK / 16; ++k) {
+              const uint64_t ad = a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
+                                       : sdesc_sw128(a0 + k * 32, 16, 1024);
+              const uint64_t bd = b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
+                                       : sdesc_sw128(b0 + k * 32, 16, 1024);
+              mma_ss_pair(d, ad, bd, idesc, accumulate);
+              accumulate = 1;
+            }
+            mma_commit_pair(&empty[s], 0x3);
           }
-          mma_commit_pair(&empty[s], 0x3);
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
           }
         }
         if (!ok) break;
-        if (!(kctl.inject && l == 0)) mma_commit_pair(&tfull[acc], 0x3);
+        if (mine && !(kctl.inject && first)) mma_commit_pair(&tfull[st], 0x3);
+        first = false;
       }
       mma_commit_pair(done, 1);
       wait_bar(done, 0, ctl, kSiteDrain, false);
@@ -299,14 +392,20 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     uint8_t* my_staging = staging + (warp - 4) * 2 * kStageChunkBytes;
     int flip = 0;
     const float out_scale = e.mean ? e.scale / static_cast<float>(max(count, 1)) : e.scale;
-    int local = 0;
-    for (int t = pair; t < sh.total; t += npairs) {
-      const CeUnit u = ce_unit(sh, t);
-      bool ok = true;
+    int use[2] = {0, 0};  // of the accumulators
+    int turn = 0;
+    bool ok = true;
+    CeUnit u;
+    for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+      const CeJob& j = a.job[u.job];
+      const bool two = STREAMS == 1 && ce_two_k(u);
 #pragma unroll 1
-      for (int i = 0; i < STREAMS && ok; ++i, ++local) {
-        const int acc_i = local & 1;
-        const uint32_t aph = (local >> 1) & 1;
+      for (int i = 0; i < STREAMS; ++i) {
+        int acc_i = i;
+        if (STREAMS == 1 && !two) {
+          acc_i = turn;
+          turn ^= 1;
+        }
         const int row = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM + q * 32 + lane;
         const bool row_ok = row < count;
         int tgt = -1;
@@ -318,10 +417,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             dl = e.dl[row];
           }
         }
-        if (!wait_bar(&tfull[acc_i], aph, ctl, kSiteEpiAccFull)) {
-          ok = false;
-          break;
-        }
+        ok = wait_bar(&tfull[acc_i], (acc_i ? use[1] : use[0]) & 1, ctl, kSiteEpiAccFull);
+        if (acc_i) ++use[1];
+        else ++use[0];
+        if (ok && two) ok = wait_bar(&tfull[1], use[1]++ & 1, ctl, kSiteEpiAccFull);
+        if (!ok) break;
         tc_fence_after();
         const uint32_t tb =
             tmem_base + acc_i * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
@@ -333,12 +433,17 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           uint32_t v[32];
           tmem_ld32(tb + c * 32, v);
           tmem_wait_ld();
+          if (two) add_acc32(tb + 256 + c * 32, v);  // the odd K blocks
           if (c == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               if (leader) mbar_arrive(&tempty[acc_i]);
               else mbar_arrive_cluster(tempty_leader[acc_i]);
+              if (two) {
+                if (leader) mbar_arrive(&tempty[1]);
+                else mbar_arrive_cluster(tempty_leader[1]);
+              }
             }
           }
           if (j.mode == kCeLse) {
@@ -383,7 +488,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
               for (int k = 0; k < 32; ++k) v[k] = 0u;
             }
-            put_chunk_f32(my_staging, flip, v, &j.o, u.split * e.m_pad + row - lane, col0, j.d,
+            put_chunk_f32(my_staging, flip, v, &j.o, u.split * e.m_pad + row - lane, col0, a.d,
                           j.add != 0);
           } else {
             uint32_t w[16];
@@ -393,14 +498,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
               const float hi = __uint_as_float(v[2 * k + 1]) * out_scale;
               w[k] = u.kb0 < u.kb1 ? pack_bf16x2(lo, hi) : 0u;  // no rows: an empty sum
             }
-            store_chunk32(my_staging, flip, w, &j.o, j.v0 + row - lane, col0, j.v0 + j.cols, j.d,
+            store_chunk32(my_staging, flip, w, &j.o, j.v0 + row - lane, col0, j.v0 + j.cols, a.d,
                           pol);
           }
         }
         if (j.mode == kCeLse && row_ok)
           e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + row] = make_float2(m, sum);
       }
-      if (!ok) break;
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
@@ -492,7 +596,9 @@ __global__ void __launch_bounds__(kPrepThreads)
   }
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinRows = 8;  // rows per CTA: 64-byte segments of the partial sums
 
 // (m, s) stands for s * 2^m.
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
@@ -501,40 +607,48 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return make_float2(m, fmaf(a.y, pow2(a.x - ref), b.y * pow2(b.x - ref)));
 }
 
-// 32 scored rows per CTA: adds up each row's partial sums, writes its loss and
-// lse; the last CTA adds the CTAs' sums of losses in order for the mean.
+// Eight scored rows per CTA, 64 threads each: adds up each row's partial sums,
+// writes its loss and lse; the last CTA adds the CTAs' sums of losses in order
+// for the mean.
 __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
-  __shared__ float2 part[kJoinThreads / 32][32];
-  __shared__ double sums[kJoinThreads / 32];
+  __shared__ float2 part[kJoinWarps][kJoinRows];
+  __shared__ double sums[kJoinWarps];
   __shared__ bool last;
   griddep_launch_dependents();
   griddep_wait();
   const int count = *p.count;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 32 + lane;
+  const int row = blockIdx.x * kJoinRows + (lane & (kJoinRows - 1));
   float2 a = make_float2(-INFINITY, 0.0f);
   if (row < count) {
     const float2* src = p.part + row;
-    int n = warp;
-    constexpr int kAhead = 8, kStep = kJoinThreads / 32;
-    for (; n + (kAhead - 1) * kStep < p.parts; n += kAhead * kStep) {
+    constexpr int kAhead = 8, kStep = kJoinThreads / kJoinRows;
+    for (int n0 = threadIdx.x / kJoinRows; n0 < p.parts; n0 += kAhead * kStep) {
       float2 v[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) v[i] = src[static_cast<int64_t>(n + i * kStep) * p.M];
+      for (int i = 0; i < kAhead; ++i)
+        if (n0 + i * kStep < p.parts) v[i] = src[static_cast<int64_t>(n0 + i * kStep) * p.M];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) a = join(a, v[i]);
+      for (int i = 0; i < kAhead; ++i)
+        if (n0 + i * kStep < p.parts) a = join(a, v[i]);
     }
-    for (; n < p.parts; n += kStep) a = join(a, src[static_cast<int64_t>(n) * p.M]);
   }
-  part[warp][lane] = a;
+#pragma unroll
+  for (int o = kJoinRows; o < 32; o <<= 1) {
+    float2 b;
+    b.x = __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+    b.y = __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+    a = join(a, b);
+  }
+  if (lane < kJoinRows) part[warp][lane] = a;
   __syncthreads();
   if (warp == 0) {
     double loss = 0.0;
-    if (row < count) {
+    if (lane < kJoinRows && row < count) {
 #pragma unroll
-      for (int w = 1; w < kJoinThreads / 32; ++w) a = join(a, part[w][lane]);
-      // log2 of the sum in 64 bits: a confident row's loss is a small difference
-      const double lse = (static_cast<double>(a.x) + log2(static_cast<double>(a.y))) * kLn2;
+      for (int w = 1; w < kJoinWarps; ++w) a = join(a, part[w][lane]);
+      // the differences in 64 bits: a confident row's loss is a small one
+      const double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
       loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
       const int r = p.rows[row];
       p.loss[r] = static_cast<float>(loss);
@@ -542,7 +656,7 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     }
     if (p.mean) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
+      for (int o = kJoinRows / 2; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
       if (lane == 0) {
         p.sums[blockIdx.x] = loss;
         __threadfence();
@@ -562,7 +676,7 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     s = 0.0;
-    for (int w = 0; w < kJoinThreads / 32; ++w) s += sums[w];
+    for (int w = 0; w < kJoinWarps; ++w) s += sums[w];
     *p.mean = static_cast<float>(s / max(count, 1));
   }
 }
@@ -612,7 +726,7 @@ cudaLaunchConfig_t overlapped(int64_t grid, int threads, size_t smem, cudaStream
 }
 
 template <int STREAMS>
-cudaError_t run_ce(const CeJob& job, const CeEnd& end, const KernelCtl& ctl, int grid,
+cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ctl, int grid,
                    cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
   auto kernel = ce_gemm_kernel<STREAMS>;
@@ -633,15 +747,15 @@ cudaError_t run_ce(const CeJob& job, const CeEnd& end, const KernelCtl& ctl, int
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, job, end, ctl);
+  return cudaLaunchKernelEx(&cfg, kernel, launch, end, ctl);
 }
 
 }  // namespace
 
-cudaError_t launch_ce_gemm(const CeJob& job, const CeEnd& end, int streams, int grid,
+cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, int grid,
                            const KernelCtl& ctl, cudaStream_t stream) {
-  return streams == 2 ? run_ce<2>(job, end, ctl, grid, stream)
-                      : run_ce<1>(job, end, ctl, grid, stream);
+  return streams == 2 ? run_ce<2>(launch, end, ctl, grid, stream)
+                      : run_ce<1>(launch, end, ctl, grid, stream);
 }
 
 cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
@@ -659,7 +773,7 @@ cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
 
 cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = overlapped((p.M + 31) / 32, kJoinThreads, 0, stream, attr);
+  cudaLaunchConfig_t cfg = overlapped((p.M + kJoinRows - 1) / kJoinRows, kJoinThreads, 0, stream, attr);
   return cudaLaunchKernelEx(&cfg, ce_join_kernel, p);
 }
 
