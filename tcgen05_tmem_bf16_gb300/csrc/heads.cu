@@ -91,6 +91,12 @@ int ce_splits(int64_t M, int64_t D, int64_t cols) {
       std::max<int64_t>(1, std::min<int64_t>({ceil_div64(k, half), k / 8, 16})));
 }
 
+// Partial sums per row of the forward pass: one per 128 columns of a tile, per
+// 32 with swapped roles.
+int64_t ce_parts(int64_t M, int64_t V) {
+  return M <= kCeSwapMax ? 4 * ceil_div64(V, 128) : 2 * ceil_div64(V, kCeTileRows);
+}
+
 struct CeWs {
   int *count, *rows, *tgt;
   unsigned* ticket;
@@ -109,7 +115,7 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
   w->tgt = s.take<int>(M);
   w->xc = s.take<__nv_bfloat16>(static_cast<size_t>(M) * D);
   if (!grad) {
-    w->part = s.take<float2>(static_cast<size_t>(2 * ceil_div64(V, kCeTileRows)) * M);
+    w->part = s.take<float2>(static_cast<size_t>(ce_parts(M, V)) * M);
     w->tlog = s.take<float>(M);
     w->sums = s.take<double>(ceil_div64(M, 8));  // one per CTA of the join
   } else {
@@ -118,7 +124,8 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
     w->lse2 = s.take<float>(M);
     w->dl = s.take<float>(M);
     // G of two pieces: one is written while the other's products run
-    const size_t g = static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8);
+    const size_t g = M <= kCeSwapMax ? static_cast<size_t>(ce_swap_rows(M)) * cols
+                                     : static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8);
     w->g[0] = s.take<__nv_bfloat16>(g);
     w->g[1] = cols < V ? s.take<__nv_bfloat16>(g) : w->g[0];
     w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
@@ -149,6 +156,16 @@ bool ce_map_k(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64
 // Operand with one row per k: 64 x 64 boxes.
 bool ce_map_mn(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
   return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, 64, kBK,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Operands of the swapped roles: boxes of 64 x the padded rows, 64 x 128.
+bool ce_maps_swap(CeSwap* a, const void* w, const void* xc, const void* x, int64_t M, int64_t V,
+                  int64_t D) {
+  const uint32_t rows = static_cast<uint32_t>(ce_swap_rows(M));
+  return ce_map_k(&a->w, w, D, V, D) &&
+         lib_tmap_2d(&a->x[0], xc, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, M, D * 2, kBK, rows,
+                     CU_TENSOR_MAP_SWIZZLE_128B) &&
+         lib_tmap_2d(&a->x[1], x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, M, D * 2, kBK, rows,
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 bool ce_map_out(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
@@ -306,15 +323,23 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   p.M = static_cast<int>(M);
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);
+  const bool few = M <= kCeSwapMax;
   CeLaunch launch{};
-  launch.d = p.D;
-  CeJob& job = launch.job[1];
-  if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
-      !ce_map_k(&job.b[0], w, D, V, D))
-    return GBF_ERR_CUDA;
-  job.mode = kCeLse;
-  job.cols = p.V;
-  job.splits = 1;
+  CeSwap swap{};
+  if (few) {
+    if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
+    swap.cols = p.V;
+    swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
+  } else {
+    launch.d = p.D;
+    CeJob& job = launch.job[1];
+    if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+        !ce_map_k(&job.b[0], w, D, V, D))
+      return GBF_ERR_CUDA;
+    job.mode = kCeLse;
+    job.cols = p.V;
+    job.splits = 1;
+  }
   CeEnd end{};
   end.count = ws.count;
   end.tgt = ws.tgt;
@@ -334,11 +359,13 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   join.mean = mean;
   join.alpha = alpha;
   join.M = p.M;
-  join.parts = static_cast<int>(2 * ceil_div64(V, kCeTileRows));
+  join.parts = static_cast<int>(ce_parts(M, V));
   if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
       GBF_OK)
     return st;
-  if ((st = run_ce_gemm(launch, end, M, *dev, err, s)) != GBF_OK) return st;
+  st = few ? cuda_status(launch_ce_swap(swap, false, end, dev->sms, lib_ctl(err, 2 * dev->sms), s))
+           : run_ce_gemm(launch, end, M, *dev, err, s);
+  if (st != GBF_OK) return st;
   return cuda_status(launch_ce_join(join, s));
 }
 
@@ -381,7 +408,8 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
       GBF_OK)
     return st;
   const int64_t piece = ce_piece(M, V);
-  const int64_t ld = ceil_div64(piece, 8) * 8;
+  const bool few = M <= kCeSwapMax;  // G transposed, by the swapped roles
+  const int64_t ld = few ? ce_swap_rows(M) : ceil_div64(piece, 8) * 8;
   const int64_t m_pad = ceil_div64(M, 512) * 512;
   const int splits = ce_splits(M, D, piece);
   CeEnd end{};
@@ -399,7 +427,17 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   for (int64_t n = 0; n <= pieces; ++n) {
     CeLaunch launch{};
     launch.d = p.D;
-    if (n < pieces) {
+    if (n < pieces && few) {
+      const int64_t v0 = n * piece;
+      CeSwap swap{};
+      if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
+      swap.gt = ws.g[n & 1];
+      swap.v0 = static_cast<int>(v0);
+      swap.cols = static_cast<int>(std::min(piece, V - v0));
+      swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
+      st = cuda_status(launch_ce_swap(swap, true, end, dev->sms, lib_ctl(err, 2 * dev->sms), s));
+      if (st != GBF_OK) return st;
+    } else if (n < pieces) {
       CeJob& job = launch.job[1];
       const int64_t v0 = n * piece, cols = std::min(piece, V - v0);
       job.mode = kCeGrad;
@@ -420,7 +458,9 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
         job.v0 = static_cast<int>(v0);
         job.splits = splits;
         job.add = n > 1;
-        if (!ce_map_k(&job.a[0], g, cols, M, ld) || !ce_map_mn(&job.b[0], w, D, V, D) ||
+        job.gt = few;
+        if (!(few ? ce_map_mn(&job.a[0], g, ld, cols, ld) : ce_map_k(&job.a[0], g, cols, M, ld)) ||
+            !ce_map_mn(&job.b[0], w, D, V, D) ||
             !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
           return GBF_ERR_CUDA;
       }
@@ -430,11 +470,14 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
         job.cols = static_cast<int>(cols);
         job.v0 = static_cast<int>(v0);
         job.splits = 1;
-        if (!ce_map_mn(&job.a[0], g, cols, M, ld) || !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
+        job.gt = few;
+        if (!(few ? ce_map_k(&job.a[0], g, ld, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
+            !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
             !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_out(&job.o, dw, D, V, D))
           return GBF_ERR_CUDA;
       }
     }
+    if (few && n == 0) continue;  // no G yet
     if ((st = run_ce_gemm(launch, end, M, *dev, err, s)) != GBF_OK) return st;
   }
   if (!dx) return GBF_OK;

@@ -165,6 +165,7 @@ struct CeJob {
   int v0;      // first column of the piece
   int splits;  // parts of K (kCeDx), each with its own fp32 buffer
   int add;     // kCeDx: add to the buffer (a later piece)
+  int gt;      // kCeDx, kCeDw: G is stored transposed, [cols][rows]
 };
 // The products of one launch, none of which reads what another writes.  Job 0:
 // the one with the longest units, if any.
@@ -186,6 +187,16 @@ struct CeEnd {
   int M;
   int m_pad;          // rows between the splits' fp32 buffers
 };
+// The logits for up to kCeSwapMax rows, with swapped roles (ce_swap.cu).
+constexpr int kCeSwapMax = 128;
+int ce_swap_rows(int64_t M);  // rows padded to: 16, 64, 128; 0 above kCeSwapMax
+struct CeSwap {
+  CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored
+  __nv_bfloat16* gt;    // gradient: [cols][padded rows]
+  int cols, v0, num_kb;
+};
+cudaError_t launch_ce_swap(const CeSwap& a, bool grad, const CeEnd& end, int sms,
+                           const KernelCtl& ctl, cudaStream_t stream);
 struct CePrep {
   const __nv_bfloat16* x;
   __nv_bfloat16* xc;      // gathered rows

@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       CeUnit u;
       for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
-        const bool a_mn = j.mode == kCeDw;                     // A is read along its columns
+        // A is read along its columns: G for dw, its transpose for dx
+        const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;  // B holds one row per k
         const CUtensorMap* ma = &j.a[(j.mode == kCeLse || j.mode == kCeGrad) ? all : 0];
         const CUtensorMap* mb = &j.b[j.mode == kCeDw ? all : 0];
@@ -333,7 +334,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       CeUnit u;
       for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
-        const bool a_mn = j.mode == kCeDw;
+        const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
         const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
         const bool two = STREAMS == 1 && ce_two_k(u);

@@ -283,3 +283,15 @@ def test_a_wait_that_runs_out_is_reported(cuda_lib):
         cuda_lib.gbf_set_wait_timeout_ns(2_000_000_000)
     again, _, _ = forward(cuda_lib, x, w, t)
     assert torch.equal(loss, again)
+
+
+@pytest.mark.parametrize("M", [15, 16, 17, 63, 65, 127, 128, 130])
+@pytest.mark.parametrize("V,D", [(900, 64), (5003, 72), (1280, 2056)])
+def test_few_rows(cuda_lib, M, V, D):
+    for ignored in (0.0, 0.5):
+        x, w, t = inputs(M, V, D, ignored, seed=M * V)
+        ref = Reference(x, w, t, 1.0)
+        loss, lse, mean = forward(cuda_lib, x, w, t)
+        ref.check_forward(loss, lse, mean)
+        dx, dw = backward(cuda_lib, x, w, t, lse)
+        ref.check_backward(dx, dw)
