@@ -53,7 +53,7 @@ constexpr int kCeABytes = kBM * kBK * 2;   // 16 KB: this CTA's 128 rows of A
 constexpr int kCeBBytes = 128 * kBK * 2;   // 16 KB: this CTA's half of B
 constexpr int kCeGroup = 8;            // raster group (units of rows)
 constexpr int kCeUnitCost = 4;         // a unit's ending, in K blocks of its main loop
-constexpr int kCeTwoK = 16;            // K blocks from which a lone row tile gets both issuers
+constexpr int kCeTwoK = 24;            // K blocks from which a lone row tile's logits take two sums
 
 template <int STREAMS>
 struct CeCfg {
@@ -147,9 +147,12 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   return true;
 }
 
-// One row tile per unit: whether both MMA issuers share the tile, each over
-// every other K block into its own accumulator.
-__device__ __forceinline__ bool ce_two_k(const CeUnit& u) { return u.kb1 - u.kb0 >= kCeTwoK; }
+// One row tile per unit: whether the halves of K go to the two accumulators.
+// The tensor cores cut the sum at every step, so a logit of 4096 products is low
+// by some 4e-6 of itself and lse by 1.5e-6; two chains of half the length halve that.
+__device__ __forceinline__ bool ce_two_k(const CeJob& j, const CeUnit& u) {
+  return j.mode == kCeLse && u.kb1 - u.kb0 >= kCeTwoK;
+}
 
 // One warp's 32 rows x 32 columns of fp32 to the map's tensor, stored or added
 // there by the TMA engine, through the warp's two staging buffers (16 columns
@@ -222,13 +225,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], STREAMS);  // two streams: both issuers; else the block's one
+      mbar_init(&empty[i], STREAMS);  // every issuer
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
     }
-    mbar_init(done, 2);
+    mbar_init(done, STREAMS);
     *abort_flag = 0;
     fence_mbar_init();
     for (int i = 0; i < kCeJobs; ++i) {
@@ -317,66 +320,71 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers (even CTA)
-    // Two row tiles per unit: warp 1 the first, warp 2 the second, each in its
-    // own accumulator.  One row tile: both on it, warp 1 the even and warp 2 the
-    // odd K blocks (the ending adds the accumulators), or for a short K one of
-    // them, in turn, so that a tile's ending overlaps the next one's products.
-    // (One thread's MMAs complete one after another, about 150 cycles each.)
+    // Two row tiles per unit: warp 1 issues the first's, warp 2 the second's,
+    // each into its own accumulator; both read every stage.  One row tile: warp 1
+    // alone, accumulators in turn, so that a tile's ending overlaps the next one's
+    // products (or, ce_two_k, the halves of K into the two, which the ending
+    // adds).  One thread's MMAs complete one after another, about 150 cycles each:
+    // half the rate of two threads, but with one row tile W's 8 KB per MMA are
+    // 7.9 TB/s over all pairs, more than HBM gives.
+    // (Issuers that shared a unit's blocks would each have to wait for all of them
+    // all the same: a barrier's parity says nothing to a thread that has missed a
+    // phase.)
     const int st = warp - 1;
-    if (lane == 0 && leader) {
+    if (lane == 0 && leader && st < STREAMS) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       bool first = true;
-      int use = 0;   // of this issuer's accumulator
-      int turn = 0;  // whose turn a short unit is
-      const uint32_t d = tmem_base + st * 256;
+      int use0 = 0, use1 = 0;  // of the accumulators
+      int turn = st;
       CeUnit u;
       for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
         const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
         const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
-        const bool two = STREAMS == 1 && ce_two_k(u);
-        bool mine = true;
-        if (STREAMS == 1 && !two) {
-          mine = turn == st;
-          turn ^= 1;
-        }
-        if (mine) {
-          if (!wait_bar(&tempty[st], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
-          tc_fence_after();
-          ++use;
-        }
+        const bool two = STREAMS == 1 && ce_two_k(j, u);
+        const int kb_half = two ? (u.kb0 + u.kb1) / 2 : u.kb1;
+        int acc = two ? 0 : turn;
+        if (STREAMS == 1 && !two) turn ^= 1;
+        if (!wait_bar(&tempty[acc], ((acc ? use1 : use0) & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
+        if (acc) ++use1;
+        else ++use0;
+        if (two && !wait_bar(&tempty[1], (use1++ & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
+        tc_fence_after();
         uint32_t accumulate = 0;
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (mine && !(two && ((kb - u.kb0) & 1) != st)) {
-            if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
-            const uint32_t a0 = s0 + (STREAMS == 2 ? st : 0) * kCeABytes;
-            const uint32_t b0 = s0 + STREAMS * kCeABytes;
-#pragma unroll
-            for (int k = 0; k < kBK / 16; ++k) {
-              const uint64_t ad = a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
-                                       : sdesc_sw128(a0 + k * 32, 16, 1024);
-              const uint64_t bd = b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
-                                       : sdesc_sw128(b0 + k * 32, 16, 1024);
-              mma_ss_pair(d, ad, bd, idesc, accumulate);
-              accumulate = 1;
-            }
-            mma_commit_pair(&empty[s], 0x3);
+          if (kb == kb_half) {
+            mma_commit_pair(&tfull[0], 0x3);
+            acc = 1;
+            accumulate = 0;
           }
+          if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
+          const uint32_t a0 = s0 + st * kCeABytes;
+          const uint32_t b0 = s0 + STREAMS * kCeABytes;
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            const uint64_t ad = a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(a0 + k * 32, 16, 1024);
+            const uint64_t bd = b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
+                                     : sdesc_sw128(b0 + k * 32, 16, 1024);
+            mma_ss_pair(tmem_base + acc * 256, ad, bd, idesc, accumulate);
+            accumulate = 1;
+          }
+          mma_commit_pair(&empty[s], 0x3);
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
           }
         }
         if (!ok) break;
-        if (mine && !(kctl.inject && first)) mma_commit_pair(&tfull[st], 0x3);
+        if (!(kctl.inject && first)) mma_commit_pair(&tfull[acc], 0x3);
         first = false;
       }
       mma_commit_pair(done, 1);
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     CeUnit u;
     for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
       const CeJob& j = a.job[u.job];
-      const bool two = STREAMS == 1 && ce_two_k(u);
+      const bool two = STREAMS == 1 && ce_two_k(a.job[u.job], u);
 #pragma unroll 1
       for (int i = 0; i < STREAMS; ++i) {
         int acc_i = i;
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           uint32_t v[32];
           tmem_ld32(tb + c * 32, v);
           tmem_wait_ld();
-          if (two) add_acc32(tb + 256 + c * 32, v);  // the odd K blocks
+          if (two) add_acc32(tb + 256 + c * 32, v);  // the second half of K
           if (c == 3) {
             tc_fence_before();
             __syncwarp();

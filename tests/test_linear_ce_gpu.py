@@ -295,3 +295,24 @@ def test_few_rows(cuda_lib, M, V, D):
         ref.check_forward(loss, lse, mean)
         dx, dw = backward(cuda_lib, x, w, t, lse)
         ref.check_backward(dx, dw)
+
+
+@pytest.mark.parametrize("M,V,D", [(200, 30000, 640), (256, 20011, 968), (40, 6000, 1032), (100, 9001, 64)])
+def test_lone_row_tiles_of_short_products_again_and_again(cuda_lib, M, V, D):
+    """Up to 256 rows, whose column tiles two issuers take in turn or share by K
+    blocks, over many tiles per CTA pair, call after call without a wait between."""
+    x, w, t = inputs(M, V, D, 0.1, seed=M + D)
+    ref = Reference(x, w, t, 1.0)
+    loss, lse, mean = forward(cuda_lib, x, w, t)
+    ref.check_forward(loss, lse, mean)
+    dx, dw = backward(cuda_lib, x, w, t, lse)
+    ref.check_backward(dx, dw)
+    n = max(cuda_lib.gbf_workspace_size(op, M, V, D, True) for op in ("linear_ce", "linear_ce_grad"))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty_like(a) for a in (loss, lse, mean, dx, dw)] for _ in range(12)]
+    for o in outs:
+        cuda_lib.linear_ce(x, w, t, o[0], o[1], o[2], M, V, D, workspace=ws, workspace_bytes=n)
+        cuda_lib.linear_ce_grad(x, w, t, o[1], None, o[3], o[4], M, V, D, workspace=ws, workspace_bytes=n)
+    assert cuda_lib.gbf_check_device_error() == 0
+    for o in outs:
+        assert all(torch.equal(a, b) for a, b in zip(o, (loss, lse, mean, dx, dw)))
