@@ -112,7 +112,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, nullptr};
+  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, prof_slots(kctl.prof)};
+  const long long t_start = clock64();
   // no scored row: no logits (the gradient's G is still written, zeros)
   const int tiles = (count > 0 || GRAD) ? (a.cols + 127) / 128 : 0;
   const int num_kb = a.num_kb;
@@ -283,6 +284,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
     }
   }
 
+  if (ctl.prof && threadIdx.x == 0)
+    atomicAdd(&ctl.prof[31], static_cast<unsigned long long>(clock64() - t_start));
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {

@@ -172,6 +172,12 @@ bool ce_map_out(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int
   return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, 32, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B);
 }
+// With one row tile per unit the ending stores rows of 128 bytes.
+bool ce_map_dw(CUtensorMap* m, const void* p, int64_t D, int64_t V, bool wide) {
+  return wide ? lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D, V, D * 2, 64, 32,
+                            CU_TENSOR_MAP_SWIZZLE_128B)
+              : ce_map_out(m, p, D, V, D);
+}
 bool ce_map_out_f32(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
   return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, inner, outer, inner * 4, 16, 32,
                      CU_TENSOR_MAP_SWIZZLE_64B);
@@ -473,7 +479,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
         job.gt = few;
         if (!(few ? ce_map_k(&job.a[0], g, ld, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
             !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
-            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_out(&job.o, dw, D, V, D))
+            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, ce_streams(M) == 1))
           return GBF_ERR_CUDA;
       }
     }

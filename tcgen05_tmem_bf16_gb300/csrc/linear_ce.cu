@@ -58,9 +58,14 @@ constexpr int kCeTwoK = 24;            // K blocks from which a lone row tile's 
 template <int STREAMS>
 struct CeCfg {
   static constexpr int kStageBytes = STREAMS * kCeABytes + kCeBBytes;
-  static constexpr int kStages = STREAMS == 2 ? 4 : 6;
+  static constexpr int kStages = STREAMS == 2 ? 4 : 5;
   static constexpr int kBarBytes = 1024;
-  static constexpr int kStagingBytes = 8 * 2 * kStageChunkBytes;
+  // Two staging buffers per warp of the ending, of 32 rows x 64 bytes.  Few rows
+  // of x make dw a matter of writing: there the rows are 128 bytes.  (Stores of
+  // 128 x 256 tiles of a 32000 x 4096 tensor, by bytes of a row per request: 16:
+  // 97 us, 32: 58, 256: 41, a plain fill 38.)
+  static constexpr int kBufBytes = STREAMS == 2 ? 32 * 64 : 32 * 128;
+  static constexpr int kStagingBytes = 8 * 2 * kBufBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -138,12 +143,18 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   const int m_units = u.job == 0 ? w.m_units[0] : u.job == 1 ? w.m_units[1] : w.m_units[2];
   const int n_tiles = u.job == 0 ? w.n_tiles[0] : u.job == 1 ? w.n_tiles[1] : w.n_tiles[2];
   const int num_kb = u.job == 0 ? w.num_kb[0] : u.job == 1 ? w.num_kb[1] : w.num_kb[2];
-  const int splits = a.job[u.job].splits;
-  const int tiles = m_units * n_tiles;
-  u.split = t / tiles;
-  tile_coords(t - u.split * tiles, m_units, n_tiles, u.mp, u.nb, kCeGroup);
-  u.kb0 = static_cast<int>(static_cast<int64_t>(u.split) * num_kb / splits);
-  u.kb1 = static_cast<int>(static_cast<int64_t>(u.split + 1) * num_kb / splits);
+  u.split = 0;
+  u.kb0 = 0;
+  u.kb1 = num_kb;
+  if (u.job == 0) {  // the only product whose K is split; at most 16 parts of 2^20 blocks
+    const unsigned splits = a.job[0].splits;
+    const unsigned tiles = m_units * n_tiles;
+    u.split = static_cast<unsigned>(t) / tiles;
+    t -= u.split * tiles;
+    u.kb0 = static_cast<unsigned>(u.split * num_kb) / splits;
+    u.kb1 = static_cast<unsigned>((u.split + 1) * num_kb) / splits;
+  }
+  tile_coords(t, m_units, n_tiles, u.mp, u.nb, kCeGroup);
   return true;
 }
 
@@ -158,13 +169,13 @@ __device__ __forceinline__ bool ce_two_k(const CeJob& j, const CeUnit& u) {
 // there by the TMA engine, through the warp's two staging buffers (16 columns
 // each).  Every element is added to by one warp of one launch, so the sums do
 // not depend on timing.
-__device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int& flip, const uint32_t (&v)[32],
-                                              const CUtensorMap* map, int row0, int col0, int n,
-                                              bool add) {
+__device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int buf_bytes, int& flip,
+                                              const uint32_t (&v)[32], const CUtensorMap* map,
+                                              int row0, int col0, int n, bool some, bool add) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint8_t* buf = bufs + flip * kStageChunkBytes;
+    uint8_t* buf = bufs + flip * buf_bytes;
     if (lane == 0) bulk_wait_read<1>();
     __syncwarp();
     uint32_t w[16];
@@ -174,10 +185,48 @@ __device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int& flip, const ui
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (col0 + 16 * h < n) {
+      if (some && col0 + 16 * h < n) {
         if (add) tma_add_2d(map, buf, col0 + 16 * h, row0);
         else tma_store_2d(map, buf, col0 + 16 * h, row0, policy_evict_last());
       }
+      bulk_commit();
+    }
+    flip ^= 1;
+  }
+}
+
+// One warp's 32 rows x 32 bf16 columns through a staging buffer to the map's
+// tensor, as store_chunk32 does; WIDE: two calls with c even and odd fill rows
+// of 128 bytes (128-byte swizzle), which the second one stores.
+template <bool WIDE>
+__device__ __forceinline__ void put_chunk(uint8_t* bufs, int buf_bytes, int& flip, int c,
+                                          const uint32_t (&w)[16], const CUtensorMap* map,
+                                          int row0, int col0, int rows, int n, uint64_t pol) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* buf = bufs + flip * buf_bytes;
+  const bool first = !WIDE || (c & 1) == 0, last = !WIDE || (c & 1) == 1;
+  if (first) {
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+  }
+  if (WIDE) {
+    const uint32_t base = smem_u32(buf) + static_cast<uint32_t>(lane) * 128u;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t at = static_cast<uint32_t>((4 * (c & 1) + u) ^ (lane & 7)) << 4;
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + at), "r"(w[4 * u]),
+                   "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
+                   : "memory");
+    }
+  } else {
+    stage_row32(buf, lane, w);
+  }
+  if (last) {
+    const int at = WIDE ? col0 - 32 : col0;
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (row0 < rows && at < n) tma_store_2d(map, buf, at, row0, pol);
       bulk_commit();
     }
     flip ^= 1;
@@ -195,6 +244,126 @@ __device__ __forceinline__ void add_acc32(uint32_t taddr, uint32_t (&v)[32]) {
     for (int k = 0; k < 16; ++k)
       v[16 * h + k] = __float_as_uint(__uint_as_float(v[16 * h + k]) + __uint_as_float(o[k]));
   }
+}
+
+// How a warp of the ending gives an accumulator (or both) back to the issuers.
+struct CeFree {
+  uint64_t *mine, *other;
+  uint32_t lead_mine, lead_other;  // the even CTA's, as the odd one sees them
+  bool leader, two;
+  __device__ __forceinline__ void operator()() const {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      if (leader) mbar_arrive(mine);
+      else mbar_arrive_cluster(lead_mine);
+      if (two) {
+        if (leader) mbar_arrive(other);
+        else mbar_arrive_cluster(lead_other);
+      }
+    }
+  }
+};
+
+// What the ending of a tile needs: a thread holds one row, a warp 128 columns
+// from col0 on.
+struct CeTileArgs {
+  const CUtensorMap* out;
+  uint8_t* staging;
+  uint64_t pol;
+  int row, col0, cols, v0, d, count;
+  int buf_row;  // kDx: row in the fp32 buffers
+  bool row_ok, none, add;
+  int tgt;      // the target's column, from col0 on
+  float lse2, dl, out_scale;
+};
+
+template <int MODE, int STREAMS>
+__device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const CeTileArgs& t,
+                                         const CeEnd& e, int& flip, float& m, float& sum) {
+  constexpr int kBuf = CeCfg<STREAMS>::kBufBytes;
+  const int col0 = t.col0 + c * 32;
+  const int row0 = t.row - static_cast<int>(threadIdx.x & 31);
+  if constexpr (MODE == kCeLse) {
+    if (col0 < t.cols) {
+      float x[32];
+      float top = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        x[k] = __uint_as_float(v[k]) * e.c2;
+        if (col0 + k >= t.cols) x[k] = -INFINITY;
+        top = fmaxf(top, x[k]);
+      }
+      if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (t.tgt - c * 32 == k) e.tlog[t.row] = __uint_as_float(v[k]);
+      }
+      const float m2 = fmaxf(m, top);
+      const float ref = m2 == -INFINITY ? 0.0f : m2;  // no -inf - -inf
+      float add = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) add += pow2(x[k] - ref);
+      sum = fmaf(sum, pow2(m - ref), add);
+      m = m2;
+    }
+  } else if constexpr (MODE == kCeDx) {
+    uint32_t w[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) w[k] = t.none ? 0u : v[k];
+    put_chunk_f32(t.staging, kBuf, flip, w, t.out, t.buf_row - t.row + row0, col0, t.d,
+                  row0 < t.count, t.add);
+  } else {
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if constexpr (MODE == kCeGrad) {
+        float g[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float p = pow2(fmaf(__uint_as_float(v[2 * k + h]), e.c2, -t.lse2));
+          g[h] = t.dl * (t.tgt - c * 32 == 2 * k + h ? p - 1.0f : p);
+          if (!t.row_ok) g[h] = 0.0f;  // the rows up to a full K block of kDw
+        }
+        w[k] = pack_bf16x2(g[0], g[1]);
+      } else {
+        w[k] = t.none ? 0u  // no rows: an empty sum
+                      : pack_bf16x2(__uint_as_float(v[2 * k]) * t.out_scale,
+                                    __uint_as_float(v[2 * k + 1]) * t.out_scale);
+      }
+    }
+    if constexpr (MODE == kCeGrad)
+      put_chunk<false>(t.staging, kBuf, flip, c, w, t.out, row0, col0, e.M, t.cols, t.pol);
+    else
+      put_chunk<STREAMS == 1>(t.staging, kBuf, flip, c, w, t.out, t.v0 + row0, col0,
+                              t.v0 + t.cols, t.d, t.pol);
+  }
+}
+
+// A warp's 128 columns, 32 at a time: the next are on their way from tensor
+// memory while the ending works on the present ones; the accumulator is free
+// once the last have arrived.
+template <int MODE, int STREAMS>
+__device__ __forceinline__ void ce_tile(uint32_t tb, const CeFree& release, const CeTileArgs& t,
+                                        const CeEnd& e, int& flip, float& m, float& sum) {
+  uint32_t va[32], vb[32];
+  tmem_ld32(tb, va);
+  tmem_wait_ld();
+  if (release.two) add_acc32(tb + 256, va);  // the second half of K
+  tmem_ld32(tb + 32, vb);
+  ce_chunk<MODE, STREAMS>(0, va, t, e, flip, m, sum);
+  tmem_wait_ld();
+  if (release.two) add_acc32(tb + 256 + 32, vb);
+  tmem_ld32(tb + 64, va);
+  ce_chunk<MODE, STREAMS>(1, vb, t, e, flip, m, sum);
+  tmem_wait_ld();
+  if (release.two) add_acc32(tb + 256 + 64, va);
+  tmem_ld32(tb + 96, vb);
+  ce_chunk<MODE, STREAMS>(2, va, t, e, flip, m, sum);
+  tmem_wait_ld();
+  if (release.two) add_acc32(tb + 256 + 96, vb);
+  release();
+  ce_chunk<MODE, STREAMS>(3, vb, t, e, flip, m, sum);
 }
 
 template <int STREAMS>
@@ -249,7 +418,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, nullptr};
+  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, prof_slots(kctl.prof)};
+  const long long t_start = clock64();
   if (threadIdx.x == 0) griddep_launch_dependents();
   // the number of scored rows is an output of the kernel before
   griddep_wait();
@@ -396,18 +566,31 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     const int q = warp & 3;
     const int half = (warp - 4) >> 2;  // columns 128 * half .. of the tile
     const uint64_t pol = l2_evict_first_policy();
-    const uint32_t tempty_leader[2] = {mapa_shared(smem_u32(&tempty[0]), 0),
-                                       mapa_shared(smem_u32(&tempty[1]), 0)};
-    uint8_t* my_staging = staging + (warp - 4) * 2 * kStageChunkBytes;
+    const uint32_t lead_empty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t lead_empty1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    uint8_t* my_staging = staging + (warp - 4) * 2 * Cfg::kBufBytes;
     int flip = 0;
     const float out_scale = e.mean ? e.scale / static_cast<float>(max(count, 1)) : e.scale;
-    int use[2] = {0, 0};  // of the accumulators
+    int use0 = 0, use1 = 0;  // of the accumulators
     int turn = 0;
     bool ok = true;
     CeUnit u;
     for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
       const CeJob& j = a.job[u.job];
-      const bool two = STREAMS == 1 && ce_two_k(a.job[u.job], u);
+      const int mode = j.mode;
+      const bool two = STREAMS == 1 && ce_two_k(j, u);
+      CeTileArgs t;
+      t.out = &j.o;
+      t.staging = my_staging;
+      t.pol = pol;
+      t.col0 = u.nb * kCeTile + half * 128;
+      t.none = u.kb0 == u.kb1;  // also a split without a K block of a short piece
+      t.cols = j.cols;
+      t.v0 = j.v0;
+      t.d = a.d;
+      t.count = count;
+      t.add = j.add != 0;
+      t.out_scale = out_scale;
 #pragma unroll 1
       for (int i = 0; i < STREAMS; ++i) {
         int acc_i = i;
@@ -415,110 +598,48 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           acc_i = turn;
           turn ^= 1;
         }
-        const int row = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM + q * 32 + lane;
-        const bool row_ok = row < count;
-        int tgt = -1;
-        float lse2 = 0.0f, dl = 0.0f;
-        if ((j.mode == kCeLse || j.mode == kCeGrad) && row_ok) {
-          tgt = e.tgt[row] - j.v0 - u.nb * kCeTile - half * 128;  // column of the target here
-          if (j.mode == kCeGrad) {
-            lse2 = e.lse2[row];
-            dl = e.dl[row];
+        t.row = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM + q * 32 + lane;
+        t.row_ok = t.row < count;
+        t.buf_row = u.split * e.m_pad + t.row;
+        t.tgt = -1;
+        t.lse2 = t.dl = 0.0f;
+        if ((mode == kCeLse || mode == kCeGrad) && t.row_ok) {
+          t.tgt = e.tgt[t.row] - t.v0 - t.col0;
+          if (mode == kCeGrad) {
+            t.lse2 = e.lse2[t.row];
+            t.dl = e.dl[t.row];
           }
         }
-        ok = wait_bar(&tfull[acc_i], (acc_i ? use[1] : use[0]) & 1, ctl, kSiteEpiAccFull);
-        if (acc_i) ++use[1];
-        else ++use[0];
-        if (ok && two) ok = wait_bar(&tfull[1], use[1]++ & 1, ctl, kSiteEpiAccFull);
+        ok = wait_bar(&tfull[acc_i], (acc_i ? use1 : use0) & 1, ctl, kSiteEpiAccFull);
+        if (acc_i) ++use1;
+        else ++use0;
+        if (ok && two) ok = wait_bar(&tfull[1], use1++ & 1, ctl, kSiteEpiAccFull);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tb =
             tmem_base + acc_i * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-        const int tile_col = u.nb * kCeTile + half * 128;
+        const CeFree release{acc_i ? &tempty[1] : &tempty[0], &tempty[1],
+                             acc_i ? lead_empty1 : lead_empty0, lead_empty1, leader, two};
         float m = -INFINITY, sum = 0.0f;  // kLse
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int col0 = tile_col + c * 32;
-          uint32_t v[32];
-          tmem_ld32(tb + c * 32, v);
-          tmem_wait_ld();
-          if (two) add_acc32(tb + 256 + c * 32, v);  // the second half of K
-          if (c == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (leader) mbar_arrive(&tempty[acc_i]);
-              else mbar_arrive_cluster(tempty_leader[acc_i]);
-              if (two) {
-                if (leader) mbar_arrive(&tempty[1]);
-                else mbar_arrive_cluster(tempty_leader[1]);
-              }
-            }
-          }
-          if (j.mode == kCeLse) {
-            if (col0 < j.cols) {
-              float x[32];
-              float top = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                x[k] = __uint_as_float(v[k]) * e.c2;
-                if (col0 + k >= j.cols) x[k] = -INFINITY;
-                top = fmaxf(top, x[k]);
-              }
-              if (static_cast<unsigned>(tgt - c * 32) < 32u) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                  if (tgt - c * 32 == k) e.tlog[row] = __uint_as_float(v[k]);
-              }
-              const float m2 = fmaxf(m, top);
-              const float ref = m2 == -INFINITY ? 0.0f : m2;  // no -inf - -inf
-              float add = 0.0f;
-#pragma unroll
-              for (int k = 0; k < 32; ++k) add += pow2(x[k] - ref);
-              sum = fmaf(sum, pow2(m - ref), add);
-              m = m2;
-            }
-          } else if (j.mode == kCeGrad) {
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float g[2];
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float p = pow2(fmaf(__uint_as_float(v[2 * k + h]), e.c2, -lse2));
-                g[h] = dl * (tgt - c * 32 == 2 * k + h ? p - 1.0f : p);
-                if (!row_ok) g[h] = 0.0f;  // the rows up to a full K block of kDw
-              }
-              w[k] = pack_bf16x2(g[0], g[1]);
-            }
-            store_chunk32(my_staging, flip, w, &j.o, row - lane, col0, e.M, j.cols, pol);
-          } else if (j.mode == kCeDx) {
-            if (u.kb0 == u.kb1) {  // a split without a K block of a short piece
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] = 0u;
-            }
-            put_chunk_f32(my_staging, flip, v, &j.o, u.split * e.m_pad + row - lane, col0, a.d,
-                          j.add != 0);
-          } else {
-            uint32_t w[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float lo = __uint_as_float(v[2 * k]) * out_scale;
-              const float hi = __uint_as_float(v[2 * k + 1]) * out_scale;
-              w[k] = u.kb0 < u.kb1 ? pack_bf16x2(lo, hi) : 0u;  // no rows: an empty sum
-            }
-            store_chunk32(my_staging, flip, w, &j.o, j.v0 + row - lane, col0, j.v0 + j.cols, a.d,
-                          pol);
-          }
+        if (mode == kCeLse) {
+          ce_tile<kCeLse, STREAMS>(tb, release, t, e, flip, m, sum);
+          if (t.row_ok)
+            e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
+        } else if (mode == kCeGrad) {
+          ce_tile<kCeGrad, STREAMS>(tb, release, t, e, flip, m, sum);
+        } else if (mode == kCeDx) {
+          ce_tile<kCeDx, STREAMS>(tb, release, t, e, flip, m, sum);
+        } else {
+          ce_tile<kCeDw, STREAMS>(tb, release, t, e, flip, m, sum);
         }
-        if (j.mode == kCeLse && row_ok)
-          e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + row] = make_float2(m, sum);
       }
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
   }
 
+  if (ctl.prof && threadIdx.x == 0)
+    atomicAdd(&ctl.prof[31], static_cast<unsigned long long>(clock64() - t_start));
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // no CTA leaves while its peer may still signal it or read its memory
