@@ -3,18 +3,22 @@
 //   norm = sqrt(sum over all tensors of x^2),
 //   factor = min(1, max_norm / (norm + eps)),  out = factor * x.
 //
-// HBM-bound: one read of every tensor for the norm, then one read and one
+// HBM-bound (836M bf16 values: norm 231 us, 7.2 TB/s; scaling into other buffers
+// 510 us, 6.5 TB/s; eight 16-byte loads in flight per thread, 835 us in all with
+// four): one read of every tensor for the norm, then one read and one
 // write where the factor is below 1 (in place with a factor of 1 nothing is
 // touched again; into other buffers the values are copied).
 //
-// The tensors are cut into chunks of 32768 elements, dealt to the CTAs in a
+// The tensors are cut into chunks of 2048 to 32768 elements, dealt to the CTAs in a
 // fixed order, and every CTA writes its own partial sum, which the second
 // kernel adds in a fixed order: no atomics, the same bits on every run.
 //
 // Squares outside fp32's range: a vector of eight values whose squares add up
-// to more than 1e30 or less than 1e-30 is squared again scaled by 2^-96 or
+// to more than 1e24 or less than 1e-30 is squared again scaled by 2^-96 or
 // 2^96, into sums of their own, so that the norm neither overflows nor loses
-// small gradients.  Per chunk the sums are carried in 64 bits.
+// small gradients.  Beyond a chunk the sums are carried as pairs of fp32 values
+// (a sum and what its roundings left out): fp64 would do, but this GPU has two
+// fp64 lanes per SM, and sums and a root in fp64 took 40 of 800 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +32,7 @@ namespace gbf {
 namespace {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 32768;  // elements
+constexpr int kClipMinChunk = 2048, kClipMaxChunk = 32768;  // elements
 constexpr int kClipList = 512;     // tensors per launch at most
 
 struct ClipTensor {
@@ -38,14 +42,25 @@ struct ClipTensor {
   int64_t first_chunk;  // chunks of the launch's tensors before this one
 };
 
+// Elements of a 16-byte block before p: the chunks of a tensor are cut where
+// p - before would be, so that only the first of them begins inside a block.
+int before_of(const void* p, int type) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / (type == 1 ? 4 : 2));
+}
+template <typename T>
+__device__ __forceinline__ int before_of(const T* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+
 template <int LIST>
 struct ClipArgs {
   ClipTensor t[LIST];
   unsigned f32[LIST / 32];  // bit i: tensor i holds 32-bit values (else bf16)
   int tensors;
   int64_t chunks;
-  double* partial;        // this launch's sums: [CTA][3]
-  const double* sums;     // every launch's sums, for the second kernel
+  int chunk;              // elements
+  float2* partial;        // this launch's sums: [CTA][3]
+  const float2* sums;     // every launch's sums, for the second kernel
   int num_sums;           // triples
   float* norm;
   float max_norm, eps;
@@ -64,7 +79,27 @@ __device__ __forceinline__ int tensor_of(const ClipArgs<LIST>& a, int64_t chunk)
   return lo;
 }
 
-constexpr float kBigSum = 1e30f, kSmallSum = 1e-30f;
+// A sum and the rounding errors of its additions.
+struct Pair {
+  float hi = 0.0f, lo = 0.0f;
+  __device__ __forceinline__ void add(float x, float more = 0.0f) {
+    const float s = __fadd_rn(hi, x);
+    const float b = __fadd_rn(s, -hi);
+    // an infinite or NaN sum has no error to keep
+    const float e = __fadd_rn(__fadd_rn(hi, -__fadd_rn(s, -b)), __fadd_rn(x, -b));
+    lo += (isfinite(s) ? e : 0.0f) + more;
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Pair& o) { add(o.hi, o.lo); }
+  __device__ __forceinline__ Pair shuffled(int mask) const {
+    Pair o;
+    o.hi = __shfl_xor_sync(0xFFFFFFFFu, hi, mask);
+    o.lo = __shfl_xor_sync(0xFFFFFFFFu, lo, mask);
+    return o;
+  }
+};
+
+constexpr float kBigSum = 1e24f, kSmallSum = 1e-30f;
 constexpr float kDown = 0x1p-96f, kUp = 0x1p96f;
 
 struct Squares {
@@ -128,7 +163,7 @@ __device__ __forceinline__ void square_range(const T* p, int n, Squares& s) {
   const int head = head_of(p, n);
   const int vecs = (n - head) / kN;
   const uint4* v = reinterpret_cast<const uint4*>(p + head);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   int i = threadIdx.x;
   for (; i + (kAhead - 1) * kClipThreads < vecs; i += kAhead * kClipThreads) {
     uint4 u[kAhead];
@@ -154,42 +189,61 @@ __device__ __forceinline__ void square_range(const T* p, int n, Squares& s) {
   }
 }
 
+// The elements [at, at + n) of tensor i that chunk c holds, cut along the blocks
+// of `by`.
+template <typename T>
+__device__ __forceinline__ int chunk_of(int64_t c, int chunk, int64_t count, const T* by,
+                                        int64_t& at) {
+  const int64_t from = c * chunk - before_of(by);
+  at = from > 0 ? from : 0;
+  return static_cast<int>(min(from + chunk, count) - at);
+}
+
+// Sums over the CTA, in the same order on every run; valid in thread 0.
+__device__ __forceinline__ void block_sum(Pair (&sum)[3], Pair (&part)[kClipThreads / 32][3]) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k].add(sum[k].shuffled(o));
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[threadIdx.x >> 5][k] = sum[k];
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int w = 1; w < kClipThreads / 32; ++w)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sum[k].add(part[w][k]);
+}
+
 template <int LIST>
 __global__ void __launch_bounds__(kClipThreads)
     clip_norm_kernel(const __grid_constant__ ClipArgs<LIST> a) {
-  __shared__ double part[kClipThreads / 32][3];
+  __shared__ Pair part[kClipThreads / 32][3];
   griddep_launch_dependents();
   griddep_wait();
-  double mid = 0.0, high = 0.0, low = 0.0;
+  Pair sum[3];  // the squares as they are, scaled down, scaled up
   for (int64_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const int i = tensor_of(a, c);
-    const int64_t at = (c - a.t[i].first_chunk) * kClipChunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kClipChunk), a.t[i].n - at));
+    int64_t at;
     Squares s;
-    if ((a.f32[i >> 5] >> (i & 31)) & 1u)
-      square_range(static_cast<const float*>(a.t[i].in) + at, n, s);
-    else
-      square_range(static_cast<const __nv_bfloat16*>(a.t[i].in) + at, n, s);
-    mid += s.mid;
-    high += s.high;
-    low += s.low;
+    if ((a.f32[i >> 5] >> (i & 31)) & 1u) {
+      const float* p = static_cast<const float*>(a.t[i].in);
+      const int n = chunk_of(c - a.t[i].first_chunk, a.chunk, a.t[i].n, p, at);
+      square_range(p + at, n, s);
+    } else {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.t[i].in);
+      const int n = chunk_of(c - a.t[i].first_chunk, a.chunk, a.t[i].n, p, at);
+      square_range(p + at, n, s);
+    }
+    sum[0].add(s.mid);
+    sum[1].add(s.high);
+    sum[2].add(s.low);
   }
+  block_sum(sum, part);
+  if (threadIdx.x == 0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    mid += __shfl_xor_sync(0xFFFFFFFFu, mid, o);
-    high += __shfl_xor_sync(0xFFFFFFFFu, high, o);
-    low += __shfl_xor_sync(0xFFFFFFFFu, low, o);
-  }
-  if ((threadIdx.x & 31) == 0) {
-    part[threadIdx.x >> 5][0] = mid;
-    part[threadIdx.x >> 5][1] = high;
-    part[threadIdx.x >> 5][2] = low;
-  }
-  __syncthreads();
-  if (threadIdx.x < 3) {
-    double t = 0.0;
-    for (int w = 0; w < kClipThreads / 32; ++w) t += part[w][threadIdx.x];
-    a.partial[blockIdx.x * 3 + threadIdx.x] = t;
+    for (int k = 0; k < 3; ++k)
+      a.partial[static_cast<int64_t>(blockIdx.x) * 3 + k] = make_float2(sum[k].hi, sum[k].lo);
   }
 }
 
@@ -230,7 +284,7 @@ __device__ __forceinline__ void scale_range(const T* p, T* out, int n, float fac
     for (int j = 0; j < kN; ++j) f[j] *= factor;
     o[i] = Vec<T>::pack(f);
   };
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   int i = threadIdx.x;
   if (shift == 0) {
     for (; i + (kAhead - 1) * kClipThreads < vecs; i += kAhead * kClipThreads) {
@@ -263,53 +317,71 @@ __device__ __forceinline__ void scale_range(const T* p, T* out, int n, float fac
 template <int LIST>
 __global__ void __launch_bounds__(kClipThreads)
     clip_scale_kernel(const __grid_constant__ ClipArgs<LIST> a) {
-  __shared__ double part[kClipThreads / 32][3];
+  __shared__ Pair part[kClipThreads / 32][3];
+  __shared__ float shared_factor;
   griddep_launch_dependents();
   griddep_wait();
-  double s[3] = {0.0, 0.0, 0.0};
+  Pair sum[3];
   for (int i = threadIdx.x; i < a.num_sums; i += kClipThreads)
 #pragma unroll
-    for (int k = 0; k < 3; ++k) s[k] += a.sums[i * 3 + k];
+    for (int k = 0; k < 3; ++k) sum[k].add(a.sums[i * 3 + k].x, a.sums[i * 3 + k].y);
+  block_sum(sum, part);
+  if (threadIdx.x == 0) {
+    float norm, factor;
+    if (sum[1].hi == 0.0f && sum[0].hi >= 1e-12f) {
+      // the squares scaled up are under 1e-30 for each vector: nothing next to this
+      norm = __fsqrt_rn(sum[0].hi + sum[0].lo);
+      const float ratio = __fdiv_rn(a.max_norm, norm + a.eps);
+      factor = ratio >= 1.0f ? 1.0f : ratio;
+    } else {
+      double t[3];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) s[k] += __shfl_xor_sync(0xFFFFFFFFu, s[k], o);
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) part[threadIdx.x >> 5][k] = s[k];
+      for (int k = 0; k < 3; ++k)
+        t[k] = static_cast<double>(sum[k].hi) + static_cast<double>(sum[k].lo);
+      const double wide = sqrt(t[1] * 0x1p192 + t[0] + t[2] * 0x1p-192);
+      // a NaN norm makes the factor NaN
+      const double ratio = static_cast<double>(a.max_norm) / (wide + static_cast<double>(a.eps));
+      norm = static_cast<float>(wide);
+      factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);
+      if (wide == 0.0) factor = 1.0f;
+    }
+    if (isinf(a.max_norm)) factor = 1.0f;  // the norm alone
+    shared_factor = factor;
+    if (blockIdx.x == 0) *a.norm = norm;
+  }
   __syncthreads();
-  double t[3] = {0.0, 0.0, 0.0};
-  for (int w = 0; w < kClipThreads / 32; ++w)
-#pragma unroll
-    for (int k = 0; k < 3; ++k) t[k] += part[w][k];
-  const double norm = sqrt(t[1] * 0x1p192 + t[0] + t[2] * 0x1p-192);
-  // a NaN norm makes the factor NaN; an infinite limit means no clipping
-  const double ratio = static_cast<double>(a.max_norm) / (norm + static_cast<double>(a.eps));
-  float factor = ratio >= 1.0 ? 1.0f : static_cast<float>(ratio);
-  if (isinf(a.max_norm) || norm == 0.0) factor = 1.0f;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
+  const float factor = shared_factor;
   if (a.in_place && factor == 1.0f) return;
   for (int64_t r = blockIdx.x; r < a.chunks; r += gridDim.x) {
     const int64_t c = a.chunks - 1 - r;
     const int i = tensor_of(a, c);
-    const int64_t at = (c - a.t[i].first_chunk) * kClipChunk;
-    const int n = static_cast<int>(min(static_cast<int64_t>(kClipChunk), a.t[i].n - at));
-    if ((a.f32[i >> 5] >> (i & 31)) & 1u)
-      scale_range(static_cast<const float*>(a.t[i].in) + at, static_cast<float*>(a.t[i].out) + at,
-                  n, factor);
-    else
-      scale_range(static_cast<const __nv_bfloat16*>(a.t[i].in) + at,
-                  static_cast<__nv_bfloat16*>(a.t[i].out) + at, n, factor);
+    int64_t at;
+    if ((a.f32[i >> 5] >> (i & 31)) & 1u) {
+      float* out = static_cast<float*>(a.t[i].out);
+      const int n = chunk_of(c - a.t[i].first_chunk, a.chunk, a.t[i].n, out, at);
+      scale_range(static_cast<const float*>(a.t[i].in) + at, out + at, n, factor);
+    } else {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.t[i].out);
+      const int n = chunk_of(c - a.t[i].first_chunk, a.chunk, a.t[i].n, out, at);
+      scale_range(static_cast<const __nv_bfloat16*>(a.t[i].in) + at, out + at, n, factor);
+    }
   }
 }
 
 template <int LIST>
 cudaError_t run_clip(const void* const* in, void* const* out, const int64_t* counts,
                      const int* types, int n, float max_norm, float eps, float* norm,
-                     double* partial, int sms, cudaStream_t stream) {
+                     float2* partial, int sms, cudaStream_t stream) {
   const int launches = std::max(1, (n + LIST - 1) / LIST);
   const int most = clip_ctas(sms);
-  auto prepare = [&](int l, ClipArgs<LIST>& a) {
+  // Long chunks save the way from one to the next, short ones keep every SM busy:
+  // the longest of which there are two for each CTA.  (0.5M values in 51 tensors:
+  // 7.3 us, 7.5 with 8192 as the shortest.)
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += counts[i];
+  int chunk = kClipMaxChunk;
+  while (chunk > kClipMinChunk && total / chunk < 2 * most) chunk /= 2;
+  auto prepare = [&](int l, ClipArgs<LIST>& a, bool scale) {
     a = ClipArgs<LIST>{};
     const int first = l * LIST;
     const int last = std::min(n, first + LIST);
@@ -318,8 +390,10 @@ cudaError_t run_clip(const void* const* in, void* const* out, const int64_t* cou
       const int k = a.tensors++;
       a.t[k] = ClipTensor{in[i], out ? out[i] : const_cast<void*>(in[i]), counts[i], a.chunks};
       if (types[i] == 1) a.f32[k >> 5] |= 1u << (k & 31);
-      a.chunks += (counts[i] + kClipChunk - 1) / kClipChunk;
+      const int before = before_of(scale ? a.t[k].out : a.t[k].in, types[i]);
+      a.chunks += (counts[i] + before + chunk - 1) / chunk;
     }
+    a.chunk = chunk;
     a.max_norm = max_norm;
     a.eps = eps;
     a.norm = norm;
@@ -342,14 +416,14 @@ cudaError_t run_clip(const void* const* in, void* const* out, const int64_t* cou
   ClipArgs<LIST> a;
   int sums = 0;
   for (int l = 0; l < launches; ++l) {
-    const int grid = prepare(l, a);
+    const int grid = prepare(l, a, false);
     a.partial = partial + 3 * static_cast<int64_t>(sums);
     const cudaError_t e = launch(clip_norm_kernel<LIST>, grid, a);
     if (e != cudaSuccess) return e;
     sums += grid;
   }
   for (int l = 0; l < launches; ++l) {
-    const int grid = prepare(l, a);
+    const int grid = prepare(l, a, true);
     a.num_sums = sums;
     const cudaError_t e = launch(clip_scale_kernel<LIST>, grid, a);
     if (e != cudaSuccess) return e;
@@ -364,7 +438,7 @@ int clip_launches(int n) { return std::max(1, (n + kClipList - 1) / kClipList); 
 
 cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* counts,
                                   const int* types, int n, float max_norm, float eps, float* norm,
-                                  double* partial, int sms, cudaStream_t stream) {
+                                  float2* partial, int sms, cudaStream_t stream) {
   // a short list keeps the launch's arguments small
   return n <= 64 ? run_clip<64>(in, out, counts, types, n, max_norm, eps, norm, partial, sms,
                                 stream)

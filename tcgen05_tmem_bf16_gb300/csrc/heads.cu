@@ -210,7 +210,7 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case GBF_OP_CLIP_GRAD_NORM:
       if (M > kMaxInt) return 0;
       return align256(static_cast<size_t>(clip_launches(static_cast<int>(M))) *
-                      clip_ctas(kMaxSms) * 3 * sizeof(double));
+                      clip_ctas(kMaxSms) * 3 * sizeof(float2));
     case GBF_OP_LINEAR_CE:
     case GBF_OP_LINEAR_CE_GRAD: {
       if (M > (int64_t(1) << 24) || N > (int64_t(1) << 26) || K > (int64_t(1) << 20)) return 0;
@@ -295,7 +295,7 @@ gbf_status_t gbf_clip_grad_norm(const void* const* grads, void* const* out, cons
   if (!workspace || workspace_bytes < need) return GBF_ERR_WORKSPACE;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   return cuda_status(launch_clip_grad_norm(grads, out, counts, types, tensors, max_norm, eps, norm,
-                                           static_cast<double*>(workspace),
+                                           static_cast<float2*>(workspace),
                                            dev->sms < kMaxSms ? dev->sms : kMaxSms,
                                            reinterpret_cast<cudaStream_t>(stream)));
 }

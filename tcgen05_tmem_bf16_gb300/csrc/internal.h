@@ -146,12 +146,12 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
                                   cudaStream_t stream);
 
 // Global norm and clipping (clip.cu).  out == null: in place.  partial: three
-// doubles for each of clip_ctas() CTAs of each of clip_launches() launches.
+// float2 for each of clip_ctas() CTAs of each of clip_launches() launches.
 int clip_ctas(int sms);
 int clip_launches(int n);
 cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const int64_t* counts,
                                   const int* types, int n, float max_norm, float eps, float* norm,
-                                  double* partial, int sms, cudaStream_t stream);
+                                  float2* partial, int sms, cudaStream_t stream);
 
 // Linear cross entropy (linear_ce.cu).  One product of the kernel with its
 // ending; the scored rows are numbered 0 .. count-1 in their order.
