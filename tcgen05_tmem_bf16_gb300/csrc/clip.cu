@@ -17,8 +17,8 @@
 // to more than 1e24 or less than 1e-30 is squared again scaled by 2^-96 or
 // 2^96, into sums of their own, so that the norm neither overflows nor loses
 // small gradients.  Beyond a chunk the sums are carried as pairs of fp32 values
-// (a sum and what its roundings left out): fp64 would do, but this GPU has two
-// fp64 lanes per SM, and sums and a root in fp64 took 40 of 800 us.
+// (a sum and what its roundings left out): fp64 would do, but is slow on this
+// GPU (0.5M values in 171 chunks: 30.7 us with sums and root in fp64, 7.3 so).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -8,16 +8,16 @@
 // fp32, in the order of m.  Summing with atomics would add in an order that
 // changes from run to run, so the positions are sorted by id first and the
 // sorted list is cut into pieces of equal length, however the ids repeat:
-//   1. embed_rank_kernel (up to 8192 positions: each placed by comparison with
-//      all others) or embed_sort_kernel (a stable radix sort inside one
-//      cluster of CTAs): the positions in the order of (id, m);
+//   1. embed_sort_kernel: the positions in the order of (id, m), by a stable
+//      radix sort inside one cluster of CTAs;
 //   2. embed_sum_kernel: one piece of the list x 1024 columns per CTA.  A run
 //      of equal ids inside the piece is summed and written; the part of a run
 //      that continues from the previous piece or into the next one goes to the
-//      workspace in fp32.  Without accumulation further CTAs of kernel 1 or 2
-//      write the zero rows of the ids that do not occur;
+//      workspace in fp32.  Without accumulation further CTAs write the
+//      zero rows of the ids that do not occur;
 //   3. embed_join_kernel: the runs over several pieces, their parts added in
 //      order, written once.
+// Up to 1024 positions one kernel does without sorting (embed_direct_kernel).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -97,7 +97,7 @@ __device__ __forceinline__ int ld_dsmem_s32(uint32_t addr) {
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads)
     embed_sort_kernel(const Id* __restrict__ ids, int M, int V, int passes, int digit_bits,
-                      int* key0, int* idx0, int* key1, int* idx1, unsigned* present) {
+                      int* key0, int* idx0, int* key1, int* idx1) {
   extern __shared__ int sort_smem[];
   __shared__ int warp_sum[kSortWarps];
   int* hist = sort_smem;                            // [warps][digits]
@@ -105,16 +105,11 @@ __global__ void __launch_bounds__(kSortThreads)
   int* base = total + kMaxDigits;                    // where this CTA's digits begin
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int ctas = static_cast<int>(gridDim.x);  // one cluster
+  constexpr int ctas = kSortCluster;
   const int rank = static_cast<int>(cluster_ctarank());
   const int digits = 1 << digit_bits;
   griddep_launch_dependents();
   griddep_wait();
-  if (present) {
-    const int words = (V + 31) / 32;
-    for (int i = rank * kSortThreads + threadIdx.x; i < words; i += ctas * kSortThreads)
-      present[i] = 0u;
-  }
   // contiguous shares, multiples of 32 so that a warp's steps are full but the last
   const int64_t share =
       ((static_cast<int64_t>(M) + ctas * kSortWarps - 1) / (ctas * kSortWarps) + 31) / 32 * 32;
@@ -133,16 +128,40 @@ __global__ void __launch_bounds__(kSortThreads)
       const int64_t id = static_cast<int64_t>(ids[i]);
       return (id >= 0 && id < V) ? static_cast<int>(id) : V;
     };
+    // the first steps' items stay in registers from counting to placing
+    constexpr int kKept = 4;
+    int kept_key[kKept], kept_idx[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = lo + k * 32 + lane;
+      kept_key[k] = i < hi ? key_at(i) : 0;
+      kept_idx[k] = i < hi ? (pass > 0 ? ld_cg(isrc + i) : i) : 0;
+    }
     for (int d = lane; d < digits; d += 32) my_hist[d] = 0;
     __syncwarp();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < hi;
-      // lanes past the end form a group of their own
-      const int d = in ? ((key_at(i) >> shift) & (digits - 1)) : -1;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
-      if (in && lane == __ffs(same) - 1) my_hist[d] += __popc(same);
+    // the lanes with an item of the same digit, by one vote per bit
+    auto alike = [&](bool in, int key) -> unsigned {
+      unsigned same = __ballot_sync(0xFFFFFFFFu, in);
+      for (int b = 0; b < digit_bits; ++b) {
+        const bool one = (key >> (shift + b)) & 1;
+        const unsigned ones = __ballot_sync(0xFFFFFFFFu, one);
+        same &= one ? ones : ~ones;
+      }
+      return same;
+    };
+    auto count = [&](bool in, int key) -> unsigned {
+      const unsigned same = alike(in, key);
+      if (in && lane == __ffs(same) - 1) my_hist[(key >> shift) & (digits - 1)] += __popc(same);
       __syncwarp();
+      return same;
+    };
+    unsigned kept_same[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+      if (lo + k * 32 < hi) kept_same[k] = count(lo + k * 32 + lane < hi, kept_key[k]);
+    for (int i0 = lo + kKept * 32; i0 < hi; i0 += 32) {
+      const bool in = i0 + lane < hi;
+      count(in, in ? key_at(i0 + lane) : 0);
     }
     __syncthreads();
     // per digit: this CTA's count, and each warp's offset within it
@@ -170,7 +189,7 @@ __global__ void __launch_bounds__(kSortThreads)
         int n[kSortCluster];
 #pragma unroll
         for (int c = 0; c < kSortCluster; ++c)
-          n[c] = c < ctas ? ld_dsmem_s32(mapa_shared(at, c)) : 0;
+          n[c] = ld_dsmem_s32(mapa_shared(at, c));
 #pragma unroll
         for (int c = 0; c < kSortCluster; ++c) {
           if (c < rank) before += n[c];
@@ -190,12 +209,8 @@ __global__ void __launch_bounds__(kSortThreads)
       if (d < digits) base[d] = earlier + x - all + before;
     }
     __syncthreads();
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool in = i < hi;
-      const int key = in ? key_at(i) : 0;
-      const int d = in ? ((key >> shift) & (digits - 1)) : -1;
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, d);
+    auto place = [&](bool in, int key, int idx, unsigned same) {
+      const int d = (key >> shift) & (digits - 1);
       int at = 0;
       if (in) at = base[d] + my_hist[d] + __popc(same & ((1u << lane) - 1u));
       __syncwarp();
@@ -203,80 +218,19 @@ __global__ void __launch_bounds__(kSortThreads)
       __syncwarp();
       if (in) {
         kdst[at] = key;
-        idst[at] = pass > 0 ? ld_cg(isrc + i) : i;
-        if (pass == 0 && present && key < V) atomicOr(&present[key >> 5], 1u << (key & 31));
+        idst[at] = idx;
       }
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+      if (lo + k * 32 < hi) place(lo + k * 32 + lane < hi, kept_key[k], kept_idx[k], kept_same[k]);
+    for (int i0 = lo + kKept * 32; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      const bool in = i < hi;
+      const int key = in ? key_at(i) : 0;
+      place(in, key, in ? (pass > 0 ? ld_cg(isrc + i) : i) : 0, alike(in, key));
     }
     cluster_sync_all();  // the pass is written before the next one reads it
-  }
-}
-
-// Up to 8192 positions: the place of each in the sorted list by comparing it
-// with all others, eight positions per warp (1021 positions: 2 us against 14 of
-// the radix sort, whose passes wait on one another; 8192: 5 against 17).  The
-// CTAs from `rank_ctas` on write the zero rows of dtable meanwhile: each looks
-// through the ids for those of its rows.
-constexpr int kRankThreads = 128;
-constexpr int kRankMax = 8192;
-constexpr int kRankEach = 8;
-constexpr int kZeroRows = 1024;  // rows looked for at a time
-
-template <typename Id>
-__global__ void __launch_bounds__(kRankThreads)
-    embed_rank_kernel(const Id* __restrict__ ids, int M, int V, int D, int rank_ctas, int* key_out,
-                      int* idx_out, __nv_bfloat16* __restrict__ dtable) {
-  __shared__ int keys[kRankMax];
-  griddep_launch_dependents();
-  griddep_wait();
-  if (static_cast<int>(blockIdx.x) >= rank_ctas) {
-    unsigned* found = reinterpret_cast<unsigned*>(keys);
-    const int64_t ctas = gridDim.x - rank_ctas;
-    const int64_t me = blockIdx.x - rank_ctas;
-    const int64_t v0 = V * me / ctas, v1 = V * (me + 1) / ctas;
-    for (int64_t first = v0; first < v1; first += kZeroRows) {
-      const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), v1 - first));
-      for (int i = threadIdx.x; i < kZeroRows / 32; i += kRankThreads) found[i] = 0u;
-      __syncthreads();
-      for (int i = threadIdx.x; i < M; i += kRankThreads) {
-        const int64_t r = static_cast<int64_t>(ids[i]) - first;
-        if (r >= 0 && r < rows) atomicOr(&found[r >> 5], 1u << (r & 31));
-      }
-      __syncthreads();
-      for (int r = 0; r < rows; ++r) {
-        if ((found[r >> 5] >> (r & 31)) & 1u) continue;
-        for (int c = threadIdx.x * 8; c < D; c += kRankThreads * 8)
-          st_u4(dtable + (first + r) * D + c, make_uint4(0u, 0u, 0u, 0u));
-      }
-      __syncthreads();
-    }
-    return;
-  }
-  for (int i = threadIdx.x; i < M; i += kRankThreads) {
-    const int64_t id = static_cast<int64_t>(ids[i]);
-    keys[i] = (id >= 0 && id < V) ? static_cast<int>(id) : V;
-  }
-  __syncthreads();
-  const int lane = threadIdx.x & 31;
-  const int e0 = (blockIdx.x * (kRankThreads / 32) + (threadIdx.x >> 5)) * kRankEach;
-  int k[kRankEach], before[kRankEach];
-#pragma unroll
-  for (int e = 0; e < kRankEach; ++e) {
-    k[e] = e0 + e < M ? keys[e0 + e] : 0;
-    before[e] = 0;
-  }
-  for (int j = lane; j < M; j += 32) {
-    const int kj = keys[j];
-#pragma unroll
-    for (int e = 0; e < kRankEach; ++e)
-      before[e] += kj < k[e] || (kj == k[e] && j < e0 + e) ? 1 : 0;
-  }
-#pragma unroll
-  for (int e = 0; e < kRankEach; ++e) {
-    const int at = __reduce_add_sync(0xFFFFFFFFu, before[e]);
-    if (lane == e && e0 + e < M) {
-      key_out[at] = k[e];
-      idx_out[at] = e0 + e;
-    }
   }
 }
 
@@ -292,7 +246,6 @@ struct SumArgs {
   __nv_bfloat16* dtable;
   float* head;      // [pieces][D]: the part of a run that began in an earlier piece
   float* tail;      // [pieces][D]: the part of a run that goes on in the next piece
-  const unsigned* present;
   int M, V, D;
   int piece;        // positions per piece
   int pieces;
@@ -322,8 +275,122 @@ __device__ __forceinline__ void store_part(float* p, const float (&sum)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
 }
 
-// CTAs [0, pieces * segs): sums; the rest: zero rows, one warp per 1024
-// columns of a row.
+// The first position of the sorted list whose key is not under `key`, by one
+// warp, 32 places looked at together.
+__device__ __forceinline__ int lower_bound(const int* keys, int n, int key) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // every position before lo is under, none from hi on
+  while (lo < hi) {
+    const int step = (hi - lo + 31) / 32;
+    const int64_t at = lo + static_cast<int64_t>(lane + 1) * step - 1;
+    const bool under = at < hi && keys[at] < key;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, under));
+    const int64_t next = lo + static_cast<int64_t>(k) * step;
+    hi = static_cast<int>(min(static_cast<int64_t>(hi), next + step - 1));
+    lo = static_cast<int>(min(next, static_cast<int64_t>(hi)));
+  }
+  return lo;
+}
+
+constexpr int kZeroRows = 1024;  // rows looked for at a time
+
+// Writes the zero rows of the me-th of `ctas` equal shares of the table.
+// mark(first, rows, found) sets a bit for each of the rows from `first` on that
+// an id asks for.
+template <typename Mark>
+__device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t me, int64_t ctas, Mark mark) {
+  __shared__ unsigned found[kZeroRows / 32];
+  const int64_t v0 = a.V * me / ctas, v1 = a.V * (me + 1) / ctas;
+  for (int64_t first = v0; first < v1; first += kZeroRows) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kZeroRows), v1 - first));
+    for (int i = threadIdx.x; i < kZeroRows / 32; i += kSumThreads) found[i] = 0u;
+    __syncthreads();
+    mark(first, rows, found);
+    __syncthreads();
+    for (int r = 0; r < rows; ++r) {
+      if ((found[r >> 5] >> (r & 31)) & 1u) continue;
+      for (int c = threadIdx.x * 8; c < a.D; c += kSumThreads * 8)
+        st_u4(a.dtable + (first + r) * a.D + c, make_uint4(0u, 0u, 0u, 0u));
+    }
+    __syncthreads();
+  }
+}
+
+// Up to 1024 positions nothing is sorted: the CTA of position m (x 1024
+// columns) looks through all ids, leaves if one before m is the same, and else
+// sums the rows of those that are, in order.  One launch, no parts to join.
+constexpr int kDirectMax = 1024;
+
+template <typename Id>
+__global__ void __launch_bounds__(kSumThreads)
+    embed_direct_kernel(const Id* __restrict__ ids, const SumArgs a) {
+  __shared__ int keys[kDirectMax];
+  __shared__ int same[kDirectMax];
+  __shared__ int count;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t sums = static_cast<int64_t>(a.M) * a.segs;
+  if (static_cast<int64_t>(blockIdx.x) >= sums) {
+    zero_rows(a, blockIdx.x - sums, gridDim.x - sums,
+              [&](int64_t first, int rows, unsigned* found) {
+                for (int i = threadIdx.x; i < a.M; i += kSumThreads) {
+                  const int64_t r = static_cast<int64_t>(ids[i]) - first;
+                  if (r >= 0 && r < rows) atomicOr(&found[r >> 5], 1u << (r & 31));
+                }
+              });
+    return;
+  }
+  const int m = static_cast<int>(blockIdx.x / a.segs);
+  const int seg = static_cast<int>(blockIdx.x - static_cast<int64_t>(m) * a.segs);
+  for (int i = threadIdx.x; i < a.M; i += kSumThreads) {
+    const int64_t id = static_cast<int64_t>(ids[i]);
+    keys[i] = (id >= 0 && id < a.V) ? static_cast<int>(id) : a.V;
+  }
+  __syncthreads();
+  const int key = keys[m];
+  bool earlier = key == a.V;
+  for (int i = threadIdx.x; i < m; i += kSumThreads) earlier |= keys[i] == key;
+  if (__syncthreads_or(earlier)) return;
+  if (threadIdx.x < 32) {
+    int n = 0;
+    for (int i0 = m; i0 < a.M; i0 += 32) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      const bool hit = i < a.M && keys[i] == key;
+      const unsigned hits = __ballot_sync(0xFFFFFFFFu, hit);
+      if (hit) same[n + __popc(hits & ((1u << threadIdx.x) - 1u))] = i;
+      n += __popc(hits);
+    }
+    if (threadIdx.x == 0) count = n;
+  }
+  __syncthreads();
+  const int col = seg * kSegCols + threadIdx.x * 8;
+  if (col >= a.D) return;
+  const int n = count;
+  const uint4 old = a.accumulate ? ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  constexpr int kAhead = 8;
+  for (int i0 = 0; i0 < n; i0 += kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (i0 + u < n) v[u] = ldg_u4(a.dout + static_cast<int64_t>(same[i0 + u]) * a.D + col);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i0 + u >= n) break;
+      float f[8];
+      unpack8(v[u], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += f[j];
+    }
+  }
+  write_row(a, key, col, sum, old);
+}
+
+// CTAs [0, pieces * segs): sums; the rest: the zero rows of equal shares of the
+// table, those that the sorted list does not hold.
 __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a) {
   __shared__ int skey[kMaxPiece + 2];
   __shared__ int sidx[kMaxPiece];
@@ -331,18 +398,21 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
   griddep_wait();
   const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
   if (static_cast<int64_t>(blockIdx.x) >= sums) {
-    const int64_t step = (static_cast<int64_t>(gridDim.x) - sums) * (kSumThreads / 32);
-    const int lane = threadIdx.x & 31;
-    for (int64_t t = (blockIdx.x - sums) * (kSumThreads / 32) + (threadIdx.x >> 5);
-         t < static_cast<int64_t>(a.V) * a.segs; t += step) {
-      const int64_t v = t / a.segs;
-      if ((a.present[v >> 5] >> (v & 31)) & 1u) continue;
-      const int col0 = static_cast<int>(t - v * a.segs) * kSegCols + lane * 8;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col0 + i * 256 < a.D)
-          st_u4(a.dtable + v * a.D + col0 + i * 256, make_uint4(0u, 0u, 0u, 0u));
-    }
+    __shared__ int begin;
+    zero_rows(a, blockIdx.x - sums, gridDim.x - sums,
+              [&](int64_t first, int rows, unsigned* found) {
+                if (threadIdx.x < 32) {
+                  const int at = lower_bound(a.key, a.M, static_cast<int>(first));
+                  if (threadIdx.x == 0) begin = at;
+                }
+                __syncthreads();
+                for (int64_t i = static_cast<int64_t>(begin) + threadIdx.x; i < a.M;
+                     i += kSumThreads) {
+                  const int64_t r = a.key[i] - first;
+                  if (r >= rows) break;
+                  atomicOr(&found[r >> 5], 1u << (r & 31));
+                }
+              });
     return;
   }
   const int p = static_cast<int>(blockIdx.x / a.segs);
@@ -476,33 +546,29 @@ int bit_length(int64_t x) {
   return n;
 }
 
-template <typename Id>
-cudaError_t launch_rank(const Id* ids, int M, int V, int D, const EmbedGradWs& ws,
-                        __nv_bfloat16* zeros, int sms, cudaStream_t stream) {
-  constexpr int kPer = kRankThreads / 32 * kRankEach;
-  const int ranks = (M + kPer - 1) / kPer;
-  const int more = zeros ? std::min(V, sms * 8) : 0;
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = overlapped(ranks + more, kRankThreads, 0, stream, attr);
-  return cudaLaunchKernelEx(&cfg, embed_rank_kernel<Id>, ids, M, V, D, ranks, ws.key0, ws.idx0,
-                            zeros);
-}
-
-template <typename Id>
-cudaError_t launch_sort(const Id* ids, int M, int V, const EmbedGradWs& ws, int* passes_out,
-                        unsigned* present, cudaStream_t stream) {
-  static std::atomic<uint64_t> mask{0};  // devices on which the kernel's attribute is set
-  auto kernel = embed_sort_kernel<Id>;
+// Lets a kernel have `bytes` of dynamic shared memory, once per device.
+template <auto KERNEL>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> mask{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = uint64_t(1) << (dev & 63);
   if (!(mask.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSortSmem));
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(bytes));
     if (e != cudaSuccess) return e;
     mask.fetch_or(bit, std::memory_order_acq_rel);
   }
+  return cudaSuccess;
+}
+
+template <typename Id>
+cudaError_t launch_sort(const Id* ids, int M, int V, const EmbedGradWs& ws, int* passes_out,
+                        cudaStream_t stream) {
+  auto kernel = embed_sort_kernel<Id>;
+  const cudaError_t e = allow_smem<embed_sort_kernel<Id>>(kSortSmem);
+  if (e != cudaSuccess) return e;
   const int bits = bit_length(V);  // keys 0 .. V
   const int passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
   const int digit_bits = (bits + passes - 1) / passes;
@@ -516,7 +582,7 @@ cudaError_t launch_sort(const Id* ids, int M, int V, const EmbedGradWs& ws, int*
   cfg.numAttrs = 2;
   *passes_out = passes;
   return cudaLaunchKernelEx(&cfg, kernel, ids, M, V, passes, digit_bits, ws.key0, ws.idx0,
-                            ws.key1, ws.idx1, present);
+                            ws.key1, ws.idx1);
 }
 
 }  // namespace
@@ -548,27 +614,11 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
                                   __nv_bfloat16* dtable, int M, int V, int D, float scale,
                                   bool accumulate, const EmbedGradWs& ws, int sms,
                                   cudaStream_t stream) {
-  cudaError_t e;
-  int passes = 1;
-  const bool ranked = M <= kRankMax;
-  unsigned* present = accumulate || ranked ? nullptr : ws.present;
-  if (ranked) {
-    __nv_bfloat16* zeros = accumulate ? nullptr : dtable;
-    e = ids64 ? launch_rank(static_cast<const int64_t*>(ids), M, V, D, ws, zeros, sms, stream)
-              : launch_rank(static_cast<const int*>(ids), M, V, D, ws, zeros, sms, stream);
-  } else {
-    e = ids64 ? launch_sort(static_cast<const int64_t*>(ids), M, V, ws, &passes, present, stream)
-              : launch_sort(static_cast<const int*>(ids), M, V, ws, &passes, present, stream);
-  }
-  if (e != cudaSuccess) return e;
   SumArgs a{};
-  a.key = (passes & 1) ? ws.key0 : ws.key1;
-  a.idx = (passes & 1) ? ws.idx0 : ws.idx1;
   a.dout = dout;
   a.dtable = dtable;
   a.head = ws.head;
   a.tail = ws.tail;
-  a.present = present;
   a.M = M;
   a.V = V;
   a.D = D;
@@ -577,12 +627,24 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
   a.segs = (D + kSegCols - 1) / kSegCols;
   a.scale = scale;
   a.accumulate = accumulate ? 1 : 0;
-  const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
-  int64_t zeros = 0;
-  if (present) {
-    const int64_t warps = static_cast<int64_t>(V) * a.segs;
-    zeros = std::min<int64_t>((warps + 3) / 4, static_cast<int64_t>(sms) * 16);
+  const int64_t zeros = accumulate ? 0 : std::min(V, sms * 8);
+  cudaError_t e;
+  if (M <= kDirectMax) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg =
+        overlapped(static_cast<int64_t>(M) * a.segs + zeros, kSumThreads, 0, stream, attr);
+    return ids64 ? cudaLaunchKernelEx(&cfg, embed_direct_kernel<int64_t>,
+                                      static_cast<const int64_t*>(ids), a)
+                 : cudaLaunchKernelEx(&cfg, embed_direct_kernel<int>, static_cast<const int*>(ids),
+                                      a);
   }
+  int passes = 0;
+  e = ids64 ? launch_sort(static_cast<const int64_t*>(ids), M, V, ws, &passes, stream)
+            : launch_sort(static_cast<const int*>(ids), M, V, ws, &passes, stream);
+  if (e != cudaSuccess) return e;
+  a.key = (passes & 1) ? ws.key0 : ws.key1;
+  a.idx = (passes & 1) ? ws.idx0 : ws.idx1;
+  const int64_t sums = static_cast<int64_t>(a.pieces) * a.segs;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = overlapped(sums + zeros, kSumThreads, 0, stream, attr);
   if ((e = cudaLaunchKernelEx(&cfg, embed_sum_kernel, a)) != cudaSuccess) return e;
