@@ -101,28 +101,33 @@ __global__ void __launch_bounds__(kSwThreads, 2)
     tmem_relinquish();
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
-  griddep_wait();  // the scored rows are listed by the kernel before
-  const int count = *e.count;
+  griddep_wait();  // the gradient's scored rows are listed by the kernel before
+  const int count = GRAD ? *e.count : e.M;
   for (int i = threadIdx.x; i < MPAD; i += kSwThreads) {
-    row_tgt[i] = i < count ? e.tgt[i] - a.v0 : -1;
-    row_lse2[i] = GRAD && i < count ? e.lse2[i] : 0.0f;
-    row_dl[i] = GRAD && i < count ? e.dl[i] : 0.0f;
+    if (GRAD) {
+      row_tgt[i] = i < count ? e.tgt[i] - a.v0 : -1;
+      row_lse2[i] = i < count ? e.lse2[i] : 0.0f;
+      row_dl[i] = i < count ? e.dl[i] : 0.0f;
+    } else {
+      const int64_t t = i < count ? ce_target(a.targets, a.ids64, i) : -1;
+      row_tgt[i] = t >= 0 && t < a.cols ? static_cast<int>(t) : -1;
+    }
   }
+  if (!GRAD && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, prof_slots(kctl.prof)};
   const long long t_start = clock64();
-  // no scored row: no logits (the gradient's G is still written, zeros)
-  const int tiles = (count > 0 || GRAD) ? (a.cols + 127) / 128 : 0;
+  const int tiles = (a.cols + 127) / 128;
   const int num_kb = a.num_kb;
   const int step = static_cast<int>(gridDim.x);
 
   if (warp == 0) {
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");  // the gathered rows: plain stores
-      const CUtensorMap* mx = &a.x[count == e.M ? 1 : 0];
+      const CUtensorMap* mx = &a.x[!GRAD || count == e.M ? 1 : 0];
       uint32_t fills[kStages];
 #pragma unroll
       for (int i = 0; i < kStages; ++i) fills[i] = 0;
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           if (lane < 16 && m < count) {
             e.part[static_cast<int64_t>(4 * t + q) * e.M + m] = make_float2(m2, sum);
             const int at = row_tgt[m] - base;
-            if (at >= 0 && at < 32) e.tlog[m] = my_turn[at * 17 + lane];
+            if (row_tgt[m] >= 0 && at >= 0 && at < 32) e.tlog[m] = my_turn[at * 17 + lane];
           }
           __syncwarp();
         }

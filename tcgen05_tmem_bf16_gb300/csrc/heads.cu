@@ -45,7 +45,7 @@ gbf_status_t check_ids(const void* ids, int index_type, int64_t M, int64_t V, in
 
 constexpr int64_t kMaxSorted = int64_t(1) << 30;
 
-size_t embed_grad_sections(void* base, int64_t M, int64_t V, int64_t D, EmbedGradWs* ws) {
+size_t embed_grad_sections(void* base, int64_t M, int64_t D, EmbedGradWs* ws) {
   Sections s{static_cast<uint8_t*>(base)};
   const int64_t piece = embed_piece(M, static_cast<int>(D));
   const size_t parts = static_cast<size_t>((M + piece - 1) / piece) * D;
@@ -53,7 +53,6 @@ size_t embed_grad_sections(void* base, int64_t M, int64_t V, int64_t D, EmbedGra
   ws->idx0 = s.take<int>(M);
   ws->key1 = s.take<int>(M);
   ws->idx1 = s.take<int>(M);
-  ws->present = s.take<unsigned>((V + 31) / 32);
   ws->head = s.take<float>(parts);
   ws->tail = s.take<float>(parts);
   return s.at;
@@ -205,7 +204,7 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case GBF_OP_EMBEDDING_GRAD: {
       if (M > kMaxSorted || N > kMaxInt || K > kMaxInt) return 0;
       EmbedGradWs ws;
-      return embed_grad_sections(nullptr, M, N, K, &ws);
+      return embed_grad_sections(nullptr, M, K, &ws);
     }
     case GBF_OP_CLIP_GRAD_NORM:
       if (M > kMaxInt) return 0;
@@ -256,7 +255,7 @@ gbf_status_t gbf_embedding_grad(const void* ids, int index_type, const void* dou
   const int64_t segs = (D + 1023) / 1024;
   if (M > kMaxSorted || (D > 0 && M > kMaxInt / segs)) return GBF_ERR_UNSUPPORTED_SHAPE;
   EmbedGradWs ws;
-  const size_t need = embed_grad_sections(workspace, M, V, D, &ws);
+  const size_t need = embed_grad_sections(workspace, M, D, &ws);
   if (need && (!workspace || workspace_bytes < need)) return GBF_ERR_WORKSPACE;
   const DeviceInfo* dev;
   unsigned* err;
@@ -336,6 +335,9 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
     if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
     swap.cols = p.V;
     swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
+    swap.targets = targets;
+    swap.ids64 = index_type == GBF_INDEX_I64;
+    swap.ticket = ws.ticket;
   } else {
     launch.d = p.D;
     CeJob& job = launch.job[1];
@@ -355,7 +357,10 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   end.M = p.M;
   CeJoin join{};
   join.count = ws.count;
-  join.rows = ws.rows;
+  join.rows = few ? nullptr : ws.rows;
+  join.targets = targets;
+  join.ids64 = index_type == GBF_INDEX_I64;
+  join.V = p.V;
   join.part = ws.part;
   join.tlog = ws.tlog;
   join.ticket = ws.ticket;
@@ -366,8 +371,8 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   join.alpha = alpha;
   join.M = p.M;
   join.parts = static_cast<int>(ce_parts(M, V));
-  if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
-      GBF_OK)
+  if (!few && (st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms,
+                                               s))) != GBF_OK)
     return st;
   st = few ? cuda_status(launch_ce_swap(swap, false, end, dev->sms, lib_ctl(err, 2 * dev->sms), s))
            : run_ce_gemm(launch, end, M, *dev, err, s);

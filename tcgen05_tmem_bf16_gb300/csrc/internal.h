@@ -136,7 +136,6 @@ cudaError_t launch_embedding_lookup(const void* ids, bool ids64, const __nv_bflo
                                     cudaStream_t stream);
 struct EmbedGradWs {
   int *key0, *idx0, *key1, *idx1;  // [M] each: the sorted list, twice
-  unsigned* present;               // one bit per table row that occurs
   float *head, *tail;              // [pieces][D]: parts of runs over several pieces
 };
 int embed_piece(int64_t M, int D);  // sorted positions per piece
@@ -187,12 +186,23 @@ struct CeEnd {
   int M;
   int m_pad;          // rows between the splits' fp32 buffers
 };
+#ifdef __CUDACC__
+// Target i of an array of int64 or int32.
+__device__ __forceinline__ int64_t ce_target(const void* targets, int ids64, int64_t i) {
+  return ids64 ? static_cast<const int64_t*>(targets)[i]
+               : static_cast<int64_t>(static_cast<const int*>(targets)[i]);
+}
+#endif
 // The logits for up to kCeSwapMax rows, with swapped roles (ce_swap.cu).
 constexpr int kCeSwapMax = 128;
 int ce_swap_rows(int64_t M);  // rows padded to: 16, 64, 128; 0 above kCeSwapMax
 struct CeSwap {
-  CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored
+  CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored (and forward)
   __nv_bfloat16* gt;    // gradient: [cols][padded rows]
+  // forward: all rows as they are, scored or not (they fill the padding anyway)
+  const void* targets;
+  int ids64;
+  unsigned* ticket;     // zeroed for the join
   int cols, v0, num_kb;
 };
 cudaError_t launch_ce_swap(const CeSwap& a, bool grad, const CeEnd& end, int sms,
@@ -211,7 +221,9 @@ struct CePrep {
 };
 struct CeJoin {
   const int* count;
-  const int* rows;
+  const int* rows;      // null: the rows as they are, scored by these targets
+  const void* targets;
+  int ids64, V;
   const float2* part;
   const float* tlog;
   unsigned* ticket;

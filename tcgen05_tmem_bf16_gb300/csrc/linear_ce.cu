@@ -737,6 +737,12 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return make_float2(m, fmaf(a.y, pow2(a.x - ref), b.y * pow2(b.x - ref)));
 }
 
+__device__ __forceinline__ bool scored(const CeJoin& p, int row) {
+  const int64_t t = ce_target(p.targets, p.ids64, row);
+  return t >= 0 && t < p.V;
+}
+static_assert(kCeSwapMax <= kJoinThreads, "a thread for each row that is taken as it is");
+
 // Eight scored rows per CTA, 64 threads each: adds up each row's partial sums,
 // writes its loss and lse; the last CTA adds the CTAs' sums of losses in order
 // for the mean.
@@ -746,7 +752,7 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   __shared__ bool last;
   griddep_launch_dependents();
   griddep_wait();
-  const int count = *p.count;
+  const int count = p.rows ? *p.count : p.M;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kJoinRows + (lane & (kJoinRows - 1));
   float2 a = make_float2(-INFINITY, 0.0f);
@@ -778,9 +784,16 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
 #pragma unroll
       for (int w = 1; w < kJoinWarps; ++w) a = join(a, part[w][lane]);
       // the differences in 64 bits: a confident row's loss is a small one
-      const double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
-      loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
-      const int r = p.rows[row];
+      double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
+      int r = row;
+      if (p.rows) {
+        r = p.rows[row];
+        loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
+      } else if (scored(p, row)) {
+        loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
+      } else {
+        lse = 0.0;
+      }
       p.loss[r] = static_cast<float>(loss);
       p.lse[r] = static_cast<float>(lse);
     }
@@ -803,11 +816,13 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
   if (lane == 0) sums[warp] = s;
-  __syncthreads();
+  int n = count;
+  if (!p.rows) n = __syncthreads_count(static_cast<int>(threadIdx.x) < p.M && scored(p, threadIdx.x));
+  else __syncthreads();
   if (threadIdx.x == 0) {
     s = 0.0;
     for (int w = 0; w < kJoinWarps; ++w) s += sums[w];
-    *p.mean = static_cast<float>(s / max(count, 1));
+    *p.mean = static_cast<float>(s / max(n, 1));
   }
 }
 
