@@ -286,24 +286,38 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
   const int row0 = t.row - static_cast<int>(threadIdx.x & 31);
   if constexpr (MODE == kCeLse) {
     if (col0 < t.cols) {
-      float x[32];
-      float top = -INFINITY;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        x[k] = __uint_as_float(v[k]) * e.c2;
-        if (col0 + k >= t.cols) x[k] = -INFINITY;
-        top = fmaxf(top, x[k]);
-      }
       if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (t.tgt - c * 32 == k) e.tlog[t.row] = __uint_as_float(v[k]);
       }
+      float top = -INFINITY, add = 0.0f;
+      if (col0 + 32 <= t.cols) {
+        // the largest scaled value is the scaled largest (smallest) one
+        float ext = __uint_as_float(v[0]);
+        if (e.c2 >= 0.0f) {
+#pragma unroll
+          for (int k = 1; k < 32; ++k) ext = fmaxf(ext, __uint_as_float(v[k]));
+        } else {
+#pragma unroll
+          for (int k = 1; k < 32; ++k) ext = fminf(ext, __uint_as_float(v[k]));
+        }
+        top = ext * e.c2;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (col0 + k < t.cols) top = fmaxf(top, __uint_as_float(v[k]) * e.c2);
+      }
       const float m2 = fmaxf(m, top);
       const float ref = m2 == -INFINITY ? 0.0f : m2;  // no -inf - -inf
-      float add = 0.0f;
+      if (col0 + 32 <= t.cols) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) add += pow2(x[k] - ref);
+        for (int k = 0; k < 32; ++k) add += pow2(fmaf(__uint_as_float(v[k]), e.c2, -ref));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (col0 + k < t.cols) add += pow2(fmaf(__uint_as_float(v[k]), e.c2, -ref));
+      }
       sum = fmaf(sum, pow2(m - ref), add);
       m = m2;
     }
@@ -315,22 +329,24 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
                   row0 < t.count, t.add);
   } else {
     uint32_t w[16];
+    if constexpr (MODE == kCeGrad) {
+      float g[32];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if constexpr (MODE == kCeGrad) {
-        float g[2];
+      for (int k = 0; k < 32; ++k) g[k] = pow2(fmaf(__uint_as_float(v[k]), e.c2, -t.lse2));
+      if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float p = pow2(fmaf(__uint_as_float(v[2 * k + h]), e.c2, -t.lse2));
-          g[h] = t.dl * (t.tgt - c * 32 == 2 * k + h ? p - 1.0f : p);
-          if (!t.row_ok) g[h] = 0.0f;  // the rows up to a full K block of kDw
-        }
-        w[k] = pack_bf16x2(g[0], g[1]);
-      } else {
+        for (int k = 0; k < 32; ++k)
+          g[k] += t.tgt - c * 32 == k ? -1.0f : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < 16; ++k)  // zeros in the rows up to a full K block of kDw
+        w[k] = t.row_ok ? pack_bf16x2(t.dl * g[2 * k], t.dl * g[2 * k + 1]) : 0u;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
         w[k] = t.none ? 0u  // no rows: an empty sum
                       : pack_bf16x2(__uint_as_float(v[2 * k]) * t.out_scale,
                                     __uint_as_float(v[2 * k + 1]) * t.out_scale);
-      }
     }
     if constexpr (MODE == kCeGrad)
       put_chunk<false>(t.staging, kBuf, flip, c, w, t.out, row0, col0, e.M, t.cols, t.pol);
