@@ -77,17 +77,22 @@ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // there is no second.
 int ce_streams(int64_t M) { return M > kCeTileRows ? 2 : 1; }
 
-// Parts of K of the product for dx, where its units of work are long next to
-// all work that its launch has for a pair: no part is longer than half of that,
-// or shorter than 8 K blocks.
+// Parts of K of the product for dx, each with an fp32 buffer of its own, 16 at
+// most and none shorter than 8 K blocks.  With one row tile: as many as give one
+// round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 108
+// us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
+// beside dw).  Else: none longer than half of what a pair has to do in all.
 int ce_splits(int64_t M, int64_t D, int64_t cols) {
-  const int64_t rows = kCeTileRows * ce_streams(M);
-  const int64_t m = ceil_div64(M, rows), v = ceil_div64(cols, kCeTileRows);
   const int64_t d = ceil_div64(D, kCeTileRows), k = ceil_div64(cols, 64);
-  const int64_t all = m * d * k + m * v * ceil_div64(D, 64) + ceil_div64(cols, rows) * d * ceil_div64(M, 64);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
+  if (ce_streams(M) == 1)
+    return static_cast<int>(std::max<int64_t>(1, std::min(most, kCePairs / d)));
+  const int64_t rows = 2 * kCeTileRows;
+  const int64_t m = ceil_div64(M, rows), v = ceil_div64(cols, kCeTileRows);
+  const int64_t all = m * d * k + m * v * ceil_div64(D, 64) +
+                      ceil_div64(cols, rows) * d * ceil_div64(M, 64);
   const int64_t half = std::max<int64_t>(1, all / kCePairs / 2);
-  return static_cast<int>(
-      std::max<int64_t>(1, std::min<int64_t>({ceil_div64(k, half), k / 8, 16})));
+  return static_cast<int>(std::min(most, ceil_div64(k, half)));
 }
 
 // Partial sums per row of the forward pass: one per 128 columns of a tile, per
