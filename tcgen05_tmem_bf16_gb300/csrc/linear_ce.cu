@@ -687,6 +687,19 @@ __device__ __forceinline__ int2 block_sum2(int a, int b) {
   return s;
 }
 
+// One row by one warp, four 16-byte vectors per lane in flight; zeros without src.
+__device__ __forceinline__ void copy_row(__nv_bfloat16* dst, const __nv_bfloat16* src, int D) {
+  for (int c0 = (threadIdx.x & 31) * 8; c0 < D; c0 += 4 * 256) {
+    uint4 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      v[k] = src && c0 + k * 256 < D ? ldg_u4(src + c0 + k * 256) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c0 + k * 256 < D) st_u4(dst + c0 + k * 256, v[k]);
+  }
+}
+
 // CTA b takes the rows [b * rows_per, ...): it counts the scored rows before
 // them itself (all targets are a few KB in L2), so one launch lists the scored
 // rows in order, gathers their x where not all are scored, and writes the
@@ -699,6 +712,7 @@ __global__ void __launch_bounds__(kPrepThreads)
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per;
   const int64_t r1 = min(r0 + p.rows_per, static_cast<int64_t>(p.M));
   int total = 0, before = 0;
+#pragma unroll 8
   for (int64_t i = threadIdx.x; i < p.M; i += kPrepThreads) {
     const int64_t t = static_cast<int64_t>(targets[i]);
     const int scored = t >= 0 && t < p.V;
@@ -714,31 +728,40 @@ __global__ void __launch_bounds__(kPrepThreads)
     *p.count = total;
     if (p.ticket) *p.ticket = 0u;
   }
-  for (int64_t r = r0; r < r1; ++r) {
-    const int64_t t = static_cast<int64_t>(targets[r]);
-    if (t >= 0 && t < p.V) {
-      if (threadIdx.x == 0) {
-        p.rows[slot] = static_cast<int>(r);
-        p.tgt[slot] = static_cast<int>(t);
+  // 32 rows at a time: a lane's row in the lists, a warp's row in the copies
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int64_t b0 = r0; b0 < r1; b0 += 32) {
+    const int n = static_cast<int>(min(r1 - b0, static_cast<int64_t>(32)));
+    const int64_t t = lane < n ? static_cast<int64_t>(targets[b0 + lane]) : -1;
+    const bool scored = t >= 0 && t < p.V;
+    const unsigned mask = __ballot_sync(0xFFFFFFFFu, scored);
+    if (warp == 0) {
+      const int64_t r = b0 + lane;
+      if (scored) {
+        const int at = slot + __popc(mask & ((1u << lane) - 1u));
+        p.rows[at] = static_cast<int>(r);
+        p.tgt[at] = static_cast<int>(t);
         if (p.lse2) {
-          p.lse2[slot] = p.lse_in[r] * kLog2e;
-          p.dl[slot] = p.dloss ? p.dloss[r] : 1.0f;
+          p.lse2[at] = p.lse_in[r] * kLog2e;
+          p.dl[at] = p.dloss ? p.dloss[r] : 1.0f;
         }
+      } else if (lane < n && p.loss) {
+        p.loss[r] = 0.0f;
+        p.lse_out[r] = 0.0f;
       }
-      if (gather)
-        for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
-          st_u4(p.xc + static_cast<int64_t>(slot) * p.D + c, ldg_u4(p.x + r * p.D + c));
-      ++slot;
-    } else if (p.dx) {
-      for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
-        st_u4(p.dx + r * p.D + c, make_uint4(0u, 0u, 0u, 0u));
-    } else if (p.loss && threadIdx.x == 0) {
-      p.loss[r] = 0.0f;
-      p.lse_out[r] = 0.0f;
     }
-    if (gather && r >= total && r < zero_to)  // slots past the scored rows
-      for (int c = threadIdx.x * 8; c < p.D; c += kPrepThreads * 8)
-        st_u4(p.xc + r * p.D + c, make_uint4(0u, 0u, 0u, 0u));
+    for (int i = warp; i < n; i += kPrepThreads / 32) {
+      const int64_t r = b0 + i;
+      if ((mask >> i) & 1u) {
+        if (gather) copy_row(p.xc + (slot + __popc(mask & ((1u << i) - 1u))) *
+                                        static_cast<int64_t>(p.D), p.x + r * p.D, p.D);
+      } else if (p.dx) {
+        copy_row(p.dx + r * p.D, nullptr, p.D);
+      }
+      if (gather && r >= total && r < zero_to)  // slots past the scored rows
+        copy_row(p.xc + r * p.D, nullptr, p.D);
+    }
+    slot += __popc(mask);
   }
 }
 
@@ -780,9 +803,16 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (n0 + i * kStep < p.parts) v[i] = src[static_cast<int64_t>(n0 + i * kStep) * p.M];
+      float m = a.x;
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
-        if (n0 + i * kStep < p.parts) a = join(a, v[i]);
+        if (n0 + i * kStep < p.parts) m = fmaxf(m, v[i].x);
+      const float ref = m == -INFINITY ? 0.0f : m;
+      float sum = a.y * pow2(a.x - ref);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (n0 + i * kStep < p.parts) sum = fmaf(v[i].y, pow2(v[i].x - ref), sum);
+      a = make_float2(m, sum);
     }
   }
 #pragma unroll
@@ -795,10 +825,21 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   if (lane < kJoinRows) part[warp][lane] = a;
   __syncthreads();
   if (warp == 0) {
+    // four lanes per row: each joins the parts of four warps, then they join
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; w += 32 / kJoinRows) {
+      const float2 b = part[w + lane / kJoinRows][lane & (kJoinRows - 1)];
+      a = w == 0 ? b : join(a, b);
+    }
+#pragma unroll
+    for (int o = kJoinRows; o < 32; o <<= 1) {
+      float2 b;
+      b.x = __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+      b.y = __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+      a = join(a, b);
+    }
     double loss = 0.0;
     if (lane < kJoinRows && row < count) {
-#pragma unroll
-      for (int w = 1; w < kJoinWarps; ++w) a = join(a, part[w][lane]);
       // the differences in 64 bits: a confident row's loss is a small one
       double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
       int r = row;
