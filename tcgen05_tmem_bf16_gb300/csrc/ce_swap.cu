@@ -40,10 +40,14 @@ struct SwCfg {
   static constexpr int kXBytes = MPAD * kBK * 2;
   static constexpr int kStageBytes = kSwWBytes + kXBytes;
   static constexpr int kStages = MPAD == 16 ? 5 : MPAD == 64 ? 4 : 3;
-  static constexpr int kGroups = MPAD == 16 ? 4 : 2;  // accumulators of a tile
-  static constexpr int kBufs = MPAD == 128 ? 1 : 2;   // tiles in tensor memory
-  static constexpr int kTmemCols = MPAD * kGroups * kBufs;  // 128 or 256: two CTAs fit
-  static constexpr int kTileCols = MPAD * kGroups;
+  static constexpr int kAccs = MPAD == 16 ? 8 : MPAD == 64 ? 4 : 2;  // accumulators
+  static constexpr int kTmemCols = MPAD * kAccs;  // 128 or 256: two CTAs fit
+  // Accumulators of a tile: four, or two where that leaves another tile in
+  // tensor memory and K is not over 4096 (64 rows x 128000 x 2048: 99 us, with
+  // four 102; lse off by 6e-7 of itself at K = 4096, at 8192 it would be 1.3e-6).
+  static __host__ __device__ constexpr int groups(int num_kb) {
+    return MPAD == 64 && num_kb <= 64 ? 2 : kAccs < 4 ? kAccs : 4;
+  }
   static constexpr int kBarBytes = 256;
   static constexpr int kRowBytes = 3 * MPAD * 4;            // lse2, dl, targets
   static constexpr int kTurnBytes = 4 * 32 * 17 * 4;        // transposition, per warp
@@ -69,8 +73,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * Cfg::kStageBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + Cfg::kBufs;
-  uint64_t* done = tempty + Cfg::kBufs;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   uint8_t* after = smem + kStages * Cfg::kStageBytes + Cfg::kBarBytes;
@@ -86,7 +90,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < Cfg::kBufs; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 4);
     }
@@ -122,6 +126,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   const long long t_start = clock64();
   const int tiles = (a.cols + 127) / 128;
   const int num_kb = a.num_kb;
+  const int per_tile = Cfg::groups(num_kb);
+  const int two_bufs = Cfg::kAccs / per_tile == 2 ? 1 : 0;  // tiles in tensor memory: 2 or 1
   const int step = static_cast<int>(gridDim.x);
 
   if (warp == 0) {
@@ -170,8 +176,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       bool ok = true;
       int l = 0;
       for (int t = blockIdx.x; t < tiles && ok; t += step, ++l) {
-        const int buf = l % Cfg::kBufs;
-        const int use = l / Cfg::kBufs;
+        const int buf = l & two_bufs;
+        const int use = l >> two_bufs;
         if (!wait_bar(&tempty[buf], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
         tc_fence_after();
         for (int i = 0; i < num_kb; ++i) {
@@ -182,11 +188,11 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           tc_fence_after();
           const uint32_t w0 = smem_u32(stages + s * Cfg::kStageBytes);
           const uint32_t x0 = w0 + kSwWBytes;
-          const uint32_t d = tmem_base + buf * Cfg::kTileCols + (i % Cfg::kGroups) * MPAD;
+          const uint32_t d = tmem_base + (buf * per_tile + (i & (per_tile - 1))) * MPAD;
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             mma_ss(d, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024),
-                   idesc, (i >= Cfg::kGroups || k != 0) ? 1u : 0u);
+                   idesc, (i >= per_tile || k != 0) ? 1u : 0u);
           mma_commit(&empty[s]);
           if (++s == kStages) {
             s = 0;
@@ -203,15 +209,15 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   } else {
     const int q = warp & 3;  // the quarter of tensor memory that this warp reads
     float* my_turn = turn + q * 32 * 17;
-    const int groups = min(Cfg::kGroups, num_kb);
+    const int groups = min(per_tile, num_kb);
     const int chunks = (count + 15) / 16;  // of 16 rows
     int l = 0;
     for (int t = blockIdx.x; t < tiles; t += step, ++l) {
-      const int buf = l % Cfg::kBufs;
-      if (!wait_bar(&tfull[buf], (l / Cfg::kBufs) & 1, ctl, kSiteEpiAccFull)) break;
+      const int buf = l & two_bufs;
+      if (!wait_bar(&tfull[buf], (l >> two_bufs) & 1, ctl, kSiteEpiAccFull)) break;
       tc_fence_after();
       const uint32_t tb =
-          tmem_base + buf * Cfg::kTileCols + (static_cast<uint32_t>(q * 32) << 16);
+          tmem_base + buf * per_tile * MPAD + (static_cast<uint32_t>(q * 32) << 16);
       const int col = t * 128 + q * 32 + lane;  // of the piece
 #pragma unroll 1
       for (int c = 0; c < MPAD / 16; ++c) {

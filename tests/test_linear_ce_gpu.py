@@ -316,3 +316,14 @@ def test_lone_row_tiles_of_short_products_again_and_again(cuda_lib, M, V, D):
     assert cuda_lib.gbf_check_device_error() == 0
     for o in outs:
         assert all(torch.equal(a, b) for a, b in zip(o, (loss, lse, mean, dx, dw)))
+
+
+@pytest.mark.parametrize("M", [3, 40, 100, 200, 300])
+def test_wide_hidden_states(cuda_lib, M):
+    """K over 4096: more sums per tile."""
+    x, w, t = inputs(M, 700, 4104, 0.2, seed=M)
+    ref = Reference(x, w, t, 1.0)
+    loss, lse, mean = forward(cuda_lib, x, w, t)
+    ref.check_forward(loss, lse, mean)
+    dx, dw = backward(cuda_lib, x, w, t, lse)
+    ref.check_backward(dx, dw)
