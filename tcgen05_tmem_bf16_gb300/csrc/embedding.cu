@@ -2,7 +2,7 @@
 //
 // Lookup: out[m] = bf16(scale * table[id_m]), zeros for an id outside [0, V).
 // HBM-bound: a warp moves 1024 columns of one row, four 16-byte vectors per
-// lane in flight.
+// lane in flight (16383 rows of 8192: 59 us, 334 MB of 510 from and to HBM).
 //
 // Gradient: dtable[v] (+)= scale * sum over {m : id_m = v} of dout[m], in
 // fp32, in the order of m.  Summing with atomics would add in an order that
@@ -18,6 +18,9 @@
 //   3. embed_join_kernel: the runs over several pieces, their parts added in
 //      order, written once.
 // Up to 1024 positions one kernel does without sorting (embed_direct_kernel).
+// HBM-bound but for the sort: 16384 x 4096 into a tied table of 128000 rows takes
+// 64.5 us, 15 of them the sort (twelve short phases that wait on one another),
+// 42 the sums (5 to 6.4 TB/s), 8 the join.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -319,6 +322,9 @@ __device__ __forceinline__ void zero_rows(const SumArgs& a, int64_t me, int64_t 
 // Up to 1024 positions nothing is sorted: the CTA of position m (x 1024
 // columns) looks through all ids, leaves if one before m is the same, and else
 // sums the rows of those that are, in order.  One launch, no parts to join.
+// (1021 ids x 1024 into 32000 rows: 16.4 us, 21.3 sorted; 1024 x 4096 into a tied
+// table 9.4, 11.7 sorted; 4096 x 4096 69.7, 24.2 sorted; 1024 ids all the same
+// 55, 1025 sorted 18.)
 constexpr int kDirectMax = 1024;
 
 template <typename Id>
@@ -470,11 +476,107 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
   }
 }
 
+// Adds up to sum the parts [q0, q1) of a run, in order, eight in flight.
+__device__ __forceinline__ void add_parts(const SumArgs& a, const float* base, int q0, int q1,
+                                          int col, float (&sum)[8]) {
+  constexpr int kAhead = 8;
+  for (; q0 < q1; q0 += kAhead) {
+    float4 g[kAhead][2];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (q0 + u < q1) {
+        const float4* t = reinterpret_cast<const float4*>(base + static_cast<int64_t>(q0 + u) * a.D + col);
+        g[u][0] = t[0];
+        g[u][1] = t[1];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (q0 + u >= q1) break;
+      sum[0] += g[u][0].x; sum[1] += g[u][0].y; sum[2] += g[u][0].z; sum[3] += g[u][0].w;
+      sum[4] += g[u][1].x; sum[5] += g[u][1].y; sum[6] += g[u][1].z; sum[7] += g[u][1].w;
+    }
+  }
+}
+
+// How many pieces from `piece` on begin with `key`: as many as the CTA has
+// threads looked at together.
+__device__ __forceinline__ int pieces_begun(const SumArgs& a, int64_t piece, int key) {
+  int n = 0;
+  for (;;) {
+    const int64_t at = (piece + n + threadIdx.x) * a.piece;
+    const int here = __syncthreads_count(at < a.M && a.key[at] == key);
+    n += here;
+    if (here < static_cast<int>(blockDim.x)) return n;
+  }
+}
+
+// Runs with parts in more than this many pieces after their first are long.
+constexpr int kLongRun = 64;
+constexpr int kLongCols = 256;  // columns of a CTA that joins a long run
+constexpr int kRanges = kSumThreads / 32;
+
+// A long run (an id that fills much of a long list, such as a padding token that
+// is not -1): the run that goes on into piece 64 k, if it did not into the one 64
+// before.  256 columns per CTA: the parts are cut into four ranges, one for each
+// warp, whose sums are added in order.  (16384 ids, half of them the same, D =
+// 1024: 122 us with the runs' own CTAs alone, 48 so.)
+__device__ __forceinline__ void join_long(const SumArgs& a, int k, int block) {
+  __shared__ float range_sum[kRanges - 1][8][32];
+  const int b = k * kLongRun;  // a piece that begins inside the run
+  const int64_t at = static_cast<int64_t>(b) * a.piece;
+  if (at >= a.M) return;
+  const int key = a.key[at];
+  if (key >= a.V || a.key[at - 1] != key) return;
+  const int64_t earlier = static_cast<int64_t>(b - kLongRun) * a.piece;
+  if (earlier > 0 && a.key[earlier] == key && a.key[earlier - 1] == key) return;  // of k - 1
+  // the run began in the piece before the earliest whose beginning is inside it
+  const int64_t before = static_cast<int64_t>(b - static_cast<int>(threadIdx.x)) * a.piece;
+  const int inside = __syncthreads_count(static_cast<int>(threadIdx.x) < kLongRun && before > 0 &&
+                                         a.key[before > 0 ? before - 1 : 0] == key);
+  const int p = b - inside;
+  const int more = b - 1 - p + pieces_begun(a, b, key);
+  if (more <= kLongRun) return;
+  const int range = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int col = block * kLongCols + lane * 8;
+  const bool in = col < a.D;
+  float sum[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  if (in) {
+    if (range == 0) add_parts(a, a.tail, p, p + 1, col, sum);
+    const int each = (more + kRanges - 1) / kRanges;
+    add_parts(a, a.head, p + 1 + range * each, p + 1 + min(more, (range + 1) * each), col, sum);
+    if (range > 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) range_sum[range - 1][j][lane] = sum[j];
+  }
+  __syncthreads();
+  if (!in || range > 0) return;
+#pragma unroll
+  for (int r = 0; r < kRanges - 1; ++r)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum[j] += range_sum[r][j][lane];
+  write_row(a, key, col, sum,
+            a.accumulate ? ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col)
+                         : make_uint4(0u, 0u, 0u, 0u));
+}
+
 // One CTA per piece x segment: where the piece's last run began in it and goes
-// on, adds the run's parts in order and writes the row.
+// on, adds the run's parts in order and writes the row.  Long runs are left to
+// the CTAs after those.
 __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a) {
   griddep_launch_dependents();
   griddep_wait();
+  const int64_t runs = static_cast<int64_t>(a.pieces) * a.segs;
+  if (static_cast<int64_t>(blockIdx.x) >= runs) {
+    const int64_t t = blockIdx.x - runs;
+    const int blocks = (a.D + kLongCols - 1) / kLongCols;
+    const int k = static_cast<int>(t / blocks);
+    join_long(a, k + 1, static_cast<int>(t - static_cast<int64_t>(k) * blocks));
+    return;
+  }
   const int p = static_cast<int>(blockIdx.x / a.segs);
   const int seg = static_cast<int>(blockIdx.x - static_cast<int64_t>(p) * a.segs);
   const int64_t next = static_cast<int64_t>(p + 1) * a.piece;  // first position after the piece
@@ -483,41 +585,16 @@ __global__ void __launch_bounds__(kSumThreads) embed_join_kernel(const SumArgs a
   if (key >= a.V || a.key[next] != key) return;                     // the last run ends here
   const int64_t first = static_cast<int64_t>(p) * a.piece;
   if (a.key[first] == key && first > 0 && a.key[first - 1] == key) return;  // began earlier
-  // how many of the next pieces begin with the run: 128 looked at together
-  int more = 0;
-  for (;;) {
-    const int64_t at = next + (more + static_cast<int64_t>(threadIdx.x)) * a.piece;
-    const int here = __syncthreads_count(at < a.M && a.key[at] == key);
-    more += here;
-    if (here < kSumThreads) break;
-  }
+  const int more = pieces_begun(a, p + 1, key);
   const int col = seg * kSegCols + threadIdx.x * 8;
-  if (col >= a.D) return;
+  if (more > kLongRun || col >= a.D) return;
   const uint4 old = a.accumulate ? ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col)
                                  : make_uint4(0u, 0u, 0u, 0u);
   float sum[8];
-  auto part = [&](const float* base, int q, float4 (&f)[2]) {
-    const float4* t = reinterpret_cast<const float4*>(base + static_cast<int64_t>(q) * a.D + col);
-    f[0] = t[0];
-    f[1] = t[1];
-  };
-  float4 f[2];
-  part(a.tail, p, f);
-  sum[0] = f[0].x; sum[1] = f[0].y; sum[2] = f[0].z; sum[3] = f[0].w;
-  sum[4] = f[1].x; sum[5] = f[1].y; sum[6] = f[1].z; sum[7] = f[1].w;
-  constexpr int kAhead = 8;
-  for (int q0 = p + 1; q0 <= p + more; q0 += kAhead) {
-    float4 g[kAhead][2];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (q0 + u <= p + more) part(a.head, q0 + u, g[u]);
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      if (q0 + u > p + more) break;
-      sum[0] += g[u][0].x; sum[1] += g[u][0].y; sum[2] += g[u][0].z; sum[3] += g[u][0].w;
-      sum[4] += g[u][1].x; sum[5] += g[u][1].y; sum[6] += g[u][1].z; sum[7] += g[u][1].w;
-    }
-  }
+  for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+  add_parts(a, a.tail, p, p + 1, col, sum);
+  add_parts(a, a.head, p + 1, p + 1 + more, col, sum);
   write_row(a, key, col, sum, old);
 }
 
@@ -602,7 +679,8 @@ cudaError_t launch_embedding_lookup(const void* ids, bool ids64, const __nv_bflo
                                     table, out, M, V, D, segs, scale);
 }
 
-// Positions per piece: 32, fewer while that leaves under eight CTAs per SM.
+// Positions per piece: 32 (16384 x 4096: 66 us in all, 74 with 16), fewer while
+// that leaves under eight CTAs per SM.
 int embed_piece(int64_t M, int D) {
   const int segs = (D + kSegCols - 1) / kSegCols;
   int piece = kMaxPiece;
@@ -649,7 +727,10 @@ cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat
   cudaLaunchConfig_t cfg = overlapped(sums + zeros, kSumThreads, 0, stream, attr);
   if ((e = cudaLaunchKernelEx(&cfg, embed_sum_kernel, a)) != cudaSuccess) return e;
   cudaLaunchAttribute attr2[1];
-  cudaLaunchConfig_t cfg2 = overlapped(sums, kSumThreads, 0, stream, attr2);
+  // and one for each place where a long run is looked for, x 256 columns
+  const int64_t longs = static_cast<int64_t>((a.pieces - 1) / kLongRun) *
+                        ((D + kLongCols - 1) / kLongCols);
+  cudaLaunchConfig_t cfg2 = overlapped(sums + longs, kSumThreads, 0, stream, attr2);
   return cudaLaunchKernelEx(&cfg2, embed_join_kernel, a);
 }
 

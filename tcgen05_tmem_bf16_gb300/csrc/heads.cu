@@ -79,7 +79,7 @@ int ce_streams(int64_t M) { return M > kCeTileRows ? 2 : 1; }
 
 // Parts of K of the product for dx, each with an fp32 buffer of its own, 16 at
 // most and none shorter than 8 K blocks.  With one row tile: as many as give one
-// round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 108
+// round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 103
 // us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
 // beside dw).  Else: none longer than half of what a pair has to do in all.
 int ce_splits(int64_t M, int64_t D, int64_t cols) {

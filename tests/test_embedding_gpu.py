@@ -167,3 +167,28 @@ def test_on_another_stream_and_in_a_graph(cuda_lib):
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_gradient_where_the_way_of_sorting_changes(cuda_lib, M, accumulate):
     test_gradient(cuda_lib, M, 1500, 64, "mixed", accumulate)
+
+
+@pytest.mark.parametrize("D", [264, 1288])
+@pytest.mark.parametrize("share", [0.3, 0.7, 0.95])
+def test_gradient_of_runs_over_many_pieces(cuda_lib, D, share):
+    """A few ids that fill most of a long list, at its beginning, middle and end."""
+    M, V = 20011, 900
+    g = torch.Generator(device="cuda").manual_seed(D)
+    ids = torch.randint(0, V, (M,), generator=g, device="cuda")
+    often = torch.tensor([0, 400, 401, V - 1], device="cuda")
+    pick = torch.rand(M, generator=g, device="cuda") < share
+    ids = torch.where(pick, often[torch.randint(0, 4, (M,), generator=g, device="cuda")], ids)
+    dout = torch.randn(M, D, generator=g, device="cuda").bfloat16()
+    n = cuda_lib.gbf_workspace_size("embedding_grad", M, V, D, True)
+    for accumulate in (False, True):
+        before = torch.randn(V, D, generator=g, device="cuda").bfloat16() if accumulate else None
+        want, tol = grad_reference(ids, dout, V, 1.5, before)
+        got = []
+        for _ in range(2):
+            ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+            dtable = before.clone() if accumulate else torch.full((V, D), float("nan"), device="cuda", dtype=torch.bfloat16)
+            cuda_lib.embedding_grad(ids, dout, dtable, M, V, D, 1.5, accumulate, workspace=ws, workspace_bytes=n)
+            assert ((dtable.double() - want).abs() <= tol).all()
+            got.append(dtable)
+        assert torch.equal(got[0], got[1])
