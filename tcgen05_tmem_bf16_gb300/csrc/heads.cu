@@ -95,10 +95,21 @@ int ce_splits(int64_t M, int64_t D, int64_t cols) {
   return static_cast<int>(std::min(most, ceil_div64(k, half)));
 }
 
-// Partial sums per row of the forward pass: one per 128 columns of a tile, per
-// 32 with swapped roles.
+// Columns of a tile of the forward pass: 224 where the rounds of such tiles over
+// the pairs are shorter than those of 256 (1024 rows x 32000 x 4096, four rounds
+// either way: 157 us, 175 with 256; 700 x 50001 x 2048: 128, 140).
+int ce_tile_cols(int64_t M, int64_t V) {
+  if (ce_streams(M) == 1) return 256;
+  const int64_t m = ceil_div64(M, 2 * kCeTileRows);
+  const int64_t wide = ceil_div64(m * ceil_div64(V, 256), kCePairs) * 256;
+  const int64_t narrow = ceil_div64(m * ceil_div64(V, 224), kCePairs) * 224;
+  return narrow * 102 < wide * 100 ? 224 : 256;
+}
+
+// Partial sums per row of the forward pass: two per tile, with swapped roles one
+// per 32 columns.
 int64_t ce_parts(int64_t M, int64_t V) {
-  return M <= kCeSwapMax ? 4 * ceil_div64(V, 128) : 2 * ceil_div64(V, kCeTileRows);
+  return M <= kCeSwapMax ? 4 * ceil_div64(V, 128) : 2 * ceil_div64(V, ce_tile_cols(M, V));
 }
 
 struct CeWs {
@@ -152,9 +163,10 @@ gbf_status_t check_ce(const void* x, const void* w, const void* targets, int ind
   return GBF_OK;
 }
 
-// K-major operand: rows of D values, 64 x 128 boxes.
-bool ce_map_k(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld) {
-  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, kBK, 128,
+// K-major operand: rows of D values, 64 x 128 boxes (half a tile's columns of W).
+bool ce_map_k(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t ld,
+              uint32_t rows = 128) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, ld * 2, kBK, rows,
                      CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // Operand with one row per k: 64 x 64 boxes.
@@ -196,7 +208,7 @@ gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M,
     if (j.mode == kCeNone) continue;
     const int64_t rows = j.mode == kCeDw ? j.cols : M;
     const int64_t n = j.mode == kCeLse || j.mode == kCeGrad ? j.cols : launch.d;
-    units += ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, kCeTileRows) * j.splits;
+    units += ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, j.bn) * j.splits;
   }
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, dev.pairs));
   return cuda_status(launch_ce_gemm(launch, end, streams, grid, lib_ctl(err, grid), s));
@@ -335,6 +347,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   p.D = static_cast<int>(D);
   const bool few = M <= kCeSwapMax;
   CeLaunch launch{};
+  for (CeJob& j : launch.job) j.bn = 256;
   CeSwap swap{};
   if (few) {
     if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
@@ -346,8 +359,9 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   } else {
     launch.d = p.D;
     CeJob& job = launch.job[1];
+    job.bn = ce_tile_cols(M, V);
     if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
-        !ce_map_k(&job.b[0], w, D, V, D))
+        !ce_map_k(&job.b[0], w, D, V, D, job.bn / 2))
       return GBF_ERR_CUDA;
     job.mode = kCeLse;
     job.cols = p.V;
@@ -443,6 +457,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   for (int64_t n = 0; n <= pieces; ++n) {
     CeLaunch launch{};
     launch.d = p.D;
+    for (CeJob& j : launch.job) j.bn = 256;
     if (n < pieces && few) {
       const int64_t v0 = n * piece;
       CeSwap swap{};

@@ -160,6 +160,7 @@ struct CeJob {
   // scored; [0] the gathered rows (or the operand's only map)
   CUtensorMap a[2], b[2], o;
   int mode;
+  int bn;      // columns of a tile: 256, or for kLse 224
   int cols;    // columns of the vocabulary: all (kCeLse) or the piece's
   int v0;      // first column of the piece
   int splits;  // parts of K (kCeDx), each with its own fp32 buffer

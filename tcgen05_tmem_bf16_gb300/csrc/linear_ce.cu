@@ -106,7 +106,7 @@ __device__ __forceinline__ CeWork ce_work(const CeLaunch& a, int count, int stre
     const int n = (j.mode == kCeLse || j.mode == kCeGrad) ? j.cols : a.d;
     const int k = j.mode == kCeDw ? count : (j.mode == kCeDx ? j.cols : a.d);
     w.m_units[i] = (rows + kCeTile * streams - 1) / (kCeTile * streams);
-    w.n_tiles[i] = (n + kCeTile - 1) / kCeTile;
+    w.n_tiles[i] = (n + j.bn - 1) / j.bn;
     w.num_kb[i] = (k + kBK - 1) / kBK;
     w.units[i] = w.m_units[i] * w.n_tiles[i] * j.splits;
     if (i > 0) blocks += static_cast<int64_t>(w.units[i]) * (w.num_kb[i] + kCeUnitCost);
@@ -392,7 +392,6 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeLaunch a, const CeEnd e, const KernelCtl kctl) {
   using Cfg = CeCfg<STREAMS>;
   constexpr int kStages = Cfg::kStages;
-  constexpr int kLoadBytes = STREAMS * kCeABytes + kCeBBytes;  // into one CTA's stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* stages = smem;
@@ -466,7 +465,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;  // B holds one row per k
         const CUtensorMap* ma = &j.a[(j.mode == kCeLse || j.mode == kCeGrad) ? all : 0];
         const CUtensorMap* mb = &j.b[j.mode == kCeDw ? all : 0];
-        const int n0 = u.nb * kCeTile + static_cast<int>(rank) * 128;
+        const int n0 = u.nb * j.bn + static_cast<int>(rank) * (j.bn / 2);
+        // into one CTA's stage; a box of W's rows holds bn / 2 of them
+        const int load_bytes = STREAMS * kCeABytes + (b_mn ? kCeBBytes : (j.bn / 2) * kBK * 2);
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
           if (!wait_bar(&empty[s], ph ^ 1, ctl, kSiteProducerEmpty)) {
             ok = false;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           uint8_t* sa = stages + s * Cfg::kStageBytes;
           uint8_t* sb = sa + STREAMS * kCeABytes;
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
-          if (leader) mbar_arrive_expect_tx(&full[s], 2 * kLoadBytes);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * load_bytes);
 #pragma unroll
           for (int i = 0; i < STREAMS; ++i) {
             const int m0 = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM;
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const CeJob& j = a.job[u.job];
         const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
-        const uint32_t idesc = idesc_bf16(kCeTile, kCeTile, a_mn, b_mn);
+        const uint32_t idesc = idesc_bf16(kCeTile, j.bn, a_mn, b_mn);
         const bool two = STREAMS == 1 && ce_two_k(j, u);
         const int kb_half = two ? (u.kb0 + u.kb1) / 2 : u.kb1;
         int acc = two ? 0 : turn;
@@ -604,9 +605,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       t.out = &j.o;
       t.staging = my_staging;
       t.pol = pol;
-      t.col0 = u.nb * kCeTile + half * 128;
+      t.col0 = u.nb * j.bn + half * 128;
       t.none = u.kb0 == u.kb1;  // also a split without a K block of a short piece
-      t.cols = j.cols;
+      // the forward pass takes the tile's columns only: a narrow one ends inside
+      // the accumulator
+      t.cols = mode == kCeLse ? min(j.cols, (u.nb + 1) * j.bn) : j.cols;
       t.v0 = j.v0;
       t.d = a.d;
       t.count = count;
