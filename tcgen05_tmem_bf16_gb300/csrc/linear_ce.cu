@@ -802,10 +802,19 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   const int count = p.rows ? *p.count : p.M;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x * kJoinRows + (lane & (kJoinRows - 1));
+  // what the row's result takes beside the sums, on its way meanwhile
+  float target = 0.0f;  // the target's product
+  int r = row;
+  bool counts = true;
+  if (warp == 0 && lane < kJoinRows && row < count) {
+    target = p.tlog[row];
+    if (p.rows) r = p.rows[row];
+    else counts = scored(p, row);
+  }
   float2 a = make_float2(-INFINITY, 0.0f);
   if (row < count) {
     const float2* src = p.part + row;
-    constexpr int kAhead = 8, kStep = kJoinThreads / kJoinRows;
+    constexpr int kAhead = 16, kStep = kJoinThreads / kJoinRows;
     for (int n0 = threadIdx.x / kJoinRows; n0 < p.parts; n0 += kAhead * kStep) {
       float2 v[kAhead];
 #pragma unroll
@@ -849,33 +858,29 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     double loss = 0.0;
     if (lane < kJoinRows && row < count) {
       // the differences in 64 bits: a confident row's loss is a small one
-      double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
-      int r = row;
-      if (p.rows) {
-        r = p.rows[row];
-        loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
-      } else if (scored(p, row)) {
-        loss = lse - static_cast<double>(p.alpha) * static_cast<double>(p.tlog[row]);
-      } else {
-        lse = 0.0;
-      }
+      const double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
+      if (counts) loss = lse - static_cast<double>(p.alpha) * static_cast<double>(target);
       p.loss[r] = static_cast<float>(loss);
-      p.lse[r] = static_cast<float>(lse);
+      p.lse[r] = counts ? static_cast<float>(lse) : 0.0f;
     }
     if (p.mean) {
 #pragma unroll
       for (int o = kJoinRows / 2; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
       if (lane == 0) {
         p.sums[blockIdx.x] = loss;
-        __threadfence();
-        last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        if (gridDim.x > 1) {
+          __threadfence();
+          last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
+        } else {
+          last = true;
+        }
       }
     }
   }
   if (!p.mean) return;
   __syncthreads();
   if (!last) return;
-  __threadfence();
+  if (gridDim.x > 1) __threadfence();
   double s = 0.0;
   for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) s += __ldcg(p.sums + i);
 #pragma unroll
