@@ -351,10 +351,10 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
  *   loss, lse [M] fp32, 4-byte aligned; mean (may be NULL) one fp32, 0 where
  *   no row is scored.
  *   D % 8 == 0, D >= 8, V >= 1; M <= 2^24, V <= 2^26, D <= 2^20; alpha finite.
- *   Products accumulated in fp32 on the tensor cores (whose additions cut: lse
- *   is low by about 1.3e-6 of itself at D = 4096 above 256 rows, by half of that
- *   or less below), sums of exponentials in fp32 relative to their maximum.
- *   Workspace:
+ *   Products accumulated in fp32 on the tensor cores, whose additions cut; the
+ *   mean of the cut, D * 2^-30 of a logit, is put back (lse is off by about 1e-7
+ *   of itself at D = 4096; by 1e-5 where all products of a logit have one sign).
+ *   Sums of exponentials in fp32 relative to their maximum.  Workspace:
  *   gbf_workspace_size(GBF_OP_LINEAR_CE, M, V, D, 1) bytes.
  * gbf_linear_ce_grad -- its gradients, from the lse that gbf_linear_ce wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - [v == targets[m]])

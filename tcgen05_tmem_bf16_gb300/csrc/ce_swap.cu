@@ -9,8 +9,8 @@
 // another place, so that the CTAs do not all ask for the same lines of x.
 //
 // A tile's K blocks are dealt to several accumulators, which the ending adds in
-// fp32: shorter chains of additions on the tensor cores, whose rounding cuts
-// (four chains at N = 16 where one of 4096 products was 1.5e-6 low in lse).
+// fp32: shorter chains of additions on the tensor cores, which cut (four chains
+// at N = 16: a quarter of the cut and of its scatter).
 //
 // Endings, a thread per column of the vocabulary:
 //   LSE   the tile is transposed 16 rows at a time through shared memory; per
@@ -44,7 +44,7 @@ struct SwCfg {
   static constexpr int kTmemCols = MPAD * kAccs;  // 128 or 256: two CTAs fit
   // Accumulators of a tile: four, or two where that leaves another tile in
   // tensor memory and K is not over 4096 (64 rows x 128000 x 2048: 99 us, with
-  // four 102; lse off by 6e-7 of itself at K = 4096, at 8192 it would be 1.3e-6).
+  // four 102).
   static __host__ __device__ constexpr int groups(int num_kb) {
     return MPAD == 64 && num_kb <= 64 ? 2 : kAccs < 4 ? kAccs : 4;
   }
@@ -336,6 +336,13 @@ cudaError_t run_swap(const CeSwap& a, const CeEnd& end, const KernelCtl& ctl, in
 }  // namespace
 
 int ce_swap_rows(int64_t M) { return M <= 16 ? 16 : M <= 64 ? 64 : M <= kCeSwapMax ? 128 : 0; }
+
+int ce_swap_chains(int64_t M, int k_blocks) {
+  const int n = M <= 16   ? SwCfg<16>::groups(k_blocks)
+                : M <= 64 ? SwCfg<64>::groups(k_blocks)
+                          : SwCfg<128>::groups(k_blocks);
+  return std::min(n, std::max(1, k_blocks));
+}
 
 cudaError_t launch_ce_swap(const CeSwap& a, bool grad, const CeEnd& end, int sms,
                            const KernelCtl& ctl, cudaStream_t stream) {

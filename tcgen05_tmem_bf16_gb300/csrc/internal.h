@@ -196,6 +196,8 @@ __device__ __forceinline__ int64_t ce_target(const void* targets, int ids64, int
 #endif
 // The logits for up to kCeSwapMax rows, with swapped roles (ce_swap.cu).
 constexpr int kCeSwapMax = 128;
+int ce_swap_chains(int64_t M, int k_blocks);  // sums that a logit's K is dealt to
+int ce_lone_chains(int k_blocks, bool forward);  // the same in linear_ce.cu, one row tile per unit
 int ce_swap_rows(int64_t M);  // rows padded to: 16, 64, 128; 0 above kCeSwapMax
 struct CeSwap {
   CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored (and forward)
@@ -230,7 +232,7 @@ struct CeJoin {
   unsigned* ticket;
   double* sums;  // per 8 rows
   float *loss, *lse, *mean;
-  float alpha;
+  double alpha;
   int M, parts;
 };
 struct CeDxOut {

@@ -25,8 +25,8 @@
 //
 // G is rounded to bf16 without the mean's factor: the factor multiplies the
 // fp32 sums, so it adds no rounding of its own.  The sums of the products are the
-// tensor cores' fp32, whose additions cut: lse comes out low by 1.3e-6 of itself
-// at a width of 4096 where one accumulator takes all of K.
+// tensor cores' fp32, whose additions cut; the mean of what they cut is put back
+// through alpha (ce_uncut in heads.cu).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -165,7 +165,7 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
 
 // One row tile per unit: whether the halves of K go to the two accumulators.
 // The tensor cores cut the sum at every step, so a logit of 4096 products is low
-// by some 4e-6 of itself and lse by 1.5e-6; two chains of half the length halve that.
+// by some 4e-6 of itself; two chains of half the length halve that and its scatter.
 __device__ __forceinline__ bool ce_two_k(const CeJob& j, const CeUnit& u) {
   return j.mode == kCeLse && u.kb1 - u.kb0 >= kCeTwoK;
 }
@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     if (lane < kJoinRows && row < count) {
       // the differences in 64 bits: a confident row's loss is a small one
       const double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
-      if (counts) loss = lse - static_cast<double>(p.alpha) * static_cast<double>(target);
+      if (counts) loss = lse - p.alpha * static_cast<double>(target);
       p.loss[r] = static_cast<float>(loss);
       p.lse[r] = counts ? static_cast<float>(lse) : 0.0f;
     }
@@ -966,6 +966,8 @@ cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ct
 }
 
 }  // namespace
+
+int ce_lone_chains(int k_blocks, bool forward) { return forward && k_blocks >= kCeTwoK ? 2 : 1; }
 
 cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, int grid,
                            const KernelCtl& ctl, cudaStream_t stream) {
