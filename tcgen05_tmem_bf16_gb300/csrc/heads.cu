@@ -154,7 +154,9 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
 // sum of like steps is on average half of its end on the way, so the end is low by
 // K 2^-30 of itself.  That mean is put back; what is left are the cuts' deviations
 // from it (lse off by 1.3e-6 of itself at K = 4096 without the factor).  Chains
-// of sums of one sign lose two to four times as much and get back this part.
+// of sums of one sign lose two to four times as much and get back this part; a
+// sum whose products are nearly all zero (a sparse x) is not cut and comes out high
+// by K 2^-30 of itself, the size of the error that all others would have without.
 double ce_uncut(int64_t M, int64_t D, bool forward) {
   const int64_t k_blocks = ceil_div64(D, 64);
   const int64_t chains = M <= kCeSwapMax      ? ce_swap_chains(M, static_cast<int>(k_blocks))
