@@ -166,18 +166,21 @@ double ce_uncut(int64_t M, int64_t D, bool forward) {
 }
 
 // Sizes that the kernels' 32-bit coordinates and unit counts hold.
+bool ce_sizes_held(int64_t M, int64_t V, int64_t D) {
+  if (V < 1 || D < 8 || D % 8 != 0 || M > (int64_t(1) << 24) || V > (int64_t(1) << 26) ||
+      D > (int64_t(1) << 20))
+    return false;
+  const int64_t m = ceil_div64(M, 256), v = ceil_div64(V, 256), d = ceil_div64(D, 256);
+  return m * v <= kMaxInt / 2 && m * d * 16 <= kMaxInt / 2 && v * d <= kMaxInt / 2;
+}
+
 gbf_status_t check_ce(const void* x, const void* w, const void* targets, int index_type,
                       int64_t M, int64_t V, int64_t D, float alpha) {
   gbf_status_t st = check_ids(targets, index_type, M, V, D);
   if (st != GBF_OK) return st;
   if (!x || !w || !std::isfinite(alpha)) return GBF_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16)) return GBF_ERR_MISALIGNED;
-  if (V < 1 || D < 8 || M > (int64_t(1) << 24) || V > (int64_t(1) << 26) || D > (int64_t(1) << 20))
-    return GBF_ERR_UNSUPPORTED_SHAPE;
-  const int64_t m = ceil_div64(M, 256), v = ceil_div64(V, 256), d = ceil_div64(D, 256);
-  if (m * v > kMaxInt / 2 || m * d * 16 > kMaxInt / 2 || v * d > kMaxInt / 2)
-    return GBF_ERR_UNSUPPORTED_SHAPE;
-  return GBF_OK;
+  return ce_sizes_held(M, V, D) ? GBF_OK : GBF_ERR_UNSUPPORTED_SHAPE;
 }
 
 // K-major operand: rows of D values, 64 x 128 boxes (half a tile's columns of W).
@@ -246,7 +249,7 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
                       clip_ctas(kMaxSms) * 3 * sizeof(float2));
     case GBF_OP_LINEAR_CE:
     case GBF_OP_LINEAR_CE_GRAD: {
-      if (M > (int64_t(1) << 24) || N > (int64_t(1) << 26) || K > (int64_t(1) << 20)) return 0;
+      if (!ce_sizes_held(M, N, K)) return 0;  // as the entry points refuse them
       CeWs w;
       return ce_sections(nullptr, M, N, K, op == GBF_OP_LINEAR_CE_GRAD, &w);
     }
