@@ -313,6 +313,9 @@ GBF_API gbf_status_t gemm_epilogue_unfused_noalloc(const void *A, const void *B,
                                                    int act, gbf_stream_t stream);
 
 /*
+ * The operators at a model's two ends, from here to gbf_clip_grad_norm: an array
+ * without elements (M == 0, ...) may be a null pointer.
+ *
  * gbf_embedding_lookup -- out[m][D] = bf16( scale * table[ids[m]][D] ), one rounding.
  *   ids    [M] of index_type (aligned to its size, not to 16 bytes).  An id
  *          outside [0, V) reads nothing and its row of out is zero (use -1

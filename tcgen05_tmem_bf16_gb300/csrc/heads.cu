@@ -35,8 +35,9 @@ struct Sections {
   }
 };
 
+// The address of an array without elements may be null, as torch gives it.
 gbf_status_t check_ids(const void* ids, int index_type, int64_t M, int64_t V, int64_t D) {
-  if (!ids || M < 0 || V < 0 || D < 0) return GBF_ERR_INVALID_ARG;
+  if ((!ids && M != 0) || M < 0 || V < 0 || D < 0) return GBF_ERR_INVALID_ARG;
   if (index_type != GBF_INDEX_I64 && index_type != GBF_INDEX_I32) return GBF_ERR_INVALID_ARG;
   if (!aligned(ids, index_type == GBF_INDEX_I64 ? 8 : 4)) return GBF_ERR_MISALIGNED;
   if (D % 8 != 0 || M > kMaxInt || V > kMaxInt - 1 || D > kMaxInt) return GBF_ERR_UNSUPPORTED_SHAPE;
@@ -178,7 +179,7 @@ gbf_status_t check_ce(const void* x, const void* w, const void* targets, int ind
                       int64_t M, int64_t V, int64_t D, float alpha) {
   gbf_status_t st = check_ids(targets, index_type, M, V, D);
   if (st != GBF_OK) return st;
-  if (!x || !w || !std::isfinite(alpha)) return GBF_ERR_INVALID_ARG;
+  if ((!x && M > 0) || !w || !std::isfinite(alpha)) return GBF_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(w, 16)) return GBF_ERR_MISALIGNED;
   return ce_sizes_held(M, V, D) ? GBF_OK : GBF_ERR_UNSUPPORTED_SHAPE;
 }
@@ -267,7 +268,7 @@ gbf_status_t gbf_embedding_lookup(const void* ids, int index_type, const void* t
                               int64_t M, int64_t V, int64_t D, float scale, gbf_stream_t stream) {
   gbf_status_t st = check_ids(ids, index_type, M, V, D);
   if (st != GBF_OK) return st;
-  if (!table || !out) return GBF_ERR_INVALID_ARG;
+  if ((!table && V > 0 && D > 0) || (!out && M > 0 && D > 0)) return GBF_ERR_INVALID_ARG;
   if (!aligned(table, 16) || !aligned(out, 16)) return GBF_ERR_MISALIGNED;
   // one warp per 1024 columns of a row, four warps per CTA
   if (D > 0 && M > kMaxInt / ((D + 1023) / 1024)) return GBF_ERR_UNSUPPORTED_SHAPE;
@@ -286,7 +287,9 @@ gbf_status_t gbf_embedding_grad(const void* ids, int index_type, const void* dou
                             void* workspace, size_t workspace_bytes, gbf_stream_t stream) {
   gbf_status_t st = check_ids(ids, index_type, M, V, D);
   if (st != GBF_OK) return st;
-  if (!dout || !dtable || (accumulate != 0 && accumulate != 1)) return GBF_ERR_INVALID_ARG;
+  if ((!dout && M > 0 && D > 0) || (!dtable && V > 0 && D > 0) ||
+      (accumulate != 0 && accumulate != 1))
+    return GBF_ERR_INVALID_ARG;
   if (!aligned(dout, 16) || !aligned(dtable, 16) || !aligned(workspace, 16))
     return GBF_ERR_MISALIGNED;
   const int64_t segs = (D + 1023) / 1024;
@@ -342,7 +345,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
                            gbf_stream_t stream) {
   gbf_status_t st = check_ce(x, w, targets, index_type, M, V, D, alpha);
   if (st != GBF_OK) return st;
-  if (!loss || !lse) return GBF_ERR_INVALID_ARG;
+  if (M > 0 && (!loss || !lse)) return GBF_ERR_INVALID_ARG;
   if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(mean, 4) || !aligned(workspace, 16))
     return GBF_ERR_MISALIGNED;
   CeWs ws;
@@ -427,7 +430,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
                                 gbf_stream_t stream) {
   gbf_status_t st = check_ce(x, w, targets, index_type, M, V, D, alpha);
   if (st != GBF_OK) return st;
-  if (!lse || (!dx && !dw) || (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
+  if ((M > 0 && (!lse || (!dx && !dw))) || (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
     return GBF_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16) ||
       !aligned(workspace, 16))
