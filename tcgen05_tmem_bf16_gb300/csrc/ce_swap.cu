@@ -268,14 +268,14 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           float x[16], top = -INFINITY;
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            x[k] = my_turn[(first + k) * 17 + (lane & 15)] * e.c2;
-            if (base + first + k >= a.cols) x[k] = -INFINITY;
-            top = fmaxf(top, x[k]);
+            x[k] = my_turn[(first + k) * 17 + (lane & 15)];
+            if (base + first + k < a.cols) top = fmaxf(top, x[k] * e.c2);
           }
           const float ref = top == -INFINITY ? 0.0f : top;
           float sum = 0.0f;
 #pragma unroll
-          for (int k = 0; k < 16; ++k) sum += sw_pow2(x[k] - ref);
+          for (int k = 0; k < 16; ++k)  // one rounding less than x c2 - ref
+            if (base + first + k < a.cols) sum += sw_pow2(fmaf(x[k], e.c2, -ref));
           const float top2 = __shfl_xor_sync(0xFFFFFFFFu, top, 16);
           const float sum2 = __shfl_xor_sync(0xFFFFFFFFu, sum, 16);
           const float m2 = fmaxf(top, top2);

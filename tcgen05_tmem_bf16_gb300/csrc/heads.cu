@@ -395,8 +395,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   end.tgt = ws.tgt;
   end.part = ws.part;
   end.tlog = ws.tlog;
-  const double uncut = ce_uncut(M, D, true);
-  end.c2 = static_cast<float>(alpha * uncut * 1.4426950408889634);
+  end.c2 = static_cast<float>(alpha * ce_uncut(M, D, true) * 1.4426950408889634);
   end.M = p.M;
   CeJoin join{};
   join.count = ws.count;
@@ -411,7 +410,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   join.loss = loss;
   join.lse = lse;
   join.mean = mean;
-  join.alpha = alpha * uncut;
+  join.c2 = end.c2;
   join.M = p.M;
   join.parts = static_cast<int>(ce_parts(M, V));
   if (!few && (st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms,

@@ -232,7 +232,7 @@ struct CeJoin {
   unsigned* ticket;
   double* sums;  // per 8 rows
   float *loss, *lse, *mean;
-  double alpha;
+  float c2;      // as in CeEnd: what the maxima were made with
   int M, parts;
 };
 struct CeDxOut {

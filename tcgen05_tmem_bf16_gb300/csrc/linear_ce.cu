@@ -857,9 +857,16 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     }
     double loss = 0.0;
     if (lane < kJoinRows && row < count) {
-      // the differences in 64 bits: a confident row's loss is a small one
-      const double lse = (static_cast<double>(a.x) + static_cast<double>(log2f(a.y))) * kLn2;
-      if (counts) loss = lse - p.alpha * static_cast<double>(target);
+      // A confident row's loss is a small difference: in 64 bits, and of powers of
+      // two by the same fp32 factor c2 (its rounding is then one of the loss, not
+      // one of the logits that outlives the subtraction).  What is left is the
+      // rounding of the powers, 2^-22; the exact loss is never below zero.
+      const double sum2 = static_cast<double>(log2f(a.y));
+      const double lse = (static_cast<double>(a.x) + sum2) * kLn2;
+      if (counts) {
+        loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * target) + sum2) * kLn2;
+        if (loss < 0.0) loss = 0.0;
+      }
       p.loss[r] = static_cast<float>(loss);
       p.lse[r] = counts ? static_cast<float>(lse) : 0.0f;
     }
