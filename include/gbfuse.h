@@ -354,10 +354,12 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
  *   loss, lse [M] fp32, 4-byte aligned; mean (may be NULL) one fp32, 0 where
  *   no row is scored.
  *   D % 8 == 0, D >= 8, V >= 1; M <= 2^24, V <= 2^26, D <= 2^20; alpha finite.
- *   Products accumulated in fp32 on the tensor cores, whose additions cut; the
- *   mean of the cut, D * 2^-30 of a logit, is put back (lse is off by about 1e-7
- *   of itself at D = 4096; by 1e-5 where all products of a logit have one sign).
- *   Sums of exponentials in fp32 relative to their maximum.  Workspace:
+ *   Products accumulated in fp32 on the tensor cores, whose additions cut: in
+ *   chains of at most 1024 products, whose sums are added in rounded fp32.
+ *   Whatever D, lse and loss are off by up to about 5e-7 of themselves where the
+ *   products have random signs, lse by 2e-6 where they all have one; sums that
+ *   fp32 holds exactly stay exact.  Sums of exponentials in fp32 relative to their
+ *   maximum; a loss is never below zero.  Workspace:
  *   gbf_workspace_size(GBF_OP_LINEAR_CE, M, V, D, 1) bytes.
  * gbf_linear_ce_grad -- its gradients, from the lse that gbf_linear_ce wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - [v == targets[m]])
@@ -367,8 +369,9 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
  *   dloss [M] fp32 or NULL (1 for every row); dx [M][D], dw [V][D] bf16, either
  *   may be NULL (not computed), every row of the others is written.  The
  *   logits are computed again, a piece of the vocabulary at a time; G of the
- *   piece is rounded to bf16 (before f), the sums are fp32, dx and dw are
- *   rounded once.  The same bits on every run.  Workspace:
+ *   piece is rounded to bf16 (before f), dx and dw are summed in fp32 on the tensor
+ *   cores (one chain of additions, which cut about 1e-9 of the sum per product)
+ *   and rounded once.  The same bits on every run.  Workspace:
  *   gbf_workspace_size(GBF_OP_LINEAR_CE_GRAD, M, V, D, 1) bytes.
  */
 GBF_API gbf_status_t gbf_linear_ce(const void *x, const void *w, const void *targets,

@@ -9,8 +9,9 @@
 // another place, so that the CTAs do not all ask for the same lines of x.
 //
 // A tile's K blocks are dealt to several accumulators, which the ending adds in
-// fp32: shorter chains of additions on the tensor cores, which cut (four chains
-// at N = 16: a quarter of the cut and of its scatter).
+// fp32: shorter chains of additions on the tensor cores, which cut.  Where a chain
+// would still be longer than kCeChain blocks, K is taken in segments, and the
+// ending keeps the sums of those before the last in a buffer of the CTA's own.
 //
 // Endings, a thread per column of the vocabulary:
 //   LSE   the tile is transposed 16 rows at a time through shared memory; per
@@ -43,10 +44,10 @@ struct SwCfg {
   static constexpr int kAccs = MPAD == 16 ? 8 : MPAD == 64 ? 4 : 2;  // accumulators
   static constexpr int kTmemCols = MPAD * kAccs;  // 128 or 256: two CTAs fit
   // Accumulators of a tile: four, or two where that leaves another tile in
-  // tensor memory and K is not over 4096 (64 rows x 128000 x 2048: 99 us, with
-  // four 102).
+  // tensor memory and their chains are short enough (64 rows x 128000 x 2048: 99
+  // us, with four 102).
   static __host__ __device__ constexpr int groups(int num_kb) {
-    return MPAD == 64 && num_kb <= 64 ? 2 : kAccs < 4 ? kAccs : 4;
+    return MPAD == 64 && num_kb <= 2 * kCeChain ? 2 : kAccs < 4 ? kAccs : 4;
   }
   static constexpr int kBarBytes = 256;
   static constexpr int kRowBytes = 3 * MPAD * 4;            // lse2, dl, targets
@@ -127,7 +128,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   const int tiles = (a.cols + 127) / 128;
   const int num_kb = a.num_kb;
   const int per_tile = Cfg::groups(num_kb);
-  const int two_bufs = Cfg::kAccs / per_tile == 2 ? 1 : 0;  // tiles in tensor memory: 2 or 1
+  const int two_bufs = Cfg::kAccs / per_tile == 2 ? 1 : 0;  // segments in tensor memory: 2 or 1
+  const int seg_kb = per_tile * kCeChain;
   const int step = static_cast<int>(gridDim.x);
 
   if (warp == 0) {
@@ -141,7 +143,9 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       uint32_t ph = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < tiles && ok; t += step) {
-        int kb = static_cast<int>(static_cast<unsigned>(t) * 13u % static_cast<unsigned>(num_kb));
+        // by the column of W, so that both passes add in the same order
+        int kb = static_cast<int>(static_cast<unsigned>(a.v0 / 128 + t) * 13u %
+                                  static_cast<unsigned>(num_kb));
         for (int i = 0; i < num_kb; ++i) {
           if (!wait_bar(&empty[s], ph ^ 1, ctl, kSiteProducerEmpty)) {
             ok = false;
@@ -174,13 +178,14 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
-      int l = 0;
-      for (int t = blockIdx.x; t < tiles && ok; t += step, ++l) {
+      int l = 0, seg = 0;
+      for (int t = blockIdx.x; t < tiles && ok; ++l) {
         const int buf = l & two_bufs;
         const int use = l >> two_bufs;
         if (!wait_bar(&tempty[buf], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
         tc_fence_after();
-        for (int i = 0; i < num_kb; ++i) {
+        const int seg_end = min(seg + seg_kb, num_kb);
+        for (int i = seg; i < seg_end; ++i) {
           if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
             ok = false;
             break;
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
             mma_ss(d, sdesc_sw128(w0 + k * 32, 16, 1024), sdesc_sw128(x0 + k * 32, 16, 1024),
-                   idesc, (i >= per_tile || k != 0) ? 1u : 0u);
+                   idesc, (i - seg >= per_tile || k != 0) ? 1u : 0u);
           mma_commit(&empty[s]);
           if (++s == kStages) {
             s = 0;
@@ -201,6 +206,11 @@ __global__ void __launch_bounds__(kSwThreads, 2)
         }
         if (!ok) break;
         if (!(kctl.inject && l == 0)) mma_commit(&tfull[buf]);
+        seg = seg_end;
+        if (seg == num_kb) {
+          seg = 0;
+          t += step;
+        }
       }
       mma_commit(done);
       wait_bar(done, 0, ctl, kSiteDrain, false);
@@ -209,13 +219,21 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   } else {
     const int q = warp & 3;  // the quarter of tensor memory that this warp reads
     float* my_turn = turn + q * 32 * 17;
-    const int groups = min(per_tile, num_kb);
     const int chunks = (count + 15) / 16;  // of 16 rows
-    int l = 0;
-    for (int t = blockIdx.x; t < tiles; t += step, ++l) {
+    // sums of the segments before: [row][column], this thread's column
+    float* part = e.chain + static_cast<int64_t>(blockIdx.x) * MPAD * 128 + q * 32 + lane;
+    int seg = 0;
+    for (int t = blockIdx.x, l = 0; t < tiles; ++l) {
       const int buf = l & two_bufs;
+      float before[16];  // of the next 16 rows, on their way meanwhile
+      if (seg > 0) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) before[k] = __ldcg(part + k * 128);
+      }
       if (!wait_bar(&tfull[buf], (l >> two_bufs) & 1, ctl, kSiteEpiAccFull)) break;
       tc_fence_after();
+      const int groups = min(per_tile, num_kb - seg);
+      const bool last = seg + seg_kb >= num_kb;
       const uint32_t tb =
           tmem_base + buf * per_tile * MPAD + (static_cast<uint32_t>(q * 32) << 16);
       const int col = t * 128 + q * 32 + lane;  // of the piece
@@ -234,8 +252,21 @@ __global__ void __launch_bounds__(kSwThreads, 2)
 #pragma unroll
             for (int k = 0; k < 16; ++k) v[k] += __uint_as_float(r[k]);
           }
+          if (seg > 0) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = before[k] + v[k];
+            if (c + 1 < chunks) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) before[k] = __ldcg(part + ((c + 1) * 16 + k) * 128);
+            }
+          }
         }
-        if (GRAD) {
+        if (!last) {
+          if (c < chunks) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) __stcg(part + (c * 16 + k) * 128, v[k]);
+          }
+        } else if (GRAD) {
           float f[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -292,6 +323,11 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[buf]);
+      seg += seg_kb;
+      if (last) {
+        seg = 0;
+        t += step;
+      }
     }
   }
 
@@ -337,11 +373,11 @@ cudaError_t run_swap(const CeSwap& a, const CeEnd& end, const KernelCtl& ctl, in
 
 int ce_swap_rows(int64_t M) { return M <= 16 ? 16 : M <= 64 ? 64 : M <= kCeSwapMax ? 128 : 0; }
 
-int ce_swap_chains(int64_t M, int k_blocks) {
+int ce_swap_segments(int64_t M, int k_blocks) {
   const int n = M <= 16   ? SwCfg<16>::groups(k_blocks)
                 : M <= 64 ? SwCfg<64>::groups(k_blocks)
                           : SwCfg<128>::groups(k_blocks);
-  return std::min(n, std::max(1, k_blocks));
+  return (k_blocks + n * kCeChain - 1) / (n * kCeChain);
 }
 
 cudaError_t launch_ce_swap(const CeSwap& a, bool grad, const CeEnd& end, int sms,

@@ -77,6 +77,9 @@ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row tiles per unit of work: two that share a column tile, or a lone one where
 // there is no second.
 int ce_streams(int64_t M) { return M > kCeTileRows ? 2 : 1; }
+// Whether the logits' K is taken in several chains (above kCeSwapMax rows): then in
+// units of one row tile, by a launch of their own (linear_ce.cu).
+bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
 
 // Parts of K of the product for dx, each with an fp32 buffer of its own, 16 at
 // most and none shorter than 8 K blocks.  With one row tile: as many as give one
@@ -97,10 +100,11 @@ int ce_splits(int64_t M, int64_t D, int64_t cols) {
 }
 
 // Columns of a tile of the forward pass: 224 where the rounds of such tiles over
-// the pairs are shorter than those of 256 (1024 rows x 32000 x 4096, four rounds
-// either way: 157 us, 175 with 256; 700 x 50001 x 2048: 128, 140).
-int ce_tile_cols(int64_t M, int64_t V) {
-  if (ce_streams(M) == 1) return 256;
+// the pairs are shorter than those of 256 (1024 rows x 32000 x 1024, four rounds
+// either way: 59.5 us, 64.4 with 256; 700 x 50001 x 1024: 81.5, 87.6).  In chains,
+// units of one row tile, an MMA takes as long for 224 columns as for 256.
+int ce_tile_cols(int64_t M, int64_t V, int64_t D) {
+  if (ce_streams(M) == 1 || ce_chained(D)) return 256;
   const int64_t m = ceil_div64(M, 2 * kCeTileRows);
   const int64_t wide = ceil_div64(m * ceil_div64(V, 256), kCePairs) * 256;
   const int64_t narrow = ceil_div64(m * ceil_div64(V, 224), kCePairs) * 224;
@@ -109,18 +113,25 @@ int ce_tile_cols(int64_t M, int64_t V) {
 
 // Partial sums per row of the forward pass: two per tile, with swapped roles one
 // per 32 columns.
-int64_t ce_parts(int64_t M, int64_t V) {
-  return M <= kCeSwapMax ? 4 * ceil_div64(V, 128) : 2 * ceil_div64(V, ce_tile_cols(M, V));
+int64_t ce_parts(int64_t M, int64_t V, int64_t D) {
+  return M <= kCeSwapMax ? 4 * ceil_div64(V, 128) : 2 * ceil_div64(V, ce_tile_cols(M, V, D));
 }
 
 struct CeWs {
   int *count, *rows, *tgt;
   unsigned* ticket;
-  float *lse2, *dl, *tlog, *dxacc;
+  float *lse2, *dl, *tlog, *dxacc, *chain;
   float2* part;
   double* sums;
   __nv_bfloat16 *xc, *g[2];
 };
+
+// Sums over the segments before the last of a logit's K: for each CTA the padded
+// rows x 128 columns.
+size_t ce_chain_floats(int64_t M, int64_t D) {
+  if (M > kCeSwapMax || ce_swap_segments(M, static_cast<int>(ceil_div64(D, kBK))) == 1) return 0;
+  return size_t(2) * kMaxSms * ce_swap_rows(M) * 128;
+}
 
 size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs* w) {
   Sections s{static_cast<uint8_t*>(base)};
@@ -130,8 +141,9 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
   w->rows = s.take<int>(M);
   w->tgt = s.take<int>(M);
   w->xc = s.take<__nv_bfloat16>(static_cast<size_t>(M) * D);
+  w->chain = s.take<float>(ce_chain_floats(M, D));
   if (!grad) {
-    w->part = s.take<float2>(static_cast<size_t>(ce_parts(M, V)) * M);
+    w->part = s.take<float2>(static_cast<size_t>(ce_parts(M, V, D)) * M);
     w->tlog = s.take<float>(M);
     w->sums = s.take<double>(ceil_div64(M, 8));  // one per CTA of the join
   } else {
@@ -147,23 +159,6 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
     w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
   }
   return s.at;
-}
-
-// The factor by which a logit's products have to be taken for the tensor cores'
-// additions.  They cut: of the K / 16 additions of a chain each takes on average
-// 2^-25 off the running sum (measured: 3.1e-8, the same at K = 512 to 8192), and a
-// sum of like steps is on average half of its end on the way, so the end is low by
-// K 2^-30 of itself.  That mean is put back; what is left are the cuts' deviations
-// from it (lse off by 1.3e-6 of itself at K = 4096 without the factor).  Chains
-// of sums of one sign lose two to four times as much and get back this part; a
-// sum whose products are nearly all zero (a sparse x) is not cut and comes out high
-// by K 2^-30 of itself, the size of the error that all others would have without.
-double ce_uncut(int64_t M, int64_t D, bool forward) {
-  const int64_t k_blocks = ceil_div64(D, 64);
-  const int64_t chains = M <= kCeSwapMax      ? ce_swap_chains(M, static_cast<int>(k_blocks))
-                         : ce_streams(M) == 1 ? ce_lone_chains(static_cast<int>(k_blocks), forward)
-                                              : 1;
-  return 1.0 + static_cast<double>(D) / chains * 0x1p-30;
 }
 
 // Sizes that the kernels' 32-bit coordinates and unit counts hold.
@@ -221,9 +216,9 @@ bool ce_map_out_f32(CUtensorMap* m, const void* p, int64_t inner, int64_t outer)
 }
 
 // One launch: a CTA pair per unit of work at most, with M rows scored.
-gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M,
+gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M, bool chains,
                          const DeviceInfo& dev, unsigned* err, cudaStream_t s) {
-  const int streams = ce_streams(M);
+  const int streams = chains ? 1 : ce_streams(M);
   int64_t units = 0;
   for (const CeJob& j : launch.job) {
     if (j.mode == kCeNone) continue;
@@ -232,7 +227,7 @@ gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M,
     units += ceil_div64(rows, kCeTileRows * streams) * ceil_div64(n, j.bn) * j.splits;
   }
   const int grid = 2 * static_cast<int>(std::min<int64_t>(units, dev.pairs));
-  return cuda_status(launch_ce_gemm(launch, end, streams, grid, lib_ctl(err, grid), s));
+  return cuda_status(launch_ce_gemm(launch, end, streams, chains, grid, lib_ctl(err, grid), s));
 }
 
 }  // namespace
@@ -355,6 +350,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int swap_sms = std::min(dev->sms, kMaxSms);
   if (M == 0) return mean ? cuda_status(cudaMemsetAsync(mean, 0, 4, s)) : GBF_OK;
   CePrep p{};
   p.x = static_cast<const __nv_bfloat16*>(x);
@@ -382,7 +378,7 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   } else {
     launch.d = p.D;
     CeJob& job = launch.job[1];
-    job.bn = ce_tile_cols(M, V);
+    job.bn = ce_tile_cols(M, V, D);
     if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
         !ce_map_k(&job.b[0], w, D, V, D, job.bn / 2))
       return GBF_ERR_CUDA;
@@ -395,7 +391,8 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   end.tgt = ws.tgt;
   end.part = ws.part;
   end.tlog = ws.tlog;
-  end.c2 = static_cast<float>(alpha * ce_uncut(M, D, true) * 1.4426950408889634);
+  end.chain = ws.chain;
+  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
   end.M = p.M;
   CeJoin join{};
   join.count = ws.count;
@@ -412,12 +409,12 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   join.mean = mean;
   join.c2 = end.c2;
   join.M = p.M;
-  join.parts = static_cast<int>(ce_parts(M, V));
+  join.parts = static_cast<int>(ce_parts(M, V, D));
   if (!few && (st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms,
                                                s))) != GBF_OK)
     return st;
-  st = few ? cuda_status(launch_ce_swap(swap, false, end, dev->sms, lib_ctl(err, 2 * dev->sms), s))
-           : run_ce_gemm(launch, end, M, *dev, err, s);
+  st = few ? cuda_status(launch_ce_swap(swap, false, end, swap_sms, lib_ctl(err, 2 * swap_sms), s))
+           : run_ce_gemm(launch, end, M, ce_chained(D), *dev, err, s);
   if (st != GBF_OK) return st;
   return cuda_status(launch_ce_join(join, s));
 }
@@ -429,7 +426,8 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
                                 gbf_stream_t stream) {
   gbf_status_t st = check_ce(x, w, targets, index_type, M, V, D, alpha);
   if (st != GBF_OK) return st;
-  if ((M > 0 && (!lse || (!dx && !dw))) || (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
+  if ((M > 0 && (!lse || (!dx && !dw))) ||
+      (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
     return GBF_ERR_INVALID_ARG;
   if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16) ||
       !aligned(workspace, 16))
@@ -441,6 +439,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int swap_sms = std::min(dev->sms, kMaxSms);
   if (M == 0)
     return dw ? cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, s)) : GBF_OK;
   CePrep p{};
@@ -462,6 +461,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
     return st;
   const int64_t piece = ce_piece(M, V);
   const bool few = M <= kCeSwapMax;  // G transposed, by the swapped roles
+  const bool chains = !few && ce_chained(D);
   const int64_t ld = few ? ce_swap_rows(M) : ceil_div64(piece, 8) * 8;
   const int64_t m_pad = ceil_div64(M, 512) * 512;
   const int splits = ce_splits(M, D, piece);
@@ -470,7 +470,8 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   end.tgt = ws.tgt;
   end.lse2 = ws.lse2;
   end.dl = ws.dl;
-  end.c2 = static_cast<float>(alpha * ce_uncut(M, D, false) * 1.4426950408889634);
+  end.chain = ws.chain;
+  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
   end.scale = alpha * scale;
   end.mean = reduction == GBF_REDUCE_MEAN;
   end.M = p.M;
@@ -478,9 +479,10 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   // Launch n: G of piece n, and the products of piece n - 1's G.
   const int64_t pieces = ceil_div64(V, piece);
   for (int64_t n = 0; n <= pieces; ++n) {
-    CeLaunch launch{};
-    launch.d = p.D;
+    CeLaunch launch{}, logits{};
+    launch.d = logits.d = p.D;
     for (CeJob& j : launch.job) j.bn = 256;
+    for (CeJob& j : logits.job) j.bn = 256;
     if (n < pieces && few) {
       const int64_t v0 = n * piece;
       CeSwap swap{};
@@ -489,10 +491,10 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
       swap.v0 = static_cast<int>(v0);
       swap.cols = static_cast<int>(std::min(piece, V - v0));
       swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
-      st = cuda_status(launch_ce_swap(swap, true, end, dev->sms, lib_ctl(err, 2 * dev->sms), s));
+      st = cuda_status(launch_ce_swap(swap, true, end, swap_sms, lib_ctl(err, 2 * swap_sms), s));
       if (st != GBF_OK) return st;
     } else if (n < pieces) {
-      CeJob& job = launch.job[1];
+      CeJob& job = chains ? logits.job[1] : launch.job[1];
       const int64_t v0 = n * piece, cols = std::min(piece, V - v0);
       job.mode = kCeGrad;
       job.cols = static_cast<int>(cols);
@@ -501,6 +503,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
       if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
           !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g[n & 1], cols, M, ld))
         return GBF_ERR_CUDA;
+      if (chains && (st = run_ce_gemm(logits, end, M, true, *dev, err, s)) != GBF_OK) return st;
     }
     if (n > 0) {
       const int64_t v0 = (n - 1) * piece, cols = std::min(piece, V - v0);
@@ -531,8 +534,8 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
           return GBF_ERR_CUDA;
       }
     }
-    if (few && n == 0) continue;  // no G yet
-    if ((st = run_ce_gemm(launch, end, M, *dev, err, s)) != GBF_OK) return st;
+    if ((few || chains) && n == 0) continue;  // no G yet
+    if ((st = run_ce_gemm(launch, end, M, false, *dev, err, s)) != GBF_OK) return st;
   }
   if (!dx) return GBF_OK;
   CeDxOut out{};

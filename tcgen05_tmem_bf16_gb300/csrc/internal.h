@@ -182,6 +182,7 @@ struct CeEnd {
   float2* part;       // [2 per column tile][M] (maximum, sum), powers of two
   float* tlog;        // [count] the targets' products
   float c2;           // alpha / ln 2
+  float* chain;       // ce_swap.cu: sums over the segments before the last
   float scale;        // of dw
   int mean;           // divide by the number of scored rows
   int M;
@@ -196,8 +197,12 @@ __device__ __forceinline__ int64_t ce_target(const void* targets, int ids64, int
 #endif
 // The logits for up to kCeSwapMax rows, with swapped roles (ce_swap.cu).
 constexpr int kCeSwapMax = 128;
-int ce_swap_chains(int64_t M, int k_blocks);  // sums that a logit's K is dealt to
-int ce_lone_chains(int k_blocks, bool forward);  // the same in linear_ce.cu, one row tile per unit
+// K blocks whose products the tensor cores add up in one chain for a logit.  Each
+// addition cuts 2^-25 off the running sum on average, so that a sum of 16 K blocks
+// of 64 is low by 1e-6 of itself (measured: 9.8e-10 per product for random signs,
+// up to 3.9e-9 for one sign).
+constexpr int kCeChain = 16;
+int ce_swap_segments(int64_t M, int k_blocks);  // parts of K between which the ending adds
 int ce_swap_rows(int64_t M);  // rows padded to: 16, 64, 128; 0 above kCeSwapMax
 struct CeSwap {
   CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored (and forward)
@@ -243,8 +248,9 @@ struct CeDxOut {
   float scale;
   int mean, m_pad, splits, D;
 };
-cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, int grid,
-                           const KernelCtl& ctl, cudaStream_t stream);
+// chains: one product, the logits, in units of one row tile (streams 1).
+cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, bool chains,
+                           int grid, const KernelCtl& ctl, cudaStream_t stream);
 cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
                            cudaStream_t stream);
 cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream);

@@ -24,9 +24,22 @@
 // included) reaches no result.
 //
 // G is rounded to bf16 without the mean's factor: the factor multiplies the
-// fp32 sums, so it adds no rounding of its own.  The sums of the products are the
-// tensor cores' fp32, whose additions cut; the mean of what they cut is put back
-// through alpha (ce_uncut in heads.cu).
+// fp32 sums, so it adds no rounding of its own.
+//
+// The sums of the products are the tensor cores' fp32, whose additions cut instead
+// of rounding: one chain over all of K loses 1e-9 K of a logit, and up to 4e-9 K
+// where its products have one sign (lse off by 1.5e-6 of itself at K = 4096, 6e-5
+// at 65536).  So a logit's K is taken in chains of kCeChain blocks, whose sums the
+// ending adds in fp32 (lse off by 3 to 4e-7 at any K).  Up to 1024 products one
+// chain is enough, and the logits are tiles of two row tiles like the others.  Above
+// that they run in units of one row tile (kCeChains), because a thread of the
+// ending then holds its 128 sums in registers and one accumulator is emptied
+// while the other is filled.  (Forward pass, 8192 x 65536 x 4096: 2.68 ms, one
+// chain with two row tiles 2.47; 1024 x 128000 x 4096 612 and 593 us; 2868 x
+// 50001 x 2048 388 and 397.  The sums of two row tiles do not fit in registers:
+// kept in L2, 3.42 ms.)  Both passes cut K at the same places: the backward
+// pass's powers then add up to the forward's sum, and a confident row's p - 1
+// holds no error of the products.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -58,18 +71,22 @@ constexpr int kCeABytes = kBM * kBK * 2;   // 16 KB: this CTA's 128 rows of A
 constexpr int kCeBBytes = 128 * kBK * 2;   // 16 KB: this CTA's half of B
 constexpr int kCeGroup = 8;            // raster group (units of rows)
 constexpr int kCeUnitCost = 4;         // a unit's ending, in K blocks of its main loop
-constexpr int kCeTwoK = 24;            // K blocks from which a lone row tile's logits take two sums
 
-template <int STREAMS>
+// Two row tiles per unit, a lone one, or a lone one of logits in chains.
+enum CeForm { kCeTwo, kCeLone, kCeChains };
+
+template <int FORM>
 struct CeCfg {
-  static constexpr int kStageBytes = STREAMS * kCeABytes + kCeBBytes;
-  static constexpr int kStages = STREAMS == 2 ? 4 : 5;
+  static constexpr int kStreams = FORM == kCeTwo ? 2 : 1;
+  static constexpr int kStageBytes = kStreams * kCeABytes + kCeBBytes;
+  static constexpr int kStages = FORM == kCeTwo ? 4 : FORM == kCeLone ? 5 : 6;
   static constexpr int kBarBytes = 1024;
   // Two staging buffers per warp of the ending, of 32 rows x 64 bytes.  Few rows
   // of x make dw a matter of writing: there the rows are 128 bytes.  (Stores of
   // 128 x 256 tiles of a 32000 x 4096 tensor, by bytes of a row per request: 16:
   // 97 us, 32: 58, 256: 41, a plain fill 38.)
-  static constexpr int kBufBytes = STREAMS == 2 ? 32 * 64 : 32 * 128;
+  static constexpr bool kWide = FORM == kCeLone;
+  static constexpr int kBufBytes = kWide ? 32 * 128 : 32 * 64;
   static constexpr int kStagingBytes = 8 * 2 * kBufBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -163,13 +180,6 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   return true;
 }
 
-// One row tile per unit: whether the halves of K go to the two accumulators.
-// The tensor cores cut the sum at every step, so a logit of 4096 products is low
-// by some 4e-6 of itself; two chains of half the length halve that and its scatter.
-__device__ __forceinline__ bool ce_two_k(const CeJob& j, const CeUnit& u) {
-  return j.mode == kCeLse && u.kb1 - u.kb0 >= kCeTwoK;
-}
-
 // One warp's 32 rows x 32 columns of fp32 to the map's tensor, stored or added
 // there by the TMA engine, through the warp's two staging buffers (16 columns
 // each).  Every element is added to by one warp of one launch, so the sums do
@@ -238,37 +248,45 @@ __device__ __forceinline__ void put_chunk(uint8_t* bufs, int buf_bytes, int& fli
   }
 }
 
-// v[k] += the accumulator's column k of this thread's lane at taddr.
-__device__ __forceinline__ void add_acc32(uint32_t taddr, uint32_t (&v)[32]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t o[16];
-    tmem_ld16(taddr + 16 * h, o);
-    tmem_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      v[16 * h + k] = __float_as_uint(__uint_as_float(v[16 * h + k]) + __uint_as_float(o[k]));
-  }
-}
-
-// How a warp of the ending gives an accumulator (or both) back to the issuers.
+// How a warp of the ending gives an accumulator back to the issuers.
 struct CeFree {
-  uint64_t *mine, *other;
-  uint32_t lead_mine, lead_other;  // the even CTA's, as the odd one sees them
-  bool leader, two;
+  uint64_t* mine;
+  uint32_t lead;  // the even CTA's, as the odd one sees it
+  bool leader;
   __device__ __forceinline__ void operator()() const {
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
       if (leader) mbar_arrive(mine);
-      else mbar_arrive_cluster(lead_mine);
-      if (two) {
-        if (leader) mbar_arrive(other);
-        else mbar_arrive_cluster(lead_other);
-      }
+      else mbar_arrive_cluster(lead);
     }
   }
 };
+
+// A warp's 128 columns of an accumulator, which is then given back.
+__device__ __forceinline__ void ce_read(uint32_t tb, const CeFree& release,
+                                        uint32_t (&v)[4][32]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tmem_ld32(tb + 32 * c, v[c]);
+  tmem_wait_ld();
+  release();
+}
+// The same, added to v.
+__device__ __forceinline__ void ce_add(uint32_t tb, const CeFree& release,
+                                       uint32_t (&v)[4][32]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t o[16];
+    tmem_ld16(tb + 16 * c, o);
+    tmem_wait_ld();
+    if (c == 7) release();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      uint32_t& x = v[c / 2][16 * (c & 1) + k];
+      x = __float_as_uint(__uint_as_float(x) + __uint_as_float(o[k]));
+    }
+  }
+}
 
 // What the ending of a tile needs: a thread holds one row, a warp 128 columns
 // from col0 on.
@@ -283,10 +301,10 @@ struct CeTileArgs {
   float lse2, dl, out_scale;
 };
 
-template <int MODE, int STREAMS>
+template <int MODE, int FORM>
 __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const CeTileArgs& t,
                                          const CeEnd& e, int& flip, float& m, float& sum) {
-  constexpr int kBuf = CeCfg<STREAMS>::kBufBytes;
+  constexpr int kBuf = CeCfg<FORM>::kBufBytes;
   const int col0 = t.col0 + c * 32;
   const int row0 = t.row - static_cast<int>(threadIdx.x & 31);
   if constexpr (MODE == kCeLse) {
@@ -356,7 +374,7 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
     if constexpr (MODE == kCeGrad)
       put_chunk<false>(t.staging, kBuf, flip, c, w, t.out, row0, col0, e.M, t.cols, t.pol);
     else
-      put_chunk<STREAMS == 1>(t.staging, kBuf, flip, c, w, t.out, t.v0 + row0, col0,
+      put_chunk<CeCfg<FORM>::kWide>(t.staging, kBuf, flip, c, w, t.out, t.v0 + row0, col0,
                               t.v0 + t.cols, t.d, t.pol);
   }
 }
@@ -364,33 +382,30 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
 // A warp's 128 columns, 32 at a time: the next are on their way from tensor
 // memory while the ending works on the present ones; the accumulator is free
 // once the last have arrived.
-template <int MODE, int STREAMS>
+template <int MODE, int FORM>
 __device__ __forceinline__ void ce_tile(uint32_t tb, const CeFree& release, const CeTileArgs& t,
                                         const CeEnd& e, int& flip, float& m, float& sum) {
   uint32_t va[32], vb[32];
   tmem_ld32(tb, va);
   tmem_wait_ld();
-  if (release.two) add_acc32(tb + 256, va);  // the second half of K
   tmem_ld32(tb + 32, vb);
-  ce_chunk<MODE, STREAMS>(0, va, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM>(0, va, t, e, flip, m, sum);
   tmem_wait_ld();
-  if (release.two) add_acc32(tb + 256 + 32, vb);
   tmem_ld32(tb + 64, va);
-  ce_chunk<MODE, STREAMS>(1, vb, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM>(1, vb, t, e, flip, m, sum);
   tmem_wait_ld();
-  if (release.two) add_acc32(tb + 256 + 64, va);
   tmem_ld32(tb + 96, vb);
-  ce_chunk<MODE, STREAMS>(2, va, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM>(2, va, t, e, flip, m, sum);
   tmem_wait_ld();
-  if (release.two) add_acc32(tb + 256 + 96, vb);
   release();
-  ce_chunk<MODE, STREAMS>(3, vb, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM>(3, vb, t, e, flip, m, sum);
 }
 
-template <int STREAMS>
+template <int FORM>
 __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeLaunch a, const CeEnd e, const KernelCtl kctl) {
-  using Cfg = CeCfg<STREAMS>;
+  using Cfg = CeCfg<FORM>;
+  constexpr int STREAMS = Cfg::kStreams;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -514,11 +529,10 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     // ------------------------------------------------------------ MMA issuers (even CTA)
     // Two row tiles per unit: warp 1 issues the first's, warp 2 the second's,
     // each into its own accumulator; both read every stage.  One row tile: warp 1
-    // alone, accumulators in turn, so that a tile's ending overlaps the next one's
-    // products (or, ce_two_k, the halves of K into the two, which the ending
-    // adds).  One thread's MMAs complete one after another, about 150 cycles each:
-    // half the rate of two threads, but with one row tile W's 8 KB per MMA are
-    // 7.9 TB/s over all pairs, more than HBM gives.
+    // alone, accumulators in turn, so that a chain's ending overlaps the next one's
+    // products.  One thread's MMAs complete one after another, about 150 cycles each,
+    // where two threads' reach the tensor pipe's 128; with one row tile in all W's 8
+    // KB per MMA are 7.9 TB/s over all pairs, more than HBM gives.
     // (Issuers that shared a unit's blocks would each have to wait for all of them
     // all the same: a barrier's parity says nothing to a thread that has missed a
     // phase.)
@@ -529,28 +543,37 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       bool ok = true;
       bool first = true;
       int use0 = 0, use1 = 0;  // of the accumulators
-      int turn = st;
+      int turn = 0;
       CeUnit u;
       for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
         const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
         const uint32_t idesc = idesc_bf16(kCeTile, j.bn, a_mn, b_mn);
-        const bool two = STREAMS == 1 && ce_two_k(j, u);
-        const int kb_half = two ? (u.kb0 + u.kb1) / 2 : u.kb1;
-        int acc = two ? 0 : turn;
-        if (STREAMS == 1 && !two) turn ^= 1;
-        if (!wait_bar(&tempty[acc], ((acc ? use1 : use0) & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
-        if (acc) ++use1;
-        else ++use0;
-        if (two && !wait_bar(&tempty[1], (use1++ & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
-        tc_fence_after();
+        int acc = st;
+        // the next accumulator, when the ending has emptied it
+        auto take = [&]() -> bool {
+          if (STREAMS == 1) {
+            acc = turn;
+            turn ^= 1;
+          }
+          if (!wait_bar(&tempty[acc], ((acc ? use1 : use0) & 1) ^ 1, ctl, kSiteMmaAccEmpty))
+            return false;
+          if (acc) ++use1;
+          else ++use0;
+          tc_fence_after();
+          return true;
+        };
+        if (!take()) break;
         uint32_t accumulate = 0;
         for (int kb = u.kb0; kb < u.kb1; ++kb) {
-          if (kb == kb_half) {
-            mma_commit_pair(&tfull[0], 0x3);
-            acc = 1;
+          if (FORM == kCeChains && kb > 0 && kb % kCeChain == 0) {
+            mma_commit_pair(&tfull[acc], 0x3);
             accumulate = 0;
+            if (!take()) {
+              ok = false;
+              break;
+            }
           }
           if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
             ok = false;
@@ -600,7 +623,6 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
       const CeJob& j = a.job[u.job];
       const int mode = j.mode;
-      const bool two = STREAMS == 1 && ce_two_k(j, u);
       CeTileArgs t;
       t.out = &j.o;
       t.staging = my_staging;
@@ -615,13 +637,27 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       t.count = count;
       t.add = j.add != 0;
       t.out_scale = out_scale;
-#pragma unroll 1
-      for (int i = 0; i < STREAMS; ++i) {
-        int acc_i = i;
-        if (STREAMS == 1 && !two) {
-          acc_i = turn;
+      // waits for the next sums of row tile i: their accumulator's index, or -1
+      auto next = [&](int i) -> int {
+        int acc = i;
+        if (STREAMS == 1) {
+          acc = turn;
           turn ^= 1;
         }
+        if (!wait_bar(&tfull[acc], (acc ? use1 : use0) & 1, ctl, kSiteEpiAccFull)) return -1;
+        if (acc) ++use1;
+        else ++use0;
+        tc_fence_after();
+        return acc;
+      };
+      auto columns = [&](int acc) -> uint32_t {
+        return tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
+      };
+      auto free_of = [&](int acc) -> CeFree {
+        return CeFree{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0, leader};
+      };
+#pragma unroll 1
+      for (int i = 0; i < STREAMS; ++i) {
         t.row = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM + q * 32 + lane;
         t.row_ok = t.row < count;
         t.buf_row = u.split * e.m_pad + t.row;
@@ -634,27 +670,40 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             t.dl = e.dl[t.row];
           }
         }
-        ok = wait_bar(&tfull[acc_i], (acc_i ? use1 : use0) & 1, ctl, kSiteEpiAccFull);
-        if (acc_i) ++use1;
-        else ++use0;
-        if (ok && two) ok = wait_bar(&tfull[1], use1++ & 1, ctl, kSiteEpiAccFull);
+        const int acc = next(i);
+        ok = acc >= 0;
         if (!ok) break;
-        tc_fence_after();
-        const uint32_t tb =
-            tmem_base + acc_i * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-        const CeFree release{acc_i ? &tempty[1] : &tempty[0], &tempty[1],
-                             acc_i ? lead_empty1 : lead_empty0, lead_empty1, leader, two};
+        const uint32_t tb = columns(acc);
+        const CeFree release = free_of(acc);
         float m = -INFINITY, sum = 0.0f;  // kLse
-        if (mode == kCeLse) {
-          ce_tile<kCeLse, STREAMS>(tb, release, t, e, flip, m, sum);
+        if constexpr (FORM == kCeChains) {
+          uint32_t v[4][32];  // the sums over the chains
+          ce_read(tb, release, v);
+          for (int kb = kCeChain; ok && kb < u.kb1; kb += kCeChain) {
+            const int more = next(i);
+            ok = more >= 0;
+            if (ok) ce_add(columns(more), free_of(more), v);
+          }
+          if (!ok) break;
+          if (mode == kCeLse) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ce_chunk<kCeLse, FORM>(c, v[c], t, e, flip, m, sum);
+            if (t.row_ok)
+              e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ce_chunk<kCeGrad, FORM>(c, v[c], t, e, flip, m, sum);
+          }
+        } else if (mode == kCeLse) {
+          ce_tile<kCeLse, FORM>(tb, release, t, e, flip, m, sum);
           if (t.row_ok)
             e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
         } else if (mode == kCeGrad) {
-          ce_tile<kCeGrad, STREAMS>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeGrad, FORM>(tb, release, t, e, flip, m, sum);
         } else if (mode == kCeDx) {
-          ce_tile<kCeDx, STREAMS>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeDx, FORM>(tb, release, t, e, flip, m, sum);
         } else {
-          ce_tile<kCeDw, STREAMS>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeDw, FORM>(tb, release, t, e, flip, m, sum);
         }
       }
     }
@@ -947,12 +996,12 @@ cudaLaunchConfig_t overlapped(int64_t grid, int threads, size_t smem, cudaStream
   return cfg;
 }
 
-template <int STREAMS>
+template <int FORM>
 cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ctl, int grid,
                    cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = ce_gemm_kernel<STREAMS>;
-  constexpr int smem = CeCfg<STREAMS>::kSmem;
+  auto kernel = ce_gemm_kernel<FORM>;
+  constexpr int smem = CeCfg<FORM>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -974,12 +1023,11 @@ cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ct
 
 }  // namespace
 
-int ce_lone_chains(int k_blocks, bool forward) { return forward && k_blocks >= kCeTwoK ? 2 : 1; }
-
-cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, int grid,
-                           const KernelCtl& ctl, cudaStream_t stream) {
-  return streams == 2 ? run_ce<2>(launch, end, ctl, grid, stream)
-                      : run_ce<1>(launch, end, ctl, grid, stream);
+cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, bool chains,
+                           int grid, const KernelCtl& ctl, cudaStream_t stream) {
+  return chains         ? run_ce<kCeChains>(launch, end, ctl, grid, stream)
+         : streams == 2 ? run_ce<kCeTwo>(launch, end, ctl, grid, stream)
+                        : run_ce<kCeLone>(launch, end, ctl, grid, stream);
 }
 
 cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
