@@ -85,7 +85,9 @@ bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
 // most and none shorter than 8 K blocks.  With one row tile: as many as give one
 // round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 103
 // us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
-// beside dw).  Else: none longer than half of what a pair has to do in all.
+// beside dw).  Else: none longer than half of what a pair has to do in all, the
+// logits among it also where their launch is another (without them there are more
+// parts: 1024 x 32000 x 4096 491 us, 501; 4096 x 32000 x 8192 3.59 ms, 3.66).
 int ce_splits(int64_t M, int64_t D, int64_t cols) {
   const int64_t d = ceil_div64(D, kCeTileRows), k = ceil_div64(cols, 64);
   const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
