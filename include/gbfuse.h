@@ -83,6 +83,8 @@ typedef int gbf_status_t;
 #define GBF_OP_CLIP_GRAD_NORM 7 /* gbf_workspace_size(op, tensors, 0, 0, 1) */
 #define GBF_OP_LINEAR_CE 8        /* gbf_workspace_size(op, M, V, D, 1) */
 #define GBF_OP_LINEAR_CE_GRAD 9   /* gbf_workspace_size(op, M, V, D, 1) */
+#define GBF_OP_MLP_GRAD 10         /* gbf_workspace_size(op, M, D, F, 1) */
+#define GBF_OP_ADD_RMSNORM_GRAD 11 /* gbf_workspace_size(op, M, N, 0, 1) */
 
 /* Type of an array of ids (`ids`, `targets`). */
 #define GBF_INDEX_I64 0
@@ -406,6 +408,59 @@ GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *o
                                     const int64_t *counts, const int *types, int tensors,
                                     float max_norm, float eps, float *norm, void *workspace,
                                     size_t workspace_bytes, gbf_stream_t stream);
+
+/*
+ * The operators of a gated block that is trained, from here to
+ * gbf_add_rmsnorm_grad: an array without elements (M == 0, ...) may be a null
+ * pointer.
+ *
+ * gbf_mlp_train -- mlp_swiglu_down with any gate, keeping what its gradient needs:
+ *   g = x*Wg^T,  u = x*Wu^T                            [M][F], each rounded to bf16
+ *   h = bf16( act(g) * u )  from the unrounded g and u    [M][F]
+ *   out = bf16( h*Wd^T + residual )                       [M][D], of the rounded h
+ *   x [M][D]; w_gate, w_up [F][D]; w_down [D][F] (all K-contiguous); residual
+ *   [M][D] or NULL (may equal out); every other array is required.  No workspace.
+ *   D, F >= 8, multiples of 8, <= 2^20; M <= 2^24.
+ * gbf_mlp_grad -- the gradient of out (its part through h; the residual's is dout
+ *   itself) from the g, u and h that gbf_mlp_train kept:
+ *     dh = dout*Wd;   dg = dh * u * act'(g),  du = dh * act(g)    (rounded to bf16)
+ *     dx = dg*Wg + du*Wu,   dw_gate = dg^T*x,  dw_up = du^T*x,  dw_down = dout^T*h
+ *   act' of GBF_ACT_RELU is 0 at 0.  dx [M][D], dw_gate, dw_up [F][D], dw_down
+ *   [D][F] bf16; any of the four may be NULL (not computed), not all.  dh is never
+ *   in memory.  Sums in fp32 on the tensor cores (whose additions cut about 1e-9 of
+ *   the sum per product), rounded once.  The same bits on every run.  M == 0 gives
+ *   zero weight gradients.  Workspace: gbf_workspace_size(GBF_OP_MLP_GRAD, M, D, F,
+ *   1) bytes.
+ */
+GBF_API gbf_status_t gbf_mlp_train(const void *x, const void *w_gate, const void *w_up,
+                                   const void *w_down, const void *residual, void *out, void *g,
+                                   void *u, void *h, int64_t M, int64_t D, int64_t F, int act,
+                                   gbf_stream_t stream);
+GBF_API gbf_status_t gbf_mlp_grad(const void *dout, const void *x, const void *g, const void *u,
+                                  const void *h, const void *w_gate, const void *w_up,
+                                  const void *w_down, void *dx, void *dw_gate, void *dw_up,
+                                  void *dw_down, int64_t M, int64_t D, int64_t F, int act,
+                                  void *workspace, size_t workspace_bytes, gbf_stream_t stream);
+
+/*
+ * gbf_add_rmsnorm_grad -- the gradient of add_rmsnorm, by the sum r (its
+ *   out_resid), which is also the gradient by each of a and x:
+ *     s = rsqrt(mean_j(r_j^2) + eps)
+ *     dr = dresid + s * (dnorm * weight - r * s^2 * mean_j(dnorm_j * weight_j * r_j))
+ *     dweight = sum over the rows of dnorm * r * s
+ *   dnorm [M][N] is the gradient of out_norm, dresid [M][N] that of out_resid
+ *   (NULL: zero); resid [M][N] the r that add_rmsnorm stored (bf16); weight [N];
+ *   dr [M][N] (may equal dnorm or dresid); dweight [N] or NULL (not computed).
+ *   All bf16; sums in fp32, one rounding; the same bits on every run.  N % 8 == 0
+ *   and N <= 16384; eps >= 0.  M == 0 gives a zero dweight.  HBM-bound: reads
+ *   dnorm, dresid and r once, writes dr once.  Workspace (not without dweight):
+ *   gbf_workspace_size(GBF_OP_ADD_RMSNORM_GRAD, M, N, 0, 1) bytes.
+ */
+GBF_API gbf_status_t gbf_add_rmsnorm_grad(const void *dnorm, const void *dresid,
+                                          const void *resid, const void *weight, void *dr,
+                                          void *dweight, int64_t M, int64_t N, float eps,
+                                          void *workspace, size_t workspace_bytes,
+                                          gbf_stream_t stream);
 
 /* Workspace bytes an entry point needs (0 for the fused ones).  `op` is a
  * GBF_OP_* id; `fused` selects the fused (1) or unfused (0) entry point. */

@@ -22,6 +22,12 @@ The operators at a model's two ends carry the prefix gbf_ in the C ABI only:
   linear_ce          softmax cross entropy of a linear head, the logits never stored
   linear_ce_grad     its gradients by the head's input and weight
   clip_grad_norm     global 2-norm over many gradients, and clipping
+
+So do those of the gated blocks between them, when they are trained:
+
+  mlp_train          the gated MLP block, keeping g, u and h for its gradient
+  mlp_grad           its gradients by x and by the three weights
+  add_rmsnorm_grad   the gradient of add_rmsnorm
 """
 from __future__ import annotations
 
@@ -34,7 +40,8 @@ from . import build as _build
 ACT = {"identity": 0, "relu": 1, "silu": 2, "gelu_tanh": 3}
 LAYOUT = {"kn": 0, "nk": 1}
 OP = {"gemm_epilogue": 0, "swiglu": 1, "w4a16": 2, "mlp": 3, "w8a16_fp8": 4, "w4a16_nvfp4": 5,
-      "embedding_grad": 6, "clip_grad_norm": 7, "linear_ce": 8, "linear_ce_grad": 9}
+      "embedding_grad": 6, "clip_grad_norm": 7, "linear_ce": 8, "linear_ce_grad": 9,
+      "mlp_grad": 10, "add_rmsnorm_grad": 11}
 INDEX = {"i64": 0, "i32": 1}
 REDUCTION = {"sum": 0, "mean": 1}
 TYPE = {"bf16": 0, "f32": 1}
@@ -52,7 +59,8 @@ EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unf
            "swiglu_pointwise", "add_rmsnorm", "add_rmsnorm_unfused", "mlp_swiglu_down",
            "mlp_swiglu_down_unfused", "w8a16_fp8_gemm", "w8a16_fp8_gemm_unfused",
            "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused", "gbf_embedding_lookup",
-           "gbf_embedding_grad", "gbf_clip_grad_norm", "gbf_linear_ce", "gbf_linear_ce_grad")
+           "gbf_embedding_grad", "gbf_clip_grad_norm", "gbf_linear_ce", "gbf_linear_ce_grad",
+           "gbf_mlp_train", "gbf_mlp_grad", "gbf_add_rmsnorm_grad")
 
 _lock = threading.Lock()
 _lib = None
@@ -115,6 +123,13 @@ def load(path: str | None = None):
         lib.gbf_linear_ce_grad.restype = I
         lib.gbf_clip_grad_norm.argtypes = [V, V, V, V, I, F, F, V, V, SZ, V]
         lib.gbf_clip_grad_norm.restype = I
+        lib.gbf_mlp_train.argtypes = [V, V, V, V, V, V, V, V, V, I64, I64, I64, I, V]
+        lib.gbf_mlp_train.restype = I
+        lib.gbf_mlp_grad.argtypes = [V, V, V, V, V, V, V, V, V, V, V, V, I64, I64, I64, I, V, SZ,
+                                     V]
+        lib.gbf_mlp_grad.restype = I
+        lib.gbf_add_rmsnorm_grad.argtypes = [V, V, V, V, V, V, I64, I64, F, V, SZ, V]
+        lib.gbf_add_rmsnorm_grad.restype = I
         lib.swiglu_pointwise.argtypes = [V, V, V, V, I64, I64, F, F, I, V]
         lib.swiglu_pointwise.restype = I
         lib.gemm_epilogue_unfused_noalloc.argtypes = [V, V, I, V, V, V, V, I64, I64, I64, F, F,
@@ -382,6 +397,29 @@ def clip_grad_norm(grads, out, max_norm, norm, eps=1e-6, workspace=None, workspa
                                grads.counts, grads.types, len(grads), max_norm, eps, _p(norm),
                                _p(workspace), workspace_bytes, _s(stream))
     return _check(st, "clip_grad_norm", raise_on_error)
+
+
+def mlp_train(x, w_gate, w_up, w_down, residual, out, g, u, h, M, D, F, act="silu", stream=None,
+              raise_on_error=True):
+    st = load().gbf_mlp_train(_p(x), _p(w_gate), _p(w_up), _p(w_down), _p(residual), _p(out),
+                              _p(g), _p(u), _p(h), M, D, F, _code(act, ACT), _s(stream))
+    return _check(st, "mlp_train", raise_on_error)
+
+
+def mlp_grad(dout, x, g, u, h, w_gate, w_up, w_down, dx, dw_gate, dw_up, dw_down, M, D, F,
+             act="silu", workspace=None, workspace_bytes=0, stream=None, raise_on_error=True):
+    st = load().gbf_mlp_grad(_p(dout), _p(x), _p(g), _p(u), _p(h), _p(w_gate), _p(w_up),
+                             _p(w_down), _p(dx), _p(dw_gate), _p(dw_up), _p(dw_down), M, D, F,
+                             _code(act, ACT), _p(workspace), workspace_bytes, _s(stream))
+    return _check(st, "mlp_grad", raise_on_error)
+
+
+def add_rmsnorm_grad(dnorm, dresid, resid, weight, dr, dweight, M, N, eps=1e-5, workspace=None,
+                     workspace_bytes=0, stream=None, raise_on_error=True):
+    st = load().gbf_add_rmsnorm_grad(_p(dnorm), _p(dresid), _p(resid), _p(weight), _p(dr),
+                                     _p(dweight), M, N, eps, _p(workspace), workspace_bytes,
+                                     _s(stream))
+    return _check(st, "add_rmsnorm_grad", raise_on_error)
 
 
 def gbf_workspace_size(op, M, N, K, fused) -> int:

@@ -679,6 +679,7 @@ size_t gbf_workspace_size(int op, int64_t M, int64_t N, int64_t K, int fused) {
     if (fused) return h;
     return 4 * h + align256(static_cast<size_t>(M * N) * 2);  // g, u (2h), h, D
   }
+  if (op >= GBF_OP_MLP_GRAD) return blocks_workspace_size(op, M, N, K);
   if (op >= GBF_OP_EMBEDDING_GRAD) return heads_workspace_size(op, M, N, K);
   if (fused) return 0;
   switch (op) {

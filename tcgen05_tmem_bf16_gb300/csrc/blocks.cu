@@ -1,0 +1,285 @@
+// blocks.cu -- entry points of the operators between a model's two ends when it
+// is trained: the gated MLP block and its gradient, the gradient of the fused
+// residual add + RMSNorm.  Argument checks, workspace layout, launch.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "../../include/gbfuse.h"
+#include "internal.h"
+
+namespace gbf {
+
+namespace {
+
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int kMaxSms = 152;   // of the device this library is built for
+constexpr int kMlpPairs = 76;  // CTA pairs that run at once
+constexpr int kMlpRows = 256;  // of a pair's tile
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+gbf_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? GBF_OK : GBF_ERR_CUDA; }
+int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Row tiles per unit of work: two that share a column tile, or a lone one where
+// there is no second.
+int mlp_streams(int64_t M) { return M > kMlpRows ? 2 : 1; }
+
+// Parts of K of the product for dx, each with an fp32 buffer of its own: 16 at
+// most and none shorter than 8 K blocks.  With one row tile as many as give one
+// round of units over the pairs.  Else: none longer than half of what a pair has
+// to do in the launch, the weights' gradients among it.
+int mlp_dx_splits(int64_t M, int64_t D, int64_t F) {
+  const int64_t k = 2 * ceil_div64(F, kBK), d = ceil_div64(D, 256);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
+  if (mlp_streams(M) == 1)
+    return static_cast<int>(std::max<int64_t>(1, std::min(most, kMlpPairs / d)));
+  const int64_t all = ceil_div64(M, 512) * d * k +
+                      2 * ceil_div64(F, 512) * d * ceil_div64(M, kBK);
+  const int64_t half = std::max<int64_t>(1, all / kMlpPairs / 2);
+  return static_cast<int>(std::min(most, ceil_div64(k, half)));
+}
+
+int64_t mlp_m_pad(int64_t M) { return ceil_div64(M, 512) * 512; }
+
+struct MlpGradWs {
+  __nv_bfloat16 *dg, *du;
+  float* parts;
+};
+size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, MlpGradWs* w) {
+  uint8_t* p = static_cast<uint8_t*>(base);
+  const size_t act = align256(static_cast<size_t>(M) * F * 2);
+  const int splits = mlp_dx_splits(M, D, F);
+  const size_t parts =
+      splits > 1 ? align256(static_cast<size_t>(splits) * mlp_m_pad(M) * D * 4) : 0;
+  w->dg = reinterpret_cast<__nv_bfloat16*>(p);
+  w->du = p ? reinterpret_cast<__nv_bfloat16*>(p + act) : nullptr;
+  w->parts = p ? reinterpret_cast<float*>(p + 2 * act) : nullptr;
+  return 2 * act + parts;
+}
+
+// Sizes that the kernels' 32-bit coordinates and unit counts hold.
+bool mlp_sizes_held(int64_t M, int64_t D, int64_t F) {
+  if (D < 8 || F < 8 || D % 8 != 0 || F % 8 != 0 || M > (int64_t(1) << 24) ||
+      D > (int64_t(1) << 20) || F > (int64_t(1) << 20))
+    return false;
+  const int64_t m = ceil_div64(M, 256), d = ceil_div64(D, 256), f = ceil_div64(F, 128);
+  return m * f <= kMaxInt / 4 && m * d * 16 <= kMaxInt / 4 && d * f <= kMaxInt / 4;
+}
+
+gbf_status_t check_mlp(int64_t M, int64_t D, int64_t F, int act) {
+  if (M < 0 || D < 0 || F < 0 || act < GBF_ACT_IDENTITY || act > GBF_ACT_GELU_TANH)
+    return GBF_ERR_INVALID_ARG;
+  return mlp_sizes_held(M, D, F) ? GBF_OK : GBF_ERR_UNSUPPORTED_SHAPE;
+}
+
+gbf_status_t check_all(std::initializer_list<const void*> required,
+                       std::initializer_list<const void*> optional) {
+  for (const void* p : required)
+    if (!p) return GBF_ERR_INVALID_ARG;
+  for (const void* p : required)
+    if (!aligned(p, 16)) return GBF_ERR_MISALIGNED;
+  for (const void* p : optional)
+    if (!aligned(p, 16)) return GBF_ERR_MISALIGNED;
+  return GBF_OK;
+}
+
+// K-major operand (rows of `inner` values along K): 64 x 128 boxes.
+bool map_k(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, inner * 2, kBK, 128,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Operand with one row per k: 64 x 64 boxes.
+bool map_mn(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, inner * 2, 64, kBK,
+                     CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool map_out(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, bool wide) {
+  return wide ? lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, inner * 2, 64, 32,
+                            CU_TENSOR_MAP_SWIZZLE_128B)
+              : lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, inner, outer, inner * 2, 32, 32,
+                            CU_TENSOR_MAP_SWIZZLE_64B);
+}
+bool map_parts(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
+  return lib_tmap_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, inner, outer, inner * 4, 16, 32,
+                     CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+void set_job(MbJob* j, int mode, int64_t rows, int64_t cols, int64_t k, bool a_mn, bool b_mn) {
+  j->mode = mode;
+  j->rows = static_cast<int>(rows);
+  j->cols = static_cast<int>(cols);
+  j->a_mn = a_mn;
+  j->b_mn = b_mn;
+  j->num_kb = j->kb_first = static_cast<int>(ceil_div64(k, kBK));
+  j->splits = 1;
+  j->m_pad = 0;
+}
+
+// The gradient of a weight: out [rows][cols] = a^T b over the M rows of a and b.
+bool set_dw(MbJob* j, const void* a, const void* b, const void* out, int64_t rows, int64_t cols,
+            int64_t M) {
+  set_job(j, kMbStore, rows, cols, M, true, true);
+  return map_mn(&j->a[0], a, rows, M) && map_mn(&j->b[0], b, cols, M) &&
+         map_out(&j->o[0], out, cols, rows, mlp_streams(M) == 1);
+}
+
+gbf_status_t run_launch(MbLaunch* l, int64_t M, const DeviceInfo& dev, unsigned* err,
+                        cudaStream_t s) {
+  const int streams = mlp_streams(M);
+  plan_mlp_launch(l, streams, dev.pairs);
+  if (l->longs + l->shorts == 0) return GBF_OK;
+  return cuda_status(launch_mlp_train(*l, streams, lib_ctl(err, 2 * l->pairs), s));
+}
+
+}  // namespace
+
+size_t blocks_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
+  if (op == GBF_OP_MLP_GRAD) {
+    if (!mlp_sizes_held(M, N, K)) return 0;  // as the entry point refuses them
+    MlpGradWs w;
+    return mlp_grad_sections(nullptr, M, N, K, &w);
+  }
+  if (op == GBF_OP_ADD_RMSNORM_GRAD) {
+    if (N % 8 != 0 || N > kRmsMaxN || M > kMaxInt) return 0;
+    return align256(static_cast<size_t>(rms_grad_ctas(M, static_cast<int>(N), kMaxSms)) * N * 4);
+  }
+  return 0;
+}
+
+}  // namespace gbf
+
+using namespace gbf;
+
+extern "C" {
+
+gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
+                           const void* w_down, const void* residual, void* out, void* g, void* u,
+                           void* h, int64_t M, int64_t D, int64_t F, int act,
+                           gbf_stream_t stream) {
+  gbf_status_t st = check_mlp(M, D, F, act);
+  if (st != GBF_OK) return st;
+  if (M == 0) {  // arrays without elements may be null
+    if ((st = check_all({w_gate, w_up, w_down}, {x, residual, out, g, u, h})) != GBF_OK) return st;
+  } else {
+    st = check_all({x, w_gate, w_up, w_down, out, g, u, h}, {residual});
+    if (st != GBF_OK) return st;
+  }
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  if (M == 0) return GBF_OK;
+  MbLaunch l{};
+  MbJob& j = l.job[1];
+  set_job(&j, kMbGlu, M, F, D, false, false);
+  l.act = act;
+  if (!map_k(&j.a[0], x, D, M) || !map_k(&j.b[0], w_gate, D, F) || !map_k(&j.b[1], w_up, D, F) ||
+      !map_out(&j.o[0], h, F, M, false) || !map_out(&j.o[1], g, F, M, false) ||
+      !map_out(&j.o[2], u, F, M, false))
+    return GBF_ERR_CUDA;
+  if ((st = run_launch(&l, M, *dev, err, reinterpret_cast<cudaStream_t>(stream))) != GBF_OK)
+    return st;
+  return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
+                       GBF_ACT_IDENTITY, nullptr, 0, stream);
+}
+
+gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const void* u,
+                          const void* h, const void* w_gate, const void* w_up, const void* w_down,
+                          void* dx, void* dw_gate, void* dw_up, void* dw_down, int64_t M,
+                          int64_t D, int64_t F, int act, void* workspace, size_t workspace_bytes,
+                          gbf_stream_t stream) {
+  gbf_status_t st = check_mlp(M, D, F, act);
+  if (st != GBF_OK) return st;
+  if (M == 0) {
+    st = check_all({w_gate, w_up, w_down},
+                   {dout, x, g, u, h, dx, dw_gate, dw_up, dw_down, workspace});
+  } else {
+    if (!dx && !dw_gate && !dw_up && !dw_down) return GBF_ERR_INVALID_ARG;
+    st = check_all({dout, x, g, u, h, w_gate, w_up, w_down},
+                   {dx, dw_gate, dw_up, dw_down, workspace});
+  }
+  if (st != GBF_OK) return st;
+  MlpGradWs ws;
+  const size_t need = mlp_grad_sections(workspace, M, D, F, &ws);
+  if (need && (!workspace || workspace_bytes < need)) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) {  // no rows: empty sums
+    for (void* dw : {dw_gate, dw_up, dw_down})
+      if (dw && (st = cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(D) * F * 2, s))) !=
+                    GBF_OK)
+        return st;
+    return GBF_OK;
+  }
+  const bool hidden = dx || dw_gate || dw_up;
+  MbLaunch first{}, then{};
+  first.act = act;
+  if (hidden) {
+    MbJob& j = first.job[1];
+    set_job(&j, kMbGluGrad, M, F, D, false, true);
+    first.g = static_cast<const __nv_bfloat16*>(g);
+    first.u = static_cast<const __nv_bfloat16*>(u);
+    if (!map_k(&j.a[0], dout, D, M) || !map_mn(&j.b[0], w_down, F, D) ||
+        !map_out(&j.o[0], ws.dg, F, M, false) || !map_out(&j.o[1], ws.du, F, M, false))
+      return GBF_ERR_CUDA;
+  }
+  if (dw_down && !set_dw(&first.job[2], dout, h, dw_down, D, F, M)) return GBF_ERR_CUDA;
+  if ((st = run_launch(&first, M, *dev, err, s)) != GBF_OK || !hidden) return st;
+  const int splits = mlp_dx_splits(M, D, F);
+  if (dx) {
+    MbJob& j = then.job[0];
+    set_job(&j, kMbStore, M, D, F, false, true);
+    j.num_kb = 2 * j.kb_first;
+    j.splits = splits;
+    j.m_pad = static_cast<int>(mlp_m_pad(M));
+    if (!map_k(&j.a[0], ws.dg, F, M) || !map_k(&j.a[1], ws.du, F, M) ||
+        !map_mn(&j.b[0], w_gate, D, F) || !map_mn(&j.b[1], w_up, D, F) ||
+        !(splits > 1 ? map_parts(&j.o[0], ws.parts, D, splits * mlp_m_pad(M))
+                     : map_out(&j.o[0], dx, D, M, mlp_streams(M) == 1)))
+      return GBF_ERR_CUDA;
+  }
+  if ((dw_gate && !set_dw(&then.job[1], ws.dg, x, dw_gate, F, D, M)) ||
+      (dw_up && !set_dw(&then.job[2], ws.du, x, dw_up, F, D, M)))
+    return GBF_ERR_CUDA;
+  if ((st = run_launch(&then, M, *dev, err, s)) != GBF_OK) return st;
+  if (!dx || splits == 1) return GBF_OK;
+  return cuda_status(launch_mlp_sum(ws.parts, static_cast<__nv_bfloat16*>(dx), M * D,
+                                    mlp_m_pad(M) * D, splits, dev->sms, s));
+}
+
+gbf_status_t gbf_add_rmsnorm_grad(const void* dnorm, const void* dresid, const void* resid,
+                                  const void* weight, void* dr, void* dweight, int64_t M,
+                                  int64_t N, float eps, void* workspace, size_t workspace_bytes,
+                                  gbf_stream_t stream) {
+  if (M < 0 || N < 0 || !(eps >= 0.0f)) return GBF_ERR_INVALID_ARG;
+  gbf_status_t st =
+      M == 0 || N == 0
+          ? check_all({}, {dnorm, dresid, resid, weight, dr, dweight, workspace})
+          : check_all({dnorm, resid, weight, dr}, {dresid, dweight, workspace});
+  if (st != GBF_OK) return st;
+  if (N % 8 != 0 || N > kRmsMaxN || M > kMaxInt) return GBF_ERR_UNSUPPORTED_SHAPE;
+  const size_t need = dweight ? gbf_workspace_size(GBF_OP_ADD_RMSNORM_GRAD, M, N, 0, 1) : 0;
+  if (need && (!workspace || workspace_bytes < need)) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (N == 0) return GBF_OK;
+  if (M == 0)
+    return dweight ? cuda_status(cudaMemsetAsync(dweight, 0, static_cast<size_t>(N) * 2, s)) : GBF_OK;
+  return cuda_status(launch_add_rmsnorm_grad(
+      static_cast<const __nv_bfloat16*>(dnorm), static_cast<const __nv_bfloat16*>(dresid),
+      static_cast<const __nv_bfloat16*>(resid), static_cast<const __nv_bfloat16*>(weight),
+      static_cast<__nv_bfloat16*>(dr), static_cast<__nv_bfloat16*>(dweight), M,
+      static_cast<int>(N), eps, static_cast<float*>(workspace), std::min(dev->sms, kMaxSms), s));
+}
+
+}  // extern "C"

@@ -256,6 +256,44 @@ cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
 cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream);
 cudaError_t launch_ce_dx(const CeDxOut& p, int M, int sms, cudaStream_t stream);
 
+// Products of a gated MLP block that is trained, and of its gradient
+// (mlp_train.cu): up to three per launch, none of which reads what another writes.
+enum MbMode { kMbNone = 0, kMbStore = 1, kMbGlu = 2, kMbGluGrad = 3 };
+struct MbJob {
+  // [1]: of a second pair of operands, whose K blocks follow the first's; kMbGlu: b[1] Wu
+  CUtensorMap a[2], b[2];
+  CUtensorMap o[3];  // the result; kMbGlu: h, g, u; kMbGluGrad: dg, du
+  int mode;
+  int rows, cols;    // of the result
+  int a_mn, b_mn;    // an operand is read along its columns: it holds one row per k
+  int num_kb;        // 64-wide K blocks in all
+  int kb_first;      // of the first pair of operands (num_kb: there is no second)
+  int splits;        // parts of K, each with its own fp32 rows in o[0] (job 0 only)
+  int m_pad;         // rows between them
+  int m_units, n_tiles, units;  // by plan_mlp_launch
+};
+constexpr int kMbJobs = 3;
+struct MbLaunch {
+  MbJob job[kMbJobs];  // job 0: the one with the longest units, if any
+  const __nv_bfloat16 *g, *u;  // kMbGluGrad
+  int act;
+  int longs, extra, skip, shorts, pairs;  // by plan_mlp_launch
+};
+// The launch's units dealt to CTA pairs, npairs at most (pairs: how many).
+void plan_mlp_launch(MbLaunch* l, int streams, int npairs);
+cudaError_t launch_mlp_train(const MbLaunch& launch, int streams, const KernelCtl& ctl,
+                             cudaStream_t stream);
+cudaError_t launch_mlp_sum(const float* parts, __nv_bfloat16* dx, int64_t n, int64_t stride,
+                           int splits, int sms, cudaStream_t stream);
+
+// Gradient of add_rmsnorm (rmsnorm_grad.cu).  dresid, dweight: may be null.
+// partial: [rms_grad_ctas(N, sms)][N] fp32 where dweight is wanted.
+int rms_grad_ctas(int64_t M, int N, int sms);
+cudaError_t launch_add_rmsnorm_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
+                                    const __nv_bfloat16* r, const __nv_bfloat16* weight,
+                                    __nv_bfloat16* dr, __nv_bfloat16* dweight, int64_t M, int N,
+                                    float eps, float* partial, int sms, cudaStream_t stream);
+
 // ---- shared with the other entry-point files (api.cu) ---------------------------
 // The current device and the address of its error word (a GBF_* status).
 int lib_device(const DeviceInfo** info, unsigned** err);
@@ -265,8 +303,9 @@ bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint6
                  CUtensorMapSwizzle swz);
 // Launch control of a grid of `ctas`.
 KernelCtl lib_ctl(unsigned* err, int64_t ctas);
-// gbf_workspace_size() of the operators in heads.cu.
+// gbf_workspace_size() of the operators in heads.cu and blocks.cu.
 size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K);
+size_t blocks_workspace_size(int op, int64_t M, int64_t N, int64_t K);
 
 // Tile geometry shared by the planner and the kernels.
 constexpr int kBM = 128;        // MMA M: rows of TMEM / output tile height

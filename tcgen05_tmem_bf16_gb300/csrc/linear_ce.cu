@@ -50,6 +50,7 @@
 #include "common.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
+#include "pair_end.cuh"
 #include "ptx.cuh"
 
 namespace gbf {
@@ -180,91 +181,8 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   return true;
 }
 
-// One warp's 32 rows x 32 columns of fp32 to the map's tensor, stored or added
-// there by the TMA engine, through the warp's two staging buffers (16 columns
-// each).  Every element is added to by one warp of one launch, so the sums do
-// not depend on timing.
-__device__ __forceinline__ void put_chunk_f32(uint8_t* bufs, int buf_bytes, int& flip,
-                                              const uint32_t (&v)[32], const CUtensorMap* map,
-                                              int row0, int col0, int n, bool some, bool add) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint8_t* buf = bufs + flip * buf_bytes;
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-    uint32_t w[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = v[16 * h + j];
-    stage_row32(buf, lane, w);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (some && col0 + 16 * h < n) {
-        if (add) tma_add_2d(map, buf, col0 + 16 * h, row0);
-        else tma_store_2d(map, buf, col0 + 16 * h, row0, policy_evict_last());
-      }
-      bulk_commit();
-    }
-    flip ^= 1;
-  }
-}
-
-// One warp's 32 rows x 32 bf16 columns through a staging buffer to the map's
-// tensor, as store_chunk32 does; WIDE: two calls with c even and odd fill rows
-// of 128 bytes (128-byte swizzle), which the second one stores.
-template <bool WIDE>
-__device__ __forceinline__ void put_chunk(uint8_t* bufs, int buf_bytes, int& flip, int c,
-                                          const uint32_t (&w)[16], const CUtensorMap* map,
-                                          int row0, int col0, int rows, int n, uint64_t pol) {
-  const int lane = threadIdx.x & 31;
-  uint8_t* buf = bufs + flip * buf_bytes;
-  const bool first = !WIDE || (c & 1) == 0, last = !WIDE || (c & 1) == 1;
-  if (first) {
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-  }
-  if (WIDE) {
-    const uint32_t base = smem_u32(buf) + static_cast<uint32_t>(lane) * 128u;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint32_t at = static_cast<uint32_t>((4 * (c & 1) + u) ^ (lane & 7)) << 4;
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(base + at), "r"(w[4 * u]),
-                   "r"(w[4 * u + 1]), "r"(w[4 * u + 2]), "r"(w[4 * u + 3])
-                   : "memory");
-    }
-  } else {
-    stage_row32(buf, lane, w);
-  }
-  if (last) {
-    const int at = WIDE ? col0 - 32 : col0;
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      if (row0 < rows && at < n) tma_store_2d(map, buf, at, row0, pol);
-      bulk_commit();
-    }
-    flip ^= 1;
-  }
-}
-
-// How a warp of the ending gives an accumulator back to the issuers.
-struct CeFree {
-  uint64_t* mine;
-  uint32_t lead;  // the even CTA's, as the odd one sees it
-  bool leader;
-  __device__ __forceinline__ void operator()() const {
-    tc_fence_before();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      if (leader) mbar_arrive(mine);
-      else mbar_arrive_cluster(lead);
-    }
-  }
-};
-
 // A warp's 128 columns of an accumulator, which is then given back.
-__device__ __forceinline__ void ce_read(uint32_t tb, const CeFree& release,
+__device__ __forceinline__ void ce_read(uint32_t tb, const AccFree& release,
                                         uint32_t (&v)[4][32]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) tmem_ld32(tb + 32 * c, v[c]);
@@ -272,7 +190,7 @@ __device__ __forceinline__ void ce_read(uint32_t tb, const CeFree& release,
   release();
 }
 // The same, added to v.
-__device__ __forceinline__ void ce_add(uint32_t tb, const CeFree& release,
+__device__ __forceinline__ void ce_add(uint32_t tb, const AccFree& release,
                                        uint32_t (&v)[4][32]) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
@@ -383,7 +301,7 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
 // memory while the ending works on the present ones; the accumulator is free
 // once the last have arrived.
 template <int MODE, int FORM>
-__device__ __forceinline__ void ce_tile(uint32_t tb, const CeFree& release, const CeTileArgs& t,
+__device__ __forceinline__ void ce_tile(uint32_t tb, const AccFree& release, const CeTileArgs& t,
                                         const CeEnd& e, int& flip, float& m, float& sum) {
   uint32_t va[32], vb[32];
   tmem_ld32(tb, va);
@@ -653,8 +571,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       auto columns = [&](int acc) -> uint32_t {
         return tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
       };
-      auto free_of = [&](int acc) -> CeFree {
-        return CeFree{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0, leader};
+      auto free_of = [&](int acc) -> AccFree {
+        return AccFree{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0, leader};
       };
 #pragma unroll 1
       for (int i = 0; i < STREAMS; ++i) {
@@ -674,7 +592,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         ok = acc >= 0;
         if (!ok) break;
         const uint32_t tb = columns(acc);
-        const CeFree release = free_of(acc);
+        const AccFree release = free_of(acc);
         float m = -INFINITY, sum = 0.0f;  // kLse
         if constexpr (FORM == kCeChains) {
           uint32_t v[4][32];  // the sums over the chains

@@ -1,0 +1,562 @@
+// mlp_train.cu -- the products of a gated MLP block that is trained, and of its
+// gradient, each with its ending.
+//
+//   g = x Wg^T, u = x Wu^T, h = act(g) u               (kMbGlu: all three stored)
+//   dh = dout Wd;  dg = dh u act'(g), du = dh act(g)    (kMbGluGrad)
+//   dx = dg Wg + du Wu                                  (one product over both halves of K)
+//   dWg = dg^T x, dWu = du^T x, dWd = dout^T h
+//
+// One kernel does them all: the CTA-pair main loop of gemm_pair.cu (256 x 256
+// tiles on two SMs, tcgen05.mma.cta_group::2, TMA-fed), working through a list of
+// up to three products per launch that do not depend on one another.  dh never
+// reaches memory: its tile ends as dg and du.  Every operand is read in the layout
+// in which it lies, along rows or columns, so nothing is transposed in memory.
+//
+// The gradient takes two launches: {dh, dWd}, then {dx, dWg, dWu}.  Products of
+// one launch fill each other's last round of units, and where rows are few (M <=
+// 256) the reading of the weights for dh overlaps the writing of dWd.
+//
+// Bound by the tensor pipe above some 500 rows, by the weights' bytes below.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "common.cuh"
+#include "epilogue.cuh"
+#include "internal.h"
+#include "pair_end.cuh"
+#include "ptx.cuh"
+
+namespace gbf {
+
+namespace {
+
+constexpr int kMbThreads = 384;          // warps 0-3 roles, 4-11 ending
+constexpr int kMbTile = 256;             // rows and columns of a pair's tile
+constexpr int kMbABytes = kBM * kBK * 2;  // 16 KB: this CTA's 128 rows of A
+constexpr int kMbBBytes = 128 * kBK * 2;  // 16 KB: this CTA's half of B
+constexpr int kMbGroup = 8;              // raster group (units of rows)
+
+// STREAMS row tiles per unit of work, as in linear_ce.cu: two that share each B
+// tile, or a lone one (up to 256 rows), whose ending stores rows of 128 bytes.
+template <int STREAMS>
+struct MbCfg {
+  static constexpr int kStageBytes = STREAMS * kMbABytes + kMbBBytes;
+  static constexpr int kStages = STREAMS == 2 ? 4 : 5;
+  static constexpr int kBarBytes = 1024;
+  static constexpr bool kWide = STREAMS == 1;
+  static constexpr int kBufBytes = kWide ? 32 * 128 : 32 * 64;
+  static constexpr int kStagingBytes = 8 * 2 * kBufBytes;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+// A unit of work: STREAMS row tiles x one column tile x a range of K blocks of
+// one of the launch's products.
+struct MbUnit {
+  int job, mp, nb, split, kb0, kb1;
+};
+
+// The n-th unit of a pair; false after its last.  The units of job 0 are long;
+// they are dealt out first, one per pair and round, and the pairs that got one more
+// than the others sit out `skip` rounds of the short ones.
+__device__ __forceinline__ bool mb_unit(const MbLaunch& a, int pair, int npairs, int n, MbUnit& u) {
+  const int mine = a.longs / npairs + (pair < a.extra ? 1 : 0);
+  int t;
+  if (n < mine) {
+    t = n * npairs + pair;
+    u.job = 0;
+  } else {
+    const int round = n - mine + (pair < a.extra ? a.skip : 0);
+    if (round < a.skip)
+      t = round * (npairs - a.extra) + pair - a.extra;
+    else
+      t = a.skip * (npairs - a.extra) + (round - a.skip) * npairs + pair;
+    if (t >= a.shorts) return false;
+    u.job = 1;
+    if (t >= a.job[1].units) {
+      t -= a.job[1].units;
+      u.job = 2;
+    }
+  }
+  const MbJob& j = a.job[u.job];
+  u.split = 0;
+  u.kb0 = 0;
+  u.kb1 = j.num_kb;
+  if (u.job == 0 && j.splits > 1) {
+    const unsigned tiles = j.m_units * j.n_tiles;
+    u.split = static_cast<unsigned>(t) / tiles;
+    t -= u.split * tiles;
+    u.kb0 = static_cast<unsigned>(u.split * j.num_kb) / static_cast<unsigned>(j.splits);
+    u.kb1 = static_cast<unsigned>((u.split + 1) * j.num_kb) / static_cast<unsigned>(j.splits);
+  }
+  tile_coords(t, j.m_units, j.n_tiles, u.mp, u.nb, kMbGroup);
+  return true;
+}
+
+// Activation and derivative, as act_apply computes the former.
+template <int ACT>
+__device__ __forceinline__ void act_both(float v, float& y, float& dy) {
+  if constexpr (ACT == kActRelu) {
+    y = fmaxf(v, 0.0f);
+    dy = v > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == kActSilu) {
+    const float s = __fdividef(1.0f, 1.0f + __expf(-v));
+    y = v * s;
+    dy = s * fmaf(v, 1.0f - s, 1.0f);
+  } else if constexpr (ACT == kActGeluTanh) {
+    // v s(2 z), z = c (v + k v^3):  s + v s (1 - s) 2 c (1 + 3 k v^2)
+    constexpr float c = 0.7978845608028654f, k = 0.044715f;
+    const float z = c * fmaf(k * v, v * v, v);
+    const float s = __fdividef(1.0f, 1.0f + __expf(-2.0f * z));
+    y = v * s;
+    const float t = s * (1.0f - s);  // 0 where v^2 may overflow
+    dy = t == 0.0f ? s : fmaf(v * t, 2.0f * c * fmaf(3.0f * k * v, v, 1.0f), s);
+  } else {
+    y = v;
+    dy = 1.0f;
+  }
+}
+
+// 32 columns of a row of bf16; zeros outside.
+__device__ __forceinline__ void load_row32(uint4 (&d)[4], const __nv_bfloat16* p, int64_t row,
+                                           int col, int rows, int cols, uint64_t pol) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    d[v] = row < rows && col + 8 * v < cols ? ld_stream_u4(p + row * cols + col + 8 * v, pol)
+                                            : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int ACT>
+__device__ __forceinline__ void glu_pack(const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                         uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    w[k] = pack_bf16x2(
+        act_apply<ACT>(__uint_as_float(g[2 * k])) * __uint_as_float(u[2 * k]),
+        act_apply<ACT>(__uint_as_float(g[2 * k + 1])) * __uint_as_float(u[2 * k + 1]));
+}
+
+template <int ACT>
+__device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[32], const uint4 (&g4)[4],
+                                              const uint4 (&u4)[4], uint32_t (&dg)[16],
+                                              uint32_t (&du)[16]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    float g[8], u[8], a[8], b[8];
+    unpack8(g4[v], g);
+    unpack8(u4[v], u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float y, dy;
+      act_both<ACT>(g[i], y, dy);
+      const float d = __uint_as_float(dh[8 * v + i]);
+      a[i] = d * u[i] * dy;
+      b[i] = d * y;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dg[4 * v + i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
+      du[4 * v + i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
+    }
+  }
+}
+
+template <int STREAMS>
+__global__ void __launch_bounds__(kMbThreads, 1)
+    mlp_train_kernel(const __grid_constant__ MbLaunch a, const KernelCtl kctl) {
+  using Cfg = MbCfg<STREAMS>;
+  constexpr int kStages = Cfg::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint8_t* stages = smem;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * Cfg::kStageBytes);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* done = tempty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
+  uint8_t* staging = smem + kStages * Cfg::kStageBytes + Cfg::kBarBytes;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();  // 0: the even CTA, which issues the MMAs
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int npairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], STREAMS);  // every issuer
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
+    }
+    mbar_init(done, STREAMS);
+    *abort_flag = 0;
+    fence_mbar_init();
+    for (int i = 0; i < kMbJobs; ++i) {
+      if (a.job[i].mode == kMbNone) continue;
+      tma_prefetch_desc(&a.job[i].a[0]);
+      tma_prefetch_desc(&a.job[i].b[0]);
+      tma_prefetch_desc(&a.job[i].o[0]);
+    }
+  }
+  if (warp == 2) {
+    tmem_alloc_pair(tmem_holder, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const WaitCtl ctl{kctl.err, kctl.timeout_ns, abort_flag, prof_slots(kctl.prof)};
+  const long long t_start = clock64();
+  if (threadIdx.x == 0) griddep_launch_dependents();
+  griddep_wait();  // operands may be the previous kernel's results
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      uint32_t fills[kStages];
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) fills[i] = 0;
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      MbUnit u;
+      for (int n = 0; ok && mb_unit(a, pair, npairs, n, u); ++n) {
+        const MbJob& j = a.job[u.job];
+        const bool glu = j.mode == kMbGlu;  // the even CTA's half of B is Wg's, the odd one's Wu's
+        const int n0 = glu ? u.nb * 128 : u.nb * kMbTile + static_cast<int>(rank) * 128;
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!wait_bar(&empty[s], ph ^ 1, ctl, kSiteProducerEmpty)) {
+            ok = false;
+            break;
+          }
+          const int second = kb >= j.kb_first ? 1 : 0;  // K blocks of the second pair of operands
+          const int k0 = (kb - second * j.kb_first) * kBK;
+          const CUtensorMap* ma = &j.a[second];
+          const CUtensorMap* mb = &j.b[glu ? static_cast<int>(rank) : second];
+          uint8_t* sa = stages + s * Cfg::kStageBytes;
+          uint8_t* sb = sa + STREAMS * kMbABytes;
+          const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[s], 2 * Cfg::kStageBytes);
+#pragma unroll
+          for (int i = 0; i < STREAMS; ++i) {
+            const int m0 = (STREAMS * u.mp + i) * kMbTile + static_cast<int>(rank) * kBM;
+            if (j.a_mn) {
+              tma_load_2d_pair(sa + i * kMbABytes, ma, bar, m0, k0);
+              tma_load_2d_pair(sa + i * kMbABytes + 8192, ma, bar, m0 + 64, k0);
+            } else {
+              tma_load_2d_pair(sa + i * kMbABytes, ma, bar, k0, m0);
+            }
+          }
+          if (j.b_mn) {
+            tma_load_2d_pair(sb, mb, bar, n0, k0);
+            tma_load_2d_pair(sb + 8192, mb, bar, n0 + 64, k0);
+          } else {
+            tma_load_2d_pair(sb, mb, bar, k0, n0);
+          }
+          fills[s]++;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (ok) {
+        for (int i = 0; i < kStages; ++i)
+          if (fills[i]) wait_bar(&empty[i], (fills[i] - 1) & 1, ctl, kSiteDrain, false);
+      } else {
+        const uint64_t t0 = globaltimer_ns();  // let the copies in flight land (bounded)
+        while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------------ MMA issuers (even CTA)
+    // Two row tiles per unit: warp 1 issues the first's, warp 2 the second's, each
+    // into its own accumulator.  One row tile: warp 1 alone, accumulators in turn.
+    const int st = warp - 1;
+    if (lane == 0 && leader && st < STREAMS) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      MbUnit u;
+      for (int n = 0; ok && mb_unit(a, pair, npairs, n, u); ++n) {
+        const MbJob& j = a.job[u.job];
+        const uint32_t idesc = idesc_bf16(kMbTile, 256, j.a_mn != 0, j.b_mn != 0);
+        const int acc = STREAMS == 2 ? st : n & 1;
+        const int use = STREAMS == 2 ? n : n >> 1;
+        if (!wait_bar(&tempty[acc], (use & 1) ^ 1, ctl, kSiteMmaAccEmpty)) break;
+        tc_fence_after();
+        for (int kb = u.kb0; kb < u.kb1; ++kb) {
+          if (!wait_bar(&full[s], ph, ctl, kSiteMmaFull)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t s0 = smem_u32(stages + s * Cfg::kStageBytes);
+          const uint32_t a0 = s0 + st * kMbABytes;
+          const uint32_t b0 = s0 + STREAMS * kMbABytes;
+#pragma unroll
+          for (int k = 0; k < kBK / 16; ++k) {
+            const uint64_t ad = j.a_mn ? sdesc_sw128(a0 + k * 2048, 8192, 1024)
+                                       : sdesc_sw128(a0 + k * 32, 16, 1024);
+            const uint64_t bd = j.b_mn ? sdesc_sw128(b0 + k * 2048, 8192, 1024)
+                                       : sdesc_sw128(b0 + k * 32, 16, 1024);
+            mma_ss_pair(tmem_base + acc * 256, ad, bd, idesc, (kb != u.kb0 || k != 0) ? 1u : 0u);
+          }
+          mma_commit_pair(&empty[s], 0x3);
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (!(kctl.inject && n == 0)) mma_commit_pair(&tfull[acc], 0x3);
+      }
+      mma_commit_pair(done, 1);
+      wait_bar(done, 0, ctl, kSiteDrain, false);
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ ending (both CTAs)
+    const int q = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const uint64_t first = l2_evict_first_policy();
+    const uint32_t lead_empty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t lead_empty1 = mapa_shared(smem_u32(&tempty[1]), 0);
+    uint8_t* bufs = staging + (warp - 4) * 2 * Cfg::kBufBytes;
+    int flip = 0;
+    bool ok = true;
+    MbUnit u;
+    for (int n = 0; ok && mb_unit(a, pair, npairs, n, u); ++n) {
+      const MbJob& j = a.job[u.job];
+#pragma unroll 1
+      for (int i = 0; i < STREAMS; ++i) {
+        const int acc = STREAMS == 2 ? i : n & 1;
+        const int use = STREAMS == 2 ? n : n >> 1;
+        const int row0 = (STREAMS * u.mp + i) * kMbTile + static_cast<int>(rank) * kBM + q * 32;
+        const uint32_t tb = tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
+        const AccFree release{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0,
+                              leader};
+        const int col0 = j.mode == kMbGlu ? u.nb * 128 + half * 64 : u.nb * kMbTile + half * 128;
+        uint4 g4[4], u4[4];
+        if (j.mode == kMbGluGrad) {
+          // the first 32 columns of g and u on their way, the others into L2
+          if (row0 + lane < j.rows) {
+            const int64_t at = static_cast<int64_t>(row0 + lane) * j.cols;
+            if (col0 + 64 < j.cols) {
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.g + at + col0 + 64));
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.u + at + col0 + 64));
+            }
+          }
+          load_row32(g4, a.g, row0 + lane, col0, j.rows, j.cols, first);
+          load_row32(u4, a.u, row0 + lane, col0, j.rows, j.cols, first);
+        }
+        ok = wait_bar(&tfull[acc], use & 1, ctl, kSiteEpiAccFull);
+        if (!ok) break;
+        tc_fence_after();
+        if (j.mode == kMbGlu) {
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t g[32], up[32], w[16];
+            tmem_ld32(tb + half * 64 + c * 32, g);
+            tmem_ld32(tb + 128 + half * 64 + c * 32, up);
+            tmem_wait_ld();
+            if (c == 1) release();
+            const int col = col0 + c * 32;
+            switch (a.act) {
+              case kActRelu: glu_pack<kActRelu>(g, up, w); break;
+              case kActSilu: glu_pack<kActSilu>(g, up, w); break;
+              case kActGeluTanh: glu_pack<kActGeluTanh>(g, up, w); break;
+              default: glu_pack<kActIdentity>(g, up, w); break;
+            }
+            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[0], row0, col, j.rows, j.cols,
+                             first);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1]));
+            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[1], row0, col, j.rows, j.cols,
+                             first);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[k] = pack_bf16x2(__uint_as_float(up[2 * k]), __uint_as_float(up[2 * k + 1]));
+            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[2], row0, col, j.rows, j.cols,
+                             first);
+          }
+        } else if (j.mode == kMbGluGrad) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32], dg[16], du[16];
+            tmem_ld32(tb + half * 128 + c * 32, v);
+            tmem_wait_ld();
+            if (c == 3) release();
+            switch (a.act) {
+              case kActRelu: glu_grad_pack<kActRelu>(v, g4, u4, dg, du); break;
+              case kActSilu: glu_grad_pack<kActSilu>(v, g4, u4, dg, du); break;
+              case kActGeluTanh: glu_grad_pack<kActGeluTanh>(v, g4, u4, dg, du); break;
+              default: glu_grad_pack<kActIdentity>(v, g4, u4, dg, du); break;
+            }
+            const int col = col0 + c * 32;
+            if (c < 3) {
+              load_row32(g4, a.g, row0 + lane, col + 32, j.rows, j.cols, first);
+              load_row32(u4, a.u, row0 + lane, col + 32, j.rows, j.cols, first);
+            }
+            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, dg, &j.o[0], row0, col, j.rows, j.cols,
+                             policy_evict_last());
+            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, du, &j.o[1], row0, col, j.rows, j.cols,
+                             policy_evict_last());
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t v[32];
+            tmem_ld32(tb + half * 128 + c * 32, v);
+            tmem_wait_ld();
+            if (c == 3) release();
+            const int col = col0 + c * 32;
+            if (j.splits > 1) {
+              put_chunk_f32(bufs, Cfg::kBufBytes, flip, v, &j.o[0], u.split * j.m_pad + row0, col,
+                            j.cols, row0 < j.rows, false);
+            } else {
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                w[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+              put_chunk<Cfg::kWide>(bufs, Cfg::kBufBytes, flip, c, w, &j.o[0], row0, col, j.rows,
+                                    j.cols, first);
+            }
+          }
+        }
+      }
+    }
+    if (lane == 0) bulk_wait<0>();
+    __syncwarp();
+  }
+
+  if (ctl.prof && threadIdx.x == 0)
+    atomicAdd(&ctl.prof[31], static_cast<unsigned long long>(clock64() - t_start));
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no CTA leaves while its peer may still signal it or read its memory
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// dx from the parts of its K: added in their order in fp32, rounded once.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads)
+    mlp_sum_kernel(const float* __restrict__ parts, __nv_bfloat16* __restrict__ dx, int64_t n,
+                   int64_t stride, int splits) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kSumThreads * 8;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x) * 8; i < n;
+       i += step) {
+    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s) {
+      const float4* src = reinterpret_cast<const float4*>(parts + s * stride + i);
+      const float4 x = __ldcs(src), y = __ldcs(src + 1);
+      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+    }
+    st_u4(dx + i, pack8(f));
+  }
+}
+
+template <int STREAMS>
+cudaError_t run_mb(const MbLaunch& launch, const KernelCtl& ctl, int grid, cudaStream_t stream) {
+  static std::atomic<uint64_t> mask{0};
+  auto kernel = mlp_train_kernel<STREAMS>;
+  constexpr int smem = MbCfg<STREAMS>::kSmem;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(mask.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    mask.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kMbThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, launch, ctl);
+}
+
+}  // namespace
+
+void plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
+  constexpr int kUnitCost = 4;  // a unit's ending, in K blocks of its main loop
+  int64_t blocks = 0;
+  for (int i = 0; i < kMbJobs; ++i) {
+    MbJob& j = l->job[i];
+    j.units = j.m_units = j.n_tiles = 0;
+    if (j.mode == kMbNone) continue;
+    const int bn = j.mode == kMbGlu ? 128 : kMbTile;
+    j.m_units = (j.rows + kMbTile * streams - 1) / (kMbTile * streams);
+    j.n_tiles = (j.cols + bn - 1) / bn;
+    j.units = j.m_units * j.n_tiles * j.splits;
+    if (i > 0) blocks += static_cast<int64_t>(j.units) * (j.num_kb + kUnitCost);
+  }
+  l->longs = l->job[0].units;
+  l->shorts = l->job[1].units + l->job[2].units;
+  l->pairs = std::max(1, std::min(npairs, l->longs + l->shorts));
+  l->extra = l->longs % l->pairs;
+  l->skip = 0;
+  if (l->extra > 0 && l->shorts > 0) {
+    // rounds of short units that one of the long ones takes
+    const int64_t len = l->job[0].num_kb / l->job[0].splits + kUnitCost;
+    const int64_t fit = static_cast<int64_t>(l->shorts) / (l->pairs - l->extra) + 1;
+    l->skip = static_cast<int>(
+        std::min(len * l->shorts / std::max<int64_t>(blocks, 1), fit));
+  }
+}
+
+cudaError_t launch_mlp_train(const MbLaunch& launch, int streams, const KernelCtl& ctl,
+                             cudaStream_t stream) {
+  const int grid = 2 * launch.pairs;
+  return streams == 2 ? run_mb<2>(launch, ctl, grid, stream)
+                      : run_mb<1>(launch, ctl, grid, stream);
+}
+
+cudaError_t launch_mlp_sum(const float* parts, __nv_bfloat16* dx, int64_t n, int64_t stride,
+                           int splits, int sms, cudaStream_t stream) {
+  const int64_t ctas = std::min<int64_t>((n / 8 + kSumThreads - 1) / kSumThreads,
+                                         static_cast<int64_t>(sms) * 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(kSumThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mlp_sum_kernel, parts, dx, n, stride, splits);
+}
+
+}  // namespace gbf

@@ -1,0 +1,200 @@
+// rmsnorm_grad.cu -- the gradient of the fused residual add + RMSNorm.
+//
+// Per row, with s = rsqrt(mean(r^2) + eps) and n = r s w the forward's result:
+//   dr = dresid + s (dn w - r s^2 mean(dn w r))
+//   dweight = sum over the rows of dn r s
+// Both row sums, of r^2 and of dn w r, are taken in one pass over the row, which
+// stays in registers; so r, dn and dresid are read once and dr is written once.
+//
+// HBM-bound.  A CTA takes rows in turn and loads its next row before it reduces
+// the present one.  A thread holds the same columns of every row, so dweight's
+// sums stay in its registers in fp32 and leave the CTA once, as one row of
+// partial sums; a second kernel adds those rows in their order (the same bits on
+// every run).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gbf {
+
+namespace {
+
+// T threads hold R 16-byte vectors each of a row; PER_SM CTAs at a time.
+template <int T, int R, int PER_SM>
+__global__ void __launch_bounds__(T, PER_SM)
+    rmsnorm_grad_kernel(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
+                        const __nv_bfloat16* r, const __nv_bfloat16* __restrict__ w,
+                        __nv_bfloat16* dr, float* __restrict__ partial, int64_t M, int N,
+                        float eps) {
+  __shared__ float2 sums[2][T / 32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const uint64_t pol = l2_evict_first_policy();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 wv[R], vr[R], vn[R], vd[R];
+  float acc[R][8];
+#pragma unroll
+  for (int v = 0; v < R; ++v) {
+    const int col = (threadIdx.x + v * T) * 8;
+    wv[v] = col < N ? ldg_u4(w + col) : zero;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
+  }
+  auto load_row = [&](int64_t row) {
+#pragma unroll
+    for (int v = 0; v < R; ++v) {
+      const int col = (threadIdx.x + v * T) * 8;
+      const bool ok = col < N && row < M;
+      const int64_t at = row * N + col;
+      vr[v] = ok ? ld_stream_u4(r + at, pol) : zero;
+      vn[v] = ok ? ld_stream_u4(dnorm + at, pol) : zero;
+      vd[v] = ok && dresid ? ld_stream_u4(dresid + at, pol) : zero;
+    }
+  };
+  load_row(blockIdx.x);
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < M; row += gridDim.x, flip ^= 1) {
+    float ss = 0.0f, t = 0.0f;
+    uint4 cr[R], cn[R], cd[R];
+#pragma unroll
+    for (int v = 0; v < R; ++v) {
+      cr[v] = vr[v];
+      cn[v] = vn[v];
+      cd[v] = vd[v];
+      float a[8], b[8], c[8];
+      unpack8(cr[v], a);
+      unpack8(cn[v], b);
+      unpack8(wv[v], c);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(a[i], a[i], ss);
+        t = fmaf(b[i] * c[i], a[i], t);
+      }
+    }
+    load_row(row + gridDim.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    }
+    if (lane == 0) sums[flip][warp] = make_float2(ss, t);
+    __syncthreads();  // one per row: the other buffer is free once all have passed it
+    ss = t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < T / 32; ++i) {
+      ss += sums[flip][i].x;
+      t += sums[flip][i].y;
+    }
+    const float s = rsqrtf(ss / static_cast<float>(N) + eps);
+    const float k = s * s * (t / static_cast<float>(N));
+#pragma unroll
+    for (int v = 0; v < R; ++v) {
+      const int col = (threadIdx.x + v * T) * 8;
+      float a[8], b[8], c[8], d[8];
+      unpack8(cr[v], a);
+      unpack8(cn[v], b);
+      unpack8(wv[v], c);
+      unpack8(cd[v], d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        acc[v][i] = fmaf(b[i], a[i] * s, acc[v][i]);
+        d[i] = fmaf(s, fmaf(-a[i], k, b[i] * c[i]), d[i]);
+      }
+      if (col < N) st_stream_u4(dr + row * N + col, pack8(d), pol);
+    }
+  }
+  if (!partial) return;
+#pragma unroll
+  for (int v = 0; v < R; ++v) {
+    const int col = (threadIdx.x + v * T) * 8;
+    if (col >= N) continue;
+    float4* dst = reinterpret_cast<float4*>(partial + static_cast<int64_t>(blockIdx.x) * N + col);
+    dst[0] = make_float4(acc[v][0], acc[v][1], acc[v][2], acc[v][3]);
+    dst[1] = make_float4(acc[v][4], acc[v][5], acc[v][6], acc[v][7]);
+  }
+}
+
+// dweight: 32 columns per CTA, whose warps share out the rows of partial sums.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    rmsnorm_grad_join_kernel(const float* __restrict__ partial, __nv_bfloat16* __restrict__ dweight,
+                             int rows, int N) {
+  __shared__ float part[kJoinWarps][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = blockIdx.x * 32 + lane;
+  float sum = 0.0f;
+  if (col < N) {
+#pragma unroll 8
+    for (int i = warp; i < rows; i += kJoinWarps)
+      sum += __ldcg(partial + static_cast<int64_t>(i) * N + col);
+  }
+  part[warp][lane] = sum;
+  __syncthreads();
+  if (warp != 0 || col >= N) return;
+  sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kJoinWarps; ++i) sum += part[i][lane];
+  dweight[col] = __float2bfloat16_rn(sum);
+}
+
+// 512 threads per SM, of up to 128 registers each.
+int rms_grad_threads(int N) { return N <= 1024 ? 128 : N <= 4096 ? 256 : 512; }
+
+template <int T, int R>
+cudaError_t run_rms_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
+                         const __nv_bfloat16* r, const __nv_bfloat16* weight, __nv_bfloat16* dr,
+                         float* partial, int64_t M, int N, float eps, int grid,
+                         cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(T, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_grad_kernel<T, R, 512 / T>, dnorm, dresid, r, weight, dr,
+                            partial, M, N, eps);
+}
+
+}  // namespace
+
+int rms_grad_ctas(int64_t M, int N, int sms) {
+  return static_cast<int>(std::min<int64_t>(M, static_cast<int64_t>(sms) * (512 / rms_grad_threads(N))));
+}
+
+cudaError_t launch_add_rmsnorm_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
+                                    const __nv_bfloat16* r, const __nv_bfloat16* weight,
+                                    __nv_bfloat16* dr, __nv_bfloat16* dweight, int64_t M, int N,
+                                    float eps, float* partial, int sms, cudaStream_t stream) {
+  const int grid = rms_grad_ctas(M, N, sms);
+  float* p = dweight ? partial : nullptr;
+  cudaError_t e;
+  if (N <= 1024) e = run_rms_grad<128, 1>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
+  else if (N <= 2048) e = run_rms_grad<256, 1>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
+  else if (N <= 4096) e = run_rms_grad<256, 2>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
+  else if (N <= 8192) e = run_rms_grad<512, 2>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
+  else e = run_rms_grad<512, 4>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
+  if (e != cudaSuccess || !dweight) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((N + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rmsnorm_grad_join_kernel, static_cast<const float*>(partial),
+                            dweight, grid, N);
+}
+
+}  // namespace gbf
