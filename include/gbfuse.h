@@ -387,6 +387,47 @@ GBF_API gbf_status_t gbf_linear_ce_grad(const void *x, const void *w, const void
                                         size_t workspace_bytes, gbf_stream_t stream);
 
 /*
+ * gbf_linear_distill -- the loss of a linear head against a teacher's top logits, row
+ *   by row, the head's logits never in memory:
+ *     l = alpha * x w^T,  lse[m] = log sum_v exp(l[m][v])
+ *     q[m] = softmax over the row's valid entries k of beta * logits[m][k];  q[m][v]: the
+ *            sum of those with ids[m][k] == v
+ *     loss[m] = sum_v q[m][v] * (log q[m][v] + lse[m] - l[m][v])
+ *     mean[0] = mean of loss over the scored rows
+ *   the Kullback-Leibler divergence of softmax(l) from the teacher's distribution on its
+ *   K top entries.  (Temperature T: 1/T in alpha and beta, T^2 in the gradient's scale.)
+ *   x [M][D], w [V][D] bf16; ids [M][K] of index_type, logits [M][K] of teacher_type
+ *   (GBF_TYPE_*), aligned to their elements' sizes.  An entry whose id is outside [0, V)
+ *   (-1 for padding) or whose logit is minus infinity is left out, whatever else it
+ *   holds; entries may be in any order, and the same id may come twice.  A row without a
+ *   valid entry is not scored: its loss and lse are 0, it costs no products (above 128
+ *   rows), and whatever its row of x holds reaches no result.
+ *   K in 1 .. 1024; beta > 0 and finite; other arguments, sizes, alignments and
+ *   accuracies as gbf_linear_ce (a loss is never below zero).  Workspace:
+ *   gbf_linear_distill_workspace_size(M, V, D, K, 0) bytes.
+ * gbf_linear_distill_grad -- its gradients, from the lse that gbf_linear_distill wrote:
+ *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - q[m][v])
+ *     dx = f * G w,   dw = f * G^T x,   f, dloss, dx, dw as gbf_linear_ce_grad.
+ *   The same bits on every run.  Workspace:
+ *   gbf_linear_distill_workspace_size(M, V, D, K, 1) bytes.
+ */
+GBF_API gbf_status_t gbf_linear_distill(const void *x, const void *w, const void *ids,
+                                        int index_type, const void *logits, int teacher_type,
+                                        float *loss, float *lse, float *mean, int64_t M, int64_t V,
+                                        int64_t D, int64_t K, float alpha, float beta,
+                                        void *workspace, size_t workspace_bytes,
+                                        gbf_stream_t stream);
+GBF_API gbf_status_t gbf_linear_distill_grad(const void *x, const void *w, const void *ids,
+                                             int index_type, const void *logits, int teacher_type,
+                                             const float *lse, const float *dloss, void *dx,
+                                             void *dw, int64_t M, int64_t V, int64_t D, int64_t K,
+                                             float alpha, float beta, float scale, int reduction,
+                                             void *workspace, size_t workspace_bytes,
+                                             gbf_stream_t stream);
+GBF_API size_t gbf_linear_distill_workspace_size(int64_t M, int64_t V, int64_t D, int64_t K,
+                                                 int grad);
+
+/*
  * gbf_clip_grad_norm -- the 2-norm over all values of `tensors` gradients, and
  *   the gradients scaled so that it is at most max_norm:
  *     norm   = sqrt( sum x^2 )                     written to norm[0], fp32

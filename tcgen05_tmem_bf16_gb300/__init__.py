@@ -21,6 +21,8 @@ The operators at a model's two ends carry the prefix gbf_ in the C ABI only:
   embedding_grad     the table's gradient, by sorted ids
   linear_ce          softmax cross entropy of a linear head, the logits never stored
   linear_ce_grad     its gradients by the head's input and weight
+  linear_distill     a linear head's loss against a teacher's top logits
+  linear_distill_grad  its gradients
   clip_grad_norm     global 2-norm over many gradients, and clipping
 
 So do those of the gated blocks between them, when they are trained:
@@ -60,7 +62,8 @@ EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unf
            "mlp_swiglu_down_unfused", "w8a16_fp8_gemm", "w8a16_fp8_gemm_unfused",
            "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused", "gbf_embedding_lookup",
            "gbf_embedding_grad", "gbf_clip_grad_norm", "gbf_linear_ce", "gbf_linear_ce_grad",
-           "gbf_mlp_train", "gbf_mlp_grad", "gbf_add_rmsnorm_grad")
+           "gbf_mlp_train", "gbf_mlp_grad", "gbf_add_rmsnorm_grad", "gbf_linear_distill",
+           "gbf_linear_distill_grad", "gbf_linear_distill_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -121,6 +124,14 @@ def load(path: str | None = None):
         lib.gbf_linear_ce_grad.argtypes = [V, V, V, I, V, V, V, V, I64, I64, I64, F, F, I, V, SZ,
                                            V]
         lib.gbf_linear_ce_grad.restype = I
+        lib.gbf_linear_distill.argtypes = [V, V, V, I, V, I, V, V, V, I64, I64, I64, I64, F, F, V,
+                                           SZ, V]
+        lib.gbf_linear_distill.restype = I
+        lib.gbf_linear_distill_grad.argtypes = [V, V, V, I, V, I, V, V, V, V, I64, I64, I64, I64,
+                                                F, F, F, I, V, SZ, V]
+        lib.gbf_linear_distill_grad.restype = I
+        lib.gbf_linear_distill_workspace_size.argtypes = [I64, I64, I64, I64, I]
+        lib.gbf_linear_distill_workspace_size.restype = SZ
         lib.gbf_clip_grad_norm.argtypes = [V, V, V, V, I, F, F, V, V, SZ, V]
         lib.gbf_clip_grad_norm.restype = I
         lib.gbf_mlp_train.argtypes = [V, V, V, V, V, V, V, V, V, I64, I64, I64, I, V]
@@ -359,6 +370,31 @@ def linear_ce_grad(x, w, targets, lse, dloss, dx, dw, M, V, D, alpha=1.0, scale=
                                    _code(reduction, REDUCTION), _p(workspace), workspace_bytes,
                                    _s(stream))
     return _check(st, "linear_ce_grad", raise_on_error)
+
+
+def linear_distill(x, w, ids, logits, loss, lse, mean, M, V, D, K, alpha=1.0, beta=1.0,
+                   index_type="i64", teacher_type="f32", workspace=None, workspace_bytes=0,
+                   stream=None, raise_on_error=True):
+    st = load().gbf_linear_distill(_p(x), _p(w), _p(ids), _code(index_type, INDEX), _p(logits),
+                                   _code(teacher_type, TYPE), _p(loss), _p(lse), _p(mean), M, V,
+                                   D, K, alpha, beta, _p(workspace), workspace_bytes, _s(stream))
+    return _check(st, "linear_distill", raise_on_error)
+
+
+def linear_distill_grad(x, w, ids, logits, lse, dloss, dx, dw, M, V, D, K, alpha=1.0, beta=1.0,
+                        scale=1.0, reduction="mean", index_type="i64", teacher_type="f32",
+                        workspace=None, workspace_bytes=0, stream=None, raise_on_error=True):
+    st = load().gbf_linear_distill_grad(_p(x), _p(w), _p(ids), _code(index_type, INDEX),
+                                        _p(logits), _code(teacher_type, TYPE), _p(lse), _p(dloss),
+                                        _p(dx), _p(dw), M, V, D, K, alpha, beta, scale,
+                                        _code(reduction, REDUCTION), _p(workspace),
+                                        workspace_bytes, _s(stream))
+    return _check(st, "linear_distill_grad", raise_on_error)
+
+
+def linear_distill_workspace_size(M, V, D, K, grad) -> int:
+    """Bytes that linear_distill (``grad`` false) or linear_distill_grad needs."""
+    return int(load().gbf_linear_distill_workspace_size(M, V, D, K, int(bool(grad))))
 
 
 class TensorList:

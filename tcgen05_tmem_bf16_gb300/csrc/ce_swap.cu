@@ -65,7 +65,8 @@ __device__ __forceinline__ float sw_pow2(float x) {
   return y;
 }
 
-template <int MPAD, bool GRAD>
+// PICK: lists of columns with their shares instead of one target per row (CePick).
+template <int MPAD, bool GRAD, bool PICK>
 __global__ void __launch_bounds__(kSwThreads, 2)
     ce_swap_kernel(const __grid_constant__ CeSwap a, const CeEnd e, const KernelCtl kctl) {
   using Cfg = SwCfg<MPAD>;
@@ -112,10 +113,10 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   const int count = GRAD ? *e.count : e.M;
   for (int i = threadIdx.x; i < MPAD; i += kSwThreads) {
     if (GRAD) {
-      row_tgt[i] = i < count ? e.tgt[i] - a.v0 : -1;
+      row_tgt[i] = i < count ? (PICK ? e.rows[i] : e.tgt[i] - a.v0) : -1;
       row_lse2[i] = i < count ? e.lse2[i] : 0.0f;
       row_dl[i] = i < count ? e.dl[i] : 0.0f;
-    } else {
+    } else if (!PICK) {
       const int64_t t = i < count ? ce_target(a.targets, a.ids64, i) : -1;
       row_tgt[i] = t >= 0 && t < a.cols ? static_cast<int>(t) : -1;
     }
@@ -242,6 +243,17 @@ __global__ void __launch_bounds__(kSwThreads, 2)
 #pragma unroll 1
       for (int c = 0; c < MPAD / 16; ++c) {
         float v[16];
+        // lanes 0-15: the entries of row c * 16 + lane in this warp's 32 columns
+        int pick_row = 0, pick_at = 0, pick_n = 0;
+        if (PICK && last && lane < 16 && c * 16 + lane < count) {
+          pick_row = GRAD ? row_tgt[c * 16 + lane] : c * 16 + lane;
+          const uint16_t* at = e.pick.at + static_cast<int64_t>(pick_row) * e.pick.stride +
+                               ((a.v0 + t * 128 + q * 32) >> 5);
+          if (t * 128 + q * 32 < a.cols) {
+            pick_at = at[0];
+            pick_n = at[1] - pick_at;
+          }
+        }
         if (c < chunks) {
           uint32_t r[16];
           tmem_ld16(tb + c * 16, r);
@@ -276,7 +288,25 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             f[k] = 0.0f;
             if (m < count) {
               const float p = sw_pow2(fmaf(v[k], e.c2, -row_lse2[m]));
-              f[k] = row_dl[m] * (row_tgt[m] == col ? p - 1.0f : p);
+              if constexpr (PICK) f[k] = p;
+              else f[k] = row_dl[m] * (row_tgt[m] == col ? p - 1.0f : p);
+            }
+          }
+          if constexpr (PICK) {
+            const unsigned some = __ballot_sync(0xFFFFFFFFu, pick_n > 0);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              if ((some >> k) & 1u) {
+                const int64_t row = __shfl_sync(0xFFFFFFFFu, pick_row, k);
+                const int n = __shfl_sync(0xFFFFFFFFu, pick_n, k);
+                const int2* list = e.pick.list + row * (e.pick.K + 1) +
+                                   __shfl_sync(0xFFFFFFFFu, pick_at, k);
+                for (int i = 0; i < n; ++i) {
+                  const int2 x = list[i];
+                  if (x.x == a.v0 + col) f[k] -= __int_as_float(x.y);
+                }
+              }
+              if (c * 16 + k < count) f[k] *= row_dl[c * 16 + k];
             }
           }
           if (col < a.cols) {
@@ -316,8 +346,14 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           sum = fmaf(sum, sw_pow2(top - ref2), sum2 * sw_pow2(top2 - ref2));
           if (lane < 16 && m < count) {
             e.part[static_cast<int64_t>(4 * t + q) * e.M + m] = make_float2(m2, sum);
-            const int at = row_tgt[m] - base;
-            if (row_tgt[m] >= 0 && at >= 0 && at < 32) e.tlog[m] = my_turn[at * 17 + lane];
+            if constexpr (PICK) {
+              const int2* list = e.pick.list + static_cast<int64_t>(m) * (e.pick.K + 1) + pick_at;
+              float* dots = e.pick.dots + static_cast<int64_t>(m) * e.pick.K + pick_at;
+              for (int i = 0; i < pick_n; ++i) dots[i] = my_turn[(list[i].x - base) * 17 + lane];
+            } else {
+              const int at = row_tgt[m] - base;
+              if (row_tgt[m] >= 0 && at >= 0 && at < 32) e.tlog[m] = my_turn[at * 17 + lane];
+            }
           }
           __syncwarp();
         }
@@ -343,11 +379,11 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   }
 }
 
-template <int MPAD, bool GRAD>
+template <int MPAD, bool GRAD, bool PICK>
 cudaError_t run_swap(const CeSwap& a, const CeEnd& end, const KernelCtl& ctl, int grid,
                      cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = ce_swap_kernel<MPAD, GRAD>;
+  auto kernel = ce_swap_kernel<MPAD, GRAD, PICK>;
   constexpr int smem = SwCfg<MPAD>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -382,18 +418,25 @@ int ce_swap_segments(int64_t M, int k_blocks) {
   return (k_blocks + n * kCeChain - 1) / (n * kCeChain);
 }
 
+template <bool GRAD, bool PICK>
+static cudaError_t run_swap_rows(const CeSwap& a, const CeEnd& end, const KernelCtl& ctl, int grid,
+                                 cudaStream_t stream) {
+  switch (ce_swap_rows(end.M)) {
+    case 16: return run_swap<16, GRAD, PICK>(a, end, ctl, grid, stream);
+    case 64: return run_swap<64, GRAD, PICK>(a, end, ctl, grid, stream);
+    case 128: return run_swap<128, GRAD, PICK>(a, end, ctl, grid, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 cudaError_t launch_ce_swap(const CeSwap& a, bool grad, const CeEnd& end, int sms,
                            const KernelCtl& ctl, cudaStream_t stream) {
   const int grid = std::min((a.cols + 127) / 128, 2 * sms);
-  switch (ce_swap_rows(end.M)) {
-    case 16: return grad ? run_swap<16, true>(a, end, ctl, grid, stream)
-                         : run_swap<16, false>(a, end, ctl, grid, stream);
-    case 64: return grad ? run_swap<64, true>(a, end, ctl, grid, stream)
-                         : run_swap<64, false>(a, end, ctl, grid, stream);
-    case 128: return grad ? run_swap<128, true>(a, end, ctl, grid, stream)
-                          : run_swap<128, false>(a, end, ctl, grid, stream);
-    default: return cudaErrorInvalidValue;
-  }
+  if (end.pick.list)
+    return grad ? run_swap_rows<true, true>(a, end, ctl, grid, stream)
+                : run_swap_rows<false, true>(a, end, ctl, grid, stream);
+  return grad ? run_swap_rows<true, false>(a, end, ctl, grid, stream)
+              : run_swap_rows<false, false>(a, end, ctl, grid, stream);
 }
 
 }  // namespace gbf

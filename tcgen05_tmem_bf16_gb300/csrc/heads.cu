@@ -232,6 +232,272 @@ gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M, bo
   return cuda_status(launch_ce_gemm(launch, end, streams, chains, grid, lib_ctl(err, grid), s));
 }
 
+// The sizes and arrays that both passes of both losses work on; pick.list null: the
+// hard targets' loss.
+struct CeCall {
+  const void *x, *w, *targets;
+  bool ids64;
+  int64_t M, V, D;
+  float alpha;
+  CeWs ws;
+  CePick pick;
+  const DeviceInfo* dev;
+  unsigned* err;
+  cudaStream_t s;
+};
+
+// Forward pass of rows > 0.
+gbf_status_t ce_forward(const CeCall& call, float* loss, float* lse, float* mean) {
+  const auto [x, w, targets, ids64, M, V, D, alpha, ws, pick, dev, err, s] = call;
+  const int swap_sms = std::min(dev->sms, kMaxSms);
+  gbf_status_t st;
+  CePrep p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.xc = ws.xc;
+  p.loss = loss;
+  p.lse_out = lse;
+  p.count = ws.count;
+  p.rows = ws.rows;
+  p.tgt = ws.tgt;
+  p.ticket = ws.ticket;
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.D = static_cast<int>(D);
+  const bool few = M <= kCeSwapMax;
+  CeLaunch launch{};
+  for (CeJob& j : launch.job) j.bn = 256;
+  CeSwap swap{};
+  if (few) {
+    if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
+    swap.cols = p.V;
+    swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
+    swap.targets = targets;
+    swap.ids64 = ids64;
+    swap.ticket = ws.ticket;
+  } else {
+    launch.d = p.D;
+    CeJob& job = launch.job[1];
+    job.bn = pick.list ? 256 : ce_tile_cols(M, V, D);
+    if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+        !ce_map_k(&job.b[0], w, D, V, D, job.bn / 2))
+      return GBF_ERR_CUDA;
+    job.mode = kCeLse;
+    job.cols = p.V;
+    job.splits = 1;
+  }
+  CeEnd end{};
+  end.count = ws.count;
+  end.tgt = ws.tgt;
+  end.part = ws.part;
+  end.tlog = ws.tlog;
+  end.chain = ws.chain;
+  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
+  end.M = p.M;
+  end.rows = ws.rows;
+  end.pick = pick;
+  CeJoin join{};
+  join.count = ws.count;
+  join.rows = few ? nullptr : ws.rows;
+  join.targets = targets;
+  join.ids64 = ids64;
+  join.V = p.V;
+  join.part = ws.part;
+  join.tlog = ws.tlog;
+  join.ticket = ws.ticket;
+  join.sums = ws.sums;
+  join.loss = loss;
+  join.lse = lse;
+  join.mean = mean;
+  join.c2 = end.c2;
+  join.M = p.M;
+  join.parts = static_cast<int>(few || !pick.list ? ce_parts(M, V, D) : 2 * ceil_div64(V, 256));
+  join.pick = pick;
+  if (!few && (st = cuda_status(launch_ce_prep(targets, ids64, p, dev->sms,
+                                               s))) != GBF_OK)
+    return st;
+  st = few ? cuda_status(launch_ce_swap(swap, false, end, swap_sms, lib_ctl(err, 2 * swap_sms), s))
+           : run_ce_gemm(launch, end, M, ce_chained(D), *dev, err, s);
+  if (st != GBF_OK) return st;
+  return cuda_status(launch_ce_join(join, s));
+}
+
+// Backward pass of rows > 0.
+gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dloss, void* dx,
+                         void* dw, float scale, int reduction) {
+  const auto [x, w, targets, ids64, M, V, D, alpha, ws, pick, dev, err, s] = call;
+  const int swap_sms = std::min(dev->sms, kMaxSms);
+  gbf_status_t st;
+  CePrep p{};
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.xc = ws.xc;
+  p.lse_in = lse;
+  p.dloss = dloss;
+  p.dx = static_cast<__nv_bfloat16*>(dx);
+  p.count = ws.count;
+  p.rows = ws.rows;
+  p.tgt = ws.tgt;
+  p.lse2 = ws.lse2;
+  p.dl = ws.dl;
+  p.soft = pick.list != nullptr;
+  p.M = static_cast<int>(M);
+  p.V = static_cast<int>(V);
+  p.D = static_cast<int>(D);
+  if ((st = cuda_status(launch_ce_prep(targets, ids64, p, dev->sms, s))) !=
+      GBF_OK)
+    return st;
+  const int64_t piece = ce_piece(M, V);
+  const bool few = M <= kCeSwapMax;  // G transposed, by the swapped roles
+  const bool chains = !few && ce_chained(D);
+  const int64_t ld = few ? ce_swap_rows(M) : ceil_div64(piece, 8) * 8;
+  const int64_t m_pad = ceil_div64(M, 512) * 512;
+  const int splits = ce_splits(M, D, piece);
+  CeEnd end{};
+  end.count = ws.count;
+  end.tgt = ws.tgt;
+  end.lse2 = ws.lse2;
+  end.dl = ws.dl;
+  end.chain = ws.chain;
+  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
+  end.scale = alpha * scale;
+  end.mean = reduction == GBF_REDUCE_MEAN;
+  end.M = p.M;
+  end.m_pad = static_cast<int>(m_pad);
+  end.rows = ws.rows;
+  end.pick = pick;
+  // Launch n: G of piece n, and the products of piece n - 1's G.
+  const int64_t pieces = ceil_div64(V, piece);
+  for (int64_t n = 0; n <= pieces; ++n) {
+    CeLaunch launch{}, logits{};
+    launch.d = logits.d = p.D;
+    for (CeJob& j : launch.job) j.bn = 256;
+    for (CeJob& j : logits.job) j.bn = 256;
+    if (n < pieces && few) {
+      const int64_t v0 = n * piece;
+      CeSwap swap{};
+      if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
+      swap.gt = ws.g[n & 1];
+      swap.v0 = static_cast<int>(v0);
+      swap.cols = static_cast<int>(std::min(piece, V - v0));
+      swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
+      st = cuda_status(launch_ce_swap(swap, true, end, swap_sms, lib_ctl(err, 2 * swap_sms), s));
+      if (st != GBF_OK) return st;
+    } else if (n < pieces) {
+      CeJob& job = chains ? logits.job[1] : launch.job[1];
+      const int64_t v0 = n * piece, cols = std::min(piece, V - v0);
+      job.mode = kCeGrad;
+      job.cols = static_cast<int>(cols);
+      job.v0 = static_cast<int>(v0);
+      job.splits = 1;
+      if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
+          !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g[n & 1], cols, M, ld))
+        return GBF_ERR_CUDA;
+      if (chains && (st = run_ce_gemm(logits, end, M, true, *dev, err, s)) != GBF_OK) return st;
+    }
+    if (n > 0) {
+      const int64_t v0 = (n - 1) * piece, cols = std::min(piece, V - v0);
+      const __nv_bfloat16* g = ws.g[(n - 1) & 1];
+      if (dx) {
+        CeJob& job = launch.job[0];
+        job.mode = kCeDx;
+        job.cols = static_cast<int>(cols);
+        job.v0 = static_cast<int>(v0);
+        job.splits = splits;
+        job.add = n > 1;
+        job.gt = few;
+        if (!(few ? ce_map_mn(&job.a[0], g, ld, cols, ld) : ce_map_k(&job.a[0], g, cols, M, ld)) ||
+            !ce_map_mn(&job.b[0], w, D, V, D) ||
+            !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
+          return GBF_ERR_CUDA;
+      }
+      if (dw) {
+        CeJob& job = launch.job[2];
+        job.mode = kCeDw;
+        job.cols = static_cast<int>(cols);
+        job.v0 = static_cast<int>(v0);
+        job.splits = 1;
+        job.gt = few;
+        if (!(few ? ce_map_k(&job.a[0], g, ld, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
+            !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
+            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, ce_streams(M) == 1))
+          return GBF_ERR_CUDA;
+      }
+    }
+    if ((few || chains) && n == 0) continue;  // no G yet
+    if ((st = run_ce_gemm(launch, end, M, false, *dev, err, s)) != GBF_OK) return st;
+  }
+  if (!dx) return GBF_OK;
+  CeDxOut out{};
+  out.count = ws.count;
+  out.rows = ws.rows;
+  out.acc = ws.dxacc;
+  out.dx = p.dx;
+  out.scale = end.scale;
+  out.mean = end.mean;
+  out.m_pad = end.m_pad;
+  out.splits = splits;
+  out.D = p.D;
+  return cuda_status(launch_ce_dx(out, p.M, dev->sms, s));
+}
+
+// ---- distillation from a teacher's top logits
+
+struct DistillWs {
+  CeWs ce;
+  int2* list;
+  uint16_t* at;
+  int* tgt;
+  float* dots;
+};
+// Columns per entry of `at`: those that a warp of the ending holds at a time.
+int pick_shift(int64_t M) { return M <= kCeSwapMax ? 5 : 7; }
+int64_t pick_stride(int64_t M, int64_t V) { return (V >> pick_shift(M)) + 2; }
+
+size_t distill_sections(void* base, int64_t M, int64_t V, int64_t D, int64_t K, bool grad,
+                        DistillWs* w) {
+  const size_t at = ce_sections(base, M, V, D, grad, &w->ce);
+  Sections s{static_cast<uint8_t*>(base), at};
+  w->list = s.take<int2>(static_cast<size_t>(M) * (K + 1));
+  w->at = s.take<uint16_t>(static_cast<size_t>(M) * pick_stride(M, V));
+  w->tgt = s.take<int>(M);
+  w->dots = grad ? nullptr : s.take<float>(static_cast<size_t>(M) * K);
+  return s.at;
+}
+
+gbf_status_t check_distill(const void* x, const void* w, const void* ids, const void* logits,
+                           int index_type, int teacher_type, int64_t M, int64_t V, int64_t D,
+                           int64_t K, float alpha, float beta) {
+  gbf_status_t st = check_ce(x, w, ids, index_type, M, V, D, alpha);
+  if (st != GBF_OK) return st;
+  if ((!logits && M > 0) || K < 0 || !std::isfinite(beta) || !(beta > 0.0f) ||
+      (teacher_type != GBF_TYPE_BF16 && teacher_type != GBF_TYPE_F32))
+    return GBF_ERR_INVALID_ARG;
+  if (!aligned(logits, teacher_type == GBF_TYPE_F32 ? 4 : 2)) return GBF_ERR_MISALIGNED;
+  return K >= 1 && K <= kPickMax ? GBF_OK : GBF_ERR_UNSUPPORTED_SHAPE;
+}
+
+// Launches the lists and fills in what a pass takes of them.
+gbf_status_t make_lists(const void* ids, const void* logits, int teacher_type, float beta,
+                        int64_t K, const DistillWs& ws, CeCall* call) {
+  CeLists p{};
+  p.ids = ids;
+  p.logits = logits;
+  p.ids64 = call->ids64;
+  p.bf16 = teacher_type == GBF_TYPE_BF16;
+  p.beta = beta;
+  p.list = ws.list;
+  p.at = ws.at;
+  p.tgt = ws.tgt;
+  p.M = call->M;
+  p.V = static_cast<int>(call->V);
+  p.K = static_cast<int>(K);
+  p.stride = static_cast<int>(pick_stride(call->M, call->V));
+  p.shift = pick_shift(call->M);
+  call->pick = CePick{ws.list, ws.at, ws.dots, p.K, p.stride, p.shift};
+  call->targets = ws.tgt;
+  call->ids64 = false;
+  return cuda_status(launch_ce_lists(p, call->dev->sms, call->s));
+}
+
 }  // namespace
 
 size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
@@ -352,73 +618,9 @@ gbf_status_t gbf_linear_ce(const void* x, const void* w, const void* targets, in
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int swap_sms = std::min(dev->sms, kMaxSms);
   if (M == 0) return mean ? cuda_status(cudaMemsetAsync(mean, 0, 4, s)) : GBF_OK;
-  CePrep p{};
-  p.x = static_cast<const __nv_bfloat16*>(x);
-  p.xc = ws.xc;
-  p.loss = loss;
-  p.lse_out = lse;
-  p.count = ws.count;
-  p.rows = ws.rows;
-  p.tgt = ws.tgt;
-  p.ticket = ws.ticket;
-  p.M = static_cast<int>(M);
-  p.V = static_cast<int>(V);
-  p.D = static_cast<int>(D);
-  const bool few = M <= kCeSwapMax;
-  CeLaunch launch{};
-  for (CeJob& j : launch.job) j.bn = 256;
-  CeSwap swap{};
-  if (few) {
-    if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
-    swap.cols = p.V;
-    swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
-    swap.targets = targets;
-    swap.ids64 = index_type == GBF_INDEX_I64;
-    swap.ticket = ws.ticket;
-  } else {
-    launch.d = p.D;
-    CeJob& job = launch.job[1];
-    job.bn = ce_tile_cols(M, V, D);
-    if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
-        !ce_map_k(&job.b[0], w, D, V, D, job.bn / 2))
-      return GBF_ERR_CUDA;
-    job.mode = kCeLse;
-    job.cols = p.V;
-    job.splits = 1;
-  }
-  CeEnd end{};
-  end.count = ws.count;
-  end.tgt = ws.tgt;
-  end.part = ws.part;
-  end.tlog = ws.tlog;
-  end.chain = ws.chain;
-  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
-  end.M = p.M;
-  CeJoin join{};
-  join.count = ws.count;
-  join.rows = few ? nullptr : ws.rows;
-  join.targets = targets;
-  join.ids64 = index_type == GBF_INDEX_I64;
-  join.V = p.V;
-  join.part = ws.part;
-  join.tlog = ws.tlog;
-  join.ticket = ws.ticket;
-  join.sums = ws.sums;
-  join.loss = loss;
-  join.lse = lse;
-  join.mean = mean;
-  join.c2 = end.c2;
-  join.M = p.M;
-  join.parts = static_cast<int>(ce_parts(M, V, D));
-  if (!few && (st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms,
-                                               s))) != GBF_OK)
-    return st;
-  st = few ? cuda_status(launch_ce_swap(swap, false, end, swap_sms, lib_ctl(err, 2 * swap_sms), s))
-           : run_ce_gemm(launch, end, M, ce_chained(D), *dev, err, s);
-  if (st != GBF_OK) return st;
-  return cuda_status(launch_ce_join(join, s));
+  return ce_forward({x, w, targets, index_type == GBF_INDEX_I64, M, V, D, alpha, ws, CePick{}, dev, err, s},
+                    loss, lse, mean);
 }
 
 gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* targets, int index_type,
@@ -441,116 +643,69 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int swap_sms = std::min(dev->sms, kMaxSms);
   if (M == 0)
     return dw ? cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, s)) : GBF_OK;
-  CePrep p{};
-  p.x = static_cast<const __nv_bfloat16*>(x);
-  p.xc = ws.xc;
-  p.lse_in = lse;
-  p.dloss = dloss;
-  p.dx = static_cast<__nv_bfloat16*>(dx);
-  p.count = ws.count;
-  p.rows = ws.rows;
-  p.tgt = ws.tgt;
-  p.lse2 = ws.lse2;
-  p.dl = ws.dl;
-  p.M = static_cast<int>(M);
-  p.V = static_cast<int>(V);
-  p.D = static_cast<int>(D);
-  if ((st = cuda_status(launch_ce_prep(targets, index_type == GBF_INDEX_I64, p, dev->sms, s))) !=
-      GBF_OK)
-    return st;
-  const int64_t piece = ce_piece(M, V);
-  const bool few = M <= kCeSwapMax;  // G transposed, by the swapped roles
-  const bool chains = !few && ce_chained(D);
-  const int64_t ld = few ? ce_swap_rows(M) : ceil_div64(piece, 8) * 8;
-  const int64_t m_pad = ceil_div64(M, 512) * 512;
-  const int splits = ce_splits(M, D, piece);
-  CeEnd end{};
-  end.count = ws.count;
-  end.tgt = ws.tgt;
-  end.lse2 = ws.lse2;
-  end.dl = ws.dl;
-  end.chain = ws.chain;
-  end.c2 = static_cast<float>(alpha * 1.4426950408889634);
-  end.scale = alpha * scale;
-  end.mean = reduction == GBF_REDUCE_MEAN;
-  end.M = p.M;
-  end.m_pad = static_cast<int>(m_pad);
-  // Launch n: G of piece n, and the products of piece n - 1's G.
-  const int64_t pieces = ceil_div64(V, piece);
-  for (int64_t n = 0; n <= pieces; ++n) {
-    CeLaunch launch{}, logits{};
-    launch.d = logits.d = p.D;
-    for (CeJob& j : launch.job) j.bn = 256;
-    for (CeJob& j : logits.job) j.bn = 256;
-    if (n < pieces && few) {
-      const int64_t v0 = n * piece;
-      CeSwap swap{};
-      if (!ce_maps_swap(&swap, w, ws.xc, x, M, V, D)) return GBF_ERR_CUDA;
-      swap.gt = ws.g[n & 1];
-      swap.v0 = static_cast<int>(v0);
-      swap.cols = static_cast<int>(std::min(piece, V - v0));
-      swap.num_kb = static_cast<int>(ceil_div64(D, kBK));
-      st = cuda_status(launch_ce_swap(swap, true, end, swap_sms, lib_ctl(err, 2 * swap_sms), s));
-      if (st != GBF_OK) return st;
-    } else if (n < pieces) {
-      CeJob& job = chains ? logits.job[1] : launch.job[1];
-      const int64_t v0 = n * piece, cols = std::min(piece, V - v0);
-      job.mode = kCeGrad;
-      job.cols = static_cast<int>(cols);
-      job.v0 = static_cast<int>(v0);
-      job.splits = 1;
-      if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
-          !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g[n & 1], cols, M, ld))
-        return GBF_ERR_CUDA;
-      if (chains && (st = run_ce_gemm(logits, end, M, true, *dev, err, s)) != GBF_OK) return st;
-    }
-    if (n > 0) {
-      const int64_t v0 = (n - 1) * piece, cols = std::min(piece, V - v0);
-      const __nv_bfloat16* g = ws.g[(n - 1) & 1];
-      if (dx) {
-        CeJob& job = launch.job[0];
-        job.mode = kCeDx;
-        job.cols = static_cast<int>(cols);
-        job.v0 = static_cast<int>(v0);
-        job.splits = splits;
-        job.add = n > 1;
-        job.gt = few;
-        if (!(few ? ce_map_mn(&job.a[0], g, ld, cols, ld) : ce_map_k(&job.a[0], g, cols, M, ld)) ||
-            !ce_map_mn(&job.b[0], w, D, V, D) ||
-            !ce_map_out_f32(&job.o, ws.dxacc, D, splits * m_pad))
-          return GBF_ERR_CUDA;
-      }
-      if (dw) {
-        CeJob& job = launch.job[2];
-        job.mode = kCeDw;
-        job.cols = static_cast<int>(cols);
-        job.v0 = static_cast<int>(v0);
-        job.splits = 1;
-        job.gt = few;
-        if (!(few ? ce_map_k(&job.a[0], g, ld, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
-            !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
-            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, ce_streams(M) == 1))
-          return GBF_ERR_CUDA;
-      }
-    }
-    if ((few || chains) && n == 0) continue;  // no G yet
-    if ((st = run_ce_gemm(launch, end, M, false, *dev, err, s)) != GBF_OK) return st;
-  }
-  if (!dx) return GBF_OK;
-  CeDxOut out{};
-  out.count = ws.count;
-  out.rows = ws.rows;
-  out.acc = ws.dxacc;
-  out.dx = p.dx;
-  out.scale = end.scale;
-  out.mean = end.mean;
-  out.m_pad = end.m_pad;
-  out.splits = splits;
-  out.D = p.D;
-  return cuda_status(launch_ce_dx(out, p.M, dev->sms, s));
+  return ce_backward({x, w, targets, index_type == GBF_INDEX_I64, M, V, D, alpha, ws, CePick{}, dev, err, s},
+                     lse, dloss, dx, dw, scale, reduction);
+}
+
+size_t gbf_linear_distill_workspace_size(int64_t M, int64_t V, int64_t D, int64_t K, int grad) {
+  if (M < 0 || K < 1 || K > kPickMax || !ce_sizes_held(M, V, D)) return 0;  // as refused
+  DistillWs ws;
+  return distill_sections(nullptr, M, V, D, K, grad != 0, &ws);
+}
+
+gbf_status_t gbf_linear_distill(const void* x, const void* w, const void* ids, int index_type,
+                                const void* logits, int teacher_type, float* loss, float* lse,
+                                float* mean, int64_t M, int64_t V, int64_t D, int64_t K,
+                                float alpha, float beta, void* workspace, size_t workspace_bytes,
+                                gbf_stream_t stream) {
+  gbf_status_t st =
+      check_distill(x, w, ids, logits, index_type, teacher_type, M, V, D, K, alpha, beta);
+  if (st != GBF_OK) return st;
+  if (M > 0 && (!loss || !lse)) return GBF_ERR_INVALID_ARG;
+  if (!aligned(loss, 4) || !aligned(lse, 4) || !aligned(mean, 4) || !aligned(workspace, 16))
+    return GBF_ERR_MISALIGNED;
+  DistillWs ws;
+  const size_t need = distill_sections(workspace, M, V, D, K, false, &ws);
+  if (!workspace || workspace_bytes < need) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0) return mean ? cuda_status(cudaMemsetAsync(mean, 0, 4, s)) : GBF_OK;
+  CeCall call{x, w, nullptr, index_type == GBF_INDEX_I64, M, V, D, alpha, ws.ce, CePick{}, dev, err, s};
+  if ((st = make_lists(ids, logits, teacher_type, beta, K, ws, &call)) != GBF_OK) return st;
+  return ce_forward(call, loss, lse, mean);
+}
+
+gbf_status_t gbf_linear_distill_grad(const void* x, const void* w, const void* ids, int index_type,
+                                     const void* logits, int teacher_type, const float* lse,
+                                     const float* dloss, void* dx, void* dw, int64_t M, int64_t V,
+                                     int64_t D, int64_t K, float alpha, float beta, float scale,
+                                     int reduction, void* workspace, size_t workspace_bytes,
+                                     gbf_stream_t stream) {
+  gbf_status_t st =
+      check_distill(x, w, ids, logits, index_type, teacher_type, M, V, D, K, alpha, beta);
+  if (st != GBF_OK) return st;
+  if ((M > 0 && (!lse || (!dx && !dw))) ||
+      (reduction != GBF_REDUCE_SUM && reduction != GBF_REDUCE_MEAN))
+    return GBF_ERR_INVALID_ARG;
+  if (!aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dx, 16) || !aligned(dw, 16) ||
+      !aligned(workspace, 16))
+    return GBF_ERR_MISALIGNED;
+  DistillWs ws;
+  const size_t need = distill_sections(workspace, M, V, D, K, true, &ws);
+  if (!workspace || workspace_bytes < need) return GBF_ERR_WORKSPACE;
+  const DeviceInfo* dev;
+  unsigned* err;
+  if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (M == 0)
+    return dw ? cuda_status(cudaMemsetAsync(dw, 0, static_cast<size_t>(V) * D * 2, s)) : GBF_OK;
+  CeCall call{x, w, nullptr, index_type == GBF_INDEX_I64, M, V, D, alpha, ws.ce, CePick{}, dev, err, s};
+  if ((st = make_lists(ids, logits, teacher_type, beta, K, ws, &call)) != GBF_OK) return st;
+  return ce_backward(call, lse, dloss, dx, dw, scale, reduction);
 }
 
 }  // extern "C"

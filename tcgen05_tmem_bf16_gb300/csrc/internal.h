@@ -174,6 +174,14 @@ struct CeLaunch {
   CeJob job[kCeJobs];
   int d;  // hidden width
 };
+// Distillation: a row's softmax target is a list of columns with their shares
+// (distill.cu), instead of one column.
+struct CePick {
+  const int2* list;    // [M][K + 1]: (column, bits of its share), columns ascending, INT_MAX last
+  const uint16_t* at;  // [M][stride]: the first entry of each 2^shift columns
+  float* dots;         // [M][K]: the entries' products, in the list's order (forward)
+  int K, stride, shift;
+};
 struct CeEnd {
   const int* count;   // scored rows
   const int* tgt;     // [count] targets
@@ -187,6 +195,8 @@ struct CeEnd {
   int mean;           // divide by the number of scored rows
   int M;
   int m_pad;          // rows between the splits' fp32 buffers
+  const int* rows;    // [count] scored rows' numbers among all (with a pick)
+  CePick pick;        // list null: none
 };
 #ifdef __CUDACC__
 // Target i of an array of int64 or int32.
@@ -226,6 +236,7 @@ struct CePrep {
   unsigned* ticket;
   float *lse2, *dl;
   int M, V, D, rows_per;
+  int soft;               // targets only say which rows are scored: tgt is -1
 };
 struct CeJoin {
   const int* count;
@@ -239,6 +250,7 @@ struct CeJoin {
   float *loss, *lse, *mean;
   float c2;      // as in CeEnd: what the maxima were made with
   int M, parts;
+  CePick pick;   // list null: none
 };
 struct CeDxOut {
   const int* count;
@@ -255,6 +267,22 @@ cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
                            cudaStream_t stream);
 cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream);
 cudaError_t launch_ce_dx(const CeDxOut& p, int M, int sms, cudaStream_t stream);
+// The lists of a distillation from a teacher's top logits (distill.cu): shares
+// softmax(beta * logits) over a row's valid entries, sorted by column, and tgt[m]: a
+// column of the row, -1 without any.
+constexpr int kPickMax = 1024;  // entries per row
+struct CeLists {
+  const void* ids;
+  const void* logits;
+  int ids64, bf16;
+  float beta;
+  int2* list;
+  uint16_t* at;
+  int* tgt;
+  int64_t M;
+  int V, K, stride, shift;
+};
+cudaError_t launch_ce_lists(const CeLists& p, int sms, cudaStream_t stream);
 
 // Products of a gated MLP block that is trained, and of its gradient
 // (mlp_train.cu): up to three per launch, none of which reads what another writes.

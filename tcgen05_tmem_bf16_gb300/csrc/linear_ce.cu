@@ -46,6 +46,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "common.cuh"
 #include "epilogue.cuh"
@@ -219,15 +220,68 @@ struct CeTileArgs {
   float lse2, dl, out_scale;
 };
 
-template <int MODE, int FORM>
+// Where a row's thread stands in its list of columns (PICK): the next entry at or
+// behind the present column, its column from the tile's first on.
+struct CeCursor {
+  const int2* entry;
+  int col, base;
+  float share;
+  float* dot;
+  __device__ __forceinline__ void read() {
+    const int2 x = *entry;
+    col = x.x - base;  // the sentinel stays far behind any tile
+    share = __int_as_float(x.y);
+  }
+  __device__ __forceinline__ void start(const CeEnd& e, int row, int first) {
+    const CePick& p = e.pick;
+    const int64_t r = e.rows[row];
+    const int i = p.at[r * p.stride + (first >> p.shift)];
+    base = first;
+    entry = p.list + r * (p.K + 1) + i;
+    dot = p.dots ? p.dots + r * p.K + i : nullptr;
+    read();
+  }
+  __device__ __forceinline__ void none() { col = INT_MAX; }
+  __device__ __forceinline__ void next() {
+    ++entry;
+    read();
+  }
+};
+
+// Value i of a thread's 32, and a subtraction from it, with the values left in
+// registers: written out, since an index of the language's would put all of them in
+// local memory for every chunk, entries or none.
+__device__ __forceinline__ float pick_of(const uint32_t (&v)[32], int i) {
+  uint32_t d = 0u;
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, %2;\n\t@p mov.b32 %0, %3;\n\t}"
+        : "+r"(d) : "r"(i), "r"(k), "r"(v[k]));
+  return __uint_as_float(d);
+}
+__device__ __forceinline__ void take_from(float (&g)[32], int i, float x) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, %2;\n\t@p sub.f32 %0, %0, %3;\n\t}"
+        : "+f"(g[k]) : "r"(i), "r"(k), "f"(x));
+}
+
+template <int MODE, int FORM, bool PICK>
 __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const CeTileArgs& t,
-                                         const CeEnd& e, int& flip, float& m, float& sum) {
+                                         const CeEnd& e, int& flip, float& m, float& sum,
+                                         CeCursor& cur) {
   constexpr int kBuf = CeCfg<FORM>::kBufBytes;
   const int col0 = t.col0 + c * 32;
   const int row0 = t.row - static_cast<int>(threadIdx.x & 31);
   if constexpr (MODE == kCeLse) {
     if (col0 < t.cols) {
-      if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
+      if constexpr (PICK) {
+        while (cur.col < c * 32 + 32) {
+          *cur.dot++ = pick_of(v, cur.col - c * 32);
+          cur.next();
+        }
+        __syncwarp();
+      } else if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           if (t.tgt - c * 32 == k) e.tlog[t.row] = __uint_as_float(v[k]);
@@ -274,7 +328,13 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
       float g[32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) g[k] = pow2(fmaf(__uint_as_float(v[k]), e.c2, -t.lse2));
-      if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
+      if constexpr (PICK) {
+        while (cur.col < c * 32 + 32) {
+          take_from(g, cur.col - c * 32, cur.share);
+          cur.next();
+        }
+        __syncwarp();
+      } else if (static_cast<unsigned>(t.tgt - c * 32) < 32u) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
           g[k] += t.tgt - c * 32 == k ? -1.0f : 0.0f;
@@ -300,26 +360,27 @@ __device__ __forceinline__ void ce_chunk(int c, const uint32_t (&v)[32], const C
 // A warp's 128 columns, 32 at a time: the next are on their way from tensor
 // memory while the ending works on the present ones; the accumulator is free
 // once the last have arrived.
-template <int MODE, int FORM>
+template <int MODE, int FORM, bool PICK>
 __device__ __forceinline__ void ce_tile(uint32_t tb, const AccFree& release, const CeTileArgs& t,
-                                        const CeEnd& e, int& flip, float& m, float& sum) {
+                                        const CeEnd& e, int& flip, float& m, float& sum,
+                                        CeCursor& cur) {
   uint32_t va[32], vb[32];
   tmem_ld32(tb, va);
   tmem_wait_ld();
   tmem_ld32(tb + 32, vb);
-  ce_chunk<MODE, FORM>(0, va, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM, PICK>(0, va, t, e, flip, m, sum, cur);
   tmem_wait_ld();
   tmem_ld32(tb + 64, va);
-  ce_chunk<MODE, FORM>(1, vb, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM, PICK>(1, vb, t, e, flip, m, sum, cur);
   tmem_wait_ld();
   tmem_ld32(tb + 96, vb);
-  ce_chunk<MODE, FORM>(2, va, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM, PICK>(2, va, t, e, flip, m, sum, cur);
   tmem_wait_ld();
   release();
-  ce_chunk<MODE, FORM>(3, vb, t, e, flip, m, sum);
+  ce_chunk<MODE, FORM, PICK>(3, vb, t, e, flip, m, sum, cur);
 }
 
-template <int FORM>
+template <int FORM, bool PICK>
 __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeLaunch a, const CeEnd e, const KernelCtl kctl) {
   using Cfg = CeCfg<FORM>;
@@ -581,8 +642,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         t.buf_row = u.split * e.m_pad + t.row;
         t.tgt = -1;
         t.lse2 = t.dl = 0.0f;
+        CeCursor cur;
+        cur.none();
         if ((mode == kCeLse || mode == kCeGrad) && t.row_ok) {
-          t.tgt = e.tgt[t.row] - t.v0 - t.col0;
+          if constexpr (PICK) cur.start(e, t.row, t.v0 + t.col0);
+          else t.tgt = e.tgt[t.row] - t.v0 - t.col0;
           if (mode == kCeGrad) {
             t.lse2 = e.lse2[t.row];
             t.dl = e.dl[t.row];
@@ -605,23 +669,23 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           if (!ok) break;
           if (mode == kCeLse) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ce_chunk<kCeLse, FORM>(c, v[c], t, e, flip, m, sum);
+            for (int c = 0; c < 4; ++c) ce_chunk<kCeLse, FORM, PICK>(c, v[c], t, e, flip, m, sum, cur);
             if (t.row_ok)
               e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
           } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ce_chunk<kCeGrad, FORM>(c, v[c], t, e, flip, m, sum);
+            for (int c = 0; c < 4; ++c) ce_chunk<kCeGrad, FORM, PICK>(c, v[c], t, e, flip, m, sum, cur);
           }
         } else if (mode == kCeLse) {
-          ce_tile<kCeLse, FORM>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeLse, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
           if (t.row_ok)
             e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
         } else if (mode == kCeGrad) {
-          ce_tile<kCeGrad, FORM>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeGrad, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
         } else if (mode == kCeDx) {
-          ce_tile<kCeDx, FORM>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeDx, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
         } else {
-          ce_tile<kCeDw, FORM>(tb, release, t, e, flip, m, sum);
+          ce_tile<kCeDw, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
         }
       }
     }
@@ -715,7 +779,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       if (scored) {
         const int at = slot + __popc(mask & ((1u << lane) - 1u));
         p.rows[at] = static_cast<int>(r);
-        p.tgt[at] = static_cast<int>(t);
+        p.tgt[at] = p.soft ? -1 : static_cast<int>(t);
         if (p.lse2) {
           p.lse2[at] = p.lse_in[r] * kLog2e;
           p.dl[at] = p.dloss ? p.dloss[r] : 1.0f;
@@ -760,8 +824,15 @@ static_assert(kCeSwapMax <= kJoinThreads, "a thread for each row that is taken a
 // Eight scored rows per CTA, 64 threads each: adds up each row's partial sums,
 // writes its loss and lse; the last CTA adds the CTAs' sums of losses in order
 // for the mean.
+//
+// PICK: the loss against shares q of several columns, sum_k q_k (ln q_k + lse - l_k).
+// All 64 threads of a row add up its list, in 64 bits: the loss may be a small
+// difference of large sums, and dividing by the shares' sum takes out what their
+// rounding leaves it off 1.
+template <bool PICK>
 __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   __shared__ float2 part[kJoinWarps][kJoinRows];
+  __shared__ double lists[PICK ? 3 : 1][kJoinWarps][kJoinRows];
   __shared__ double sums[kJoinWarps];
   __shared__ bool last;
   griddep_launch_dependents();
@@ -774,9 +845,33 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   int r = row;
   bool counts = true;
   if (warp == 0 && lane < kJoinRows && row < count) {
-    target = p.tlog[row];
+    if constexpr (!PICK) target = p.tlog[row];
     if (p.rows) r = p.rows[row];
     else counts = scored(p, row);
+  }
+  if constexpr (PICK) {
+    double s[3] = {0.0, 0.0, 0.0};  // q, q ln q, q times the product
+    if (row < count) {
+      const int64_t at = p.rows ? p.rows[row] : row;
+      const int2* list = p.pick.list + at * (p.pick.K + 1);
+      const float* dots = p.pick.dots + at * p.pick.K;
+      for (int k = threadIdx.x / kJoinRows; k < p.pick.K; k += kJoinThreads / kJoinRows) {
+        const int2 x = list[k];
+        if (x.x == INT_MAX) break;
+        const float q = __int_as_float(x.y);
+        s[0] += q;
+        if (q != 0.0f) {  // a share of zero takes no part (0 ln 0 = 0)
+          s[1] += static_cast<double>(q) * logf(q);
+          s[2] += static_cast<double>(q) * dots[k];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+      for (int o = kJoinRows; o < 32; o <<= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], o);
+      if (lane < kJoinRows) lists[i][warp][lane] = s[i];
+    }
   }
   float2 a = make_float2(-INFINITY, 0.0f);
   if (row < count) {
@@ -831,7 +926,18 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
       const double sum2 = static_cast<double>(log2f(a.y));
       const double lse = (static_cast<double>(a.x) + sum2) * kLn2;
       if (counts) {
-        loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * target) + sum2) * kLn2;
+        if constexpr (PICK) {
+          double q = 0.0, plogp = 0.0, dot = 0.0;
+          for (int w = 0; w < kJoinWarps; ++w) {
+            q += lists[0][w][lane];
+            plogp += lists[1][w][lane];
+            dot += lists[2][w][lane];
+          }
+          loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * (dot / q)) + sum2) * kLn2 +
+                 (plogp / q - log(q));
+        } else {
+          loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * target) + sum2) * kLn2;
+        }
         if (loss < 0.0) loss = 0.0;
       }
       p.loss[r] = static_cast<float>(loss);
@@ -914,11 +1020,11 @@ cudaLaunchConfig_t overlapped(int64_t grid, int threads, size_t smem, cudaStream
   return cfg;
 }
 
-template <int FORM>
+template <int FORM, bool PICK>
 cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ctl, int grid,
                    cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = ce_gemm_kernel<FORM>;
+  auto kernel = ce_gemm_kernel<FORM, PICK>;
   constexpr int smem = CeCfg<FORM>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -941,11 +1047,21 @@ cudaError_t run_ce(const CeLaunch& launch, const CeEnd& end, const KernelCtl& ct
 
 }  // namespace
 
+template <bool PICK>
+static cudaError_t run_ce_form(const CeLaunch& launch, const CeEnd& end, int streams, bool chains,
+                               int grid, const KernelCtl& ctl, cudaStream_t stream) {
+  return chains         ? run_ce<kCeChains, PICK>(launch, end, ctl, grid, stream)
+         : streams == 2 ? run_ce<kCeTwo, PICK>(launch, end, ctl, grid, stream)
+                        : run_ce<kCeLone, PICK>(launch, end, ctl, grid, stream);
+}
+
 cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, bool chains,
                            int grid, const KernelCtl& ctl, cudaStream_t stream) {
-  return chains         ? run_ce<kCeChains>(launch, end, ctl, grid, stream)
-         : streams == 2 ? run_ce<kCeTwo>(launch, end, ctl, grid, stream)
-                        : run_ce<kCeLone>(launch, end, ctl, grid, stream);
+  // the form with lists only where a product's ending reads them
+  bool pick = false;
+  for (const CeJob& j : launch.job) pick = pick || j.mode == kCeLse || j.mode == kCeGrad;
+  return pick && end.pick.list ? run_ce_form<true>(launch, end, streams, chains, grid, ctl, stream)
+                               : run_ce_form<false>(launch, end, streams, chains, grid, ctl, stream);
 }
 
 cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
@@ -964,7 +1080,8 @@ cudaError_t launch_ce_prep(const void* targets, bool ids64, CePrep p, int sms,
 cudaError_t launch_ce_join(const CeJoin& p, cudaStream_t stream) {
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = overlapped((p.M + kJoinRows - 1) / kJoinRows, kJoinThreads, 0, stream, attr);
-  return cudaLaunchKernelEx(&cfg, ce_join_kernel, p);
+  return p.pick.list ? cudaLaunchKernelEx(&cfg, ce_join_kernel<true>, p)
+                     : cudaLaunchKernelEx(&cfg, ce_join_kernel<false>, p);
 }
 
 cudaError_t launch_ce_dx(const CeDxOut& p, int M, int sms, cudaStream_t stream) {
