@@ -27,26 +27,78 @@ bool aligned(const void* p, size_t to) { return (reinterpret_cast<uintptr_t>(p) 
 gbf_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? GBF_OK : GBF_ERR_CUDA; }
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Row tiles per unit of work: two that share a column tile, or a lone one where
-// there is no second.
-int mlp_streams(int64_t M) { return M > kMlpRows ? 2 : 1; }
-
-// Parts of K of the product for dx, each with an fp32 buffer of its own: 16 at
-// most and none shorter than 8 K blocks.  With one row tile as many as give one
-// round of units over the pairs.  Else: none longer than half of what a pair has
-// to do in the launch, the weights' gradients among it.
-int mlp_dx_splits(int64_t M, int64_t D, int64_t F) {
-  const int64_t k = 2 * ceil_div64(F, kBK), d = ceil_div64(D, 256);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
-  if (mlp_streams(M) == 1)
-    return static_cast<int>(std::max<int64_t>(1, std::min(most, kMlpPairs / d)));
-  const int64_t all = ceil_div64(M, 512) * d * k +
-                      2 * ceil_div64(F, 512) * d * ceil_div64(M, kBK);
-  const int64_t half = std::max<int64_t>(1, all / kMlpPairs / 2);
-  return static_cast<int>(std::min(most, ceil_div64(k, half)));
+// Rows and products of one launch, without its tensor maps.
+void set_job(MbJob* j, int mode, int64_t rows, int64_t cols, int64_t k, bool a_mn, bool b_mn) {
+  j->mode = mode;
+  j->rows = static_cast<int>(rows);
+  j->cols = static_cast<int>(cols);
+  j->a_mn = a_mn;
+  j->b_mn = b_mn;
+  j->num_kb = j->kb_first = static_cast<int>(ceil_div64(k, kBK));
+  j->splits = 1;
+  j->m_pad = 0;
+}
+int64_t mlp_m_pad(int64_t M) { return ceil_div64(M, 512) * 512; }
+void set_dx(MbJob* j, int64_t M, int64_t D, int64_t F, int splits) {
+  set_job(j, kMbStore, M, D, F, false, true);
+  j->num_kb = 2 * j->kb_first;
+  j->splits = splits;
+  j->m_pad = static_cast<int>(mlp_m_pad(M));
 }
 
-int64_t mlp_m_pad(int64_t M) { return ceil_div64(M, 512) * 512; }
+// Row tiles per unit of work: one, or two that share a column tile where that is
+// estimated to be faster.
+struct MlpPlan {
+  int streams[2];  // of the two launches of the gradient
+  int dx_splits;   // parts of K of the product for dx, each with an fp32 buffer of its own
+};
+
+int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
+  const int64_t one = plan_mlp_launch(l, 1, kMlpPairs);
+  const int64_t two = M > kMlpRows ? plan_mlp_launch(l, 2, kMlpPairs) : one + 1;
+  if (cycles) *cycles = std::min(one, two);
+  return two < one ? 2 : 1;
+}
+
+// The first launch: dh and dw_down, the one with the longer K first.
+void first_jobs(MbLaunch* l, int64_t M, int64_t D, int64_t F, bool hidden, bool down, MbJob** dh,
+                MbJob** dw) {
+  const int at = D > M ? 0 : 1;
+  *dh = &l->job[at];
+  *dw = &l->job[2];
+  if (hidden) set_job(*dh, kMbGluGrad, M, F, D, false, true);
+  if (down) set_job(*dw, kMbStore, D, F, M, true, true);
+}
+
+// dx is split as the whole second launch (with dw_gate and dw_up) is fastest by the
+// estimate: 16 parts at most, none shorter than 8 K blocks.  Adding the parts costs a
+// launch and their traffic.
+MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
+  MlpPlan p{};
+  {
+    MbLaunch l{};
+    MbJob *dh, *dw;
+    first_jobs(&l, M, D, F, true, true, &dh, &dw);
+    p.streams[0] = faster_streams(&l, M, nullptr);
+  }
+  int64_t best = 0;
+  const int64_t k = 2 * ceil_div64(F, kBK);
+  for (int splits = 1; splits <= std::max<int64_t>(1, std::min<int64_t>(k / 8, 16)); ++splits) {
+    MbLaunch l{};
+    set_dx(&l.job[0], M, D, F, splits);
+    set_job(&l.job[1], kMbStore, F, D, M, true, true);
+    set_job(&l.job[2], kMbStore, F, D, M, true, true);
+    int64_t cycles;
+    const int streams = faster_streams(&l, M, &cycles);
+    if (splits > 1) cycles += 6000 + 8 * splits * M * D / 2500;  // bytes at about 4.8 TB/s
+    if (splits == 1 || cycles < best) {
+      best = cycles;
+      p.streams[1] = streams;
+      p.dx_splits = splits;
+    }
+  }
+  return p;
+}
 
 struct MlpGradWs {
   __nv_bfloat16 *dg, *du;
@@ -55,7 +107,7 @@ struct MlpGradWs {
 size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, MlpGradWs* w) {
   uint8_t* p = static_cast<uint8_t*>(base);
   const size_t act = align256(static_cast<size_t>(M) * F * 2);
-  const int splits = mlp_dx_splits(M, D, F);
+  const int splits = plan_mlp(M, D, F).dx_splits;
   const size_t parts =
       splits > 1 ? align256(static_cast<size_t>(splits) * mlp_m_pad(M) * D * 4) : 0;
   w->dg = reinterpret_cast<__nv_bfloat16*>(p);
@@ -111,30 +163,18 @@ bool map_parts(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
                      CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-void set_job(MbJob* j, int mode, int64_t rows, int64_t cols, int64_t k, bool a_mn, bool b_mn) {
-  j->mode = mode;
-  j->rows = static_cast<int>(rows);
-  j->cols = static_cast<int>(cols);
-  j->a_mn = a_mn;
-  j->b_mn = b_mn;
-  j->num_kb = j->kb_first = static_cast<int>(ceil_div64(k, kBK));
-  j->splits = 1;
-  j->m_pad = 0;
-}
-
 // The gradient of a weight: out [rows][cols] = a^T b over the M rows of a and b.
 bool set_dw(MbJob* j, const void* a, const void* b, const void* out, int64_t rows, int64_t cols,
-            int64_t M) {
+            int64_t M, int streams) {
   set_job(j, kMbStore, rows, cols, M, true, true);
   return map_mn(&j->a[0], a, rows, M) && map_mn(&j->b[0], b, cols, M) &&
-         map_out(&j->o[0], out, cols, rows, mlp_streams(M) == 1);
+         map_out(&j->o[0], out, cols, rows, streams == 1);
 }
 
-gbf_status_t run_launch(MbLaunch* l, int64_t M, const DeviceInfo& dev, unsigned* err,
+gbf_status_t run_launch(MbLaunch* l, int streams, const DeviceInfo& dev, unsigned* err,
                         cudaStream_t s) {
-  const int streams = mlp_streams(M);
   plan_mlp_launch(l, streams, dev.pairs);
-  if (l->longs + l->shorts == 0) return GBF_OK;
+  if (l->job[0].units + l->shorts == 0) return GBF_OK;
   return cuda_status(launch_mlp_train(*l, streams, lib_ctl(err, 2 * l->pairs), s));
 }
 
@@ -183,7 +223,8 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
       !map_out(&j.o[0], h, F, M, false) || !map_out(&j.o[1], g, F, M, false) ||
       !map_out(&j.o[2], u, F, M, false))
     return GBF_ERR_CUDA;
-  if ((st = run_launch(&l, M, *dev, err, reinterpret_cast<cudaStream_t>(stream))) != GBF_OK)
+  if ((st = run_launch(&l, faster_streams(&l, M, nullptr), *dev, err,
+                       reinterpret_cast<cudaStream_t>(stream))) != GBF_OK)
     return st;
   return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
                        GBF_ACT_IDENTITY, nullptr, 0, stream);
@@ -220,36 +261,33 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
     return GBF_OK;
   }
   const bool hidden = dx || dw_gate || dw_up;
+  const MlpPlan plan = plan_mlp(M, D, F);
   MbLaunch first{}, then{};
+  MbJob *dh, *dw;
+  first_jobs(&first, M, D, F, hidden, dw_down != nullptr, &dh, &dw);
   first.act = act;
-  if (hidden) {
-    MbJob& j = first.job[1];
-    set_job(&j, kMbGluGrad, M, F, D, false, true);
-    first.g = static_cast<const __nv_bfloat16*>(g);
-    first.u = static_cast<const __nv_bfloat16*>(u);
-    if (!map_k(&j.a[0], dout, D, M) || !map_mn(&j.b[0], w_down, F, D) ||
-        !map_out(&j.o[0], ws.dg, F, M, false) || !map_out(&j.o[1], ws.du, F, M, false))
-      return GBF_ERR_CUDA;
-  }
-  if (dw_down && !set_dw(&first.job[2], dout, h, dw_down, D, F, M)) return GBF_ERR_CUDA;
-  if ((st = run_launch(&first, M, *dev, err, s)) != GBF_OK || !hidden) return st;
-  const int splits = mlp_dx_splits(M, D, F);
+  first.g = static_cast<const __nv_bfloat16*>(g);
+  first.u = static_cast<const __nv_bfloat16*>(u);
+  if (hidden && (!map_k(&dh->a[0], dout, D, M) || !map_mn(&dh->b[0], w_down, F, D) ||
+                 !map_out(&dh->o[0], ws.dg, F, M, false) || !map_out(&dh->o[1], ws.du, F, M, false)))
+    return GBF_ERR_CUDA;
+  if (dw_down && !set_dw(dw, dout, h, dw_down, D, F, M, plan.streams[0])) return GBF_ERR_CUDA;
+  if ((st = run_launch(&first, plan.streams[0], *dev, err, s)) != GBF_OK || !hidden) return st;
+  const int splits = plan.dx_splits;
+  const int streams = plan.streams[1];
   if (dx) {
     MbJob& j = then.job[0];
-    set_job(&j, kMbStore, M, D, F, false, true);
-    j.num_kb = 2 * j.kb_first;
-    j.splits = splits;
-    j.m_pad = static_cast<int>(mlp_m_pad(M));
+    set_dx(&j, M, D, F, splits);
     if (!map_k(&j.a[0], ws.dg, F, M) || !map_k(&j.a[1], ws.du, F, M) ||
         !map_mn(&j.b[0], w_gate, D, F) || !map_mn(&j.b[1], w_up, D, F) ||
         !(splits > 1 ? map_parts(&j.o[0], ws.parts, D, splits * mlp_m_pad(M))
-                     : map_out(&j.o[0], dx, D, M, mlp_streams(M) == 1)))
+                     : map_out(&j.o[0], dx, D, M, streams == 1)))
       return GBF_ERR_CUDA;
   }
-  if ((dw_gate && !set_dw(&then.job[1], ws.dg, x, dw_gate, F, D, M)) ||
-      (dw_up && !set_dw(&then.job[2], ws.du, x, dw_up, F, D, M)))
+  if ((dw_gate && !set_dw(&then.job[1], ws.dg, x, dw_gate, F, D, M, streams)) ||
+      (dw_up && !set_dw(&then.job[2], ws.du, x, dw_up, F, D, M, streams)))
     return GBF_ERR_CUDA;
-  if ((st = run_launch(&then, M, *dev, err, s)) != GBF_OK) return st;
+  if ((st = run_launch(&then, streams, *dev, err, s)) != GBF_OK) return st;
   if (!dx || splits == 1) return GBF_OK;
   return cuda_status(launch_mlp_sum(ws.parts, static_cast<__nv_bfloat16*>(dx), M * D,
                                     mlp_m_pad(M) * D, splits, dev->sms, s));

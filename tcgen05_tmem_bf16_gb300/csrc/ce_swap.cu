@@ -229,6 +229,23 @@ __global__ void __launch_bounds__(kSwThreads, 2)
     for (int t = blockIdx.x, l = 0; t < tiles; ++l) {
       const int buf = l & two_bufs;
       float before[16];  // of the next 16 rows, on their way meanwhile
+      // PICK: rows lane, lane + 32, ...: number, and entries in this warp's 32 columns
+      constexpr int kRows = PICK ? (MPAD + 31) / 32 : 1;
+      int pick_row[kRows], pick_at[kRows], pick_n[kRows];
+      if constexpr (PICK) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int m = i * 32 + lane;
+          pick_row[i] = pick_at[i] = pick_n[i] = 0;
+          if (seg + seg_kb >= num_kb && m < count && t * 128 + q * 32 < a.cols) {
+            pick_row[i] = GRAD ? row_tgt[m] : m;
+            const uint16_t* at = e.pick.at + static_cast<int64_t>(pick_row[i]) * e.pick.stride +
+                                 ((a.v0 + t * 128 + q * 32) >> 5);
+            pick_at[i] = at[0];
+            pick_n[i] = at[1] - pick_at[i];
+          }
+        }
+      }
       if (seg > 0) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) before[k] = __ldcg(part + k * 128);
@@ -243,16 +260,16 @@ __global__ void __launch_bounds__(kSwThreads, 2)
 #pragma unroll 1
       for (int c = 0; c < MPAD / 16; ++c) {
         float v[16];
-        // lanes 0-15: the entries of row c * 16 + lane in this warp's 32 columns
-        int pick_row = 0, pick_at = 0, pick_n = 0;
-        if (PICK && last && lane < 16 && c * 16 + lane < count) {
-          pick_row = GRAD ? row_tgt[c * 16 + lane] : c * 16 + lane;
-          const uint16_t* at = e.pick.at + static_cast<int64_t>(pick_row) * e.pick.stride +
-                               ((a.v0 + t * 128 + q * 32) >> 5);
-          if (t * 128 + q * 32 < a.cols) {
-            pick_at = at[0];
-            pick_n = at[1] - pick_at;
-          }
+        // the same of the chunk's rows: lanes 16 (c & 1) + k
+        int row_c = 0, at_c = 0, n_c = 0;
+        if constexpr (PICK) {
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            if (c / 2 == i) {
+              row_c = pick_row[i];
+              at_c = pick_at[i];
+              n_c = pick_n[i];
+            }
         }
         if (c < chunks) {
           uint32_t r[16];
@@ -293,21 +310,37 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             }
           }
           if constexpr (PICK) {
-            const unsigned some = __ballot_sync(0xFFFFFFFFu, pick_n > 0);
+            // A row's entries here are at most 32, their columns differ and ascend: a lane
+            // reads one entry of each row, and finds its own column's by counting the
+            // columns below it.  (Entry after entry by all lanes: 64 rows x 32000 x 4096
+            // 81 us, since half of the entries are in the first tile, so 49.)
+            const unsigned some =
+                __ballot_sync(0xFFFFFFFFu, n_c > 0) >> (16 * (c & 1)) & 0xFFFFu;
+            if (some) {
+              int2 x[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              if ((some >> k) & 1u) {
-                const int64_t row = __shfl_sync(0xFFFFFFFFu, pick_row, k);
-                const int n = __shfl_sync(0xFFFFFFFFu, pick_n, k);
-                const int2* list = e.pick.list + row * (e.pick.K + 1) +
-                                   __shfl_sync(0xFFFFFFFFu, pick_at, k);
-                for (int i = 0; i < n; ++i) {
-                  const int2 x = list[i];
-                  if (x.x == a.v0 + col) f[k] -= __int_as_float(x.y);
-                }
+              for (int k = 0; k < 16; ++k) {
+                const int from = 16 * (c & 1) + k;
+                const int64_t row = __shfl_sync(0xFFFFFFFFu, row_c, from);
+                const int at = __shfl_sync(0xFFFFFFFFu, at_c, from);
+                const int n = __shfl_sync(0xFFFFFFFFu, n_c, from);
+                x[k] = make_int2(-1, 0);
+                if (lane < n) x[k] = e.pick.list[row * (e.pick.K + 1) + at + lane];
               }
-              if (c * 16 + k < count) f[k] *= row_dl[c * 16 + k];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                if (!((some >> k) & 1u)) continue;
+                const unsigned bit =
+                    x[k].x < 0 ? 0u : 1u << (x[k].x - (a.v0 + t * 128 + q * 32));
+                const unsigned cols = __reduce_or_sync(0xFFFFFFFFu, bit);
+                const int share =
+                    __shfl_sync(0xFFFFFFFFu, x[k].y, __popc(cols & ((1u << lane) - 1u)));
+                if ((cols >> lane) & 1u) f[k] -= __int_as_float(share);
+              }
             }
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              if (c * 16 + k < count) f[k] *= row_dl[c * 16 + k];
           }
           if (col < a.cols) {
             __nv_bfloat16* dst = a.gt + static_cast<int64_t>(col) * MPAD + c * 16;
@@ -344,13 +377,18 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           const float m2 = fmaxf(top, top2);
           const float ref2 = m2 == -INFINITY ? 0.0f : m2;
           sum = fmaf(sum, sw_pow2(top - ref2), sum2 * sw_pow2(top2 - ref2));
+          // each row's entries by the lane that holds their places
+          if constexpr (PICK) {
+            if (lane / 16 == (c & 1)) {
+              const int2* list = e.pick.list + static_cast<int64_t>(row_c) * (e.pick.K + 1) + at_c;
+              float* dots = e.pick.dots + static_cast<int64_t>(row_c) * e.pick.K + at_c;
+              for (int i = 0; i < n_c; ++i)
+                dots[i] = my_turn[(list[i].x - base) * 17 + (lane & 15)];
+            }
+          }
           if (lane < 16 && m < count) {
             e.part[static_cast<int64_t>(4 * t + q) * e.M + m] = make_float2(m2, sum);
-            if constexpr (PICK) {
-              const int2* list = e.pick.list + static_cast<int64_t>(m) * (e.pick.K + 1) + pick_at;
-              float* dots = e.pick.dots + static_cast<int64_t>(m) * e.pick.K + pick_at;
-              for (int i = 0; i < pick_n; ++i) dots[i] = my_turn[(list[i].x - base) * 17 + lane];
-            } else {
+            if constexpr (!PICK) {
               const int at = row_tgt[m] - base;
               if (row_tgt[m] >= 0 && at >= 0 && at < 32) e.tlog[m] = my_turn[at * 17 + lane];
             }

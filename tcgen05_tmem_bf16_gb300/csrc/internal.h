@@ -287,6 +287,11 @@ cudaError_t launch_ce_lists(const CeLists& p, int sms, cudaStream_t stream);
 // Products of a gated MLP block that is trained, and of its gradient
 // (mlp_train.cu): up to three per launch, none of which reads what another writes.
 enum MbMode { kMbNone = 0, kMbStore = 1, kMbGlu = 2, kMbGluGrad = 3 };
+struct MbDiv {  // x / by == __umulhi(x, mul) >> shift, x < 2^31
+  int by;
+  uint32_t mul;
+  int shift;
+};
 struct MbJob {
   // [1]: of a second pair of operands, whose K blocks follow the first's; kMbGlu: b[1] Wu
   CUtensorMap a[2], b[2];
@@ -296,19 +301,23 @@ struct MbJob {
   int a_mn, b_mn;    // an operand is read along its columns: it holds one row per k
   int num_kb;        // 64-wide K blocks in all
   int kb_first;      // of the first pair of operands (num_kb: there is no second)
-  int splits;        // parts of K, each with its own fp32 rows in o[0] (job 0 only)
+  int splits;        // parts of K, each with its own fp32 rows in o[0] (kMbStore)
   int m_pad;         // rows between them
-  int m_units, n_tiles, units;  // by plan_mlp_launch
+  // by plan_mlp_launch: units, and the divisors of a unit's number
+  int units, full_groups;
+  MbDiv group, last, tiles, parts;
 };
 constexpr int kMbJobs = 3;
 struct MbLaunch {
   MbJob job[kMbJobs];  // job 0: the one with the longest units, if any
   const __nv_bfloat16 *g, *u;  // kMbGluGrad
   int act;
-  int longs, extra, skip, shorts, pairs;  // by plan_mlp_launch
+  // by plan_mlp_launch: units of job 0 that every pair has, pairs that have one more,
+  // rounds of the others' units that those sit out, units of the others, pairs
+  int longs_each, extra, skip, shorts, pairs;
 };
-// The launch's units dealt to CTA pairs, npairs at most (pairs: how many).
-void plan_mlp_launch(MbLaunch* l, int streams, int npairs);
+// The launch's units dealt to CTA pairs, npairs at most; about how many cycles it takes.
+int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs);
 cudaError_t launch_mlp_train(const MbLaunch& launch, int streams, const KernelCtl& ctl,
                              cudaStream_t stream);
 cudaError_t launch_mlp_sum(const float* parts, __nv_bfloat16* dx, int64_t n, int64_t stride,

@@ -826,13 +826,15 @@ static_assert(kCeSwapMax <= kJoinThreads, "a thread for each row that is taken a
 // for the mean.
 //
 // PICK: the loss against shares q of several columns, sum_k q_k (ln q_k + lse - l_k).
-// All 64 threads of a row add up its list, in 64 bits: the loss may be a small
-// difference of large sums, and dividing by the shares' sum takes out what their
-// rounding leaves it off 1.
+// Once lse is known, all 64 threads of a row add up its list: each term is a
+// difference of its own, taken before anything is added, so fp32 holds it (in 64 bits
+// the kernel took twice as long).  Shares that add up to 1 + d give the sum over 1 + d
+// less log(1 + d) = d.
 template <bool PICK>
 __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   __shared__ float2 part[kJoinWarps][kJoinRows];
-  __shared__ double lists[PICK ? 3 : 1][kJoinWarps][kJoinRows];
+  __shared__ float2 lists[PICK ? kJoinWarps : 1][kJoinRows];
+  __shared__ float2 row_lse[kJoinRows];  // of PICK: (maximum, log2 of the sum)
   __shared__ double sums[kJoinWarps];
   __shared__ bool last;
   griddep_launch_dependents();
@@ -849,29 +851,15 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     if (p.rows) r = p.rows[row];
     else counts = scored(p, row);
   }
-  if constexpr (PICK) {
-    double s[3] = {0.0, 0.0, 0.0};  // q, q ln q, q times the product
-    if (row < count) {
-      const int64_t at = p.rows ? p.rows[row] : row;
-      const int2* list = p.pick.list + at * (p.pick.K + 1);
-      const float* dots = p.pick.dots + at * p.pick.K;
-      for (int k = threadIdx.x / kJoinRows; k < p.pick.K; k += kJoinThreads / kJoinRows) {
-        const int2 x = list[k];
-        if (x.x == INT_MAX) break;
-        const float q = __int_as_float(x.y);
-        s[0] += q;
-        if (q != 0.0f) {  // a share of zero takes no part (0 ln 0 = 0)
-          s[1] += static_cast<double>(q) * logf(q);
-          s[2] += static_cast<double>(q) * dots[k];
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-#pragma unroll
-      for (int o = kJoinRows; o < 32; o <<= 1) s[i] += __shfl_xor_sync(0xFFFFFFFFu, s[i], o);
-      if (lane < kJoinRows) lists[i][warp][lane] = s[i];
-    }
+  // PICK: this thread's first entry, on its way meanwhile
+  const int64_t at = PICK && row < count ? (p.rows ? p.rows[row] : row) : 0;
+  const int2* list = PICK ? p.pick.list + at * (p.pick.K + 1) : nullptr;
+  const float* dots = PICK ? p.pick.dots + at * p.pick.K : nullptr;
+  int2 entry = make_int2(INT_MAX, 0);
+  float dot = 0.0f;
+  if (PICK && row < count && static_cast<int>(threadIdx.x) / kJoinRows < p.pick.K) {
+    entry = list[threadIdx.x / kJoinRows];
+    dot = dots[threadIdx.x / kJoinRows];  // written for the entries that there are
   }
   float2 a = make_float2(-INFINITY, 0.0f);
   if (row < count) {
@@ -917,6 +905,45 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
       b.y = __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
       a = join(a, b);
     }
+    if constexpr (PICK) {
+      if (lane < kJoinRows) row_lse[lane] = make_float2(a.x, log2f(a.y));
+    }
+  }
+  float2 sum_q = make_float2(0.0f, 0.0f);  // PICK: of q, of the terms
+  if constexpr (PICK) {
+    __syncthreads();
+    const float2 z = row_lse[lane & (kJoinRows - 1)];
+    float2 s = make_float2(0.0f, 0.0f);
+    for (int k = threadIdx.x / kJoinRows; entry.x != INT_MAX;) {
+      const float q = __int_as_float(entry.y);
+      s.x += q;
+      // a share of zero takes no part (0 ln 0 = 0); of powers of two by the same c2
+      // as the maximum, in one rounding
+      if (q != 0.0f)
+        s.y = fmaf(q, fmaf(static_cast<float>(kLn2), fmaf(-p.c2, dot, z.x) + z.y, logf(q)), s.y);
+      k += kJoinThreads / kJoinRows;
+      entry.x = INT_MAX;
+      if (k < p.pick.K) {
+        entry = list[k];
+        dot = dots[k];
+      }
+    }
+#pragma unroll
+    for (int o = kJoinRows; o < 32; o <<= 1) {
+      s.x += __shfl_xor_sync(0xFFFFFFFFu, s.x, o);
+      s.y += __shfl_xor_sync(0xFFFFFFFFu, s.y, o);
+    }
+    if (lane < kJoinRows) lists[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && lane < kJoinRows) {
+#pragma unroll
+      for (int w = 0; w < kJoinWarps; ++w) {
+        sum_q.x += lists[w][lane].x;
+        sum_q.y += lists[w][lane].y;
+      }
+    }
+  }
+  if (warp == 0) {
     double loss = 0.0;
     if (lane < kJoinRows && row < count) {
       // A confident row's loss is a small difference: in 64 bits, and of powers of
@@ -927,14 +954,8 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
       const double lse = (static_cast<double>(a.x) + sum2) * kLn2;
       if (counts) {
         if constexpr (PICK) {
-          double q = 0.0, plogp = 0.0, dot = 0.0;
-          for (int w = 0; w < kJoinWarps; ++w) {
-            q += lists[0][w][lane];
-            plogp += lists[1][w][lane];
-            dot += lists[2][w][lane];
-          }
-          loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * (dot / q)) + sum2) * kLn2 +
-                 (plogp / q - log(q));
+          const float d = sum_q.x - 1.0f;
+          loss = static_cast<double>(fmaf(sum_q.y, -d, sum_q.y) - d);
         } else {
           loss = ((static_cast<double>(a.x) - static_cast<double>(p.c2) * target) + sum2) * kLn2;
         }

@@ -62,9 +62,14 @@ struct MbUnit {
 
 // The n-th unit of a pair; false after its last.  The units of job 0 are long;
 // they are dealt out first, one per pair and round, and the pairs that got one more
-// than the others sit out `skip` rounds of the short ones.
+// than the others sit out `skip` rounds of the short ones.  (Every role of a CTA
+// computes this for every unit, so it does without divisions: the divisors are the
+// launch's, their reciprocals the host's.)
+__device__ __forceinline__ uint32_t mb_div(uint32_t x, const MbDiv& d) {
+  return d.by == 1 ? x : __umulhi(x, d.mul) >> d.shift;
+}
 __device__ __forceinline__ bool mb_unit(const MbLaunch& a, int pair, int npairs, int n, MbUnit& u) {
-  const int mine = a.longs / npairs + (pair < a.extra ? 1 : 0);
+  const int mine = a.longs_each + (pair < a.extra ? 1 : 0);
   int t;
   if (n < mine) {
     t = n * npairs + pair;
@@ -86,46 +91,74 @@ __device__ __forceinline__ bool mb_unit(const MbLaunch& a, int pair, int npairs,
   u.split = 0;
   u.kb0 = 0;
   u.kb1 = j.num_kb;
-  if (u.job == 0 && j.splits > 1) {
-    const unsigned tiles = j.m_units * j.n_tiles;
-    u.split = static_cast<unsigned>(t) / tiles;
-    t -= u.split * tiles;
-    u.kb0 = static_cast<unsigned>(u.split * j.num_kb) / static_cast<unsigned>(j.splits);
-    u.kb1 = static_cast<unsigned>((u.split + 1) * j.num_kb) / static_cast<unsigned>(j.splits);
+  if (j.splits > 1) {
+    u.split = mb_div(t, j.tiles);
+    t -= u.split * j.tiles.by;
+    u.kb0 = mb_div(u.split * j.num_kb, j.parts);
+    u.kb1 = mb_div((u.split + 1) * j.num_kb, j.parts);
   }
-  tile_coords(t, j.m_units, j.n_tiles, u.mp, u.nb, kMbGroup);
+  // as tile_coords: groups of kMbGroup units of rows, the column tile slowest
+  const int g = mb_div(t, j.group);
+  const int local = t - g * j.group.by;
+  if (g < j.full_groups) {
+    u.nb = local / kMbGroup;
+    u.mp = g * kMbGroup + local % kMbGroup;
+  } else {
+    u.nb = mb_div(local, j.last);
+    u.mp = g * kMbGroup + local - u.nb * j.last.by;
+  }
   return true;
 }
 
-// Activation and derivative, as act_apply computes the former.
+__device__ __forceinline__ float mb_pow2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float mb_rcp(float x) {  // 0 for infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float mb_clamp(float v, float most) {  // a NaN stays one
+  float y;
+  asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}"
+      : "=f"(y) : "f"(v), "f"(most), "f"(-most));
+  return y;
+}
+
+// Activation and derivative, in as few operations as it takes: they run on every
+// element of dh, and with a short K (D = 1000) the ending is what a unit waits for.
 template <int ACT>
 __device__ __forceinline__ void act_both(float v, float& y, float& dy) {
+  constexpr float kLog2e = 1.4426950408889634f;
   if constexpr (ACT == kActRelu) {
     y = fmaxf(v, 0.0f);
     dy = v > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == kActSilu) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-v));
+    const float s = mb_rcp(1.0f + mb_pow2(-kLog2e * v));
     y = v * s;
     dy = s * fmaf(v, 1.0f - s, 1.0f);
   } else if constexpr (ACT == kActGeluTanh) {
-    // v s(2 z), z = c (v + k v^3):  s + v s (1 - s) 2 c (1 + 3 k v^2)
+    // y = v s(2 z), z = c (v + k v^3);  y' = s + s (1 - s) v 2 c (1 + 3 k v^2).  From
+    // |v| = 30 on s is 0 or 1 and the second term 0; v^2 stays in range.
     constexpr float c = 0.7978845608028654f, k = 0.044715f;
-    const float z = c * fmaf(k * v, v * v, v);
-    const float s = __fdividef(1.0f, 1.0f + __expf(-2.0f * z));
+    const float x = mb_clamp(v, 30.0f);
+    const float x2 = x * x;
+    const float s = mb_rcp(1.0f + mb_pow2(x * fmaf(-2.0f * kLog2e * c * k, x2, -2.0f * kLog2e * c)));
     y = v * s;
-    const float t = s * (1.0f - s);  // 0 where v^2 may overflow
-    dy = t == 0.0f ? s : fmaf(v * t, 2.0f * c * fmaf(3.0f * k * v, v, 1.0f), s);
+    dy = fmaf(fmaf(-s, s, s) * x, fmaf(6.0f * c * k, x2, 2.0f * c), s);
   } else {
     y = v;
     dy = 1.0f;
   }
 }
 
-// 32 columns of a row of bf16; zeros outside.
-__device__ __forceinline__ void load_row32(uint4 (&d)[4], const __nv_bfloat16* p, int64_t row,
+// 16 columns of a row of bf16; zeros outside.
+__device__ __forceinline__ void load_row16(uint4 (&d)[2], const __nv_bfloat16* p, int64_t row,
                                            int col, int rows, int cols, uint64_t pol) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v)
+  for (int v = 0; v < 2; ++v)
     d[v] = row < rows && col + 8 * v < cols ? ld_stream_u4(p + row * cols + col + 8 * v, pol)
                                             : make_uint4(0u, 0u, 0u, 0u);
 }
@@ -140,15 +173,15 @@ __device__ __forceinline__ void glu_pack(const uint32_t (&g)[32], const uint32_t
         act_apply<ACT>(__uint_as_float(g[2 * k + 1])) * __uint_as_float(u[2 * k + 1]));
 }
 
+// dg and du of 16 columns.
 template <int ACT>
-__device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[32], const uint4 (&g4)[4],
-                                              const uint4 (&u4)[4], uint32_t (&dg)[16],
-                                              uint32_t (&du)[16]) {
+__device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[16], const uint4 (&g2)[2],
+                                              const uint4 (&u2)[2], uint32_t* dg, uint32_t* du) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
+  for (int v = 0; v < 2; ++v) {
     float g[8], u[8], a[8], b[8];
-    unpack8(g4[v], g);
-    unpack8(u4[v], u);
+    unpack8(g2[v], g);
+    unpack8(u2[v], u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float y, dy;
@@ -163,6 +196,78 @@ __device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[32], const ui
       du[4 * v + i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
     }
   }
+}
+
+// A warp's 128 columns of a tile of dh, whose first 16 columns of g and u are in g2
+// and u2.  The next 16 columns' are asked for before the present ones' arithmetic
+// (32 ahead do not fit in the registers).
+template <int ACT, int BUF>
+__device__ __forceinline__ void glu_grad_tile(uint32_t tb, const AccFree& release,
+                                              const MbLaunch& a, const MbJob& j, uint4 (&g2)[2],
+                                              uint4 (&u2)[2], uint8_t* bufs, int& flip, int row0,
+                                              int col0, uint64_t first) {
+  const int row = row0 + static_cast<int>(threadIdx.x & 31);
+  const uint64_t last = policy_evict_last();
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    const int col = col0 + c * 32;
+    uint32_t dg[16], du[16];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 gn[2], un[2];
+      if (h == 0 || c < 3) {
+        load_row16(gn, a.g, row, col + 16 * h + 16, j.rows, j.cols, first);
+        load_row16(un, a.u, row, col + 16 * h + 16, j.rows, j.cols, first);
+      }
+      uint32_t v[16];
+      tmem_ld16(tb + c * 32 + 16 * h, v);
+      tmem_wait_ld();
+      glu_grad_pack<ACT>(v, g2, u2, dg + 8 * h, du + 8 * h);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        g2[i] = gn[i];
+        u2[i] = un[i];
+      }
+    }
+    if (c == 3) release();
+    put_chunk<false>(bufs, BUF, flip, 0, dg, &j.o[0], row0, col, j.rows, j.cols, last);
+    put_chunk<false>(bufs, BUF, flip, 0, du, &j.o[1], row0, col, j.rows, j.cols, last);
+  }
+}
+
+// A warp's 128 columns of a product as they are, to bf16 or to the fp32 rows of its
+// part of K: the next 32 are on their way from tensor memory meanwhile.
+template <bool WIDE, int BUF>
+__device__ __forceinline__ void store_tile(uint32_t tb, const AccFree& release, const MbJob& j,
+                                           uint8_t* bufs, int& flip, int row0, int col0, int part,
+                                           uint64_t first) {
+  auto put = [&](int c, const uint32_t (&v)[32]) {
+    const int col = col0 + c * 32;
+    if (j.splits > 1) {
+      put_chunk_f32(bufs, BUF, flip, v, &j.o[0], part * j.m_pad + row0, col, j.cols, row0 < j.rows,
+                    false);
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        w[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+      put_chunk<WIDE>(bufs, BUF, flip, c, w, &j.o[0], row0, col, j.rows, j.cols, first);
+    }
+  };
+  uint32_t va[32], vb[32];
+  tmem_ld32(tb, va);
+  tmem_wait_ld();
+  tmem_ld32(tb + 32, vb);
+  put(0, va);
+  tmem_wait_ld();
+  tmem_ld32(tb + 64, va);
+  put(1, vb);
+  tmem_wait_ld();
+  tmem_ld32(tb + 96, vb);
+  put(2, va);
+  tmem_wait_ld();
+  release();
+  put(3, vb);
 }
 
 template <int STREAMS>
@@ -350,9 +455,9 @@ __global__ void __launch_bounds__(kMbThreads, 1)
         const AccFree release{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0,
                               leader};
         const int col0 = j.mode == kMbGlu ? u.nb * 128 + half * 64 : u.nb * kMbTile + half * 128;
-        uint4 g4[4], u4[4];
+        uint4 g2[2], u2[2];
         if (j.mode == kMbGluGrad) {
-          // the first 32 columns of g and u on their way, the others into L2
+          // the first 16 columns of g and u on their way, the others into L2
           if (row0 + lane < j.rows) {
             const int64_t at = static_cast<int64_t>(row0 + lane) * j.cols;
             if (col0 + 64 < j.cols) {
@@ -360,8 +465,8 @@ __global__ void __launch_bounds__(kMbThreads, 1)
               asm volatile("prefetch.global.L2 [%0];" ::"l"(a.u + at + col0 + 64));
             }
           }
-          load_row32(g4, a.g, row0 + lane, col0, j.rows, j.cols, first);
-          load_row32(u4, a.u, row0 + lane, col0, j.rows, j.cols, first);
+          load_row16(g2, a.g, row0 + lane, col0, j.rows, j.cols, first);
+          load_row16(u2, a.u, row0 + lane, col0, j.rows, j.cols, first);
         }
         ok = wait_bar(&tfull[acc], use & 1, ctl, kSiteEpiAccFull);
         if (!ok) break;
@@ -395,48 +500,27 @@ __global__ void __launch_bounds__(kMbThreads, 1)
                              first);
           }
         } else if (j.mode == kMbGluGrad) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32], dg[16], du[16];
-            tmem_ld32(tb + half * 128 + c * 32, v);
-            tmem_wait_ld();
-            if (c == 3) release();
-            switch (a.act) {
-              case kActRelu: glu_grad_pack<kActRelu>(v, g4, u4, dg, du); break;
-              case kActSilu: glu_grad_pack<kActSilu>(v, g4, u4, dg, du); break;
-              case kActGeluTanh: glu_grad_pack<kActGeluTanh>(v, g4, u4, dg, du); break;
-              default: glu_grad_pack<kActIdentity>(v, g4, u4, dg, du); break;
-            }
-            const int col = col0 + c * 32;
-            if (c < 3) {
-              load_row32(g4, a.g, row0 + lane, col + 32, j.rows, j.cols, first);
-              load_row32(u4, a.u, row0 + lane, col + 32, j.rows, j.cols, first);
-            }
-            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, dg, &j.o[0], row0, col, j.rows, j.cols,
-                             policy_evict_last());
-            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, du, &j.o[1], row0, col, j.rows, j.cols,
-                             policy_evict_last());
+          constexpr int kBuf = Cfg::kBufBytes;
+          const uint32_t t = tb + half * 128;
+          switch (a.act) {
+            case kActRelu:
+              glu_grad_tile<kActRelu, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0, first);
+              break;
+            case kActSilu:
+              glu_grad_tile<kActSilu, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0, first);
+              break;
+            case kActGeluTanh:
+              glu_grad_tile<kActGeluTanh, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0,
+                                                first);
+              break;
+            default:
+              glu_grad_tile<kActIdentity, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0,
+                                                first);
+              break;
           }
         } else {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t v[32];
-            tmem_ld32(tb + half * 128 + c * 32, v);
-            tmem_wait_ld();
-            if (c == 3) release();
-            const int col = col0 + c * 32;
-            if (j.splits > 1) {
-              put_chunk_f32(bufs, Cfg::kBufBytes, flip, v, &j.o[0], u.split * j.m_pad + row0, col,
-                            j.cols, row0 < j.rows, false);
-            } else {
-              uint32_t w[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                w[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-              put_chunk<Cfg::kWide>(bufs, Cfg::kBufBytes, flip, c, w, &j.o[0], row0, col, j.rows,
-                                    j.cols, first);
-            }
-          }
+          store_tile<Cfg::kWide, Cfg::kBufBytes>(tb + half * 128, release, j, bufs, flip, row0,
+                                                 col0, u.split, first);
         }
       }
     }
@@ -509,31 +593,65 @@ cudaError_t run_mb(const MbLaunch& launch, const KernelCtl& ctl, int grid, cudaS
 
 }  // namespace
 
-void plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
-  constexpr int kUnitCost = 4;  // a unit's ending, in K blocks of its main loop
-  int64_t blocks = 0;
+namespace {
+
+MbDiv div_by(int d) {  // exact for 31-bit numbers: the reciprocal is rounded up
+  MbDiv r;
+  r.by = std::max(d, 1);
+  int bits = 0;
+  while ((int64_t(1) << bits) < r.by) ++bits;
+  r.shift = bits - 1;  // of 1, whose reciprocal does not fit, unused
+  r.mul = static_cast<uint32_t>(((uint64_t(1) << (31 + bits)) + r.by - 1) / r.by);
+  return r;
+}
+
+// About how many cycles a unit keeps its pair, by its K blocks and its ending.  A
+// lone row tile's MMAs take 150 cycles each and its ending overlaps the next unit's;
+// two row tiles' share the tensor pipe at 128, and the next unit waits for the first
+// one's ending.
+int64_t unit_cycles(int mode, int64_t kb, int streams) {
+  const int64_t end = mode == kMbGluGrad ? 5000 : mode == kMbGlu ? 4000 : 2600;
+  return streams == 1 ? std::max<int64_t>(600 * kb, end) + 300
+                      : std::max<int64_t>(1024 * kb, 2 * end) + end;
+}
+
+}  // namespace
+
+int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
+  int64_t work = 0, cycles[kMbJobs] = {};
   for (int i = 0; i < kMbJobs; ++i) {
     MbJob& j = l->job[i];
-    j.units = j.m_units = j.n_tiles = 0;
+    j.units = 0;
     if (j.mode == kMbNone) continue;
     const int bn = j.mode == kMbGlu ? 128 : kMbTile;
-    j.m_units = (j.rows + kMbTile * streams - 1) / (kMbTile * streams);
-    j.n_tiles = (j.cols + bn - 1) / bn;
-    j.units = j.m_units * j.n_tiles * j.splits;
-    if (i > 0) blocks += static_cast<int64_t>(j.units) * (j.num_kb + kUnitCost);
+    const int m_units = (j.rows + kMbTile * streams - 1) / (kMbTile * streams);
+    const int n_tiles = (j.cols + bn - 1) / bn;
+    j.units = m_units * n_tiles * j.splits;
+    j.full_groups = m_units / kMbGroup;
+    j.group = div_by(kMbGroup * n_tiles);
+    j.last = div_by(m_units % kMbGroup);
+    j.tiles = div_by(m_units * n_tiles);
+    j.parts = div_by(j.splits);
+    cycles[i] = unit_cycles(j.mode, (j.num_kb + j.splits - 1) / j.splits, streams);
+    if (i > 0) work += j.units * cycles[i];
   }
-  l->longs = l->job[0].units;
+  const int longs = l->job[0].units;
   l->shorts = l->job[1].units + l->job[2].units;
-  l->pairs = std::max(1, std::min(npairs, l->longs + l->shorts));
-  l->extra = l->longs % l->pairs;
+  l->pairs = std::max(1, std::min(npairs, longs + l->shorts));
+  l->longs_each = longs / l->pairs;
+  l->extra = longs % l->pairs;
   l->skip = 0;
-  if (l->extra > 0 && l->shorts > 0) {
-    // rounds of short units that one of the long ones takes
-    const int64_t len = l->job[0].num_kb / l->job[0].splits + kUnitCost;
-    const int64_t fit = static_cast<int64_t>(l->shorts) / (l->pairs - l->extra) + 1;
-    l->skip = static_cast<int>(
-        std::min(len * l->shorts / std::max<int64_t>(blocks, 1), fit));
-  }
+  const int64_t begun = l->longs_each * cycles[0];
+  const int64_t later = l->extra > 0 ? cycles[0] : 0;  // of the pairs with one long unit more
+  if (l->shorts == 0) return begun + later;
+  // rounds of short units that the others finish meanwhile, to the nearest
+  const int64_t each = std::max<int64_t>(1, work / l->shorts);
+  const int others = l->pairs - l->extra;
+  l->skip = static_cast<int>(std::min<int64_t>((later + each / 2) / each,
+                                               l->extra > 0 ? l->shorts / others + 1 : 0));
+  const int64_t left = std::max<int64_t>(0, l->shorts - int64_t(l->skip) * others);
+  const int64_t rounds = (left + l->pairs - 1) / l->pairs;
+  return begun + std::max(later, l->skip * each) + rounds * each;
 }
 
 cudaError_t launch_mlp_train(const MbLaunch& launch, int streams, const KernelCtl& ctl,
