@@ -48,11 +48,6 @@ void set_dx(MbJob* j, int64_t M, int64_t D, int64_t F, int splits) {
 
 // Row tiles per unit of work: one, or two that share a column tile where that is
 // estimated to be faster.
-struct MlpPlan {
-  int streams[2];  // of the two launches of the gradient
-  int dx_splits;   // parts of K of the product for dx, each with an fp32 buffer of its own
-};
-
 int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
   const int64_t one = plan_mlp_launch(l, 1, kMlpPairs);
   const int64_t two = M > kMlpRows ? plan_mlp_launch(l, 2, kMlpPairs) : one + 1;
@@ -60,27 +55,15 @@ int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
   return two < one ? 2 : 1;
 }
 
-// The first launch: dh and dw_down, the one with the longer K first.
-void first_jobs(MbLaunch* l, int64_t M, int64_t D, int64_t F, bool hidden, bool down, MbJob** dh,
-                MbJob** dw) {
-  const int at = D > M ? 0 : 1;
-  *dh = &l->job[at];
-  *dw = &l->job[2];
-  if (hidden) set_job(*dh, kMbGluGrad, M, F, D, false, true);
-  if (down) set_job(*dw, kMbStore, D, F, M, true, true);
-}
-
-// dx is split as the whole second launch (with dw_gate and dw_up) is fastest by the
-// estimate: 16 parts at most, none shorter than 8 K blocks.  Adding the parts costs a
-// launch and their traffic.
+// The launch of dx and the weights' gradients: row tiles per unit, and the parts of K
+// of the product for dx, each with an fp32 buffer of its own.  As the whole launch is
+// fastest by the estimate: 16 parts at most, none shorter than 8 K blocks.  Adding the
+// parts costs a launch and their traffic.
+struct MlpPlan {
+  int streams, dx_splits;
+};
 MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
   MlpPlan p{};
-  {
-    MbLaunch l{};
-    MbJob *dh, *dw;
-    first_jobs(&l, M, D, F, true, true, &dh, &dw);
-    p.streams[0] = faster_streams(&l, M, nullptr);
-  }
   int64_t best = 0;
   const int64_t k = 2 * ceil_div64(F, kBK);
   for (int splits = 1; splits <= std::max<int64_t>(1, std::min<int64_t>(k / 8, 16)); ++splits) {
@@ -88,12 +71,13 @@ MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
     set_dx(&l.job[0], M, D, F, splits);
     set_job(&l.job[1], kMbStore, F, D, M, true, true);
     set_job(&l.job[2], kMbStore, F, D, M, true, true);
+    set_job(&l.job[3], kMbStore, D, F, M, true, true);
     int64_t cycles;
     const int streams = faster_streams(&l, M, &cycles);
     if (splits > 1) cycles += 6000 + 8 * splits * M * D / 2500;  // bytes at about 4.8 TB/s
     if (splits == 1 || cycles < best) {
       best = cycles;
-      p.streams[1] = streams;
+      p.streams = streams;
       p.dx_splits = splits;
     }
   }
@@ -262,21 +246,21 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
   }
   const bool hidden = dx || dw_gate || dw_up;
   const MlpPlan plan = plan_mlp(M, D, F);
-  MbLaunch first{}, then{};
-  MbJob *dh, *dw;
-  first_jobs(&first, M, D, F, hidden, dw_down != nullptr, &dh, &dw);
-  first.act = act;
-  first.g = static_cast<const __nv_bfloat16*>(g);
-  first.u = static_cast<const __nv_bfloat16*>(u);
-  if (hidden && (!map_k(&dh->a[0], dout, D, M) || !map_mn(&dh->b[0], w_down, F, D) ||
-                 !map_out(&dh->o[0], ws.dg, F, M, false) || !map_out(&dh->o[1], ws.du, F, M, false)))
-    return GBF_ERR_CUDA;
-  if (dw_down && !set_dw(dw, dout, h, dw_down, D, F, M, plan.streams[0])) return GBF_ERR_CUDA;
-  if ((st = run_launch(&first, plan.streams[0], *dev, err, s)) != GBF_OK || !hidden) return st;
-  const int splits = plan.dx_splits;
-  const int streams = plan.streams[1];
+  const int splits = plan.dx_splits, streams = plan.streams;
+  if (hidden) {
+    MbLaunch l{};
+    MbJob& j = l.job[0];
+    set_job(&j, kMbGluGrad, M, F, D, false, true);
+    l.act = act;
+    if (!map_k(&j.a[0], dout, D, M) || !map_mn(&j.b[0], w_down, F, D) ||
+        !map_out(&j.a[1], g, F, M, true) || !map_out(&j.b[1], u, F, M, true) ||
+        !map_out(&j.o[0], ws.dg, F, M, true) || !map_out(&j.o[1], ws.du, F, M, true))
+      return GBF_ERR_CUDA;
+    if ((st = run_launch(&l, faster_streams(&l, M, nullptr), *dev, err, s)) != GBF_OK) return st;
+  }
+  MbLaunch l{};
   if (dx) {
-    MbJob& j = then.job[0];
+    MbJob& j = l.job[0];
     set_dx(&j, M, D, F, splits);
     if (!map_k(&j.a[0], ws.dg, F, M) || !map_k(&j.a[1], ws.du, F, M) ||
         !map_mn(&j.b[0], w_gate, D, F) || !map_mn(&j.b[1], w_up, D, F) ||
@@ -284,10 +268,11 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
                      : map_out(&j.o[0], dx, D, M, streams == 1)))
       return GBF_ERR_CUDA;
   }
-  if ((dw_gate && !set_dw(&then.job[1], ws.dg, x, dw_gate, F, D, M, streams)) ||
-      (dw_up && !set_dw(&then.job[2], ws.du, x, dw_up, F, D, M, streams)))
+  if ((dw_gate && !set_dw(&l.job[1], ws.dg, x, dw_gate, F, D, M, streams)) ||
+      (dw_up && !set_dw(&l.job[2], ws.du, x, dw_up, F, D, M, streams)) ||
+      (dw_down && !set_dw(&l.job[3], dout, h, dw_down, D, F, M, streams)))
     return GBF_ERR_CUDA;
-  if ((st = run_launch(&then, streams, *dev, err, s)) != GBF_OK) return st;
+  if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
   if (!dx || splits == 1) return GBF_OK;
   return cuda_status(launch_mlp_sum(ws.parts, static_cast<__nv_bfloat16*>(dx), M * D,
                                     mlp_m_pad(M) * D, splits, dev->sms, s));

@@ -285,7 +285,7 @@ struct CeLists {
 cudaError_t launch_ce_lists(const CeLists& p, int sms, cudaStream_t stream);
 
 // Products of a gated MLP block that is trained, and of its gradient
-// (mlp_train.cu): up to three per launch, none of which reads what another writes.
+// (mlp_train.cu): up to four per launch, none of which reads what another writes.
 enum MbMode { kMbNone = 0, kMbStore = 1, kMbGlu = 2, kMbGluGrad = 3 };
 struct MbDiv {  // x / by == __umulhi(x, mul) >> shift, x < 2^31
   int by;
@@ -293,7 +293,8 @@ struct MbDiv {  // x / by == __umulhi(x, mul) >> shift, x < 2^31
   int shift;
 };
 struct MbJob {
-  // [1]: of a second pair of operands, whose K blocks follow the first's; kMbGlu: b[1] Wu
+  // [1]: of a second pair of operands, whose K blocks follow the first's; kMbGlu: b[1]
+  // Wu; kMbGluGrad: a[1] g, b[1] u (in boxes like the results')
   CUtensorMap a[2], b[2];
   CUtensorMap o[3];  // the result; kMbGlu: h, g, u; kMbGluGrad: dg, du
   int mode;
@@ -307,10 +308,9 @@ struct MbJob {
   int units, full_groups;
   MbDiv group, last, tiles, parts;
 };
-constexpr int kMbJobs = 3;
+constexpr int kMbJobs = 4;
 struct MbLaunch {
   MbJob job[kMbJobs];  // job 0: the one with the longest units, if any
-  const __nv_bfloat16 *g, *u;  // kMbGluGrad
   int act;
   // by plan_mlp_launch: units of job 0 that every pair has, pairs that have one more,
   // rounds of the others' units that those sit out, units of the others, pairs

@@ -8,13 +8,12 @@
 //
 // One kernel does them all: the CTA-pair main loop of gemm_pair.cu (256 x 256
 // tiles on two SMs, tcgen05.mma.cta_group::2, TMA-fed), working through a list of
-// up to three products per launch that do not depend on one another.  dh never
+// up to four products per launch that do not depend on one another.  dh never
 // reaches memory: its tile ends as dg and du.  Every operand is read in the layout
 // in which it lies, along rows or columns, so nothing is transposed in memory.
 //
-// The gradient takes two launches: {dh, dWd}, then {dx, dWg, dWu}.  Products of
-// one launch fill each other's last round of units, and where rows are few (M <=
-// 256) the reading of the weights for dh overlaps the writing of dWd.
+// The gradient takes two launches: dh, then {dx, dWg, dWu, dWd}, which fill each
+// other's last round of units.
 //
 // Bound by the tensor pipe above some 500 rows, by the weights' bytes below.
 #include <cuda.h>
@@ -42,14 +41,20 @@ constexpr int kMbGroup = 8;              // raster group (units of rows)
 
 // STREAMS row tiles per unit of work, as in linear_ce.cu: two that share each B
 // tile, or a lone one (up to 256 rows), whose ending stores rows of 128 bytes.
-template <int STREAMS>
+// GRAD: kMbGluGrad alone, with several pairs of buffers per two warps of the ending for
+// g and u, which become dg and du.
+constexpr int kGradBytes = 32 * 128;  // 32 rows x 64 columns
+constexpr int64_t kGradKeep = int64_t(12) << 20;  // elements of dg and of du: 48 MB of the 129 MB of L2
+template <int STREAMS, bool GRAD>
 struct MbCfg {
   static constexpr int kStageBytes = STREAMS * kMbABytes + kMbBBytes;
-  static constexpr int kStages = STREAMS == 2 ? 4 : 5;
+  static constexpr int kStages = STREAMS == 2 ? (GRAD ? 3 : 4) : GRAD ? 4 : 5;
+  static constexpr int kSlots = STREAMS == 2 ? 2 : 3;
   static constexpr int kBarBytes = 1024;
   static constexpr bool kWide = STREAMS == 1;
   static constexpr int kBufBytes = kWide ? 32 * 128 : 32 * 64;
-  static constexpr int kStagingBytes = 8 * 2 * kBufBytes;
+  static constexpr int kWarpBytes = GRAD ? kSlots * kGradBytes : 2 * kBufBytes;
+  static constexpr int kStagingBytes = 8 * kWarpBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -82,10 +87,7 @@ __device__ __forceinline__ bool mb_unit(const MbLaunch& a, int pair, int npairs,
       t = a.skip * (npairs - a.extra) + (round - a.skip) * npairs + pair;
     if (t >= a.shorts) return false;
     u.job = 1;
-    if (t >= a.job[1].units) {
-      t -= a.job[1].units;
-      u.job = 2;
-    }
+    while (t >= a.job[u.job].units) t -= a.job[u.job++].units;
   }
   const MbJob& j = a.job[u.job];
   u.split = 0;
@@ -127,40 +129,89 @@ __device__ __forceinline__ float mb_clamp(float v, float most) {  // a NaN stays
   return y;
 }
 
+// Two fp32 values at a time, each operation rounded as the scalar one.
+struct f2 {
+  uint64_t v;
+};
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 f2_all(float x) { return f2_of(x, x); }
+__device__ __forceinline__ void f2_get(f2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x.v));
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+// 1 / (1 + 2^x)
+__device__ __forceinline__ f2 f2_sigmoid2(f2 x) {
+  float a, b;
+  f2_get(x, a, b);
+  return f2_of(mb_rcp(1.0f + mb_pow2(a)), mb_rcp(1.0f + mb_pow2(b)));
+}
+
 // Activation and derivative, in as few operations as it takes: they run on every
 // element of dh, and with a short K (D = 1000) the ending is what a unit waits for.
 template <int ACT>
-__device__ __forceinline__ void act_both(float v, float& y, float& dy) {
+__device__ __forceinline__ void act_both(f2 v, f2& y, f2& dy) {
   constexpr float kLog2e = 1.4426950408889634f;
   if constexpr (ACT == kActRelu) {
-    y = fmaxf(v, 0.0f);
-    dy = v > 0.0f ? 1.0f : 0.0f;
+    float a, b;
+    f2_get(v, a, b);
+    y = f2_of(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
+    dy = f2_of(a > 0.0f ? 1.0f : 0.0f, b > 0.0f ? 1.0f : 0.0f);
   } else if constexpr (ACT == kActSilu) {
-    const float s = mb_rcp(1.0f + mb_pow2(-kLog2e * v));
-    y = v * s;
-    dy = s * fmaf(v, 1.0f - s, 1.0f);
+    const f2 s = f2_sigmoid2(f2_mul(v, f2_all(-kLog2e)));
+    y = f2_mul(v, s);
+    dy = f2_mul(s, f2_fma(v, f2_fma(s, f2_all(-1.0f), f2_all(1.0f)), f2_all(1.0f)));
   } else if constexpr (ACT == kActGeluTanh) {
     // y = v s(2 z), z = c (v + k v^3);  y' = s + s (1 - s) v 2 c (1 + 3 k v^2).  From
     // |v| = 30 on s is 0 or 1 and the second term 0; v^2 stays in range.
     constexpr float c = 0.7978845608028654f, k = 0.044715f;
-    const float x = mb_clamp(v, 30.0f);
-    const float x2 = x * x;
-    const float s = mb_rcp(1.0f + mb_pow2(x * fmaf(-2.0f * kLog2e * c * k, x2, -2.0f * kLog2e * c)));
-    y = v * s;
-    dy = fmaf(fmaf(-s, s, s) * x, fmaf(6.0f * c * k, x2, 2.0f * c), s);
+    float a, b;
+    f2_get(v, a, b);
+    const f2 x = f2_of(mb_clamp(a, 30.0f), mb_clamp(b, 30.0f));
+    const f2 x2 = f2_mul(x, x);
+    const f2 s = f2_sigmoid2(f2_mul(
+        x, f2_fma(x2, f2_all(-2.0f * kLog2e * c * k), f2_all(-2.0f * kLog2e * c))));
+    y = f2_mul(v, s);
+    const f2 t = f2_mul(f2_fma(f2_mul(s, f2_all(-1.0f)), s, s), x);
+    dy = f2_fma(t, f2_fma(x2, f2_all(6.0f * c * k), f2_all(2.0f * c)), s);
   } else {
     y = v;
-    dy = 1.0f;
+    dy = f2_all(1.0f);
   }
 }
 
-// 16 columns of a row of bf16; zeros outside.
-__device__ __forceinline__ void load_row16(uint4 (&d)[2], const __nv_bfloat16* p, int64_t row,
-                                           int col, int rows, int cols, uint64_t pol) {
+// 16 columns of this lane's row of a 32 x 64 chunk (128-byte rows, 128-byte swizzle),
+// from column 16 at on: from and to a staging buffer.
+__device__ __forceinline__ uint32_t staged_unit(const uint8_t* buf, uint32_t unit) {
+  const uint32_t lane = threadIdx.x & 31;
+  return smem_u32(buf) + lane * 128u + ((unit ^ (lane & 7u)) << 4);
+}
+__device__ __forceinline__ void staged_row16(uint4 (&d)[2], const uint8_t* buf, uint32_t at) {
 #pragma unroll
-  for (int v = 0; v < 2; ++v)
-    d[v] = row < rows && col + 8 * v < cols ? ld_stream_u4(p + row * cols + col + 8 * v, pol)
-                                            : make_uint4(0u, 0u, 0u, 0u);
+  for (uint32_t v = 0; v < 2; ++v)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(d[v].x), "=r"(d[v].y), "=r"(d[v].z), "=r"(d[v].w)
+                 : "r"(staged_unit(buf, 2 * at + v))
+                 : "memory");
+}
+__device__ __forceinline__ void stage_row16(uint8_t* buf, uint32_t at, const uint32_t (&w)[8]) {
+#pragma unroll
+  for (uint32_t v = 0; v < 2; ++v)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(staged_unit(buf, 2 * at + v)),
+                 "r"(w[4 * v]), "r"(w[4 * v + 1]), "r"(w[4 * v + 2]), "r"(w[4 * v + 3])
+                 : "memory");
 }
 
 template <int ACT>
@@ -176,62 +227,80 @@ __device__ __forceinline__ void glu_pack(const uint32_t (&g)[32], const uint32_t
 // dg and du of 16 columns.
 template <int ACT>
 __device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[16], const uint4 (&g2)[2],
-                                              const uint4 (&u2)[2], uint32_t* dg, uint32_t* du) {
+                                              const uint4 (&u2)[2], uint32_t (&dg)[8],
+                                              uint32_t (&du)[8]) {
+  const uint32_t g[8] = {g2[0].x, g2[0].y, g2[0].z, g2[0].w, g2[1].x, g2[1].y, g2[1].z, g2[1].w};
+  const uint32_t u[8] = {u2[0].x, u2[0].y, u2[0].z, u2[0].w, u2[1].x, u2[1].y, u2[1].z, u2[1].w};
 #pragma unroll
-  for (int v = 0; v < 2; ++v) {
-    float g[8], u[8], a[8], b[8];
-    unpack8(g2[v], g);
-    unpack8(u2[v], u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float y, dy;
-      act_both<ACT>(g[i], y, dy);
-      const float d = __uint_as_float(dh[8 * v + i]);
-      a[i] = d * u[i] * dy;
-      b[i] = d * y;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      dg[4 * v + i] = pack_bf16x2(a[2 * i], a[2 * i + 1]);
-      du[4 * v + i] = pack_bf16x2(b[2 * i], b[2 * i + 1]);
-    }
+  for (int i = 0; i < 8; ++i) {
+    f2 y, dy;
+    act_both<ACT>(f2_of(bf16lo(g[i]), bf16hi(g[i])), y, dy);
+    const f2 d = f2_of(__uint_as_float(dh[2 * i]), __uint_as_float(dh[2 * i + 1]));
+    float lo, hi;
+    f2_get(f2_mul(f2_mul(d, f2_of(bf16lo(u[i]), bf16hi(u[i]))), dy), lo, hi);
+    dg[i] = pack_bf16x2(lo, hi);
+    f2_get(f2_mul(d, y), lo, hi);
+    du[i] = pack_bf16x2(lo, hi);
   }
 }
 
-// A warp's 128 columns of a tile of dh, whose first 16 columns of g and u are in g2
-// and u2.  The next 16 columns' are asked for before the present ones' arithmetic
-// (32 ahead do not fit in the registers).
-template <int ACT, int BUF>
-__device__ __forceinline__ void glu_grad_tile(uint32_t tb, const AccFree& release,
-                                              const MbLaunch& a, const MbJob& j, uint4 (&g2)[2],
-                                              uint4 (&u2)[2], uint8_t* bufs, int& flip, int row0,
-                                              int col0, uint64_t first) {
-  const int row = row0 + static_cast<int>(threadIdx.x & 31);
-  const uint64_t last = policy_evict_last();
-#pragma unroll 1
-  for (int c = 0; c < 4; ++c) {
-    const int col = col0 + c * 32;
-    uint32_t dg[16], du[16];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 gn[2], un[2];
-      if (h == 0 || c < 3) {
-        load_row16(gn, a.g, row, col + 16 * h + 16, j.rows, j.cols, first);
-        load_row16(un, a.u, row, col + 16 * h + 16, j.rows, j.cols, first);
-      }
-      uint32_t v[16];
-      tmem_ld16(tb + c * 32 + 16 * h, v);
-      tmem_wait_ld();
-      glu_grad_pack<ACT>(v, g2, u2, dg + 8 * h, du + 8 * h);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        g2[i] = gn[i];
-        u2[i] = un[i];
-      }
+// The chunks of g and u of the two warps that share 32 rows of a tile, 64 columns at
+// a time, on their way ahead of the arithmetic: one lane asks the TMA engine for the
+// next chunk of the next units, into a slot whose dg and du have been stored.
+//
+// dh of 4096 x 4096 x 14336 takes 245 us without g and u.  Read by the lanes themselves
+// they cost the products their shared memory, which is the same as L1 (16 bytes of 32
+// rows at a time 450 us, 64 of 8 rows 362); by the TMA engine its requests count, one
+// per row of a box: 330 us with rows of 64 bytes, 301 with 128.
+template <int STREAMS, int SLOTS>
+struct GradLoads {
+  MbUnit u;   // of the next chunk
+  int n, c;   // its unit's number, its place in the unit: four per row tile
+  int slot;
+  bool more;
+  __device__ __forceinline__ void start(const MbLaunch& a, int pair, int npairs) {
+    n = c = slot = 0;
+    more = mb_unit(a, pair, npairs, n, u);
+  }
+  __device__ __forceinline__ void next(const MbLaunch& a, int pair, int npairs, int row,
+                                       uint8_t* slots, uint64_t* bars) {
+    if (!more) return;
+    if ((threadIdx.x & 31) == 0) {
+      const MbJob& j = a.job[u.job];
+      uint8_t* buf = slots + slot * 2 * kGradBytes;
+      mbar_arrive_expect_tx(&bars[slot], 2 * kGradBytes);
+      const int col0 = u.nb * kMbTile + (c & 3) * 64;
+      const int row0 = (STREAMS * u.mp + (c >> 2)) * kMbTile + row;
+      const uint64_t once = policy_evict_first();
+      tma_load_2d_hint(buf, &j.a[1], &bars[slot], col0, row0, once);
+      tma_load_2d_hint(buf + kGradBytes, &j.b[1], &bars[slot], col0, row0, once);
     }
-    if (c == 3) release();
-    put_chunk<false>(bufs, BUF, flip, 0, dg, &j.o[0], row0, col, j.rows, j.cols, last);
-    put_chunk<false>(bufs, BUF, flip, 0, du, &j.o[1], row0, col, j.rows, j.cols, last);
+    if (++slot == SLOTS) slot = 0;
+    if (++c == 4 * STREAMS) {
+      c = 0;
+      more = mb_unit(a, pair, npairs, ++n, u);
+    }
+  }
+};
+
+// This warp's 32 of a chunk's 64 columns of dh (half 0 or 1): dg and du in the place of
+// g and u.  `ask`, in the middle, asks for the chunk after the next.
+template <int ACT, typename Ask>
+__device__ __forceinline__ void glu_grad_chunk(uint32_t tb, uint8_t* buf, int half,
+                                               const Ask& ask) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint4 g2[2], u2[2];
+    uint32_t v[16], dg[8], du[8];
+    const uint32_t at = 2 * half + h;
+    tmem_ld16(tb + 16 * h, v);
+    staged_row16(g2, buf, at);
+    staged_row16(u2, buf + kGradBytes, at);
+    tmem_wait_ld();
+    glu_grad_pack<ACT>(v, g2, u2, dg, du);
+    stage_row16(buf, at, dg);
+    stage_row16(buf + kGradBytes, at, du);
+    if (h == 0) ask();
   }
 }
 
@@ -270,10 +339,10 @@ __device__ __forceinline__ void store_tile(uint32_t tb, const AccFree& release, 
   put(3, vb);
 }
 
-template <int STREAMS>
+template <int STREAMS, bool GRAD>
 __global__ void __launch_bounds__(kMbThreads, 1)
     mlp_train_kernel(const __grid_constant__ MbLaunch a, const KernelCtl kctl) {
-  using Cfg = MbCfg<STREAMS>;
+  using Cfg = MbCfg<STREAMS, GRAD>;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -283,7 +352,9 @@ __global__ void __launch_bounds__(kMbThreads, 1)
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* loaded = done + 1;  // GRAD: slots of g and u, of each two warps
+  uint64_t* made = loaded + 4 * Cfg::kSlots;  // dg and du by both warps
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(made + 4 * Cfg::kSlots);
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   uint8_t* staging = smem + kStages * Cfg::kStageBytes + Cfg::kBarBytes;
 
@@ -304,6 +375,10 @@ __global__ void __launch_bounds__(kMbThreads, 1)
       mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
     }
     mbar_init(done, STREAMS);
+    for (int i = 0; i < 4 * Cfg::kSlots; ++i) {
+      mbar_init(&loaded[i], 1);
+      mbar_init(&made[i], 2);
+    }
     *abort_flag = 0;
     fence_mbar_init();
     for (int i = 0; i < kMbJobs; ++i) {
@@ -440,38 +515,82 @@ __global__ void __launch_bounds__(kMbThreads, 1)
     const uint64_t first = l2_evict_first_policy();
     const uint32_t lead_empty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t lead_empty1 = mapa_shared(smem_u32(&tempty[1]), 0);
-    uint8_t* bufs = staging + (warp - 4) * 2 * Cfg::kBufBytes;
+    uint8_t* bufs = staging + (warp - 4) * Cfg::kWarpBytes;
     int flip = 0;
     bool ok = true;
     MbUnit u;
+    GradLoads<STREAMS, Cfg::kSlots> loads;
+    uint64_t* bars = loaded + q * Cfg::kSlots;
+    uint8_t* slots = staging + q * 2 * Cfg::kWarpBytes;
+    const int row_in = static_cast<int>(rank) * kBM + q * 32;  // of a row tile
+    int slot = 0;  // GRAD: the present chunk's, and the phase of its barrier
+    uint32_t phase = 0;
+    if (GRAD && half == 0) {
+      loads.start(a, pair, npairs);
+      for (int i = 1; i < Cfg::kSlots; ++i) loads.next(a, pair, npairs, row_in, slots, bars);
+    }
     for (int n = 0; ok && mb_unit(a, pair, npairs, n, u); ++n) {
       const MbJob& j = a.job[u.job];
 #pragma unroll 1
       for (int i = 0; i < STREAMS; ++i) {
         const int acc = STREAMS == 2 ? i : n & 1;
         const int use = STREAMS == 2 ? n : n >> 1;
-        const int row0 = (STREAMS * u.mp + i) * kMbTile + static_cast<int>(rank) * kBM + q * 32;
+        const int row0 = (STREAMS * u.mp + i) * kMbTile + row_in;
         const uint32_t tb = tmem_base + acc * 256 + (static_cast<uint32_t>(q * 32) << 16);
         const AccFree release{acc ? &tempty[1] : &tempty[0], acc ? lead_empty1 : lead_empty0,
                               leader};
-        const int col0 = j.mode == kMbGlu ? u.nb * 128 + half * 64 : u.nb * kMbTile + half * 128;
-        uint4 g2[2], u2[2];
-        if (j.mode == kMbGluGrad) {
-          // the first 16 columns of g and u on their way, the others into L2
-          if (row0 + lane < j.rows) {
-            const int64_t at = static_cast<int64_t>(row0 + lane) * j.cols;
-            if (col0 + 64 < j.cols) {
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.g + at + col0 + 64));
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(a.u + at + col0 + 64));
-            }
-          }
-          load_row16(g2, a.g, row0 + lane, col0, j.rows, j.cols, first);
-          load_row16(u2, a.u, row0 + lane, col0, j.rows, j.cols, first);
-        }
         ok = wait_bar(&tfull[acc], use & 1, ctl, kSiteEpiAccFull);
         if (!ok) break;
         tc_fence_after();
-        if (j.mode == kMbGlu) {
+        if constexpr (GRAD) {
+          // dg and du are the next launch's operands, but they do not push this one's out
+          // of L2 (4096 x 4096 x 14336, 234 MB: 331 us with evict_last, so 290)
+          const uint64_t pol = static_cast<int64_t>(j.rows) * j.cols <= kGradKeep
+                                   ? policy_evict_last() : policy_evict_first();
+          // the slot that the present chunk's predecessor leaves, once its stores have
+          // read it
+          auto ask = [&]() {
+            if (half != 0) return;
+            if (lane == 0) bulk_wait_read<0>();
+            loads.next(a, pair, npairs, row_in, slots, bars);
+          };
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint8_t* buf = slots + slot * 2 * kGradBytes;
+            ok = wait_bar(&bars[slot], phase, ctl, kSiteXformFull);
+            if (!ok) break;
+            const uint32_t t = tb + c * 64 + half * 32;
+            switch (a.act) {
+              case kActRelu: glu_grad_chunk<kActRelu>(t, buf, half, ask); break;
+              case kActSilu: glu_grad_chunk<kActSilu>(t, buf, half, ask); break;
+              case kActGeluTanh: glu_grad_chunk<kActGeluTanh>(t, buf, half, ask); break;
+              default: glu_grad_chunk<kActIdentity>(t, buf, half, ask); break;
+            }
+            if (c == 3) release();
+            fence_proxy_async_smem();
+            __syncwarp();
+            uint64_t* both = &made[q * Cfg::kSlots + slot];
+            if (lane == 0) mbar_arrive(both);
+            if (half == 0) {
+              ok = wait_bar(both, phase, ctl, kSiteXformEmpty);
+              if (!ok) break;
+              if (lane == 0) {
+                const int col = u.nb * kMbTile + c * 64;
+                if (row0 < j.rows && col < j.cols) {
+                  tma_store_2d(&j.o[0], buf, col, row0, pol);
+                  tma_store_2d(&j.o[1], buf + kGradBytes, col, row0, pol);
+                }
+                bulk_commit();
+              }
+            }
+            if (++slot == Cfg::kSlots) {
+              slot = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+        } else if (j.mode == kMbGlu) {
+          const int col0 = u.nb * 128 + half * 64;
 #pragma unroll 1
           for (int c = 0; c < 2; ++c) {
             uint32_t g[32], up[32], w[16];
@@ -499,30 +618,15 @@ __global__ void __launch_bounds__(kMbThreads, 1)
             put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[2], row0, col, j.rows, j.cols,
                              first);
           }
-        } else if (j.mode == kMbGluGrad) {
-          constexpr int kBuf = Cfg::kBufBytes;
-          const uint32_t t = tb + half * 128;
-          switch (a.act) {
-            case kActRelu:
-              glu_grad_tile<kActRelu, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0, first);
-              break;
-            case kActSilu:
-              glu_grad_tile<kActSilu, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0, first);
-              break;
-            case kActGeluTanh:
-              glu_grad_tile<kActGeluTanh, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0,
-                                                first);
-              break;
-            default:
-              glu_grad_tile<kActIdentity, kBuf>(t, release, a, j, g2, u2, bufs, flip, row0, col0,
-                                                first);
-              break;
-          }
         } else {
           store_tile<Cfg::kWide, Cfg::kBufBytes>(tb + half * 128, release, j, bufs, flip, row0,
-                                                 col0, u.split, first);
+                                                 u.nb * kMbTile + half * 128, u.split, first);
         }
       }
+    }
+    if (GRAD && !ok && lane == 0) {
+      const uint64_t t0 = globaltimer_ns();  // let the copies in flight land (bounded)
+      while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
     }
     if (lane == 0) bulk_wait<0>();
     __syncwarp();
@@ -560,11 +664,11 @@ __global__ void __launch_bounds__(kSumThreads)
   }
 }
 
-template <int STREAMS>
+template <int STREAMS, bool GRAD>
 cudaError_t run_mb(const MbLaunch& launch, const KernelCtl& ctl, int grid, cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = mlp_train_kernel<STREAMS>;
-  constexpr int smem = MbCfg<STREAMS>::kSmem;
+  auto kernel = mlp_train_kernel<STREAMS, GRAD>;
+  constexpr int smem = MbCfg<STREAMS, GRAD>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -608,9 +712,12 @@ MbDiv div_by(int d) {  // exact for 31-bit numbers: the reciprocal is rounded up
 // About how many cycles a unit keeps its pair, by its K blocks and its ending.  A
 // lone row tile's MMAs take 150 cycles each and its ending overlaps the next unit's;
 // two row tiles' share the tensor pipe at 128, and the next unit waits for the first
-// one's ending.
+// one's ending, of kMbGluGrad for both.  Beside that ending's own traffic a lone row
+// tile's operands, 64 KB per K block, take longer from L2.
 int64_t unit_cycles(int mode, int64_t kb, int streams) {
-  const int64_t end = mode == kMbGluGrad ? 5000 : mode == kMbGlu ? 4000 : 2600;
+  if (mode == kMbGluGrad)
+    return streams == 1 ? std::max<int64_t>(800 * kb, 14000) + 300 : 1024 * kb + 17000;
+  const int64_t end = mode == kMbGlu ? 4000 : 2600;
   return streams == 1 ? std::max<int64_t>(600 * kb, end) + 300
                       : std::max<int64_t>(1024 * kb, 2 * end) + end;
 }
@@ -636,7 +743,8 @@ int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
     if (i > 0) work += j.units * cycles[i];
   }
   const int longs = l->job[0].units;
-  l->shorts = l->job[1].units + l->job[2].units;
+  l->shorts = 0;
+  for (int i = 1; i < kMbJobs; ++i) l->shorts += l->job[i].units;
   l->pairs = std::max(1, std::min(npairs, longs + l->shorts));
   l->longs_each = longs / l->pairs;
   l->extra = longs % l->pairs;
@@ -657,8 +765,11 @@ int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
 cudaError_t launch_mlp_train(const MbLaunch& launch, int streams, const KernelCtl& ctl,
                              cudaStream_t stream) {
   const int grid = 2 * launch.pairs;
-  return streams == 2 ? run_mb<2>(launch, ctl, grid, stream)
-                      : run_mb<1>(launch, ctl, grid, stream);
+  if (launch.job[0].mode == kMbGluGrad)  // alone
+    return streams == 2 ? run_mb<2, true>(launch, ctl, grid, stream)
+                        : run_mb<1, true>(launch, ctl, grid, stream);
+  return streams == 2 ? run_mb<2, false>(launch, ctl, grid, stream)
+                      : run_mb<1, false>(launch, ctl, grid, stream);
 }
 
 cudaError_t launch_mlp_sum(const float* parts, __nv_bfloat16* dx, int64_t n, int64_t stride,
