@@ -33,14 +33,16 @@ namespace gbf {
 
 namespace {
 
-constexpr int kMbThreads = 384;          // warps 0-3 roles, 4-11 ending
 constexpr int kMbTile = 256;             // rows and columns of a pair's tile
 constexpr int kMbABytes = kBM * kBK * 2;  // 16 KB: this CTA's 128 rows of A
 constexpr int kMbBBytes = 128 * kBK * 2;  // 16 KB: this CTA's half of B
 constexpr int kMbGroup = 8;              // raster group (units of rows)
 
 // STREAMS row tiles per unit of work, as in linear_ce.cu: two that share each B
-// tile, or a lone one (up to 256 rows), whose ending stores rows of 128 bytes.
+// tile, or a lone one.  Warps 0-3 have roles, the others the ending.  With few rows a
+// unit of a weight's gradient is one K block, and its ending all that counts: sixteen
+// warps with 64 columns each, stored as rows of 128 bytes (the three gradients of 16 x
+// 4096 x 14336, 352 MB: eight warps 73 us).
 // GRAD: kMbGluGrad alone, with several pairs of buffers per two warps of the ending for
 // g and u, which become dg and du.
 constexpr int kGradBytes = 32 * 128;  // 32 rows x 64 columns
@@ -51,10 +53,11 @@ struct MbCfg {
   static constexpr int kStages = STREAMS == 2 ? (GRAD ? 3 : 4) : GRAD ? 4 : 5;
   static constexpr int kSlots = STREAMS == 2 ? 2 : 3;
   static constexpr int kBarBytes = 1024;
-  static constexpr bool kWide = STREAMS == 1;
-  static constexpr int kBufBytes = kWide ? 32 * 128 : 32 * 64;
-  static constexpr int kWarpBytes = GRAD ? kSlots * kGradBytes : 2 * kBufBytes;
-  static constexpr int kStagingBytes = 8 * kWarpBytes;
+  static constexpr int kEndWarps = STREAMS == 1 && !GRAD ? 16 : 8;
+  static constexpr int kThreads = 128 + 32 * kEndWarps;
+  static constexpr int kCols = 4 * 256 / kEndWarps;  // of a tile, per warp of the ending
+  static constexpr int kWarpBytes = GRAD ? kSlots * kGradBytes : 2 * kStageChunkBytes;
+  static constexpr int kStagingBytes = kEndWarps * kWarpBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -304,24 +307,40 @@ __device__ __forceinline__ void glu_grad_chunk(uint32_t tb, uint8_t* buf, int ha
   }
 }
 
-// A warp's 128 columns of a product as they are, to bf16 or to the fp32 rows of its
-// part of K: the next 32 are on their way from tensor memory meanwhile.
-template <bool WIDE, int BUF>
-__device__ __forceinline__ void store_tile(uint32_t tb, const AccFree& release, const MbJob& j,
-                                           uint8_t* bufs, int& flip, int row0, int col0, int part,
-                                           uint64_t first) {
-  auto put = [&](int c, const uint32_t (&v)[32]) {
-    const int col = col0 + c * 32;
-    if (j.splits > 1) {
-      put_chunk_f32(bufs, BUF, flip, v, &j.o[0], part * j.m_pad + row0, col, j.cols, row0 < j.rows,
-                    false);
-    } else {
-      uint32_t w[16];
+// A warp's columns of a product, to the fp32 rows of its part of K.
+template <int COLS>
+__device__ __forceinline__ void store_part(uint32_t tb, const AccFree& release, const MbJob& j,
+                                           uint8_t* bufs, int& flip, int row0, int col0, int part) {
+  // another product's store may still read both buffers
+  if ((threadIdx.x & 31) == 0) bulk_wait_read<0>();
+  __syncwarp();
+#pragma unroll 1
+  for (int c = 0; c < COLS / 32; ++c) {
+    uint32_t v[32];
+    tmem_ld32(tb + 32 * c, v);
+    tmem_wait_ld();
+    if (c == COLS / 32 - 1) release();
+    put_chunk_f32(bufs, kStageChunkBytes, flip, v, &j.o[0], part * j.m_pad + row0, col0 + 32 * c,
+                  j.cols, row0 < j.rows, false);
+  }
+}
+
+__device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16]) {
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        w[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
-      put_chunk<WIDE>(bufs, BUF, flip, c, w, &j.o[0], row0, col, j.rows, j.cols, first);
-    }
+  for (int k = 0; k < 16; ++k)
+    w[k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+}
+
+// A warp's 128 columns to bf16, 32 at a time: the next are on their way from tensor
+// memory meanwhile.
+__device__ __forceinline__ void store_tile128(uint32_t tb, const AccFree& release, const MbJob& j,
+                                              uint8_t* bufs, int& flip, int row0, int col0,
+                                              uint64_t pol) {
+  auto put = [&](int c, const uint32_t (&v)[32]) {
+    uint32_t w[16];
+    pack32(v, w);
+    put_chunk<false>(bufs, kStageChunkBytes, flip, c, w, &j.o[0], row0, col0 + c * 32, j.rows,
+                     j.cols, pol);
   };
   uint32_t va[32], vb[32];
   tmem_ld32(tb, va);
@@ -339,8 +358,37 @@ __device__ __forceinline__ void store_tile(uint32_t tb, const AccFree& release, 
   put(3, vb);
 }
 
+// A warp's 64 columns to bf16 as rows of 128 bytes; `buf` holds them all.
+__device__ __forceinline__ void store_tile64(uint32_t tb, const AccFree& release, const MbJob& j,
+                                             uint8_t* buf, int row0, int col0, uint64_t pol) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+  uint32_t v[32], w[16], w2[16];
+  tmem_ld32(tb, v);
+  tmem_wait_ld();
+  pack32(v, w);
+  tmem_ld32(tb + 32, v);
+  tmem_wait_ld();
+  release();
+  pack32(v, w2);
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
+#pragma unroll
+  for (uint32_t u = 0; u < 8; ++u) {
+    const uint32_t* x = u < 4 ? w + 4 * u : w2 + 4 * (u - 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(staged_unit(buf, u)), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3])
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (row0 < j.rows && col0 < j.cols) tma_store_2d(&j.o[0], buf, col0, row0, pol);
+    bulk_commit();
+  }
+}
+
 template <int STREAMS, bool GRAD>
-__global__ void __launch_bounds__(kMbThreads, 1)
+__global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
     mlp_train_kernel(const __grid_constant__ MbLaunch a, const KernelCtl kctl) {
   using Cfg = MbCfg<STREAMS, GRAD>;
   constexpr int kStages = Cfg::kStages;
@@ -372,7 +420,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
+      mbar_init(&tempty[i], 2 * Cfg::kEndWarps);  // of each CTA of the pair
     }
     mbar_init(done, STREAMS);
     for (int i = 0; i < 4 * Cfg::kSlots; ++i) {
@@ -511,7 +559,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
   } else if (warp >= 4) {
     // ------------------------------------------------------------ ending (both CTAs)
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int slice = (warp - 4) >> 2;  // of the tile's columns
     const uint64_t first = l2_evict_first_policy();
     const uint32_t lead_empty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t lead_empty1 = mapa_shared(smem_u32(&tempty[1]), 0);
@@ -525,7 +573,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
     const int row_in = static_cast<int>(rank) * kBM + q * 32;  // of a row tile
     int slot = 0;  // GRAD: the present chunk's, and the phase of its barrier
     uint32_t phase = 0;
-    if (GRAD && half == 0) {
+    if (GRAD && slice == 0) {
       loads.start(a, pair, npairs);
       for (int i = 1; i < Cfg::kSlots; ++i) loads.next(a, pair, npairs, row_in, slots, bars);
     }
@@ -550,7 +598,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
           // the slot that the present chunk's predecessor leaves, once its stores have
           // read it
           auto ask = [&]() {
-            if (half != 0) return;
+            if (slice != 0) return;
             if (lane == 0) bulk_wait_read<0>();
             loads.next(a, pair, npairs, row_in, slots, bars);
           };
@@ -559,19 +607,19 @@ __global__ void __launch_bounds__(kMbThreads, 1)
             uint8_t* buf = slots + slot * 2 * kGradBytes;
             ok = wait_bar(&bars[slot], phase, ctl, kSiteXformFull);
             if (!ok) break;
-            const uint32_t t = tb + c * 64 + half * 32;
+            const uint32_t t = tb + c * 64 + slice * 32;
             switch (a.act) {
-              case kActRelu: glu_grad_chunk<kActRelu>(t, buf, half, ask); break;
-              case kActSilu: glu_grad_chunk<kActSilu>(t, buf, half, ask); break;
-              case kActGeluTanh: glu_grad_chunk<kActGeluTanh>(t, buf, half, ask); break;
-              default: glu_grad_chunk<kActIdentity>(t, buf, half, ask); break;
+              case kActRelu: glu_grad_chunk<kActRelu>(t, buf, slice, ask); break;
+              case kActSilu: glu_grad_chunk<kActSilu>(t, buf, slice, ask); break;
+              case kActGeluTanh: glu_grad_chunk<kActGeluTanh>(t, buf, slice, ask); break;
+              default: glu_grad_chunk<kActIdentity>(t, buf, slice, ask); break;
             }
             if (c == 3) release();
             fence_proxy_async_smem();
             __syncwarp();
             uint64_t* both = &made[q * Cfg::kSlots + slot];
             if (lane == 0) mbar_arrive(both);
-            if (half == 0) {
+            if (slice == 0) {
               ok = wait_bar(both, phase, ctl, kSiteXformEmpty);
               if (!ok) break;
               if (lane == 0) {
@@ -590,37 +638,40 @@ __global__ void __launch_bounds__(kMbThreads, 1)
           }
           if (!ok) break;
         } else if (j.mode == kMbGlu) {
-          const int col0 = u.nb * 128 + half * 64;
+          constexpr int kOut = Cfg::kCols / 2;  // of h, g and u each
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kOut / 32; ++c) {
             uint32_t g[32], up[32], w[16];
-            tmem_ld32(tb + half * 64 + c * 32, g);
-            tmem_ld32(tb + 128 + half * 64 + c * 32, up);
+            tmem_ld32(tb + slice * kOut + c * 32, g);
+            tmem_ld32(tb + 128 + slice * kOut + c * 32, up);
             tmem_wait_ld();
-            if (c == 1) release();
-            const int col = col0 + c * 32;
+            if (c == kOut / 32 - 1) release();
+            const int col = u.nb * 128 + slice * kOut + c * 32;
+            auto put = [&](int o) {
+              put_chunk<false>(bufs, kStageChunkBytes, flip, 0, w, &j.o[o], row0, col, j.rows,
+                               j.cols, first);
+            };
             switch (a.act) {
               case kActRelu: glu_pack<kActRelu>(g, up, w); break;
               case kActSilu: glu_pack<kActSilu>(g, up, w); break;
               case kActGeluTanh: glu_pack<kActGeluTanh>(g, up, w); break;
               default: glu_pack<kActIdentity>(g, up, w); break;
             }
-            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[0], row0, col, j.rows, j.cols,
-                             first);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(g[2 * k]), __uint_as_float(g[2 * k + 1]));
-            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[1], row0, col, j.rows, j.cols,
-                             first);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(up[2 * k]), __uint_as_float(up[2 * k + 1]));
-            put_chunk<false>(bufs, Cfg::kBufBytes, flip, 0, w, &j.o[2], row0, col, j.rows, j.cols,
-                             first);
+            put(0);
+            pack32(g, w);
+            put(1);
+            pack32(up, w);
+            put(2);
           }
         } else {
-          store_tile<Cfg::kWide, Cfg::kBufBytes>(tb + half * 128, release, j, bufs, flip, row0,
-                                                 u.nb * kMbTile + half * 128, u.split, first);
+          const int col0 = u.nb * kMbTile + slice * Cfg::kCols;
+          const uint32_t t = tb + slice * Cfg::kCols;
+          if (j.splits > 1)
+            store_part<Cfg::kCols>(t, release, j, bufs, flip, row0, col0, u.split);
+          else if constexpr (Cfg::kCols == 64)
+            store_tile64(t, release, j, bufs, row0, col0, first);
+          else
+            store_tile128(t, release, j, bufs, flip, row0, col0, first);
         }
       }
     }
@@ -680,7 +731,7 @@ cudaError_t run_mb(const MbLaunch& launch, const KernelCtl& ctl, int grid, cudaS
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(kMbThreads, 1, 1);
+  cfg.blockDim = dim3(MbCfg<STREAMS, GRAD>::kThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -713,12 +764,13 @@ MbDiv div_by(int d) {  // exact for 31-bit numbers: the reciprocal is rounded up
 // lone row tile's MMAs take 150 cycles each and its ending overlaps the next unit's;
 // two row tiles' share the tensor pipe at 128, and the next unit waits for the first
 // one's ending, of kMbGluGrad for both.  Beside that ending's own traffic a lone row
-// tile's operands, 64 KB per K block, take longer from L2.
-int64_t unit_cycles(int mode, int64_t kb, int streams) {
+// tile's operands, 64 KB per K block, take longer from L2, and weights that only one
+// row tile reads (`once`) come from memory.
+int64_t unit_cycles(int mode, int64_t kb, int streams, bool once) {
   if (mode == kMbGluGrad)
     return streams == 1 ? std::max<int64_t>(800 * kb, 14000) + 300 : 1024 * kb + 17000;
   const int64_t end = mode == kMbGlu ? 4000 : 2600;
-  return streams == 1 ? std::max<int64_t>(600 * kb, end) + 300
+  return streams == 1 ? std::max<int64_t>((once ? 750 : 600) * kb, end) + 300
                       : std::max<int64_t>(1024 * kb, 2 * end) + end;
 }
 
@@ -739,7 +791,8 @@ int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
     j.last = div_by(m_units % kMbGroup);
     j.tiles = div_by(m_units * n_tiles);
     j.parts = div_by(j.splits);
-    cycles[i] = unit_cycles(j.mode, (j.num_kb + j.splits - 1) / j.splits, streams);
+    cycles[i] = unit_cycles(j.mode, (j.num_kb + j.splits - 1) / j.splits, streams,
+                            m_units == 1);
     if (i > 0) work += j.units * cycles[i];
   }
   const int longs = l->job[0].units;

@@ -80,7 +80,12 @@ __device__ __forceinline__ void put_chunk(uint8_t* bufs, int buf_bytes, int& fli
   }
 }
 
-// How a warp of the ending gives an accumulator back to the issuers.
+// How a warp of the ending gives an accumulator back to the issuers.  What is handed
+// over is tensor memory: its loads have completed (tcgen05.wait::ld) and are ordered by
+// the fence, and no thread reads memory that the warp wrote because of this arrival.
+// So the odd CTA's is relaxed: one that releases at the cluster's scope waits for the
+// warp's stores in flight, the TMA engine's among them, and the next products wait for
+// it (weights' gradients of 16 rows, 352 MB: 75 us, relaxed 53).
 struct AccFree {
   uint64_t* mine;
   uint32_t lead;  // the even CTA's, as the odd one sees it
@@ -89,8 +94,11 @@ struct AccFree {
     tc_fence_before();
     __syncwarp();
     if ((threadIdx.x & 31) == 0) {
-      if (leader) mbar_arrive(mine);
-      else mbar_arrive_cluster(lead);
+      if (leader)
+        mbar_arrive(mine);
+      else
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(lead)
+                     : "memory");
     }
   }
 };
