@@ -21,7 +21,7 @@ SOURCES = ["api.cu", "gemm_tc.cu", "gemm_pair.cu", "wq_gemm.cu", "pointwise.cu",
            "embedding.cu", "clip.cu", "linear_ce.cu", "ce_swap.cu",
            "heads.cu", "mlp_train.cu", "rmsnorm_grad.cu", "blocks.cu",
            "distill.cu"]
-HEADERS = ["ptx.cuh", "common.cuh", "internal.h", "epilogue.cuh", "pair_end.cuh"]
+HEADERS = ["ptx.cuh", "common.cuh", "internal.h", "epilogue.cuh", "pair_end.cuh", "glu_grad.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

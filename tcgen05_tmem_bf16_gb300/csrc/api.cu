@@ -452,6 +452,29 @@ bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint6
   return tmap_2d(m, base, dt, inner, outer, row_bytes, box_inner, box_outer, swz);
 }
 
+int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,
+                 int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream) {
+  const DeviceInfo* dev;
+  unsigned* err;
+  const gbf_status_t st = current_device(&dev, &err);
+  if (st != GBF_OK) return st;
+  EpiParams ep = make_ep(nullptr, nullptr, nullptr, h, 1.0f, 0.0f, act);
+  ep.out2 = static_cast<__nv_bfloat16*>(g);
+  ep.out3 = static_cast<__nv_bfloat16*>(u);
+  return run_gemm(x, w_gate, w_up, GBF_B_NK, true, ep, M, F, D, *dev, err, stream);
+}
+
+int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void* u, void* dg,
+                 void* du, int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream) {
+  const DeviceInfo* dev;
+  unsigned* err;
+  const gbf_status_t st = current_device(&dev, &err);
+  if (st != GBF_OK) return st;
+  EpiParams ep = make_ep(g, nullptr, u, dg, 1.0f, 0.0f, act);
+  ep.out2 = static_cast<__nv_bfloat16*>(du);
+  return run_gemm(dout, w_down, nullptr, GBF_B_KN, false, ep, M, F, D, *dev, err, stream);
+}
+
 KernelCtl lib_ctl(unsigned* err, int64_t ctas) { return make_ctl(err, ctas); }
 
 int check_gemm_call(const void* A, const void* B, int b_layout, const void* C, const void* bias,

@@ -56,17 +56,22 @@ int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
 }
 
 // The launch of dx and the weights' gradients: row tiles per unit, and the parts of K
-// of the product for dx, each with an fp32 buffer of its own.  As the whole launch is
-// fastest by the estimate: 16 parts at most, none shorter than 8 K blocks.  Adding the
-// parts costs a launch and their traffic.
+// of the product for dx, each with an fp32 buffer of its own, 16 at most and none
+// shorter than 8 K blocks.  With one row tile as many as give one round of units over
+// the pairs (16 x 4096 x 14336, all of the launch: 3 parts 111 us, 4, one round, 104, 5
+// 116, 9 107).  Else as the whole launch is fastest by the estimate; adding the parts
+// costs a launch and their traffic (1021 x 1000 x 2728: none 40 us, 2 or 3 parts 30.2,
+// 4 33.6).
 struct MlpPlan {
   int streams, dx_splits;
 };
 MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
   MlpPlan p{};
   int64_t best = 0;
-  const int64_t k = 2 * ceil_div64(F, kBK);
-  for (int splits = 1; splits <= std::max<int64_t>(1, std::min<int64_t>(k / 8, 16)); ++splits) {
+  const int64_t k = 2 * ceil_div64(F, kBK), d = ceil_div64(D, 256);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
+  if (M <= kMlpRows) return {1, static_cast<int>(std::max<int64_t>(1, std::min(most, kMlpPairs / d)))};
+  for (int splits = 1; splits <= most; ++splits) {
     MbLaunch l{};
     set_dx(&l.job[0], M, D, F, splits);
     set_job(&l.job[1], kMbStore, F, D, M, true, true);
@@ -199,6 +204,14 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   if (M == 0) return GBF_OK;
+  if (M <= kSwapDualMaxM) {
+    // few rows: the weights' bytes count, and the swapped kernel splits K over clusters
+    // (16 x 4096 x 14336: 41 us, units of 256 rows 54)
+    st = lib_glu_keep(x, w_gate, w_up, h, g, u, M, F, D, act, reinterpret_cast<cudaStream_t>(stream));
+    if (st != GBF_OK) return st;
+    return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
+                         GBF_ACT_IDENTITY, nullptr, 0, stream);
+  }
   MbLaunch l{};
   MbJob& j = l.job[1];
   set_job(&j, kMbGlu, M, F, D, false, false);
@@ -247,7 +260,11 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
   const bool hidden = dx || dw_gate || dw_up;
   const MlpPlan plan = plan_mlp(M, D, F);
   const int splits = plan.dx_splits, streams = plan.streams;
-  if (hidden) {
+  if (hidden && M <= kSwapGradMaxM) {
+    // few rows, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
+    // rows 32)
+    if ((st = lib_glu_grad(dout, w_down, g, u, ws.dg, ws.du, M, F, D, act, s)) != GBF_OK) return st;
+  } else if (hidden) {
     MbLaunch l{};
     MbJob& j = l.job[0];
     set_job(&j, kMbGluGrad, M, F, D, false, true);

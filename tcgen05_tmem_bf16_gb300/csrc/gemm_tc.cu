@@ -33,6 +33,7 @@
 
 #include "common.cuh"
 #include "epilogue.cuh"
+#include "glu_grad.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -459,7 +460,63 @@ __device__ __forceinline__ void epi_col_glu(const float (&g)[R], const float (&u
   }
 }
 
-template <int MPAD, bool W_KN, bool DUAL>
+// Endings of the swapped kernel (EpiParams: out2).
+enum SwapEnd { kSwapPlain = 0, kSwapKeep = 1, kSwapGluGrad = 2 };
+
+// One output column for R consecutive rows; v1: the up product of the gate/up GEMM.
+template <int ACT, bool DUAL, int END, int R>
+__device__ __forceinline__ void swap_end_act(const float (&v0)[R], const float (&v1)[R],
+                                             const ColLoads<R>& L, int64_t m0, int n, int M, int N,
+                                             const EpiParams& e, uint64_t pol) {
+  if constexpr (END == kSwapGluGrad) {
+    if (n >= N) return;
+#pragma unroll
+    for (int j = 0; j < R; j += 2) {
+      f2 y, dy;
+      act_both<ACT>(f2_of(L.c[j], L.c[j + 1]), y, dy);
+      const f2 d = f2_of(v0[j], v0[j + 1]);
+      float dg[2], du[2];
+      f2_get(f2_mul(f2_mul(d, f2_of(L.r[j], L.r[j + 1])), dy), dg[0], dg[1]);
+      f2_get(f2_mul(d, y), du[0], du[1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t m = m0 + j + i;
+        if (m >= M) break;
+        e.out[m * N + n] = __float2bfloat16_rn(dg[i]);  // the next product's operands
+        e.out2[m * N + n] = __float2bfloat16_rn(du[i]);
+      }
+    }
+  } else if constexpr (DUAL) {
+    epi_col_glu<ACT, R>(v0, v1, L, m0, n, M, N, e, pol);
+    if constexpr (END == kSwapKeep) {
+      if (n >= N) return;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int64_t m = m0 + j;
+        if (m >= M) break;
+        st_stream_u16(e.out2 + m * N + n, f_to_bf16bits(v0[j]), pol);
+        st_stream_u16(e.out3 + m * N + n, f_to_bf16bits(v1[j]), pol);
+      }
+    }
+  } else {
+    epi_col<ACT, R>(v0, L, m0, n, M, N, e, pol);
+  }
+}
+template <bool DUAL, int END, int R>
+__device__ __forceinline__ void swap_end(const float (&v0)[R], const float (&v1)[R],
+                                         const ColLoads<R>& L, int64_t m0, int n, int M, int N,
+                                         const EpiParams& e, uint64_t pol) {
+  switch (e.act) {
+    case kActRelu: swap_end_act<kActRelu, DUAL, END, R>(v0, v1, L, m0, n, M, N, e, pol); break;
+    case kActSilu: swap_end_act<kActSilu, DUAL, END, R>(v0, v1, L, m0, n, M, N, e, pol); break;
+    case kActGeluTanh:
+      swap_end_act<kActGeluTanh, DUAL, END, R>(v0, v1, L, m0, n, M, N, e, pol);
+      break;
+    default: swap_end_act<kActIdentity, DUAL, END, R>(v0, v1, L, m0, n, M, N, e, pol); break;
+  }
+}
+
+template <int MPAD, bool W_KN, bool DUAL, int END>
 __global__ void __launch_bounds__(256, 2)
     gemm_swap_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmW,
@@ -737,23 +794,7 @@ __global__ void __launch_bounds__(256, 2)
             v[pr][3] = t.w;
           }
           const int64_t m0 = static_cast<int64_t>(mb) * MPAD + 4 * g;
-          if constexpr (DUAL) {
-            switch (a.ep.act) {
-              case kActRelu: epi_col_glu<kActRelu, 4>(v[0], v[kP - 1], L4, m0, n, a.M, a.N, a.ep, pol); break;
-              case kActSilu: epi_col_glu<kActSilu, 4>(v[0], v[kP - 1], L4, m0, n, a.M, a.N, a.ep, pol); break;
-              case kActGeluTanh:
-                epi_col_glu<kActGeluTanh, 4>(v[0], v[kP - 1], L4, m0, n, a.M, a.N, a.ep, pol);
-                break;
-              default: epi_col_glu<kActIdentity, 4>(v[0], v[kP - 1], L4, m0, n, a.M, a.N, a.ep, pol); break;
-            }
-          } else {
-            switch (a.ep.act) {
-              case kActRelu: epi_col<kActRelu, 4>(v[0], L4, m0, n, a.M, a.N, a.ep, pol); break;
-              case kActSilu: epi_col<kActSilu, 4>(v[0], L4, m0, n, a.M, a.N, a.ep, pol); break;
-              case kActGeluTanh: epi_col<kActGeluTanh, 4>(v[0], L4, m0, n, a.M, a.N, a.ep, pol); break;
-              default: epi_col<kActIdentity, 4>(v[0], L4, m0, n, a.M, a.N, a.ep, pol); break;
-            }
-          }
+          swap_end<DUAL, END, 4>(v[0], v[kP - 1], L4, m0, n, a.M, a.N, a.ep, pol);
         }
       }
       // No rank leaves while copies from or into its shared memory may be in
@@ -824,12 +865,7 @@ __global__ void __launch_bounds__(256, 2)
           }
         }
         const int64_t m0 = static_cast<int64_t>(mb) * MPAD + c * 16 + 8 * h;
-        switch (a.ep.act) {
-          case kActRelu: epi_col<kActRelu, 8>(v, L8, m0, ncol, a.M, a.N, a.ep, pol); break;
-          case kActSilu: epi_col<kActSilu, 8>(v, L8, m0, ncol, a.M, a.N, a.ep, pol); break;
-          case kActGeluTanh: epi_col<kActGeluTanh, 8>(v, L8, m0, ncol, a.M, a.N, a.ep, pol); break;
-          default: epi_col<kActIdentity, 8>(v, L8, m0, ncol, a.M, a.N, a.ep, pol); break;
-        }
+        swap_end<DUAL, END, 8>(v, v, L8, m0, ncol, a.M, a.N, a.ep, pol);
       }
       // No rank leaves while another may still read its shared memory: every
       // remote load's value has been used before its thread arrives.  The
@@ -859,23 +895,7 @@ __global__ void __launch_bounds__(256, 2)
           for (int j = 0; j < 16; ++j) v[pr][j] = have ? rr[j] : 0.0f;
         }
         const int64_t m0 = static_cast<int64_t>(mb) * MPAD + c * 16;
-        if constexpr (DUAL) {
-          switch (a.ep.act) {
-            case kActRelu: epi_col_glu<kActRelu, 16>(v[0], v[1], L, m0, n, a.M, a.N, a.ep, pol); break;
-            case kActSilu: epi_col_glu<kActSilu, 16>(v[0], v[1], L, m0, n, a.M, a.N, a.ep, pol); break;
-            case kActGeluTanh:
-              epi_col_glu<kActGeluTanh, 16>(v[0], v[1], L, m0, n, a.M, a.N, a.ep, pol);
-              break;
-            default: epi_col_glu<kActIdentity, 16>(v[0], v[1], L, m0, n, a.M, a.N, a.ep, pol); break;
-          }
-        } else {
-          switch (a.ep.act) {
-            case kActRelu: epi_col<kActRelu, 16>(v[0], L, m0, n, a.M, a.N, a.ep, pol); break;
-            case kActSilu: epi_col<kActSilu, 16>(v[0], L, m0, n, a.M, a.N, a.ep, pol); break;
-            case kActGeluTanh: epi_col<kActGeluTanh, 16>(v[0], L, m0, n, a.M, a.N, a.ep, pol); break;
-            default: epi_col<kActIdentity, 16>(v[0], L, m0, n, a.M, a.N, a.ep, pol); break;
-          }
-        }
+        swap_end<DUAL, END, 16>(v[0], v[Cfg::kProducts - 1], L, m0, n, a.M, a.N, a.ep, pol);
       }
     }
   }
@@ -942,11 +962,11 @@ cudaError_t run_persistent_split(const GemmPlan& p, const CUtensorMap& tmA,
   return cudaLaunchKernelEx(&cfg, kernel, tmA, tmW, tmW, tmO, args);
 }
 
-template <int MPAD, bool W_KN, bool DUAL>
+template <int MPAD, bool W_KN, bool DUAL, int END = kSwapPlain>
 cudaError_t run_swap(const GemmPlan& p, const CUtensorMap& tmA, const CUtensorMap& tmW,
                      const CUtensorMap& tmW2, const SwapArgs& args, cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = gemm_swap_kernel<MPAD, W_KN, DUAL>;
+  auto kernel = gemm_swap_kernel<MPAD, W_KN, DUAL, END>;
   using Cfg = SwapCfg<MPAD, DUAL>;
   cudaError_t e = ensure_smem_attr(kernel, Cfg::kSmem, mask);
   if (e != cudaSuccess) return e;
@@ -973,6 +993,26 @@ template <bool W_KN>
 cudaError_t run_swap_mpad(const GemmPlan& p, bool dual, const CUtensorMap& tmA,
                           const CUtensorMap& tmW, const CUtensorMap& tmW2, const SwapArgs& args,
                           cudaStream_t stream) {
+  if (dual && args.ep.out3) {
+    if constexpr (!W_KN) {
+      switch (p.mpad) {
+        case 16: return run_swap<16, W_KN, true, kSwapKeep>(p, tmA, tmW, tmW2, args, stream);
+        case 32: return run_swap<32, W_KN, true, kSwapKeep>(p, tmA, tmW, tmW2, args, stream);
+      }
+    }
+    return cudaErrorInvalidValue;
+  }
+  if (!dual && args.ep.out2) {
+    if constexpr (W_KN) {
+      switch (p.mpad) {
+        case 16: return run_swap<16, W_KN, false, kSwapGluGrad>(p, tmA, tmW, tmW, args, stream);
+        case 32: return run_swap<32, W_KN, false, kSwapGluGrad>(p, tmA, tmW, tmW, args, stream);
+        case 64: return run_swap<64, W_KN, false, kSwapGluGrad>(p, tmA, tmW, tmW, args, stream);
+        case 128: return run_swap<128, W_KN, false, kSwapGluGrad>(p, tmA, tmW, tmW, args, stream);
+      }
+    }
+    return cudaErrorInvalidValue;
+  }
   if (dual) {
     switch (p.mpad) {
       case 16: return run_swap<16, W_KN, true>(p, tmA, tmW, tmW2, args, stream);

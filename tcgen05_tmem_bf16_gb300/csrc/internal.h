@@ -19,6 +19,11 @@ struct EpiParams {
   float alpha;
   float beta;
   int act;
+  // Endings of the swapped kernel for a gated block that is trained.  Gate/up product,
+  // out3 set: g and u are stored as well (out2, out3).  Single product, out2 set: it is
+  // dh, C and residual are g and u, and out and out2 receive dg and du.
+  __nv_bfloat16* out2 = nullptr;
+  __nv_bfloat16* out3 = nullptr;
 };
 
 // Per-launch control: the device error word, the wait limit and the
@@ -338,6 +343,14 @@ int lib_device(const DeviceInfo** info, unsigned** err);
 bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz);
+// The products of a gated block that is trained on the swapped kernel (EpiParams:
+// out2): h, g, u = act(g) u, x Wg^T, x Wu^T for M <= kSwapDualMaxM; dg, du from dout Wd
+// for M <= 128.  Arguments as checked by the caller.
+int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,
+                 int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream);
+int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void* u, void* dg,
+                 void* du, int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream);
+constexpr int kSwapGradMaxM = 128;
 // Launch control of a grid of `ctas`.
 KernelCtl lib_ctl(unsigned* err, int64_t ctas);
 // gbf_workspace_size() of the operators in heads.cu and blocks.cu.
