@@ -109,7 +109,11 @@ __global__ void __launch_bounds__(kSwThreads, 2)
     tmem_relinquish();
   }
   if (threadIdx.x == 0) griddep_launch_dependents();
-  griddep_wait();  // the gradient's scored rows are listed by the kernel before
+  // The gradient's scored rows are listed by the kernel before.  The forward pass over
+  // lists is launched by the kernel that makes them, once everything before that one
+  // has completed: x and w are read meanwhile, and only the ending waits.
+  constexpr bool kEarly = PICK && !GRAD;
+  if (!kEarly) griddep_wait();
   const int count = GRAD ? *e.count : e.M;
   for (int i = threadIdx.x; i < MPAD; i += kSwThreads) {
     if (GRAD) {
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       row_tgt[i] = t >= 0 && t < a.cols ? static_cast<int>(t) : -1;
     }
   }
-  if (!GRAD && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
+  if (!GRAD && !PICK && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -220,6 +224,10 @@ __global__ void __launch_bounds__(kSwThreads, 2)
     }
     __syncwarp();
   } else {
+    if (kEarly) {
+      griddep_wait();
+      if (blockIdx.x == 0 && threadIdx.x == 64) *a.ticket = 0u;
+    }
     const int q = warp & 3;  // the quarter of tensor memory that this warp reads
     float* my_turn = turn + q * 32 * 17;
     const int chunks = (count + 15) / 16;  // of 16 rows

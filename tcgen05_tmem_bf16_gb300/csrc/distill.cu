@@ -10,8 +10,8 @@
 // place is the number of columns before its own, counted by its own thread: no
 // exchange, no atomics, the same sums in the same order on every run.
 //
-// One CTA per row in turn.  Bound by latency and, for a large vocabulary, by writing
-// `at` (2 bytes per 128 columns and row).
+// One CTA per row in turn.  Bound by the operations of the counting (K^2 per row) and
+// by latency.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,120 +28,171 @@ namespace {
 constexpr int kListThreads = 128;
 constexpr int kListWarps = kListThreads / 32;
 
-// SLOTS entries per thread: one for short lists (1 row of 8 entries x 32000: 6.1 us
-// with the eight that the longest take, 4.3 with one).
+// What a row's CTA holds of its entries, up to MOST of them.
+template <int MOST>
+struct ListRow {
+  int4 col[MOST / 4];    // as given; INT_MAX where not valid, and up to a multiple of four
+  float share[MOST];
+  int sorted[MOST];      // the columns in ascending order
+  float sorted_share[MOST];
+  float part[2][kListWarps];
+  int count[kListWarps];
+};
+
+// The row has a column twice: every entry looks for its column's others, and the first
+// of them takes the sum of the shares in the entries' order.  Returns the number of
+// different columns.
+template <int MOST>
+__device__ int merge_columns(ListRow<MOST>& s, int K) {
+  constexpr int kSlots = MOST / kListThreads;
+  int* col = reinterpret_cast<int*>(s.col);
+  float all[kSlots];
+  bool first[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int k = threadIdx.x + i * kListThreads;
+    first[i] = false;
+    if (k >= K) continue;
+    const int c = col[k];
+    first[i] = c != INT_MAX;
+    all[i] = 0.0f;
+    for (int j = 0; j < K; ++j) {
+      if (col[j] != c) continue;
+      first[i] = first[i] && j >= k;
+      all[i] += s.share[j];
+    }
+  }
+  __syncthreads();
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int k = threadIdx.x + i * kListThreads;
+    if (k < K && !first[i]) col[k] = INT_MAX;
+    n += first[i];
+  }
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if ((threadIdx.x & 31) == 0) s.count[threadIdx.x >> 5] = n;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int k = threadIdx.x + i * kListThreads;
+    if (!first[i]) continue;
+    int before = 0;
+    for (int j = 0; j < K; ++j) before += col[j] < col[k];
+    s.sorted[before] = col[k];
+    s.sorted_share[before] = all[i];
+  }
+  n = 0;
+  for (int w = 0; w < kListWarps; ++w) n += s.count[w];
+  return n;
+}
+
+// SLOTS entries per thread: one for short lists.
 template <int SLOTS>
 __global__ void __launch_bounds__(kListThreads) ce_lists_kernel(const CeLists p) {
-  constexpr int kMost = SLOTS * kListThreads;
-  __shared__ int col[kMost];    // as given; INT_MAX where not valid
-  __shared__ int lead[kMost];   // the same, but only at a column's first entry
-  __shared__ float share[kMost];
-  __shared__ int sorted[kMost];
-  __shared__ float part[2][kListWarps];
-  __shared__ int count[kListWarps];
-  griddep_launch_dependents();
+  __shared__ ListRow<SLOTS * kListThreads> s;
+  int* col = reinterpret_cast<int*>(s.col);
   griddep_wait();
+  // From here on the kernels before this one have completed: the next may start, and
+  // read all but this one's results before its own wait.
+  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quads = (p.K + 3) / 4;
   for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x) {
-    float t[SLOTS];  // this thread's logits, then shares
+    float t[SLOTS];  // this thread's logits, then exponentials
     float top = -INFINITY;
+    int n = 0;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int k = threadIdx.x + i * kListThreads;
       t[i] = -INFINITY;
-      if (k >= p.K) continue;
-      const int64_t at = row * p.K + k;
-      const int64_t id = p.ids64 ? static_cast<const int64_t*>(p.ids)[at]
-                                 : static_cast<const int*>(p.ids)[at];
-      const float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at])
-                             : static_cast<const float*>(p.logits)[at];
-      const bool ok = id >= 0 && id < p.V && x != -INFINITY;
-      col[k] = ok ? static_cast<int>(id) : INT_MAX;
+      if (k >= 4 * quads) continue;
+      bool ok = k < p.K;
+      int64_t id = 0;
       if (ok) {
-        t[i] = p.beta * x;
-        top = fmaxf(top, t[i]);
+        const int64_t at = row * p.K + k;
+        id = p.ids64 ? static_cast<const int64_t*>(p.ids)[at]
+                     : static_cast<const int*>(p.ids)[at];
+        const float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at])
+                               : static_cast<const float*>(p.logits)[at];
+        ok = id >= 0 && id < p.V && x != -INFINITY;
+        if (ok) {
+          t[i] = p.beta * x;
+          top = fmaxf(top, t[i]);
+          ++n;
+        }
       }
+      col[k] = ok ? static_cast<int>(id) : INT_MAX;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if (lane == 0) part[0][warp] = top;
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (lane == 0) {
+      s.part[0][warp] = top;
+      s.count[warp] = n;
+    }
     __syncthreads();
+    n = 0;
 #pragma unroll
-    for (int w = 0; w < kListWarps; ++w) top = fmaxf(top, part[0][w]);
+    for (int w = 0; w < kListWarps; ++w) {
+      top = fmaxf(top, s.part[0][w]);
+      n += s.count[w];
+    }
     float sum = 0.0f;
+    int before[SLOTS];
+    bool twice = false;
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int k = threadIdx.x + i * kListThreads;
+      before[i] = 0;
       if (k >= p.K || col[k] == INT_MAX) continue;
       // a product that has left fp32's range downwards all the same has the largest
       // logit's place: no minus infinity less minus infinity
       t[i] = expf(t[i] == top ? 0.0f : t[i] - top);
       sum += t[i];
+      const int c = col[k];
+      int same = 0;
+      for (int j = 0; j < quads; ++j) {
+        const int4 x = s.col[j];
+        before[i] += (x.x < c) + (x.y < c) + (x.z < c) + (x.w < c);
+        same += (x.x == c) + (x.y == c) + (x.z == c) + (x.w == c);
+      }
+      twice = twice || same > 1;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) part[1][warp] = sum;
-    __syncthreads();
+    if (lane == 0) s.part[1][warp] = sum;
+    const bool merge = __syncthreads_or(twice);
     sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kListWarps; ++w) sum += part[1][w];
-    int n = 0;
+    for (int w = 0; w < kListWarps; ++w) sum += s.part[1][w];
 #pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       const int k = threadIdx.x + i * kListThreads;
-      if (k >= p.K) continue;
-      share[k] = t[i] / sum;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      const int k = threadIdx.x + i * kListThreads;
-      if (k >= p.K) continue;
-      const int c = col[k];
-      bool first = c != INT_MAX;
-      float all = 0.0f;
-      for (int j = 0; j < p.K; ++j) {
-        if (col[j] != c) continue;
-        first = first && j >= k;
-        all += share[j];
+      if (k >= p.K || col[k] == INT_MAX) continue;
+      if (merge) {
+        s.share[k] = t[i] / sum;
+      } else {
+        s.sorted[before[i]] = col[k];
+        s.sorted_share[before[i]] = t[i] / sum;
       }
-      lead[k] = first ? c : INT_MAX;
-      t[i] = all;
-      n += first;
     }
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (lane == 0) count[warp] = n;
     __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int w = 0; w < kListWarps; ++w) n += count[w];
+    if (merge) {
+      n = merge_columns(s, p.K);
+      __syncthreads();
+    }
     int2* list = p.list + row * (p.K + 1);
-#pragma unroll
-    for (int i = 0; i < SLOTS; ++i) {
-      const int k = threadIdx.x + i * kListThreads;
-      if (k >= p.K) continue;
-      const int c = lead[k];
-      if (c != INT_MAX) {
-        int before = 0;
-        for (int j = 0; j < p.K; ++j) before += lead[j] < c;
-        sorted[before] = c;
-        list[before] = make_int2(c, __float_as_int(t[i]));
-      }
-      if (k >= n) list[k] = make_int2(INT_MAX, 0);
-    }
-    if (threadIdx.x == 0) list[p.K] = make_int2(INT_MAX, 0);
-    __syncthreads();
-    if (threadIdx.x == 0) p.tgt[row] = n > 0 ? sorted[0] : -1;
+    for (int i = threadIdx.x; i <= p.K; i += kListThreads)
+      list[i] = i < n ? make_int2(s.sorted[i], __float_as_int(s.sorted_share[i]))
+                      : make_int2(INT_MAX, 0);
+    if (threadIdx.x == 0) p.tgt[row] = n > 0 ? s.sorted[0] : -1;
+    // at[b] == i from behind the block of the entry before to its own block
     uint16_t* at = p.at + row * p.stride;
-    for (int b = threadIdx.x; b < p.stride; b += kListThreads) {
-      const int64_t first = static_cast<int64_t>(b) << p.shift;
-      int lo = 0, hi = n;  // the entries before column `first`
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (sorted[mid] < first) lo = mid + 1;
-        else hi = mid;
-      }
-      at[b] = static_cast<uint16_t>(lo);
+    for (int i = warp; i <= n; i += kListWarps) {
+      const int from = i > 0 ? (s.sorted[i - 1] >> p.shift) + 1 : 0;
+      const int to = i < n ? s.sorted[i] >> p.shift : p.stride - 1;
+      for (int b = from + lane; b <= to; b += 32) at[b] = static_cast<uint16_t>(i);
     }
     __syncthreads();  // the arrays are the next row's
   }
