@@ -218,6 +218,9 @@ int choose_splits(int tiles, int num_kb, const DeviceInfo& dev) {
   return s;
 }
 
+GemmPlan persistent_plan(int64_t M, int64_t N, int64_t K, bool dual, bool split,
+                         const DeviceInfo& dev);
+
 // Dense GEMM (+ dual) launch after validation.  D rows of out.
 gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, bool dual,
                       const EpiParams& ep, int64_t M, int64_t N, int64_t K,
@@ -236,7 +239,9 @@ gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, 
     return cuda_status(launch_pointwise_epilogue(nullptr, ep, M, N, dev.sms, stream));
   }
   const bool kn = layout == GBF_B_KN;
-  const GemmPlan plan = plan_gemm(M, N, K, dual, kn, dev);
+  const bool keep = dual && ep.out3;
+  const GemmPlan plan = keep && M > kSwapDualMaxM ? persistent_plan(M, N, K, true, false, dev)
+                                                  : plan_gemm(M, N, K, dual, kn, dev);
   CUtensorMap tmA, tmW, tmW2;
   const uint32_t a_rows = plan.path == kPathSwap ? plan.mpad : kBM;
   const bool pair =
@@ -267,9 +272,15 @@ gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, 
                                         static_cast<int>(N), static_cast<int>(K),
                                         make_ctl(err, plan_ctas(plan)), stream));
   }
+  CUtensorMap kept[2];
+  const __nv_bfloat16* kept_at[2] = {ep.out2, ep.out3};
+  for (int i = 0; keep && i < 2; ++i)
+    if (!tmap_2d(&kept[i], kept_at[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, N, M, N * 2, 32, 32,
+                 CU_TENSOR_MAP_SWIZZLE_64B))
+      return GBF_ERR_CUDA;
   return cuda_status(launch_gemm(plan, kn, dual, tmA, tmW, tmW2, tmO, ep, static_cast<int>(M),
                                  static_cast<int>(N), static_cast<int>(K),
-                                 make_ctl(err, plan_ctas(plan)), stream));
+                                 make_ctl(err, plan_ctas(plan)), stream, keep ? kept : nullptr));
 }
 
 // Weight-only quantised GEMM launch after validation (fmt: WqFmt).

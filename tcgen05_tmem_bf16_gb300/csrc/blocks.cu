@@ -204,25 +204,28 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
   unsigned* err;
   if ((st = lib_device(&dev, &err)) != GBF_OK) return st;
   if (M == 0) return GBF_OK;
-  if (M <= kSwapDualMaxM) {
-    // few rows: the weights' bytes count, and the swapped kernel splits K over clusters
-    // (16 x 4096 x 14336: 41 us, units of 256 rows 54)
-    st = lib_glu_keep(x, w_gate, w_up, h, g, u, M, F, D, act, reinterpret_cast<cudaStream_t>(stream));
-    if (st != GBF_OK) return st;
-    return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
-                         GBF_ACT_IDENTITY, nullptr, 0, stream);
-  }
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   MbLaunch l{};
   MbJob& j = l.job[1];
   set_job(&j, kMbGlu, M, F, D, false, false);
   l.act = act;
-  if (!map_k(&j.a[0], x, D, M) || !map_k(&j.b[0], w_gate, D, F) || !map_k(&j.b[1], w_up, D, F) ||
-      !map_out(&j.o[0], h, F, M, false) || !map_out(&j.o[1], g, F, M, false) ||
-      !map_out(&j.o[2], u, F, M, false))
-    return GBF_ERR_CUDA;
-  if ((st = run_launch(&l, faster_streams(&l, M, nullptr), *dev, err,
-                       reinterpret_cast<cudaStream_t>(stream))) != GBF_OK)
-    return st;
+  int64_t cycles;
+  const int streams = faster_streams(&l, M, &cycles);
+  // Few rows: the weights' bytes count, and the swapped kernel splits K over clusters
+  // (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
+  // rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs 56; 257 x 2048 x 5632
+  // 21, 28; 256 x 4096 x 14336 64, 56).
+  const int64_t tiles = ceil_div64(M, 128) * ceil_div64(F, 128);
+  if (M <= kSwapDualMaxM ||
+      ceil_div64(tiles, kMaxSms) * ceil_div64(D, kBK) * 680 + 9000 < cycles) {
+    if ((st = lib_glu_keep(x, w_gate, w_up, h, g, u, M, F, D, act, s)) != GBF_OK) return st;
+  } else {
+    if (!map_k(&j.a[0], x, D, M) || !map_k(&j.b[0], w_gate, D, F) || !map_k(&j.b[1], w_up, D, F) ||
+        !map_out(&j.o[0], h, F, M, false) || !map_out(&j.o[1], g, F, M, false) ||
+        !map_out(&j.o[2], u, F, M, false))
+      return GBF_ERR_CUDA;
+    if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
+  }
   return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
                        GBF_ACT_IDENTITY, nullptr, 0, stream);
 }

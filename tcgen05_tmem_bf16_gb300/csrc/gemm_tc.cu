@@ -71,12 +71,15 @@ constexpr int kPSplitHalf = kPersistBN / 2;                     // columns each 
 constexpr int kPSplitBytes = kPSplitHalf * kBM * 4;             // 64 KB of fp32 partials
 static_assert(2 * kPSplitBytes <= kPStages * kPStageBytes, "partials fit in the ring");
 
-template <bool W_KN, bool DUAL, bool SPLIT>
+// KEEP (gate/up GEMM): g and u are stored as well, to tmG and tmU (EpiParams: out3).
+template <bool W_KN, bool DUAL, bool SPLIT, bool KEEP>
 __global__ void __launch_bounds__(kPThreads, 1)
     gemm_persistent_kernel(const __grid_constant__ CUtensorMap tmA,
                            const __grid_constant__ CUtensorMap tmW,
                            const __grid_constant__ CUtensorMap tmW2,
-                           const __grid_constant__ CUtensorMap tmO, const PersistArgs a) {
+                           const __grid_constant__ CUtensorMap tmO,
+                           const __grid_constant__ CUtensorMap tmG,
+                           const __grid_constant__ CUtensorMap tmU, const PersistArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
   uint8_t* stages = smem;
@@ -90,6 +93,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   int* abort_flag = reinterpret_cast<int*>(tmem_holder + 1);
   uint8_t* staging = smem + kPStages * kPStageBytes + kPBarBytes;  // 1024-aligned
   static_assert(!(SPLIT && DUAL), "split-K form for the single product only");
+  static_assert(!KEEP || DUAL, "g and u of the gate/up GEMM");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -279,6 +283,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
           default: epi_row32_pack<kActIdentity, DUAL>(acc, up, cur, a.ep, w); break;
         }
         store_chunk32(my_staging, flip, w, &tmO, row - lane, col0, a.M, a.N, pol);
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            w[k] = pack_bf16x2(__uint_as_float(acc[2 * k]), __uint_as_float(acc[2 * k + 1]));
+          store_chunk32(my_staging, flip, w, &tmG, row - lane, col0, a.M, a.N, pol);
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            w[k] = pack_bf16x2(__uint_as_float(up[2 * k]), __uint_as_float(up[2 * k + 1]));
+          store_chunk32(my_staging, flip, w, &tmU, row - lane, col0, a.M, a.N, pol);
+        }
       }
     }
     // every staged chunk written to global memory before the CTA may exit
@@ -926,15 +940,17 @@ cudaError_t ensure_smem_attr(K kernel, int bytes, std::atomic<uint64_t>& mask) {
   return e;
 }
 
-template <bool W_KN, bool DUAL>
+template <bool W_KN, bool DUAL, bool KEEP = false>
 cudaError_t run_persistent(const GemmPlan& p, const CUtensorMap& tmA, const CUtensorMap& tmW,
                            const CUtensorMap& tmW2, const CUtensorMap& tmO,
-                           const PersistArgs& args, cudaStream_t stream) {
+                           const PersistArgs& args, cudaStream_t stream,
+                           const CUtensorMap* keep = nullptr) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = gemm_persistent_kernel<W_KN, DUAL, false>;
+  auto kernel = gemm_persistent_kernel<W_KN, DUAL, false, KEEP>;
   cudaError_t e = ensure_smem_attr(kernel, kPSmem, mask);
   if (e != cudaSuccess) return e;
-  kernel<<<p.grid, kPThreads, kPSmem, stream>>>(tmA, tmW, tmW2, tmO, args);
+  kernel<<<p.grid, kPThreads, kPSmem, stream>>>(tmA, tmW, tmW2, tmO, KEEP ? keep[0] : tmO,
+                                                 KEEP ? keep[1] : tmO, args);
   return cudaGetLastError();
 }
 
@@ -944,7 +960,7 @@ cudaError_t run_persistent_split(const GemmPlan& p, const CUtensorMap& tmA,
                                  const CUtensorMap& tmW, const CUtensorMap& tmO,
                                  const PersistArgs& args, cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
-  auto kernel = gemm_persistent_kernel<W_KN, false, true>;
+  auto kernel = gemm_persistent_kernel<W_KN, false, true, false>;
   cudaError_t e = ensure_smem_attr(kernel, kPSmem, mask);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -959,7 +975,7 @@ cudaError_t run_persistent_split(const GemmPlan& p, const CUtensorMap& tmA,
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmW, tmW, tmO, args);
+  return cudaLaunchKernelEx(&cfg, kernel, tmA, tmW, tmW, tmO, tmO, tmO, args);
 }
 
 template <int MPAD, bool W_KN, bool DUAL, int END = kSwapPlain>
@@ -1034,7 +1050,7 @@ cudaError_t run_swap_mpad(const GemmPlan& p, bool dual, const CUtensorMap& tmA,
 cudaError_t launch_gemm(const GemmPlan& plan, bool w_kn, bool dual, const CUtensorMap& tmA,
                         const CUtensorMap& tmW, const CUtensorMap& tmW2, const CUtensorMap& tmO,
                         const EpiParams& ep, int M, int N, int K, const KernelCtl& ctl,
-                        cudaStream_t stream) {
+                        cudaStream_t stream, const CUtensorMap* keep) {
   if (plan.path == kPathPersistentSplit && !dual) {
     PersistArgs args{M, N, K, plan.m_tiles, plan.n_tiles, plan.num_kb, ep, ctl};
     return w_kn ? run_persistent_split<true>(plan, tmA, tmW, tmO, args, stream)
@@ -1042,6 +1058,8 @@ cudaError_t launch_gemm(const GemmPlan& plan, bool w_kn, bool dual, const CUtens
   }
   if (plan.path == kPathPersistent) {
     PersistArgs args{M, N, K, plan.m_tiles, plan.n_tiles, plan.num_kb, ep, ctl};
+    if (keep && dual && !w_kn)
+      return run_persistent<false, true, true>(plan, tmA, tmW, tmW2, tmO, args, stream, keep);
     if (w_kn)
       return dual ? run_persistent<true, true>(plan, tmA, tmW, tmW2, tmO, args, stream)
                   : run_persistent<true, false>(plan, tmA, tmW, tmW2, tmO, args, stream);

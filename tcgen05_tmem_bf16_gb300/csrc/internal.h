@@ -19,9 +19,10 @@ struct EpiParams {
   float alpha;
   float beta;
   int act;
-  // Endings of the swapped kernel for a gated block that is trained.  Gate/up product,
-  // out3 set: g and u are stored as well (out2, out3).  Single product, out2 set: it is
-  // dh, C and residual are g and u, and out and out2 receive dg and du.
+  // Endings for a gated block that is trained.  Gate/up product of the swapped and the
+  // persistent kernel, out3 set: g and u are stored as well (out2, out3).  Single
+  // product of the swapped kernel, out2 set: it is dh, C and residual are g and u, and
+  // out and out2 receive dg and du.
   __nv_bfloat16* out2 = nullptr;
   __nv_bfloat16* out3 = nullptr;
 };
@@ -84,11 +85,12 @@ GemmPlan plan_w4a16(int64_t M, int64_t N, int64_t K, const DeviceInfo& dev);
 // Dense bf16 GEMM with fused ending (gemm_tc.cu).  tmA: activations [M][K];
 // tmW / tmW2: weights (tmW2 = up weights of the dual GEMM); tmO: the output
 // [M][N] in boxes of 32 x 32 with the 64-byte swizzle (used by the
-// persistent kernel's TMA stores; the swapped kernel writes directly).
+// persistent kernel's TMA stores; the swapped kernel writes directly).  keep: the maps
+// of g and u where the persistent gate/up GEMM stores them too (EpiParams: out3).
 cudaError_t launch_gemm(const GemmPlan& plan, bool w_kn, bool dual, const CUtensorMap& tmA,
                         const CUtensorMap& tmW, const CUtensorMap& tmW2, const CUtensorMap& tmO,
                         const EpiParams& ep, int M, int N, int K, const KernelCtl& ctl,
-                        cudaStream_t stream);
+                        cudaStream_t stream, const CUtensorMap* keep = nullptr);
 
 // The same on CTA pairs with tcgen05.mma.cta_group::2 (gemm_pair.cu).  tmO:
 // the output [M][N] bf16 in boxes of 32 x 32 with the 64-byte swizzle (the
@@ -343,9 +345,10 @@ int lib_device(const DeviceInfo** info, unsigned** err);
 bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz);
-// The products of a gated block that is trained on the swapped kernel (EpiParams:
-// out2): h, g, u = act(g) u, x Wg^T, x Wu^T for M <= kSwapDualMaxM; dg, du from dout Wd
-// for M <= 128.  Arguments as checked by the caller.
+// The products of a gated block that is trained, with the endings of EpiParams' out2
+// and out3: h, g, u = act(g) u, x Wg^T, x Wu^T on the swapped kernel for M <=
+// kSwapDualMaxM, else the persistent one; dg, du from dout Wd on the swapped kernel for
+// M <= kSwapGradMaxM.  Arguments as checked by the caller.
 int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,
                  int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream);
 int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void* u, void* dg,

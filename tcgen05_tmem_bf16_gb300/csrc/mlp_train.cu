@@ -681,18 +681,22 @@ MbDiv div_by(int d) {  // exact for 31-bit numbers: the reciprocal is rounded up
   return r;
 }
 
-// About how many cycles a unit keeps its pair, by its K blocks and its ending.  A
-// lone row tile's MMAs take 150 cycles each and its ending overlaps the next unit's;
-// two row tiles' share the tensor pipe at 128, and the next unit waits for the first
-// one's ending, of kMbGluGrad for both.  Beside that ending's own traffic a lone row
-// tile's operands, 64 KB per K block, take longer from L2, and weights that only one
-// row tile reads (`once`) come from memory.
-int64_t unit_cycles(int mode, int64_t kb, int streams, bool once) {
-  if (mode == kMbGluGrad)
-    return streams == 1 ? std::max<int64_t>(800 * kb, 14000) + 300 : 1024 * kb + 17000;
-  const int64_t end = mode == kMbGlu ? 4000 : 2600;
-  return streams == 1 ? std::max<int64_t>((once ? 750 : 600) * kb, end) + 300
-                      : std::max<int64_t>(1024 * kb, 2 * end) + end;
+// About how many cycles a unit keeps its pair, by its K blocks and its ending: from
+// measured totals over rounds of units (h of 257 to 1024 rows x 2048 x 5632 and x 4096 x
+// 14336, dh of 4096 x 4096 x 14336 and 2048 x 2048 x 8192, weights' gradients of 512 x
+// 4096 x 14336 and 1021 x 1000 x 2728).  A lone row tile's MMAs take 150 cycles each,
+// its 64 KB of operands per K block come from L2 at about the same pace, and its ending
+// overlaps the next unit's; two row tiles' MMAs share the tensor pipe at 128 cycles, and
+// the next unit waits for the first one's ending, of kMbGluGrad for both.
+int64_t unit_cycles(int mode, int64_t kb, int streams) {
+  switch (mode) {
+    case kMbGluGrad:
+      return streams == 1 ? std::max<int64_t>(800 * kb, 14000) + 300 : 1024 * kb + 20000;
+    case kMbGlu: return streams == 1 ? 640 * kb + 4000 : 1120 * kb + 6500;
+    default:
+      return streams == 1 ? std::max<int64_t>(760 * kb, 2600) + 300
+                          : std::max<int64_t>(1060 * kb, 5200) + 2600;
+  }
 }
 
 }  // namespace
@@ -712,8 +716,7 @@ int64_t plan_mlp_launch(MbLaunch* l, int streams, int npairs) {
     j.last = div_by(m_units % kMbGroup);
     j.tiles = div_by(m_units * n_tiles);
     j.parts = div_by(j.splits);
-    cycles[i] = unit_cycles(j.mode, (j.num_kb + j.splits - 1) / j.splits, streams,
-                            m_units == 1);
+    cycles[i] = unit_cycles(j.mode, (j.num_kb + j.splits - 1) / j.splits, streams);
     if (i > 0) work += j.units * cycles[i];
   }
   const int longs = l->job[0].units;
