@@ -38,7 +38,8 @@ namespace {
 constexpr int kSwThreads = 192;  // producer, MMA issuer, four warps of the ending
 constexpr int kSwWBytes = 128 * kBK * 2;
 
-template <int MPAD>
+// LISTS: the backward pass over lists, which puts the entries in shared memory.
+template <int MPAD, bool LISTS = false>
 struct SwCfg {
   static constexpr int kXBytes = MPAD * kBK * 2;
   static constexpr int kStageBytes = kSwWBytes + kXBytes;
@@ -53,7 +54,10 @@ struct SwCfg {
   }
   static constexpr int kBarBytes = 256;
   static constexpr int kRowBytes = 3 * MPAD * 4;            // lse2, dl, targets
-  static constexpr int kTurnBytes = 4 * 32 * 17 * 4;        // transposition, per warp
+  // per warp: 32 x 17 values to be transposed, or LISTS: a mask of columns per row and
+  // the shares that it stands for
+  static constexpr int kTurnWords = LISTS ? 832 : 32 * 17;
+  static constexpr int kTurnBytes = 4 * kTurnWords * 4;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kRowBytes + kTurnBytes;
   static_assert(2 * (kSmem + 1024) <= 227 * 1024, "two CTAs per SM");
   static_assert(kStageBytes % 1024 == 0, "stages stay 1024-byte aligned");
@@ -69,7 +73,7 @@ __device__ __forceinline__ float sw_pow2(float x) {
 template <int MPAD, bool GRAD, bool PICK>
 __global__ void __launch_bounds__(kSwThreads, 2)
     ce_swap_kernel(const __grid_constant__ CeSwap a, const CeEnd e, const KernelCtl kctl) {
-  using Cfg = SwCfg<MPAD>;
+  using Cfg = SwCfg<MPAD, PICK && GRAD>;
   constexpr int kStages = Cfg::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align1024(smem_raw);
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       if (blockIdx.x == 0 && threadIdx.x == 64) *a.ticket = 0u;
     }
     const int q = warp & 3;  // the quarter of tensor memory that this warp reads
-    float* my_turn = turn + q * 32 * 17;
+    float* my_turn = turn + q * Cfg::kTurnWords;
     const int chunks = (count + 15) / 16;  // of 16 rows
     // sums of the segments before: [row][column], this thread's column
     float* part = e.chain + static_cast<int64_t>(blockIdx.x) * MPAD * 128 + q * 32 + lane;
@@ -254,6 +258,60 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           }
         }
       }
+      // GRAD: one entry of each of the rows 8 g .. 8 g + 7 per lane, (-1, 0) where there
+      // is none.
+      auto entries = [&](int g, int2 (&x)[8]) {
+        int row_g = 0, at_g = 0, n_g = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (g / 4 == i) {
+            row_g = pick_row[i];
+            at_g = pick_at[i];
+            n_g = pick_n[i];
+          }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int from = 8 * (g & 3) + k;
+          const int64_t row = __shfl_sync(0xFFFFFFFFu, row_g, from);
+          const int at = __shfl_sync(0xFFFFFFFFu, at_g, from);
+          const int n = __shfl_sync(0xFFFFFFFFu, n_g, from);
+          x[k] = make_int2(-1, 0);
+          if (lane < n) x[k] = __ldg(e.pick.list + row * (e.pick.K + 1) + at + lane);
+        }
+      };
+      // The entries go to shared memory while the products are on their way: beside the
+      // stream of W a load from L2 takes microseconds, also a second one of the same
+      // line (64 rows x 32000 x 4096, read in the ending 58 us, staged 49).  Rows from
+      // `staged` on, of a warp with more entries than there is room for, are read there.
+      constexpr int kRoom = Cfg::kTurnWords - MPAD;
+      uint32_t* masks = reinterpret_cast<uint32_t*>(my_turn);
+      float* shares = my_turn + MPAD;
+      int staged = MPAD;
+      if constexpr (PICK && GRAD) {
+        if (seg + seg_kb >= num_kb) {
+          __syncwarp();
+          int at = 0;
+#pragma unroll 1
+          for (int g = 0; g < MPAD / 8; ++g) {
+            int2 x[8];
+            entries(g, x);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t cols = __reduce_or_sync(
+                  0xFFFFFFFFu, x[k].x < 0 ? 0u : 1u << (x[k].x - (a.v0 + t * 128 + q * 32)));
+              const int n = __popc(cols);
+              if (at + n > kRoom) staged = min(staged, 8 * g + k);
+              if (8 * g + k < staged) {
+                if (lane == 0) masks[8 * g + k] = cols;
+                if (lane < n) shares[at + lane] = __int_as_float(x[k].y);
+                at += n;
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      int taken = 0;  // shares of the rows before
       if (seg > 0) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) before[k] = __ldcg(part + k * 128);
@@ -318,32 +376,32 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             }
           }
           if constexpr (PICK) {
-            // A row's entries here are at most 32, their columns differ and ascend: a lane
-            // reads one entry of each row, and finds its own column's by counting the
-            // columns below it.  (Entry after entry by all lanes: 64 rows x 32000 x 4096
-            // 81 us, since half of the entries are in the first tile, so 49.)
-            const unsigned some =
-                __ballot_sync(0xFFFFFFFFu, n_c > 0) >> (16 * (c & 1)) & 0xFFFFu;
-            if (some) {
-              int2 x[16];
+            // A row's entries here are at most 32, and their columns differ and ascend: a
+            // lane finds its own column's by counting the columns below it.
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const int from = 16 * (c & 1) + k;
-                const int64_t row = __shfl_sync(0xFFFFFFFFu, row_c, from);
-                const int at = __shfl_sync(0xFFFFFFFFu, at_c, from);
-                const int n = __shfl_sync(0xFFFFFFFFu, n_c, from);
-                x[k] = make_int2(-1, 0);
-                if (lane < n) x[k] = e.pick.list[row * (e.pick.K + 1) + at + lane];
-              }
+            for (int h = 0; h < 2; ++h) {
+              const unsigned some = __ballot_sync(0xFFFFFFFFu, n_c > 0) >> (16 * (c & 1) + 8 * h);
+              if (!(some & 0xFFu)) continue;
+              int2 x[8];
+              if (c * 16 + 8 * h + 8 > staged) entries(2 * c + h, x);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                if (!((some >> k) & 1u)) continue;
-                const unsigned bit =
-                    x[k].x < 0 ? 0u : 1u << (x[k].x - (a.v0 + t * 128 + q * 32));
-                const unsigned cols = __reduce_or_sync(0xFFFFFFFFu, bit);
-                const int share =
-                    __shfl_sync(0xFFFFFFFFu, x[k].y, __popc(cols & ((1u << lane) - 1u)));
-                if ((cols >> lane) & 1u) f[k] -= __int_as_float(share);
+              for (int k = 0; k < 8; ++k) {
+                const int m = c * 16 + 8 * h + k;
+                uint32_t cols;
+                float share;
+                if (m < staged) {
+                  cols = masks[m];
+                  const int i = taken + __popc(cols & ((1u << lane) - 1u));
+                  share = (cols >> lane) & 1u ? shares[i] : 0.0f;
+                  taken += __popc(cols);
+                } else {
+                  cols = __reduce_or_sync(
+                      0xFFFFFFFFu, x[k].x < 0 ? 0u : 1u << (x[k].x - (a.v0 + t * 128 + q * 32)));
+                  share = __int_as_float(__shfl_sync(0xFFFFFFFFu, x[k].y,
+                                                     __popc(cols & ((1u << lane) - 1u))));
+                  if (!((cols >> lane) & 1u)) share = 0.0f;
+                }
+                f[8 * h + k] -= share;
               }
             }
 #pragma unroll
@@ -390,8 +448,14 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             if (lane / 16 == (c & 1)) {
               const int2* list = e.pick.list + static_cast<int64_t>(row_c) * (e.pick.K + 1) + at_c;
               float* dots = e.pick.dots + static_cast<int64_t>(row_c) * e.pick.K + at_c;
-              for (int i = 0; i < n_c; ++i)
-                dots[i] = my_turn[(list[i].x - base) * 17 + (lane & 15)];
+              for (int i0 = 0; i0 < n_c; i0 += 8) {  // eight loads in flight
+                int col8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) col8[i] = i0 + i < n_c ? __ldg(&list[i0 + i].x) : base;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (i0 + i < n_c) dots[i0 + i] = my_turn[(col8[i] - base) * 17 + (lane & 15)];
+              }
             }
           }
           if (lane < 16 && m < count) {
@@ -430,7 +494,7 @@ cudaError_t run_swap(const CeSwap& a, const CeEnd& end, const KernelCtl& ctl, in
                      cudaStream_t stream) {
   static std::atomic<uint64_t> mask{0};
   auto kernel = ce_swap_kernel<MPAD, GRAD, PICK>;
-  constexpr int smem = SwCfg<MPAD>::kSmem;
+  constexpr int smem = SwCfg<MPAD, PICK && GRAD>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -47,7 +47,6 @@ constexpr int kMbGroup = 8;              // raster group (units of rows)
 // GRAD: kMbGluGrad alone, with several pairs of buffers per two warps of the ending for
 // g and u, which become dg and du.
 constexpr int kGradBytes = 32 * 128;  // 32 rows x 64 columns
-constexpr int64_t kGradKeep = int64_t(12) << 20;  // elements of dg and of du: 48 MB of the 129 MB of L2
 template <int STREAMS, bool GRAD>
 struct MbCfg {
   static constexpr int kStageBytes = STREAMS * kMbABytes + kMbBBytes;
@@ -512,10 +511,7 @@ __global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if constexpr (GRAD) {
-          // dg and du are the next launch's operands, but they do not push this one's out
-          // of L2 (4096 x 4096 x 14336, 234 MB: 331 us with evict_last, so 290)
-          const uint64_t pol = static_cast<int64_t>(j.rows) * j.cols <= kGradKeep
-                                   ? policy_evict_last() : policy_evict_first();
+          const uint64_t pol = policy_evict_last();  // the next launch's operands
           // the slot that the present chunk's predecessor leaves, once its stores have
           // read it
           auto ask = [&]() {
