@@ -407,7 +407,8 @@ GBF_API gbf_status_t gbf_linear_ce_grad(const void *x, const void *w, const void
  *   gbf_linear_distill_workspace_size(M, V, D, K, 0) bytes.
  * gbf_linear_distill_grad -- its gradients, from the lse that gbf_linear_distill wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - q[m][v])
- *     dx = f * G w,   dw = f * G^T x,   f, dloss, dx, dw as gbf_linear_ce_grad.
+ *     dx = f * G w,   dw = f * G^T x,   f, dloss, dx, dw and roundings as
+ *     gbf_linear_ce_grad, but up to 16 rows G is the sum of two bf16.
  *   The same bits on every run.  Workspace:
  *   gbf_linear_distill_workspace_size(M, V, D, K, 1) bytes.
  */

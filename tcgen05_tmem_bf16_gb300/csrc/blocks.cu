@@ -154,10 +154,10 @@ bool map_parts(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
 
 // The gradient of a weight: out [rows][cols] = a^T b over the M rows of a and b.
 bool set_dw(MbJob* j, const void* a, const void* b, const void* out, int64_t rows, int64_t cols,
-            int64_t M, int streams) {
+            int64_t M) {
   set_job(j, kMbStore, rows, cols, M, true, true);
   return map_mn(&j->a[0], a, rows, M) && map_mn(&j->b[0], b, cols, M) &&
-         map_out(&j->o[0], out, cols, rows, streams == 1);
+         map_out(&j->o[0], out, cols, rows, false);
 }
 
 gbf_status_t run_launch(MbLaunch* l, int streams, const DeviceInfo& dev, unsigned* err,
@@ -285,12 +285,12 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
     if (!map_k(&j.a[0], ws.dg, F, M) || !map_k(&j.a[1], ws.du, F, M) ||
         !map_mn(&j.b[0], w_gate, D, F) || !map_mn(&j.b[1], w_up, D, F) ||
         !(splits > 1 ? map_parts(&j.o[0], ws.parts, D, splits * mlp_m_pad(M))
-                     : map_out(&j.o[0], dx, D, M, streams == 1)))
+                     : map_out(&j.o[0], dx, D, M, false)))
       return GBF_ERR_CUDA;
   }
-  if ((dw_gate && !set_dw(&l.job[1], ws.dg, x, dw_gate, F, D, M, streams)) ||
-      (dw_up && !set_dw(&l.job[2], ws.du, x, dw_up, F, D, M, streams)) ||
-      (dw_down && !set_dw(&l.job[3], dout, h, dw_down, D, F, M, streams)))
+  if ((dw_gate && !set_dw(&l.job[1], ws.dg, x, dw_gate, F, D, M)) ||
+      (dw_up && !set_dw(&l.job[2], ws.du, x, dw_up, F, D, M)) ||
+      (dw_down && !set_dw(&l.job[3], dout, h, dw_down, D, F, M)))
     return GBF_ERR_CUDA;
   if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
   if (!dx || splits == 1) return GBF_OK;

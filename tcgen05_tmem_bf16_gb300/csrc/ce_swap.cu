@@ -409,7 +409,9 @@ __global__ void __launch_bounds__(kSwThreads, 2)
               if (c * 16 + k < count) f[k] *= row_dl[c * 16 + k];
           }
           if (col < a.cols) {
-            __nv_bfloat16* dst = a.gt + static_cast<int64_t>(col) * MPAD + c * 16;
+            constexpr bool kTwice = PICK && MPAD <= kCeTwiceRows;
+            __nv_bfloat16* dst =
+                a.gt + static_cast<int64_t>(col) * (kTwice ? 2 * MPAD : MPAD) + c * 16;
             float lo[8], hi[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -418,6 +420,15 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             }
             st_u4(dst, pack8(lo));
             st_u4(dst + 8, pack8(hi));
+            if constexpr (kTwice) {  // what the first rounding left
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                lo[k] -= __bfloat162float(__float2bfloat16_rn(lo[k]));
+                hi[k] -= __bfloat162float(__float2bfloat16_rn(hi[k]));
+              }
+              st_u4(dst + MPAD, pack8(lo));
+              st_u4(dst + MPAD + 8, pack8(hi));
+            }
           }
         } else if (c < chunks) {
 #pragma unroll

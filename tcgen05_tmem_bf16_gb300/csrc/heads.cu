@@ -135,7 +135,8 @@ size_t ce_chain_floats(int64_t M, int64_t D) {
   return size_t(2) * kMaxSms * ce_swap_rows(M) * 128;
 }
 
-size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs* w) {
+size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs* w,
+                   bool twice = false) {
   Sections s{static_cast<uint8_t*>(base)};
   *w = CeWs{};
   w->count = s.take<int>(1);
@@ -154,7 +155,7 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
     w->lse2 = s.take<float>(M);
     w->dl = s.take<float>(M);
     // G of two pieces: one is written while the other's products run
-    const size_t g = M <= kCeSwapMax ? static_cast<size_t>(ce_swap_rows(M)) * cols
+    const size_t g = M <= kCeSwapMax ? static_cast<size_t>(ce_swap_rows(M)) * cols * (twice ? 2 : 1)
                                      : static_cast<size_t>(M) * (ceil_div64(cols, 8) * 8);
     w->g[0] = s.take<__nv_bfloat16>(g);
     w->g[1] = cols < V ? s.take<__nv_bfloat16>(g) : w->g[0];
@@ -348,7 +349,9 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   const int64_t piece = ce_piece(M, V);
   const bool few = M <= kCeSwapMax;  // G transposed, by the swapped roles
   const bool chains = !few && ce_chained(D);
-  const int64_t ld = few ? ce_swap_rows(M) : ceil_div64(piece, 8) * 8;
+  const bool twice = pick.list && M <= kCeTwiceRows;
+  const int64_t rows = ce_swap_rows(M);
+  const int64_t ld = few ? (twice ? 2 : 1) * rows : ceil_div64(piece, 8) * 8;
   const int64_t m_pad = ceil_div64(M, 512) * 512;
   const int splits = ce_splits(M, D, piece);
   CeEnd end{};
@@ -369,6 +372,7 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   for (int64_t n = 0; n <= pieces; ++n) {
     CeLaunch launch{}, logits{};
     launch.d = logits.d = p.D;
+    launch.twice = twice;
     for (CeJob& j : launch.job) j.bn = 256;
     for (CeJob& j : logits.job) j.bn = 256;
     if (n < pieces && few) {
@@ -416,7 +420,8 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
         job.v0 = static_cast<int>(v0);
         job.splits = 1;
         job.gt = few;
-        if (!(few ? ce_map_k(&job.a[0], g, ld, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
+        if (!(few ? ce_map_k(&job.a[0], g, rows, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
+            (twice && !ce_map_k(&job.a[1], g + rows, rows, cols, ld)) ||
             !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
             !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, ce_streams(M) == 1))
           return GBF_ERR_CUDA;
@@ -436,6 +441,7 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   out.m_pad = end.m_pad;
   out.splits = splits;
   out.D = p.D;
+  out.twice = twice;
   return cuda_status(launch_ce_dx(out, p.M, dev->sms, s));
 }
 
@@ -454,7 +460,7 @@ int64_t pick_stride(int64_t M, int64_t V) { return (V >> pick_shift(M)) + 2; }
 
 size_t distill_sections(void* base, int64_t M, int64_t V, int64_t D, int64_t K, bool grad,
                         DistillWs* w) {
-  const size_t at = ce_sections(base, M, V, D, grad, &w->ce);
+  const size_t at = ce_sections(base, M, V, D, grad, &w->ce, M <= kCeTwiceRows);
   Sections s{static_cast<uint8_t*>(base), at};
   w->list = s.take<int2>(static_cast<size_t>(M) * (K + 1));
   w->at = s.take<uint16_t>(static_cast<size_t>(M) * pick_stride(M, V));

@@ -180,6 +180,7 @@ constexpr int kCeJobs = 3;
 struct CeLaunch {
   CeJob job[kCeJobs];
   int d;  // hidden width
+  int twice;  // G^T of up to kCeTwiceRows rows as two bf16 each: kCeDw's a[1] the second ones
 };
 // Distillation: a row's softmax target is a list of columns with their shares
 // (distill.cu), instead of one column.
@@ -212,6 +213,10 @@ __device__ __forceinline__ int64_t ce_target(const void* targets, int ids64, int
                : static_cast<int64_t>(static_cast<const int*>(targets)[i]);
 }
 #endif
+// Up to this many rows of a distillation G is kept as the sum of two bf16: a few of its
+// values then make up the gradients, and one rounding of theirs would be all of the
+// gradients' error.
+constexpr int kCeTwiceRows = 16;
 // The logits for up to kCeSwapMax rows, with swapped roles (ce_swap.cu).
 constexpr int kCeSwapMax = 128;
 // K blocks whose products the tensor cores add up in one chain for a logit.  Each
@@ -223,7 +228,7 @@ int ce_swap_segments(int64_t M, int k_blocks);  // parts of K between which the 
 int ce_swap_rows(int64_t M);  // rows padded to: 16, 64, 128; 0 above kCeSwapMax
 struct CeSwap {
   CUtensorMap w, x[2];  // x[1]: x itself, for when every row is scored (and forward)
-  __nv_bfloat16* gt;    // gradient: [cols][padded rows]
+  __nv_bfloat16* gt;    // gradient: [cols][padded rows], twice those (kCeTwiceRows)
   // forward: all rows as they are, scored or not (they fill the padding anyway)
   const void* targets;
   int ids64;
@@ -266,6 +271,7 @@ struct CeDxOut {
   __nv_bfloat16* dx;
   float scale;
   int mean, m_pad, splits, D;
+  int twice;  // the sums of G's second parts are kCeTwiceRows rows behind
 };
 // chains: one product, the logits, in units of one row tile (streams 1).
 cudaError_t launch_ce_gemm(const CeLaunch& launch, const CeEnd& end, int streams, bool chains,

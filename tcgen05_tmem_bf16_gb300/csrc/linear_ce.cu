@@ -126,7 +126,7 @@ __device__ __forceinline__ CeWork ce_work(const CeLaunch& a, int count, int stre
     const int k = j.mode == kCeDw ? count : (j.mode == kCeDx ? j.cols : a.d);
     w.m_units[i] = (rows + kCeTile * streams - 1) / (kCeTile * streams);
     w.n_tiles[i] = (n + j.bn - 1) / j.bn;
-    w.num_kb[i] = (k + kBK - 1) / kBK;
+    w.num_kb[i] = (k + kBK - 1) / kBK << (a.twice && j.mode == kCeDw ? 1 : 0);
     w.units[i] = w.m_units[i] * w.n_tiles[i] * j.splits;
     if (i > 0) blocks += static_cast<int64_t>(w.units[i]) * (w.num_kb[i] + kCeUnitCost);
   }
@@ -470,23 +470,27 @@ __global__ void __launch_bounds__(kCeThreads, 1)
           uint8_t* sa = stages + s * Cfg::kStageBytes;
           uint8_t* sb = sa + STREAMS * kCeABytes;
           const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+          // G's second parts meet the same rows of x as the first
+          const bool again = a.twice && j.mode == kCeDw && kb >= u.kb1 / 2;
+          const int k_at = (again ? kb - u.kb1 / 2 : kb) * kBK;
+          if (again) ma = &j.a[1];
           if (leader) mbar_arrive_expect_tx(&full[s], 2 * load_bytes);
 #pragma unroll
           for (int i = 0; i < STREAMS; ++i) {
             const int m0 = (STREAMS * u.mp + i) * kCeTile + static_cast<int>(rank) * kBM;
             if (a_mn) {
-              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, m0, kb * kBK);
-              tma_load_2d_pair(sa + i * kCeABytes + 8192, ma, bar, m0 + 64, kb * kBK);
+              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, m0, k_at);
+              tma_load_2d_pair(sa + i * kCeABytes + 8192, ma, bar, m0 + 64, k_at);
             } else {
-              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, kb * kBK, m0);
+              tma_load_2d_pair(sa + i * kCeABytes, ma, bar, k_at, m0);
             }
           }
           if (b_mn) {
-            const int k0 = (j.mode == kCeDx ? j.v0 : 0) + kb * kBK;
+            const int k0 = (j.mode == kCeDx ? j.v0 : 0) + k_at;
             tma_load_2d_pair(sb, mb, bar, n0, k0);
             tma_load_2d_pair(sb + 8192, mb, bar, n0 + 64, k0);
           } else {
-            tma_load_2d_pair(sb, mb, bar, kb * kBK, j.v0 + n0);
+            tma_load_2d_pair(sb, mb, bar, k_at, j.v0 + n0);
           }
           fills[s]++;
           if (++s == kStages) {
@@ -1014,13 +1018,14 @@ __global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
     const int col = static_cast<int>(t - row * segs) * 256 + (threadIdx.x & 31) * 8;
     if (col >= p.D) continue;
     float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < p.splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(
-          p.acc + (static_cast<int64_t>(s) * p.m_pad + row) * p.D + col);
-      const float4 x = __ldcs(src), y = __ldcs(src + 1);
-      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-    }
+    for (int s = 0; s < p.splits; ++s)
+      for (int part = 0; part <= p.twice; ++part) {
+        const float4* src = reinterpret_cast<const float4*>(
+            p.acc + (static_cast<int64_t>(s) * p.m_pad + row + part * kCeTwiceRows) * p.D + col);
+        const float4 x = __ldcs(src), y = __ldcs(src + 1);
+        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+      }
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= scale;
     st_u4(p.dx + static_cast<int64_t>(p.rows[row]) * p.D + col, pack8(f));

@@ -34,16 +34,16 @@ namespace gbf {
 
 namespace {
 
+constexpr int kMbThreads = 384;          // warps 0-3 roles, 4-11 ending
 constexpr int kMbTile = 256;             // rows and columns of a pair's tile
 constexpr int kMbABytes = kBM * kBK * 2;  // 16 KB: this CTA's 128 rows of A
 constexpr int kMbBBytes = 128 * kBK * 2;  // 16 KB: this CTA's half of B
 constexpr int kMbGroup = 8;              // raster group (units of rows)
 
 // STREAMS row tiles per unit of work, as in linear_ce.cu: two that share each B
-// tile, or a lone one.  Warps 0-3 have roles, the others the ending.  With few rows a
-// unit of a weight's gradient is one K block, and its ending all that counts: sixteen
-// warps with 64 columns each, stored as rows of 128 bytes (the three gradients of 16 x
-// 4096 x 14336, 352 MB: eight warps 73 us).
+// tile, or a lone one.  (Sixteen warps for a lone one's ending, and rows of 128 bytes for
+// its stores, change nothing: the three weights' gradients of 16 x 4096 x 14336, 352 MB,
+// are 53 us either way, 6.6 TB/s.)
 // GRAD: kMbGluGrad alone, with several pairs of buffers per two warps of the ending for
 // g and u, which become dg and du.
 constexpr int kGradBytes = 32 * 128;  // 32 rows x 64 columns
@@ -53,11 +53,8 @@ struct MbCfg {
   static constexpr int kStages = STREAMS == 2 ? (GRAD ? 3 : 4) : GRAD ? 4 : 5;
   static constexpr int kSlots = STREAMS == 2 ? 2 : 3;
   static constexpr int kBarBytes = 1024;
-  static constexpr int kEndWarps = STREAMS == 1 && !GRAD ? 16 : 8;
-  static constexpr int kThreads = 128 + 32 * kEndWarps;
-  static constexpr int kCols = 4 * 256 / kEndWarps;  // of a tile, per warp of the ending
   static constexpr int kWarpBytes = GRAD ? kSlots * kGradBytes : 2 * kStageChunkBytes;
-  static constexpr int kStagingBytes = kEndWarps * kWarpBytes;
+  static constexpr int kStagingBytes = 8 * kWarpBytes;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + kBarBytes + kStagingBytes;
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -227,19 +224,15 @@ __device__ __forceinline__ void glu_grad_chunk(uint32_t tb, uint8_t* buf, int ha
   }
 }
 
-// A warp's columns of a product, to the fp32 rows of its part of K.
-template <int COLS>
+// A warp's 128 columns of a product, to the fp32 rows of its part of K.
 __device__ __forceinline__ void store_part(uint32_t tb, const AccFree& release, const MbJob& j,
                                            uint8_t* bufs, int& flip, int row0, int col0, int part) {
-  // another product's store may still read both buffers
-  if ((threadIdx.x & 31) == 0) bulk_wait_read<0>();
-  __syncwarp();
 #pragma unroll 1
-  for (int c = 0; c < COLS / 32; ++c) {
+  for (int c = 0; c < 4; ++c) {
     uint32_t v[32];
     tmem_ld32(tb + 32 * c, v);
     tmem_wait_ld();
-    if (c == COLS / 32 - 1) release();
+    if (c == 3) release();
     put_chunk_f32(bufs, kStageChunkBytes, flip, v, &j.o[0], part * j.m_pad + row0, col0 + 32 * c,
                   j.cols, row0 < j.rows, false);
   }
@@ -253,7 +246,7 @@ __device__ __forceinline__ void pack32(const uint32_t (&v)[32], uint32_t (&w)[16
 
 // A warp's 128 columns to bf16, 32 at a time: the next are on their way from tensor
 // memory meanwhile.
-__device__ __forceinline__ void store_tile128(uint32_t tb, const AccFree& release, const MbJob& j,
+__device__ __forceinline__ void store_tile(uint32_t tb, const AccFree& release, const MbJob& j,
                                               uint8_t* bufs, int& flip, int row0, int col0,
                                               uint64_t pol) {
   auto put = [&](int c, const uint32_t (&v)[32]) {
@@ -278,37 +271,8 @@ __device__ __forceinline__ void store_tile128(uint32_t tb, const AccFree& releas
   put(3, vb);
 }
 
-// A warp's 64 columns to bf16 as rows of 128 bytes; `buf` holds them all.
-__device__ __forceinline__ void store_tile64(uint32_t tb, const AccFree& release, const MbJob& j,
-                                             uint8_t* buf, int row0, int col0, uint64_t pol) {
-  const int lane = static_cast<int>(threadIdx.x & 31);
-  uint32_t v[32], w[16], w2[16];
-  tmem_ld32(tb, v);
-  tmem_wait_ld();
-  pack32(v, w);
-  tmem_ld32(tb + 32, v);
-  tmem_wait_ld();
-  release();
-  pack32(v, w2);
-  if (lane == 0) bulk_wait_read<0>();
-  __syncwarp();
-#pragma unroll
-  for (uint32_t u = 0; u < 8; ++u) {
-    const uint32_t* x = u < 4 ? w + 4 * u : w2 + 4 * (u - 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(staged_unit(buf, u)), "r"(x[0]),
-                 "r"(x[1]), "r"(x[2]), "r"(x[3])
-                 : "memory");
-  }
-  fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    if (row0 < j.rows && col0 < j.cols) tma_store_2d(&j.o[0], buf, col0, row0, pol);
-    bulk_commit();
-  }
-}
-
 template <int STREAMS, bool GRAD>
-__global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
+__global__ void __launch_bounds__(kMbThreads, 1)
     mlp_train_kernel(const __grid_constant__ MbLaunch a, const KernelCtl kctl) {
   using Cfg = MbCfg<STREAMS, GRAD>;
   constexpr int kStages = Cfg::kStages;
@@ -340,7 +304,7 @@ __global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], 2 * Cfg::kEndWarps);  // of each CTA of the pair
+      mbar_init(&tempty[i], 16);  // 8 warps in each CTA of the pair
     }
     mbar_init(done, STREAMS);
     for (int i = 0; i < 4 * Cfg::kSlots; ++i) {
@@ -555,15 +519,14 @@ __global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
           }
           if (!ok) break;
         } else if (j.mode == kMbGlu) {
-          constexpr int kOut = Cfg::kCols / 2;  // of h, g and u each
 #pragma unroll 1
-          for (int c = 0; c < kOut / 32; ++c) {
+          for (int c = 0; c < 2; ++c) {  // 64 columns of h, g and u each
             uint32_t g[32], up[32], w[16];
-            tmem_ld32(tb + slice * kOut + c * 32, g);
-            tmem_ld32(tb + 128 + slice * kOut + c * 32, up);
+            tmem_ld32(tb + slice * 64 + c * 32, g);
+            tmem_ld32(tb + 128 + slice * 64 + c * 32, up);
             tmem_wait_ld();
-            if (c == kOut / 32 - 1) release();
-            const int col = u.nb * 128 + slice * kOut + c * 32;
+            if (c == 1) release();
+            const int col = u.nb * 128 + slice * 64 + c * 32;
             auto put = [&](int o) {
               put_chunk<false>(bufs, kStageChunkBytes, flip, 0, w, &j.o[o], row0, col, j.rows,
                                j.cols, first);
@@ -581,14 +544,12 @@ __global__ void __launch_bounds__(MbCfg<STREAMS, GRAD>::kThreads, 1)
             put(2);
           }
         } else {
-          const int col0 = u.nb * kMbTile + slice * Cfg::kCols;
-          const uint32_t t = tb + slice * Cfg::kCols;
+          const int col0 = u.nb * kMbTile + slice * 128;
+          const uint32_t t = tb + slice * 128;
           if (j.splits > 1)
-            store_part<Cfg::kCols>(t, release, j, bufs, flip, row0, col0, u.split);
-          else if constexpr (Cfg::kCols == 64)
-            store_tile64(t, release, j, bufs, row0, col0, first);
+            store_part(t, release, j, bufs, flip, row0, col0, u.split);
           else
-            store_tile128(t, release, j, bufs, flip, row0, col0, first);
+            store_tile(t, release, j, bufs, flip, row0, col0, first);
         }
       }
     }
@@ -648,7 +609,7 @@ cudaError_t run_mb(const MbLaunch& launch, const KernelCtl& ctl, int grid, cudaS
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(MbCfg<STREAMS, GRAD>::kThreads, 1, 1);
+  cfg.blockDim = dim3(kMbThreads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];

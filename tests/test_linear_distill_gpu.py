@@ -133,6 +133,25 @@ def test_against_fp64(cuda_lib, M, V, D, K):
     check(cuda_lib, *inputs(M, V, D, K, seed=M + V, unscored=0.25 if M > 8 else 0.0))
 
 
+@pytest.mark.parametrize("M,V,D,K", [(1, 700, 136, 2), (1, 5001, 1032, 40), (7, 300, 64, 3), (16, 33000, 264, 20)])
+def test_few_rows_are_rounded_once(cuda_lib, M, V, D, K):
+    """Up to 16 rows G is the sum of two bf16, off by R^2 of itself: the gradients are off
+    by their own rounding and what the logits are off by."""
+    args = inputs(M, V, D, K, seed=M + V)
+    lse = forward(cuda_lib, *args)[1]
+    got = backward(cuda_lib, *args, lse, reduction="sum")
+    scored, x64, l, q, _, _ = plain(*args, 1.0, 1.0)
+    w64 = args[1].double()
+    p = (l - lse.double()[:, None]).exp()
+    G = torch.where(scored[:, None], p - q, 0.0)
+    eg = p * (2 * near(x64, args[1], 1.0)[:, None] + 2.0 ** -21) + 2.0 ** -21 * q + R * R * G.abs()
+    for name, grad, a, b, ea in (("dx", got[0], G, w64, eg), ("dw", got[1], G.T, x64, eg.T)):
+        want = a @ b
+        bound = ea @ b.abs() + (8e-9 * a.shape[1] + 2.0 ** -22) * (a.abs() @ b.abs())
+        err = (grad.double() - want).abs()
+        assert bool((err <= R * (want.abs() + bound) + bound + 1e-37).all()), name
+
+
 @pytest.mark.parametrize("M", [5, 100, 300])
 @pytest.mark.parametrize("index", [torch.int64, torch.int32])
 @pytest.mark.parametrize("teacher", [torch.float32, torch.bfloat16])
