@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   if (warp == 0) {
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");  // the gathered rows: plain stores
+      const uint64_t stream = policy_evict_first();
       const CUtensorMap* mx = &a.x[!GRAD || count == e.M ? 1 : 0];
       uint32_t fills[kStages];
 #pragma unroll
@@ -164,7 +165,13 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           }
           uint8_t* sw = stages + s * Cfg::kStageBytes;
           mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          tma_load_2d(sw, &a.w, &full[s], kb * kBK, a.v0 + t * 128);
+          // W streams past the other operands in L2, but for the last eighth of each of its
+          // rows, which the next pass may still find (64 rows x 32000 x 4096 trained
+          // 214 us, without the hint 222, all of W 216; 128 rows scored 65, 69.5, 62.5).
+          if (i < num_kb - num_kb / 8)
+            tma_load_2d_hint(sw, &a.w, &full[s], kb * kBK, a.v0 + t * 128, stream);
+          else
+            tma_load_2d(sw, &a.w, &full[s], kb * kBK, a.v0 + t * 128);
           tma_load_2d(sw + kSwWBytes, mx, &full[s], kb * kBK, 0);
           fills[s]++;
           if (++s == kStages) {
