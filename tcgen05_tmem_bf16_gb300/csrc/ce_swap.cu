@@ -148,9 +148,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       asm volatile("fence.proxy.async;" ::: "memory");  // the gathered rows: plain stores
       const uint64_t stream = policy_evict_first();
       const CUtensorMap* mx = &a.x[!GRAD || count == e.M ? 1 : 0];
-      uint32_t fills[kStages];
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) fills[i] = 0;
+      int fills = 0;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -173,7 +171,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           else
             tma_load_2d(sw, &a.w, &full[s], kb * kBK, a.v0 + t * 128);
           tma_load_2d(sw + kSwWBytes, mx, &full[s], kb * kBK, 0);
-          fills[s]++;
+          ++fills;
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
@@ -182,8 +180,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
         }
       }
       if (ok) {
-        for (int i = 0; i < kStages; ++i)
-          if (fills[i]) wait_bar(&empty[i], (fills[i] - 1) & 1, ctl, kSiteDrain, false);
+        for (int i = 0; i < kStages && i < fills; ++i)  // stage i's last fill
+          wait_bar(&empty[i], (fills - 1 - i) / kStages & 1, ctl, kSiteDrain, false);
       } else {
         const uint64_t t0 = globaltimer_ns();  // let the copies in flight land (bounded)
         while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
@@ -265,17 +263,20 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           }
         }
       }
+      // Those of one i, by masks: a choice of the language's puts the arrays in local memory.
+      auto take = [&](bool it, int i, int& row, int& at, int& n) {
+        const int mask = it ? -1 : 0;
+        row |= pick_row[i] & mask;
+        at |= pick_at[i] & mask;
+        n |= pick_n[i] & mask;
+      };
       // GRAD: one entry of each of the rows 8 g .. 8 g + 7 per lane, (-1, 0) where there
       // is none.
       auto entries = [&](int g, int2 (&x)[8]) {
         int row_g = 0, at_g = 0, n_g = 0;
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
-          if (g / 4 == i) {
-            row_g = pick_row[i];
-            at_g = pick_at[i];
-            n_g = pick_n[i];
-          }
+          take(g / 4 == i, i, row_g, at_g, n_g);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int from = 8 * (g & 3) + k;
@@ -338,11 +339,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
         if constexpr (PICK) {
 #pragma unroll
           for (int i = 0; i < kRows; ++i)
-            if (c / 2 == i) {
-              row_c = pick_row[i];
-              at_c = pick_at[i];
-              n_c = pick_n[i];
-            }
+            take(c / 2 == i, i, row_c, at_c, n_c);
         }
         if (c < chunks) {
           uint32_t r[16];

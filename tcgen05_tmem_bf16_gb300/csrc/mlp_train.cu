@@ -338,9 +338,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");
       const uint64_t stream = policy_evict_first();
-      uint32_t fills[kStages];
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) fills[i] = 0;
+      int fills = 0;
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
           } else {
             tma_load_2d_pair(sb, mb, bar, k0, n0);
           }
-          fills[s]++;
+          ++fills;
           if (++s == kStages) {
             s = 0;
             ph ^= 1;
@@ -397,8 +395,8 @@ __global__ void __launch_bounds__(kMbThreads, 1)
         }
       }
       if (ok) {
-        for (int i = 0; i < kStages; ++i)
-          if (fills[i]) wait_bar(&empty[i], (fills[i] - 1) & 1, ctl, kSiteDrain, false);
+        for (int i = 0; i < kStages && i < fills; ++i)  // stage i's last fill
+          wait_bar(&empty[i], (fills - 1 - i) / kStages & 1, ctl, kSiteDrain, false);
       } else {
         const uint64_t t0 = globaltimer_ns();  // let the copies in flight land (bounded)
         while (globaltimer_ns() - t0 < 2000000ull) __nanosleep(1000);
