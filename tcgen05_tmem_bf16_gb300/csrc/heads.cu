@@ -77,6 +77,16 @@ int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Row tiles per unit of work: two that share a column tile, or a lone one where
 // there is no second.
 int ce_streams(int64_t M) { return M > kCeTileRows ? 2 : 1; }
+// The same for lists, where a lone one is also taken if the rounds of units over the pairs
+// are shorter so (a unit of two takes about 1.7 times as long): 300 rows x 4000 x 1000
+// trained 66 us, two 80.5; 300 x 20000 x 512 86, 104; 1000 x 4000 x 1000 84, 101.
+int ce_streams(int64_t M, int64_t cols, bool lists) {
+  if (!lists || ce_streams(M) == 1) return ce_streams(M);
+  const int64_t v = ceil_div64(cols, 256);
+  const int64_t one = ceil_div64(ceil_div64(M, kCeTileRows) * v, kCePairs);
+  const int64_t two = ceil_div64(ceil_div64(M, 2 * kCeTileRows) * v, kCePairs);
+  return one * 10 < two * 17 ? 1 : 2;
+}
 // Whether the logits' K is taken in several chains (above kCeSwapMax rows): then in
 // units of one row tile, by a launch of their own (linear_ce.cu).
 bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
@@ -219,9 +229,8 @@ bool ce_map_out_f32(CUtensorMap* m, const void* p, int64_t inner, int64_t outer)
 }
 
 // One launch: a CTA pair per unit of work at most, with M rows scored.
-gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M, bool chains,
-                         const DeviceInfo& dev, unsigned* err, cudaStream_t s) {
-  const int streams = chains ? 1 : ce_streams(M);
+gbf_status_t run_ce_gemm(const CeLaunch& launch, const CeEnd& end, int64_t M, int streams,
+                         bool chains, const DeviceInfo& dev, unsigned* err, cudaStream_t s) {
   int64_t units = 0;
   for (const CeJob& j : launch.job) {
     if (j.mode == kCeNone) continue;
@@ -264,7 +273,7 @@ gbf_status_t ce_forward(const CeCall& call, float* loss, float* lse, float* mean
   p.M = static_cast<int>(M);
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);
-  const bool few = M <= kCeSwapMax;
+  const bool few = M <= kCeSwapMax, chains = ce_chained(D);
   CeLaunch launch{};
   for (CeJob& j : launch.job) j.bn = 256;
   CeSwap swap{};
@@ -317,7 +326,8 @@ gbf_status_t ce_forward(const CeCall& call, float* loss, float* lse, float* mean
                                                s))) != GBF_OK)
     return st;
   st = few ? cuda_status(launch_ce_swap(swap, false, end, swap_sms, lib_ctl(err, 2 * swap_sms), s))
-           : run_ce_gemm(launch, end, M, ce_chained(D), *dev, err, s);
+           : run_ce_gemm(launch, end, M, chains ? 1 : ce_streams(M, V, pick.list != nullptr), chains,
+                         *dev, err, s);
   if (st != GBF_OK) return st;
   return cuda_status(launch_ce_join(join, s));
 }
@@ -354,6 +364,7 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   const int64_t ld = few ? (twice ? 2 : 1) * rows : ceil_div64(piece, 8) * 8;
   const int64_t m_pad = ceil_div64(M, 512) * 512;
   const int splits = ce_splits(M, D, piece);
+  const int streams = ce_streams(M, piece, pick.list != nullptr);
   CeEnd end{};
   end.count = ws.count;
   end.tgt = ws.tgt;
@@ -395,7 +406,7 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
       if (!ce_map_k(&job.a[0], ws.xc, D, M, D) || !ce_map_k(&job.a[1], x, D, M, D) ||
           !ce_map_k(&job.b[0], w, D, V, D) || !ce_map_out(&job.o, ws.g[n & 1], cols, M, ld))
         return GBF_ERR_CUDA;
-      if (chains && (st = run_ce_gemm(logits, end, M, true, *dev, err, s)) != GBF_OK) return st;
+      if (chains && (st = run_ce_gemm(logits, end, M, 1, true, *dev, err, s)) != GBF_OK) return st;
     }
     if (n > 0) {
       const int64_t v0 = (n - 1) * piece, cols = std::min(piece, V - v0);
@@ -423,12 +434,12 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
         if (!(few ? ce_map_k(&job.a[0], g, rows, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
             (twice && !ce_map_k(&job.a[1], g + rows, rows, cols, ld)) ||
             !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
-            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, ce_streams(M) == 1))
+            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, streams == 1))
           return GBF_ERR_CUDA;
       }
     }
     if ((few || chains) && n == 0) continue;  // no G yet
-    if ((st = run_ce_gemm(launch, end, M, false, *dev, err, s)) != GBF_OK) return st;
+    if ((st = run_ce_gemm(launch, end, M, streams, false, *dev, err, s)) != GBF_OK) return st;
   }
   if (!dx) return GBF_OK;
   CeDxOut out{};

@@ -863,6 +863,8 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
     if (p.rows) r = p.rows[row];
     else counts = scored(p, row);
   }
+  // for the mean over rows taken as they are
+  const bool mine = p.mean && !p.rows && static_cast<int>(threadIdx.x) < p.M && scored(p, threadIdx.x);
   // PICK: this thread's first entry, on its way meanwhile
   const int64_t at = PICK && row < count ? (p.rows ? p.rows[row] : row) : 0;
   const int2* list = PICK ? p.pick.list + at * (p.pick.K + 1) : nullptr;
@@ -980,11 +982,12 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
 #pragma unroll
       for (int o = kJoinRows / 2; o > 0; o >>= 1) loss += __shfl_xor_sync(0xFFFFFFFFu, loss, o);
       if (lane == 0) {
-        p.sums[blockIdx.x] = loss;
         if (gridDim.x > 1) {
+          p.sums[blockIdx.x] = loss;
           __threadfence();
           last = atomicAdd(p.ticket, 1u) == gridDim.x - 1;
         } else {
+          sums[0] = loss;
           last = true;
         }
       }
@@ -993,18 +996,20 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
   if (!p.mean) return;
   __syncthreads();
   if (!last) return;
-  if (gridDim.x > 1) __threadfence();
   double s = 0.0;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) s += __ldcg(p.sums + i);
+  if (gridDim.x > 1) {
+    __threadfence();
+    for (unsigned i = threadIdx.x; i < gridDim.x; i += kJoinThreads) s += __ldcg(p.sums + i);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (lane == 0) sums[warp] = s;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) sums[warp] = s;
+  }
   int n = count;
-  if (!p.rows) n = __syncthreads_count(static_cast<int>(threadIdx.x) < p.M && scored(p, threadIdx.x));
+  if (!p.rows) n = __syncthreads_count(mine);
   else __syncthreads();
   if (threadIdx.x == 0) {
     s = 0.0;
-    for (int w = 0; w < kJoinWarps; ++w) s += sums[w];
+    for (int w = 0; w < (gridDim.x > 1 ? kJoinWarps : 1); ++w) s += sums[w];
     *p.mean = static_cast<float>(s / max(n, 1));
   }
 }
@@ -1025,18 +1030,16 @@ __global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
     const int64_t row = t / segs;
     const int col = static_cast<int>(t - row * segs) * 256 + (threadIdx.x & 31) * 8;
     if (col >= p.D) continue;
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < p.splits; ++s)
-      for (int part = 0; part <= p.twice; ++part) {
-        const float4* src = reinterpret_cast<const float4*>(
-            p.acc + (static_cast<int64_t>(s) * p.m_pad + row + part * kCeTwiceRows) * p.D + col);
-        const float4 x = __ldcs(src), y = __ldcs(src + 1);
-        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-      }
+    const int out_row = p.rows[row];
+    float f[8];
+    // of each part of K the sums of G's first and, where there are two, second parts
+    add_parts(f, p.splits << p.twice, [&](int i) {
+      const int64_t s = i >> p.twice, part = i & p.twice;
+      return p.acc + (s * p.m_pad + row + part * kCeTwiceRows) * p.D + col;
+    });
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= scale;
-    st_u4(p.dx + static_cast<int64_t>(p.rows[row]) * p.D + col, pack8(f));
+    st_u4(p.dx + static_cast<int64_t>(out_row) * p.D + col, pack8(f));
   }
 }
 

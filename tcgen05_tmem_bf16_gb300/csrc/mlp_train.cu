@@ -592,13 +592,8 @@ __global__ void __launch_bounds__(kSumThreads)
   const int64_t step = static_cast<int64_t>(gridDim.x) * kSumThreads * 8;
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x) * 8; i < n;
        i += step) {
-    float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s) {
-      const float4* src = reinterpret_cast<const float4*>(parts + s * stride + i);
-      const float4 x = __ldcs(src), y = __ldcs(src + 1);
-      f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-      f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-    }
+    float f[8];
+    add_parts(f, splits, [&](int s) { return parts + s * stride + i; });
     st_u4(dx + i, pack8(f));
   }
 }

@@ -80,6 +80,30 @@ __device__ __forceinline__ void put_chunk(uint8_t* bufs, int buf_bytes, int& fli
   }
 }
 
+// Eight columns of a product whose K was taken in n parts: at(i) is part i's address,
+// f the sums in the parts' order.  Loads of four parts are in flight at a time.
+template <typename At>
+__device__ __forceinline__ void add_parts(float (&f)[8], int n, const At& at) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= n) break;
+      const float4* src = reinterpret_cast<const float4*>(at(i0 + i));
+      x[i] = __ldcs(src);
+      y[i] = __ldcs(src + 1);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i0 + i >= n) break;
+      f[0] += x[i].x; f[1] += x[i].y; f[2] += x[i].z; f[3] += x[i].w;
+      f[4] += y[i].x; f[5] += y[i].y; f[6] += y[i].z; f[7] += y[i].w;
+    }
+  }
+}
+
 // How a warp of the ending gives an accumulator back to the issuers.  What is handed
 // over is tensor memory: its loads have completed (tcgen05.wait::ld) and are ordered by
 // the fence, and no thread reads memory that the warp wrote because of this arrival.
