@@ -163,6 +163,12 @@ def test_types_scales_and_reductions(cuda_lib, M, index, teacher):
     check(cuda_lib, *args, dloss=dloss, reduction="sum")
 
 
+@pytest.mark.parametrize("M,V,D,K", [(257, 10001, 72, 50), (300, 12000, 264, 1), (600, 9000, 1000, 128), (1030, 6000, 136, 20)])
+def test_two_row_tiles_per_unit(cuda_lib, M, V, D, K):
+    """Sizes whose units of work hold two row tiles; the last ones are ragged."""
+    check(cuda_lib, *inputs(M, V, D, K, seed=M + V, unscored=0.25))
+
+
 def edge_ids(V):
     marks = [0, 32, 64, 96, 128, 160, 192, 224, 256, 384, 512, 1024, 16384, 32768, V]
     return sorted({i for m in marks for i in (m - 1, m, m + 1) if 0 <= i < V})
@@ -178,6 +184,14 @@ def test_ids_at_the_edges_of_tiles(cuda_lib, M, V, D):
     ids = e.flip(0).repeat(M, 1)
     ids[1::2] = e[torch.rand(len(ids[1::2]), len(e), generator=g, device="cuda").argsort(dim=1)]
     check(cuda_lib, x, w, ids, torch.randn(M, len(e), generator=g, device="cuda"))
+
+
+def test_ids_at_the_edges_of_two_row_tiles(cuda_lib):
+    x, w, _, _ = inputs(300, 10100, 72, 1, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    e = torch.tensor(edge_ids(10100), device="cuda")
+    ids = e[torch.rand(300, len(e), generator=g, device="cuda").argsort(dim=1)]
+    check(cuda_lib, x, w, ids, torch.randn(300, len(e), generator=g, device="cuda"))
 
 
 @pytest.mark.parametrize("M", [40, 300])
@@ -365,6 +379,20 @@ def test_nothing_outside_is_written(cuda_lib, M):
 @pytest.mark.parametrize("M,D", [(100, 4096), (200, 64), (200, 4096), (300, 64), (300, 4096)])
 def test_a_wait_that_runs_out_is_reported(cuda_lib, M, D):
     args = inputs(M, 300, D, 5, seed=M)
+    want = forward(cuda_lib, *args)
+    try:
+        cuda_lib.gbf_set_wait_timeout_ns(20_000_000)
+        cuda_lib.gbf_debug_inject_timeout(True)
+        forward(cuda_lib, *args)
+        assert cuda_lib.gbf_check_device_error() == 6
+    finally:
+        cuda_lib.gbf_debug_inject_timeout(False)
+        cuda_lib.gbf_set_wait_timeout_ns(2_000_000_000)
+    assert all(torch.equal(a, b) for a, b in zip(forward(cuda_lib, *args), want))
+
+
+def test_a_wait_of_two_row_tiles_that_runs_out_is_reported(cuda_lib):
+    args = inputs(300, 10100, 72, 5, seed=300)
     want = forward(cuda_lib, *args)
     try:
         cuda_lib.gbf_set_wait_timeout_ns(20_000_000)
