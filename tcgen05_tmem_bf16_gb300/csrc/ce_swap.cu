@@ -312,23 +312,39 @@ __global__ void __launch_bounds__(kSwThreads, 2)
       if constexpr (PICK && GRAD) {
         if (seg + seg_kb >= num_kb) {
           __syncwarp();
-          int at = 0;
-#pragma unroll 1
-          for (int g = 0; g < MPAD / 8; ++g) {
-            int2 x[8];
-            entries(g, x);
+          int before_row = 0;  // entries of the rows before
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t cols = __reduce_or_sync(
-                  0xFFFFFFFFu, x[k].x < 0 ? 0u : 1u << (x[k].x - (a.v0 + t * 128 + q * 32)));
-              const int n = __popc(cols);
-              if (at + n > kRoom) staged = min(staged, 8 * g + k);
-              if (8 * g + k < staged) {
-                if (lane == 0) masks[8 * g + k] = cols;
-                if (lane < n) shares[at + lane] = __int_as_float(x[k].y);
-                at += n;
+          for (int i = 0; i < kRows; ++i) {  // a lane per row
+            const int m = i * 32 + lane;
+            int at = pick_n[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int up = __shfl_up_sync(0xFFFFFFFFu, at, o);
+              if (lane >= o) at += up;
+            }
+            const int all = __shfl_sync(0xFFFFFFFFu, at, 31);
+            at += before_row - pick_n[i];
+            before_row += all;
+            const unsigned over = __ballot_sync(0xFFFFFFFFu, at + pick_n[i] > kRoom);
+            if (over) staged = min(staged, i * 32 + __ffs(over) - 1);
+            uint32_t cols = 0u;
+            if (at + pick_n[i] <= kRoom) {
+              const int2* list =
+                  e.pick.list + static_cast<int64_t>(pick_row[i]) * (e.pick.K + 1) + pick_at[i];
+              for (int k0 = 0; k0 < pick_n[i]; k0 += 4) {  // four loads in flight
+                int2 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (k0 + k < pick_n[i]) x[k] = __ldg(list + k0 + k);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (k0 + k >= pick_n[i]) continue;
+                  cols |= 1u << (x[k].x - (a.v0 + t * 128 + q * 32));
+                  shares[at + k0 + k] = __int_as_float(x[k].y);
+                }
               }
             }
+            if (m < MPAD) masks[m] = cols;
           }
           __syncwarp();
         }
