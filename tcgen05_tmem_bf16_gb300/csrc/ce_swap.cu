@@ -398,15 +398,20 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             for (int k = 0; k < 16; ++k) __stcg(part + (c * 16 + k) * 128, v[k]);
           }
         } else if (GRAD) {
-          float f[16];
+          float f[16], dl[16], lse2[16];
+#pragma unroll
+          for (int k = 0; k < 16; k += 4) {
+            *reinterpret_cast<float4*>(dl + k) = *reinterpret_cast<const float4*>(row_dl + c * 16 + k);
+            *reinterpret_cast<float4*>(lse2 + k) = *reinterpret_cast<const float4*>(row_lse2 + c * 16 + k);
+          }
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const int m = c * 16 + k;
             f[k] = 0.0f;
             if (m < count) {
-              const float p = sw_pow2(fmaf(v[k], e.c2, -row_lse2[m]));
+              const float p = sw_pow2(fmaf(v[k], e.c2, -lse2[k]));
               if constexpr (PICK) f[k] = p;
-              else f[k] = row_dl[m] * (row_tgt[m] == col ? p - 1.0f : p);
+              else f[k] = dl[k] * (row_tgt[m] == col ? p - 1.0f : p);
             }
           }
           if constexpr (PICK) {
@@ -416,8 +421,21 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             for (int h = 0; h < 2; ++h) {
               const unsigned some = __ballot_sync(0xFFFFFFFFu, n_c > 0) >> (16 * (c & 1) + 8 * h);
               if (!(some & 0xFFu)) continue;
+              if (c * 16 + 8 * h + 8 <= staged) {
+                uint32_t cols[8];
+                *reinterpret_cast<uint4*>(cols) = *reinterpret_cast<const uint4*>(masks + c * 16 + 8 * h);
+                *reinterpret_cast<uint4*>(cols + 4) =
+                    *reinterpret_cast<const uint4*>(masks + c * 16 + 8 * h + 4);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int i = taken + __popc(cols[k] & ((1u << lane) - 1u));
+                  if ((cols[k] >> lane) & 1u) f[8 * h + k] -= shares[i];
+                  taken += __popc(cols[k]);
+                }
+                continue;
+              }
               int2 x[8];
-              if (c * 16 + 8 * h + 8 > staged) entries(2 * c + h, x);
+              entries(2 * c + h, x);
 #pragma unroll
               for (int k = 0; k < 8; ++k) {
                 const int m = c * 16 + 8 * h + k;
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
             }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              if (c * 16 + k < count) f[k] *= row_dl[c * 16 + k];
+              if (c * 16 + k < count) f[k] *= dl[k];
           }
           if (col < a.cols) {
             constexpr bool kTwice = PICK && MPAD <= kCeTwiceRows;
