@@ -221,6 +221,19 @@ int choose_splits(int tiles, int num_kb, const DeviceInfo& dev) {
 GemmPlan persistent_plan(int64_t M, int64_t N, int64_t K, bool dual, bool split,
                          const DeviceInfo& dev);
 
+// The swapped kernel over `rows` rows per tile, for the endings of a gated block.
+GemmPlan swap_plan(int64_t M, int64_t N, int64_t K, int64_t rows, const DeviceInfo& dev) {
+  GemmPlan p;
+  p.num_kb = ceil_div(K, kBK);
+  p.path = kPathSwap;
+  p.mpad = M <= 16 ? 16 : (M <= 32 ? 32 : (M <= 64 ? 64 : 128));
+  p.mpad = std::min(p.mpad, static_cast<int>(rows));
+  p.m_tiles = ceil_div(M, p.mpad);
+  p.n_tiles = ceil_div(N, kSwapBN);
+  p.splits = choose_splits(p.n_tiles * p.m_tiles, p.num_kb, dev);
+  return p;
+}
+
 // Dense GEMM (+ dual) launch after validation.  D rows of out.
 gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, bool dual,
                       const EpiParams& ep, int64_t M, int64_t N, int64_t K,
@@ -240,8 +253,11 @@ gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, 
   }
   const bool kn = layout == GBF_B_KN;
   const bool keep = dual && ep.out3;
-  const GemmPlan plan = keep && M > kSwapDualMaxM ? persistent_plan(M, N, K, true, false, dev)
-                                                  : plan_gemm(M, N, K, dual, kn, dev);
+  const bool grad = !dual && ep.out2;
+  const GemmPlan plan =
+      keep && !lib_glu_swap(M, N, K, true) ? persistent_plan(M, N, K, true, false, dev)
+      : keep || grad ? swap_plan(M, N, K, keep ? kSwapDualMaxM : kSwapGradMaxM, dev)
+                     : plan_gemm(M, N, K, dual, kn, dev);
   CUtensorMap tmA, tmW, tmW2;
   const uint32_t a_rows = plan.path == kPathSwap ? plan.mpad : kBM;
   const bool pair =
@@ -461,6 +477,12 @@ bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint6
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz) {
   return tmap_2d(m, base, dt, inner, outer, row_bytes, box_inner, box_outer, swz);
+}
+
+bool lib_glu_swap(int64_t M, int64_t F, int64_t D, bool keep) {
+  const int64_t rows = keep ? kSwapDualMaxM : kSwapGradMaxM;
+  const int64_t tiles = (M + rows - 1) / rows * ((F + kSwapBN - 1) / kSwapBN);
+  return M <= rows || tiles <= (keep || D >= 4096 ? 2 : 1) * kSwapGluTiles;
 }
 
 int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,

@@ -211,12 +211,12 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
   l.act = act;
   int64_t cycles;
   const int streams = faster_streams(&l, M, &cycles);
-  // Few rows: the weights' bytes count, and the swapped kernel splits K over clusters
-  // (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
+  // Few rows or tiles: the weights' bytes or the latency count, and the swapped kernel
+  // splits K over clusters (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
   // rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs 56; 257 x 2048 x 5632
   // 21, 28; 256 x 4096 x 14336 64, 56).
   const int64_t tiles = ceil_div64(M, 128) * ceil_div64(F, 128);
-  if (M <= kSwapDualMaxM ||
+  if (lib_glu_swap(M, F, D, true) ||
       ceil_div64(tiles, kMaxSms) * ceil_div64(D, kBK) * 680 + 9000 < cycles) {
     if ((st = lib_glu_keep(x, w_gate, w_up, h, g, u, M, F, D, act, s)) != GBF_OK) return st;
   } else {
@@ -263,8 +263,8 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
   const bool hidden = dx || dw_gate || dw_up;
   const MlpPlan plan = plan_mlp(M, D, F);
   const int splits = plan.dx_splits, streams = plan.streams;
-  if (hidden && M <= kSwapGradMaxM) {
-    // few rows, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
+  if (hidden && lib_glu_swap(M, F, D, false)) {
+    // few rows or tiles, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
     // rows 32)
     if ((st = lib_glu_grad(dout, w_down, g, u, ws.dg, ws.du, M, F, D, act, s)) != GBF_OK) return st;
   } else if (hidden) {

@@ -352,9 +352,18 @@ bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint6
                  uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                  CUtensorMapSwizzle swz);
 // The products of a gated block that is trained, with the endings of EpiParams' out2
-// and out3: h, g, u = act(g) u, x Wg^T, x Wu^T on the swapped kernel for M <=
-// kSwapDualMaxM, else the persistent one; dg, du from dout Wd on the swapped kernel for
-// M <= kSwapGradMaxM.  Arguments as checked by the caller.
+// and out3: h, g, u = act(g) u, x Wg^T, x Wu^T on the swapped kernel where lib_glu_swap
+// says so, else the persistent one; dg, du from dout Wd on the swapped kernel.  Arguments
+// as checked by the caller.
+//
+// The swapped kernel is taken up to kSwapDualMaxM or kSwapGradMaxM rows, one tile of them,
+// and beyond while there are so few tiles that the SMs hold 8 parts of K of each at a time,
+// or 4: forward (64 x 4096 x 2048 21 us, by the pairs' kernel 41; 64 tiles, 128 x 4096 x
+// 2048 28, 45; 100 tiles, 44 x 760 x 6280 29, 25), for the gradient, whose ending is the
+// longer one, where K is long (300 x 4096 x 1024 35, 49; 64 tiles, 1000 x 4096 x 1024 57,
+// 67; 48 tiles, 300 x 2048 x 2048 46, 41).
+bool lib_glu_swap(int64_t M, int64_t F, int64_t D, bool keep);
+constexpr int kSwapGluTiles = 38;
 int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,
                  int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream);
 int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void* u, void* dg,

@@ -137,6 +137,61 @@ def test_block_and_its_gradients(cuda_lib, M, D, F, act):
     assert cuda_lib.gbf_check_device_error() == 0
 
 
+# Many tiles, which the kernels of CTA pairs and of one SM take, with one and two row tiles
+# per unit.
+WIDE = [(129, 72, 5000), (100, 136, 10000), (300, 264, 6000), (1300, 72, 4104), (600, 72, 12000), (2500, 136, 2056)]
+
+
+@pytest.mark.parametrize("M,D,F", WIDE)
+@pytest.mark.parametrize("act", ["silu", "gelu_tanh", "relu"])
+def test_many_tiles(cuda_lib, M, D, F, act):
+    t, residual, dout = inputs(M, D, F, seed=M + D + F)
+    got = forward(cuda_lib, t, residual, act, M, D, F)
+    check_forward(t, residual, got, act, D, F)
+    check_backward(t, got[1:], dout, backward(cuda_lib, t, got[1:], dout, act, M, D, F), act, M, D, F)
+    assert cuda_lib.gbf_check_device_error() == 0
+
+
+@pytest.mark.parametrize("M,D,F", [(129, 72, 5000), (1300, 72, 4104)])
+def test_many_tiles_write_nothing_outside(cuda_lib, M, D, F):
+    t, residual, dout = inputs(M, D, F, seed=3)
+    want = forward(cuda_lib, t, residual, "silu", M, D, F)
+    grads = backward(cuda_lib, t, want[1:], dout, "silu", M, D, F)
+    shapes = dict(out=(M, D), g=(M, F), u=(M, F), h=(M, F), dx=(M, D), dw_gate=(F, D), dw_up=(F, D), dw_down=(D, F))
+    flat = {k: torch.full((a * b + 512,), 7.0, device="cuda", dtype=torch.bfloat16) for k, (a, b) in shapes.items()}
+    v = {k: f[256:-256].view(shapes[k]) for k, f in flat.items()}
+    n = cuda_lib.gbf_workspace_size("mlp_grad", M, D, F, True)
+    ws = torch.full((n + 256,), 0x55, dtype=torch.uint8, device="cuda")
+    cuda_lib.mlp_train(**t, residual=residual, out=v["out"], g=v["g"], u=v["u"], h=v["h"], M=M, D=D, F=F)
+    cuda_lib.mlp_grad(dout, t["x"], v["g"], v["u"], v["h"], t["w_gate"], t["w_up"], t["w_down"], v["dx"], v["dw_gate"],
+                      v["dw_up"], v["dw_down"], M, D, F, workspace=ws, workspace_bytes=n)
+    assert all(bool((f[:256] == 7.0).all()) and bool((f[-256:] == 7.0).all()) for f in flat.values())
+    assert bool((ws[n:] == 0x55).all())
+    assert all(torch.equal(v[k], w) for k, w in zip(("out", "g", "u", "h"), want))
+    assert all(torch.equal(v[k], grads[k]) for k in grads)
+
+
+@pytest.mark.parametrize("M,D,F", [(129, 72, 5000), (100, 136, 10000), (300, 264, 6000), (1300, 72, 4104)])
+def test_a_wait_of_many_tiles_that_runs_out_is_reported(cuda_lib, M, D, F):
+    t, residual, dout = inputs(M, D, F, seed=M)
+    want = forward(cuda_lib, t, residual, "silu", M, D, F)
+    grads = backward(cuda_lib, t, want[1:], dout, "silu", M, D, F)
+    for call in (lambda: forward(cuda_lib, t, residual, "silu", M, D, F),
+                 lambda: backward(cuda_lib, t, want[1:], dout, "silu", M, D, F)):
+        try:
+            cuda_lib.gbf_set_wait_timeout_ns(20_000_000)
+            cuda_lib.gbf_debug_inject_timeout(True)
+            call()
+            assert cuda_lib.gbf_check_device_error() == 6
+        finally:
+            cuda_lib.gbf_debug_inject_timeout(False)
+            cuda_lib.gbf_set_wait_timeout_ns(2_000_000_000)
+    assert all(torch.equal(a, b) for a, b in zip(forward(cuda_lib, t, residual, "silu", M, D, F), want))
+    again = backward(cuda_lib, t, want[1:], dout, "silu", M, D, F)
+    assert all(torch.equal(again[k], grads[k]) for k in grads)
+    assert cuda_lib.gbf_check_device_error() == 0
+
+
 @pytest.mark.parametrize("act", ["relu", "identity"])
 @pytest.mark.parametrize("M,D,F", [(40, 136, 264), (600, 264, 136)])
 def test_other_gates(cuda_lib, act, M, D, F):
