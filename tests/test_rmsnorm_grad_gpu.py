@@ -60,6 +60,19 @@ def test_against_fp64(cuda_lib, M, N, residual):
     check(call(cuda_lib, dn, dres, r, w, M, N), dn, dres, r, w)
 
 
+@pytest.mark.parametrize("M,N", [(1, 512), (9, 280), (2500, 512), (6007, 136), (3, 520), (1301, 1000), (2, 1032), (701, 2048),
+                                 (400, 12008)])
+def test_several_rows_at_a_time_and_staged_rows(cuda_lib, M, N):
+    """Short rows, of which a CTA takes 8, 4 or 2 at a time, more than once; long ones."""
+    dn, dres, r, w = inputs(M, N, seed=M + N)
+    got = call(cuda_lib, dn, dres, r, w, M, N)
+    check(got, dn, dres, r, w)
+    for k in (0, 1):  # dr in the place of dnorm, of dresid
+        args = [dn.clone(), dres.clone()]
+        again = call(cuda_lib, *args, r, w, M, N, dr=args[k])
+        assert torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
+
+
 def test_of_what_the_forward_stored(cuda_lib):
     """add_rmsnorm, then its gradient of the r it stored, against autograd through the
     unrounded sum: r's rounding moves the result by some R of its terms."""
