@@ -237,7 +237,8 @@ GemmPlan swap_plan(int64_t M, int64_t N, int64_t K, int64_t rows, const DeviceIn
 // Dense GEMM (+ dual) launch after validation.  D rows of out.
 gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, bool dual,
                       const EpiParams& ep, int64_t M, int64_t N, int64_t K,
-                      const DeviceInfo& dev, unsigned* err, cudaStream_t stream) {
+                      const DeviceInfo& dev, unsigned* err, cudaStream_t stream,
+                      bool swapped = false) {
   if (M == 0 || N == 0) return GBF_OK;
   if (K == 0) {
     if (dual) {
@@ -256,7 +257,7 @@ gbf_status_t run_gemm(const void* A, const void* W, const void* W2, int layout, 
   const bool grad = !dual && ep.out2;
   const GemmPlan plan =
       keep && !lib_glu_swap(M, N, K, true) ? persistent_plan(M, N, K, true, false, dev)
-      : keep || grad ? swap_plan(M, N, K, keep ? kSwapDualMaxM : kSwapGradMaxM, dev)
+      : keep || grad || swapped ? swap_plan(M, N, K, keep ? kSwapDualMaxM : kSwapGradMaxM, dev)
                      : plan_gemm(M, N, K, dual, kn, dev);
   CUtensorMap tmA, tmW, tmW2;
   const uint32_t a_rows = plan.path == kPathSwap ? plan.mpad : kBM;
@@ -506,6 +507,17 @@ int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void
   EpiParams ep = make_ep(g, nullptr, u, dg, 1.0f, 0.0f, act);
   ep.out2 = static_cast<__nv_bfloat16*>(du);
   return run_gemm(dout, w_down, nullptr, GBF_B_KN, false, ep, M, F, D, *dev, err, stream);
+}
+
+int lib_mlp_down(const void* h, const void* w_down, const void* residual, void* out, int64_t M,
+                 int64_t D, int64_t F, cudaStream_t stream) {
+  const DeviceInfo* dev;
+  unsigned* err;
+  const gbf_status_t st = current_device(&dev, &err);
+  if (st != GBF_OK) return st;
+  const EpiParams ep = make_ep(nullptr, nullptr, residual, out, 1.0f, 0.0f, GBF_ACT_IDENTITY);
+  return run_gemm(h, w_down, nullptr, GBF_B_NK, false, ep, M, D, F, *dev, err, stream,
+                  lib_glu_swap(M, D, F, false));
 }
 
 KernelCtl lib_ctl(unsigned* err, int64_t ctas) { return make_ctl(err, ctas); }

@@ -226,8 +226,7 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
       return GBF_ERR_CUDA;
     if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
   }
-  return gemm_epilogue(h, w_down, GBF_B_NK, nullptr, nullptr, residual, out, M, D, F, 1.0f, 0.0f,
-                       GBF_ACT_IDENTITY, nullptr, 0, stream);
+  return lib_mlp_down(h, w_down, residual, out, M, D, F, s);
 }
 
 gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const void* u,

@@ -364,6 +364,11 @@ bool lib_tmap_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint6
 // 67; 48 tiles, 300 x 2048 x 2048 46, 41).
 bool lib_glu_swap(int64_t M, int64_t F, int64_t D, bool keep);
 constexpr int kSwapGluTiles = 38;
+// out = h Wd^T + residual, on the swapped kernel by the gradient's rule (forward of 134 x 584
+// x 13704 38 us, by gemm_epilogue's choice 65; 256 x 2048 x 5632 34.6, 41.6), else as
+// gemm_epilogue.
+int lib_mlp_down(const void* h, const void* w_down, const void* residual, void* out, int64_t M,
+                 int64_t D, int64_t F, cudaStream_t stream);
 int lib_glu_keep(const void* x, const void* w_gate, const void* w_up, void* h, void* g, void* u,
                  int64_t M, int64_t F, int64_t D, int act, cudaStream_t stream);
 int lib_glu_grad(const void* dout, const void* w_down, const void* g, const void* u, void* dg,
