@@ -177,7 +177,7 @@ size_t blocks_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
   }
   if (op == GBF_OP_ADD_RMSNORM_GRAD) {
     if (N % 8 != 0 || N > kRmsMaxN || M > kMaxInt) return 0;
-    return align256(static_cast<size_t>(rms_grad_ctas(M, static_cast<int>(N), kMaxSms)) * N * 4);
+    return align256(static_cast<size_t>(rms_grad_sums(M, static_cast<int>(N), kMaxSms)) * N * 4);
   }
   return 0;
 }

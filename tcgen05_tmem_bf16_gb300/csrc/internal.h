@@ -337,8 +337,9 @@ cudaError_t launch_mlp_sum(const float* parts, __nv_bfloat16* dx, int64_t n, int
                            int splits, int sms, cudaStream_t stream);
 
 // Gradient of add_rmsnorm (rmsnorm_grad.cu).  dresid, dweight: may be null.
-// partial: [rms_grad_ctas(N, sms)][N] fp32 where dweight is wanted.
-int rms_grad_ctas(int64_t M, int N, int sms);
+// partial: a row of N fp32 sums per CTA, rms_grad_sums(M, N, sms) at most, where dweight is
+// wanted.
+int rms_grad_sums(int64_t M, int N, int sms);
 cudaError_t launch_add_rmsnorm_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
                                     const __nv_bfloat16* r, const __nv_bfloat16* weight,
                                     __nv_bfloat16* dr, __nv_bfloat16* dweight, int64_t M, int N,

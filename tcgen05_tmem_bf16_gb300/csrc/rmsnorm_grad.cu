@@ -227,17 +227,16 @@ cudaError_t run_rms_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid
 
 }  // namespace
 
-int rms_grad_ctas(int64_t M, int N, int sms) {
-  const int rows = rms_grad_rows(N);
-  return static_cast<int>(std::min<int64_t>((M + rows - 1) / rows,
-                                            static_cast<int64_t>(sms) * (512 / rms_grad_threads(N))));
+int rms_grad_sums(int64_t M, int N, int sms) {
+  return static_cast<int>(std::min<int64_t>(M, static_cast<int64_t>(sms) * (512 / rms_grad_threads(N))));
 }
 
 cudaError_t launch_add_rmsnorm_grad(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
                                     const __nv_bfloat16* r, const __nv_bfloat16* weight,
                                     __nv_bfloat16* dr, __nv_bfloat16* dweight, int64_t M, int N,
                                     float eps, float* partial, int sms, cudaStream_t stream) {
-  const int grid = rms_grad_ctas(M, N, sms);
+  const int rows = rms_grad_rows(N);
+  const int grid = rms_grad_sums((M + rows - 1) / rows, N, sms);
   float* p = dweight ? partial : nullptr;
   cudaError_t e;
   if (N <= 512) e = run_rms_grad<256, 32, 2, false>(dnorm, dresid, r, weight, dr, p, M, N, eps, grid, stream);
