@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(kSwThreads, 2)
   // The gradient's scored rows are listed by the kernel before.  The forward pass over
   // lists is launched by the kernel that makes them, once everything before that one
   // has completed: x and w are read meanwhile, and only the ending waits.
+  // (So the lists are written while this kernel runs: they are read by plain loads, not
+  // by those for data that is constant meanwhile.)
   constexpr bool kEarly = PICK && !GRAD;
   // The gradient's CTAs wait while the rows are listed; meanwhile their first blocks of W
   // go to L2, which would update them (64 rows x 32000 x 4096 trained 205.5 us, 6 blocks
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
           const int at = __shfl_sync(0xFFFFFFFFu, at_g, from);
           const int n = __shfl_sync(0xFFFFFFFFu, n_g, from);
           x[k] = make_int2(-1, 0);
-          if (lane < n) x[k] = __ldg(e.pick.list + row * (e.pick.K + 1) + at + lane);
+          if (lane < n) x[k] = e.pick.list[row * (e.pick.K + 1) + at + lane];
         }
       };
       // The entries go to shared memory while the products are on their way: beside the
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
                 int2 x[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  if (k0 + k < pick_n[i]) x[k] = __ldg(list + k0 + k);
+                  if (k0 + k < pick_n[i]) x[k] = list[k0 + k];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   if (k0 + k >= pick_n[i]) continue;
@@ -514,7 +516,7 @@ __global__ void __launch_bounds__(kSwThreads, 2)
               for (int i0 = 0; i0 < n_c; i0 += 8) {  // eight loads in flight
                 int col8[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) col8[i] = i0 + i < n_c ? __ldg(&list[i0 + i].x) : base;
+                for (int i = 0; i < 8; ++i) col8[i] = i0 + i < n_c ? list[i0 + i].x : base;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                   if (i0 + i < n_c) dots[i0 + i] = my_turn[(col8[i] - base) * 17 + (lane & 15)];
