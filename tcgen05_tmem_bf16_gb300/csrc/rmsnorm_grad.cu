@@ -119,7 +119,8 @@ __global__ void __launch_bounds__(T, PER_SM)
       }
     }
     const float s = rsqrtf(ss / static_cast<float>(N) + eps);
-    const float k = s * s * (t / static_cast<float>(N));
+    // one s at a time: s^2 leaves fp32 where the values are below 5e-20
+    const float k = s * (s * (t / static_cast<float>(N)));
 #pragma unroll
     for (int v = 0; v < R; ++v) {
       const int col = (place + v * ROW) * 8;
