@@ -32,7 +32,7 @@ namespace {
 template <int T, int ROW, int R, int PER_SM, bool STAGED>
 __global__ void __launch_bounds__(T, PER_SM)
     rmsnorm_grad_kernel(const __nv_bfloat16* dnorm, const __nv_bfloat16* dresid,
-                        const __nv_bfloat16* r, const __nv_bfloat16* __restrict__ w,
+                        const __nv_bfloat16* r, const __nv_bfloat16* w,
                         __nv_bfloat16* dr, float* __restrict__ partial, int64_t M, int N,
                         float eps) {
   constexpr int kRows = T / ROW;  // at a time
@@ -54,7 +54,8 @@ __global__ void __launch_bounds__(T, PER_SM)
 #pragma unroll
   for (int v = 0; v < R; ++v) {
     const int col = (place + v * ROW) * 8;
-    wv[v] = col < N ? ldg_u4(w + col) : zero;
+    // (a plain load: the kernel before may still have been writing w when this one began)
+    wv[v] = col < N ? ld_u4(w + col) : zero;
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[v][i] = 0.0f;
   }
