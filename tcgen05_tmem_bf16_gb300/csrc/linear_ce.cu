@@ -757,7 +757,9 @@ __device__ __forceinline__ void copy_row(__nv_bfloat16* dst, const __nv_bfloat16
 // results of the others (loss and lse 0, or a zero row of dx).
 template <typename Id>
 __global__ void __launch_bounds__(kPrepThreads)
-    ce_prep_kernel(const Id* __restrict__ targets, const CePrep p) {
+    ce_prep_kernel(const Id* targets, const CePrep p) {
+  // (targets not __restrict__: with lists the kernel before writes them while this one
+  // is already resident, so they are no constant data)
   griddep_launch_dependents();
   griddep_wait();
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * p.rows_per;
