@@ -467,7 +467,8 @@ GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *o
  *   itself) from the g, u and h that gbf_mlp_train kept:
  *     dh = dout*Wd;   dg = dh * u * act'(g),  du = dh * act(g)    (rounded to bf16)
  *     dx = dg*Wg + du*Wu,   dw_gate = dg^T*x,  dw_up = du^T*x,  dw_down = dout^T*h
- *   act' of GBF_ACT_RELU is 0 at 0.  dx [M][D], dw_gate, dw_up [F][D], dw_down
+ *   act' of GBF_ACT_RELU is 0 at 0 and at a NaN; everything else keeps a NaN (act of
+ *   GBF_ACT_RELU here and in h, unlike the endings above, which make it 0).  dx [M][D], dw_gate, dw_up [F][D], dw_down
  *   [D][F] bf16; any of the four may be NULL (not computed), not all.  dh is never
  *   in memory.  Sums in fp32 on the tensor cores (whose additions cut about 1e-9 of
  *   the sum per product), rounded once.  The same bits on every run.  M == 0 gives

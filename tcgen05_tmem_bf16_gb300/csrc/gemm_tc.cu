@@ -276,11 +276,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const RowLoads cur = L;
         if (cc + 1 < kMine) epi_row_prefetch(L, row, col0 + 32, a.M, a.N, a.ep, pol);
         uint32_t w[16];
-        switch (a.ep.act) {
-          case kActRelu: epi_row32_pack<kActRelu, DUAL>(acc, up, cur, a.ep, w); break;
-          case kActSilu: epi_row32_pack<kActSilu, DUAL>(acc, up, cur, a.ep, w); break;
-          case kActGeluTanh: epi_row32_pack<kActGeluTanh, DUAL>(acc, up, cur, a.ep, w); break;
-          default: epi_row32_pack<kActIdentity, DUAL>(acc, up, cur, a.ep, w); break;
+        if constexpr (KEEP) {
+          glu_pack(a.ep.act, acc, up, w);
+        } else {
+          switch (a.ep.act) {
+            case kActRelu: epi_row32_pack<kActRelu, DUAL>(acc, up, cur, a.ep, w); break;
+            case kActSilu: epi_row32_pack<kActSilu, DUAL>(acc, up, cur, a.ep, w); break;
+            case kActGeluTanh: epi_row32_pack<kActGeluTanh, DUAL>(acc, up, cur, a.ep, w); break;
+            default: epi_row32_pack<kActIdentity, DUAL>(acc, up, cur, a.ep, w); break;
+          }
         }
         store_chunk32(my_staging, flip, w, &tmO, row - lane, col0, a.M, a.N, pol);
         if constexpr (KEEP) {
@@ -500,18 +504,18 @@ __device__ __forceinline__ void swap_end_act(const float (&v0)[R], const float (
         e.out2[m * N + n] = __float2bfloat16_rn(du[i]);
       }
     }
+  } else if constexpr (END == kSwapKeep) {
+    if (n >= N) return;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t m = m0 + j;
+      if (m >= M) break;
+      st_stream_u16(e.out + m * N + n, f_to_bf16bits(gate<ACT>(v0[j]) * v1[j]), pol);
+      st_stream_u16(e.out2 + m * N + n, f_to_bf16bits(v0[j]), pol);
+      st_stream_u16(e.out3 + m * N + n, f_to_bf16bits(v1[j]), pol);
+    }
   } else if constexpr (DUAL) {
     epi_col_glu<ACT, R>(v0, v1, L, m0, n, M, N, e, pol);
-    if constexpr (END == kSwapKeep) {
-      if (n >= N) return;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        const int64_t m = m0 + j;
-        if (m >= M) break;
-        st_stream_u16(e.out2 + m * N + n, f_to_bf16bits(v0[j]), pol);
-        st_stream_u16(e.out3 + m * N + n, f_to_bf16bits(v1[j]), pol);
-      }
-    }
   } else {
     epi_col<ACT, R>(v0, L, m0, n, M, N, e, pol);
   }

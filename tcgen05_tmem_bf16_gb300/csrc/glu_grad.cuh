@@ -1,5 +1,6 @@
-// glu_grad.cuh -- a gate's activation and derivative, for the endings that make dg and
-// du from dh (mlp_train.cu, gemm_tc.cu).
+// glu_grad.cuh -- the gate of a block that is trained, for the endings that store h beside
+// g and u, and a gate's activation and derivative, for those that make dg and du from dh
+// (mlp_train.cu, gemm_tc.cu).
 #pragma once
 
 #include <cstdint>
@@ -23,6 +24,37 @@ __device__ __forceinline__ float mb_clamp(float v, float most) {  // a NaN stays
   asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, %2;\n\tmax.NaN.f32 %0, t, %3;\n\t}"
       : "=f"(y) : "f"(v), "f"(most), "f"(-most));
   return y;
+}
+
+__device__ __forceinline__ float mb_relu(float v) {  // a NaN stays one
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(v));
+  return y;
+}
+
+// h = act(g) u of 32 columns.  A NaN in g is one in h, with every gate.
+template <int ACT>
+__device__ __forceinline__ float gate(float g) {
+  if constexpr (ACT == kActRelu) return mb_relu(g);
+  else return act_apply<ACT>(g);
+}
+template <int ACT>
+__device__ __forceinline__ void glu_pack_act(const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                             uint32_t (&w)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    w[k] = pack_bf16x2(
+        gate<ACT>(__uint_as_float(g[2 * k])) * __uint_as_float(u[2 * k]),
+        gate<ACT>(__uint_as_float(g[2 * k + 1])) * __uint_as_float(u[2 * k + 1]));
+}
+__device__ __forceinline__ void glu_pack(int act, const uint32_t (&g)[32], const uint32_t (&u)[32],
+                                         uint32_t (&w)[16]) {
+  switch (act) {
+    case kActRelu: glu_pack_act<kActRelu>(g, u, w); break;
+    case kActSilu: glu_pack_act<kActSilu>(g, u, w); break;
+    case kActGeluTanh: glu_pack_act<kActGeluTanh>(g, u, w); break;
+    default: glu_pack_act<kActIdentity>(g, u, w); break;
+  }
 }
 
 // Two fp32 values at a time, each operation rounded as the scalar one.
@@ -63,7 +95,7 @@ __device__ __forceinline__ void act_both(f2 v, f2& y, f2& dy) {
   if constexpr (ACT == kActRelu) {
     float a, b;
     f2_get(v, a, b);
-    y = f2_of(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
+    y = f2_of(mb_relu(a), mb_relu(b));
     dy = f2_of(a > 0.0f ? 1.0f : 0.0f, b > 0.0f ? 1.0f : 0.0f);
   } else if constexpr (ACT == kActSilu) {
     const f2 s = f2_sigmoid2(f2_mul(v, f2_all(-kLog2e)));

@@ -134,16 +134,6 @@ __device__ __forceinline__ void stage_row16(uint8_t* buf, uint32_t at, const uin
                  : "memory");
 }
 
-template <int ACT>
-__device__ __forceinline__ void glu_pack(const uint32_t (&g)[32], const uint32_t (&u)[32],
-                                         uint32_t (&w)[16]) {
-#pragma unroll
-  for (int k = 0; k < 16; ++k)
-    w[k] = pack_bf16x2(
-        act_apply<ACT>(__uint_as_float(g[2 * k])) * __uint_as_float(u[2 * k]),
-        act_apply<ACT>(__uint_as_float(g[2 * k + 1])) * __uint_as_float(u[2 * k + 1]));
-}
-
 // dg and du of 16 columns.
 template <int ACT>
 __device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[16], const uint4 (&g2)[2],
@@ -541,12 +531,7 @@ __global__ void __launch_bounds__(kMbThreads, 1)
               put_chunk<false>(bufs, kStageChunkBytes, flip, 0, w, &j.o[o], row0, col, j.rows,
                                j.cols, first);
             };
-            switch (a.act) {
-              case kActRelu: glu_pack<kActRelu>(g, up, w); break;
-              case kActSilu: glu_pack<kActSilu>(g, up, w); break;
-              case kActGeluTanh: glu_pack<kActGeluTanh>(g, up, w); break;
-              default: glu_pack<kActIdentity>(g, up, w); break;
-            }
+            glu_pack(a.act, g, up, w);
             put(0);
             pack32(g, w);
             put(1);
