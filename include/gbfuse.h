@@ -473,7 +473,9 @@ GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *o
  *   in memory.  Sums in fp32 on the tensor cores (whose additions cut about 1e-9 of
  *   the sum per product), rounded once.  The same bits on every run.  M == 0 gives
  *   zero weight gradients.  Workspace: gbf_workspace_size(GBF_OP_MLP_GRAD, M, D, F,
- *   1) bytes.
+ *   1) bytes, which do not fall with M: one for the most rows serves fewer.  Without dx
+ *   2 * align256(2 * M * F) bytes do, without dx, dw_gate and dw_up none (align256: up to
+ *   the next multiple of 256).
  */
 GBF_API gbf_status_t gbf_mlp_train(const void *x, const void *w_gate, const void *w_up,
                                    const void *w_down, const void *residual, void *out, void *g,

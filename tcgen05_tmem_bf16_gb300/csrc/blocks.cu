@@ -55,9 +55,29 @@ int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
   return two < one ? 2 : 1;
 }
 
+// Parts of K of the product for dx, each with an fp32 buffer of its own: 16 at most and
+// none shorter than 8 K blocks.
+int64_t dx_most_splits(int64_t F) {
+  return std::max<int64_t>(1, std::min<int64_t>(2 * ceil_div64(F, kBK) / 8, 16));
+}
+int64_t dx_few_splits(int64_t D, int64_t F) {  // with one row tile
+  return std::max<int64_t>(1, std::min(dx_most_splits(F), kMlpPairs / ceil_div64(D, 256)));
+}
+// Bytes of all of them, for M rows and for any fewer: where there are several row tiles
+// no more than this are taken (a quarter of a percent of sizes would take more, and lose
+// up to 6 % by the estimate), so the size of a workspace never falls with M.
+constexpr int64_t kDxPartBytes = int64_t(192) << 20;
+int64_t dx_part_bytes(int64_t M, int64_t D, int64_t F, int64_t splits) {
+  return splits > 1 ? splits * mlp_m_pad(M) * D * 4 : 0;
+}
+int64_t dx_part_limit(int64_t M, int64_t D, int64_t F) {
+  const int64_t few = M > 0 ? dx_part_bytes(1, D, F, dx_few_splits(D, F)) : 0;
+  if (M <= kMlpRows) return few;
+  return std::max(few, std::min(dx_part_bytes(M, D, F, dx_most_splits(F)), kDxPartBytes));
+}
+
 // The launch of dx and the weights' gradients: row tiles per unit, and the parts of K
-// of the product for dx, each with an fp32 buffer of its own, 16 at most and none
-// shorter than 8 K blocks.  With one row tile as many as give one round of units over
+// of the product for dx.  With one row tile as many as give one round of units over
 // the pairs (16 x 4096 x 14336, all of the launch: 3 parts 111 us, 4, one round, 104, 5
 // 116, 9 107).  Else as the whole launch is fastest by the estimate; adding the parts
 // costs a launch and their traffic (1021 x 1000 x 2728: none 40 us, 2 or 3 parts 30.2,
@@ -68,10 +88,9 @@ struct MlpPlan {
 MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
   MlpPlan p{};
   int64_t best = 0;
-  const int64_t k = 2 * ceil_div64(F, kBK), d = ceil_div64(D, 256);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
-  if (M <= kMlpRows) return {1, static_cast<int>(std::max<int64_t>(1, std::min(most, kMlpPairs / d)))};
-  for (int splits = 1; splits <= most; ++splits) {
+  if (M <= kMlpRows) return {1, static_cast<int>(dx_few_splits(D, F))};
+  const int64_t most = dx_most_splits(F), limit = dx_part_limit(M, D, F);
+  for (int splits = 1; splits <= most && dx_part_bytes(M, D, F, splits) <= limit; ++splits) {
     MbLaunch l{};
     set_dx(&l.job[0], M, D, F, splits);
     set_job(&l.job[1], kMbStore, F, D, M, true, true);
@@ -93,16 +112,19 @@ struct MlpGradWs {
   __nv_bfloat16 *dg, *du;
   float* parts;
 };
-size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, MlpGradWs* w) {
+// The bytes that a call needs, dg and du (`hidden`) and the parts of dx (`splits`, 1: none).
+size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, bool hidden, int splits,
+                         MlpGradWs* w) {
   uint8_t* p = static_cast<uint8_t*>(base);
-  const size_t act = align256(static_cast<size_t>(M) * F * 2);
-  const int splits = plan_mlp(M, D, F).dx_splits;
-  const size_t parts =
-      splits > 1 ? align256(static_cast<size_t>(splits) * mlp_m_pad(M) * D * 4) : 0;
+  const size_t act = hidden ? align256(static_cast<size_t>(M) * F * 2) : 0;
   w->dg = reinterpret_cast<__nv_bfloat16*>(p);
   w->du = p ? reinterpret_cast<__nv_bfloat16*>(p + act) : nullptr;
   w->parts = p ? reinterpret_cast<float*>(p + 2 * act) : nullptr;
-  return 2 * act + parts;
+  return 2 * act + align256(dx_part_bytes(M, D, F, splits));
+}
+// What a call of all four gradients needs with M rows or fewer.
+size_t mlp_grad_workspace(int64_t M, int64_t D, int64_t F) {
+  return 2 * align256(static_cast<size_t>(M) * F * 2) + align256(dx_part_limit(M, D, F));
 }
 
 // Sizes that the kernels' 32-bit coordinates and unit counts hold.
@@ -172,8 +194,7 @@ gbf_status_t run_launch(MbLaunch* l, int streams, const DeviceInfo& dev, unsigne
 size_t blocks_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
   if (op == GBF_OP_MLP_GRAD) {
     if (!mlp_sizes_held(M, N, K)) return 0;  // as the entry point refuses them
-    MlpGradWs w;
-    return mlp_grad_sections(nullptr, M, N, K, &w);
+    return mlp_grad_workspace(M, N, K);
   }
   if (op == GBF_OP_ADD_RMSNORM_GRAD) {
     if (N % 8 != 0 || N > kRmsMaxN || M > kMaxInt) return 0;
@@ -245,8 +266,11 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
                    {dx, dw_gate, dw_up, dw_down, workspace});
   }
   if (st != GBF_OK) return st;
+  const bool hidden = dx || dw_gate || dw_up;
+  const MlpPlan plan = plan_mlp(M, D, F);
+  const int splits = plan.dx_splits, streams = plan.streams;
   MlpGradWs ws;
-  const size_t need = mlp_grad_sections(workspace, M, D, F, &ws);
+  const size_t need = mlp_grad_sections(workspace, M, D, F, hidden, dx ? splits : 1, &ws);
   if (need && (!workspace || workspace_bytes < need)) return GBF_ERR_WORKSPACE;
   const DeviceInfo* dev;
   unsigned* err;
@@ -259,9 +283,6 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
         return st;
     return GBF_OK;
   }
-  const bool hidden = dx || dw_gate || dw_up;
-  const MlpPlan plan = plan_mlp(M, D, F);
-  const int splits = plan.dx_splits, streams = plan.streams;
   if (hidden && lib_glu_swap(M, F, D, false)) {
     // few rows or tiles, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
     // rows 32)
