@@ -362,7 +362,8 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
  *   products have random signs, lse by 2e-6 where they all have one; sums that
  *   fp32 holds exactly stay exact.  Sums of exponentials in fp32 relative to their
  *   maximum; a loss is never below zero.  Workspace:
- *   gbf_workspace_size(GBF_OP_LINEAR_CE, M, V, D, 1) bytes.
+ *   gbf_workspace_size(GBF_OP_LINEAR_CE, M, V, D, 1) bytes (here and below: they do not
+ *   fall with M, so one for the most rows serves fewer).
  * gbf_linear_ce_grad -- its gradients, from the lse that gbf_linear_ce wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - [v == targets[m]])
  *     dx = f * G w (rows that are not scored: zero),   dw = f * G^T x,
@@ -404,7 +405,7 @@ GBF_API gbf_status_t gbf_linear_ce_grad(const void *x, const void *w, const void
  *   rows), and whatever its row of x holds reaches no result.
  *   K in 1 .. 1024; beta > 0 and finite; other arguments, sizes, alignments and
  *   accuracies as gbf_linear_ce (a loss is never below zero).  Workspace:
- *   gbf_linear_distill_workspace_size(M, V, D, K, 0) bytes.
+ *   gbf_linear_distill_workspace_size(M, V, D, K, 0) bytes, which do not fall with M.
  * gbf_linear_distill_grad -- its gradients, from the lse that gbf_linear_distill wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - q[m][v])
  *     dx = f * G w,   dw = f * G^T x,   f, dloss, dx, dw and roundings as

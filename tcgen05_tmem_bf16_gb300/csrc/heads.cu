@@ -98,9 +98,16 @@ bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
 // beside dw).  Else: none longer than half of what a pair has to do in all, the
 // logits among it also where their launch is another (without them there are more
 // parts: 1024 x 32000 x 4096 491 us, 501; 4096 x 32000 x 8192 3.59 ms, 3.66).
+int64_t ce_most_splits(int64_t cols) {
+  return std::max<int64_t>(1, std::min<int64_t>(ceil_div64(cols, 64) / 8, 16));
+}
+// Bytes of several of them: sizes come to 58 MB at most (of 3e7 random ones); held, so
+// that the size of a workspace never falls with M.
+constexpr int64_t kCePartBytes = int64_t(64) << 20;
+int64_t ce_part_bytes(int64_t M, int64_t D) { return ceil_div64(M, 512) * 512 * D * 4; }
 int ce_splits(int64_t M, int64_t D, int64_t cols) {
   const int64_t d = ceil_div64(D, kCeTileRows), k = ceil_div64(cols, 64);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(k / 8, 16));
+  const int64_t most = ce_most_splits(cols);
   if (ce_streams(M) == 1)
     return static_cast<int>(std::max<int64_t>(1, std::min(most, kCePairs / d)));
   const int64_t rows = 2 * kCeTileRows;
@@ -108,7 +115,8 @@ int ce_splits(int64_t M, int64_t D, int64_t cols) {
   const int64_t all = m * d * k + m * v * ceil_div64(D, 64) +
                       ceil_div64(cols, rows) * d * ceil_div64(M, 64);
   const int64_t half = std::max<int64_t>(1, all / kCePairs / 2);
-  return static_cast<int>(std::min(most, ceil_div64(k, half)));
+  const int64_t held = std::max<int64_t>(1, kCePartBytes / ce_part_bytes(M, D));
+  return static_cast<int>(std::min({most, ceil_div64(k, half), held}));
 }
 
 // Columns of a tile of the forward pass: 224 where the rounds of such tiles over
@@ -171,6 +179,59 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
     w->g[1] = cols < V ? s.take<__nv_bfloat16>(g) : w->g[0];
     w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
   }
+  return s.at;
+}
+
+// What ce_sections comes to with M rows or fewer, by the largest of each section.
+// lists: two bf16 per value of G up to kCeTwiceRows rows.
+size_t ce_workspace(int64_t M, int64_t V, int64_t D, bool grad, bool lists) {
+  Sections s{nullptr};
+  const int64_t few = std::min<int64_t>(M, kCeSwapMax);
+  s.take<int>(1);
+  s.take<unsigned>(1);
+  s.take<int>(M);
+  s.take<int>(M);
+  s.take<__nv_bfloat16>(static_cast<size_t>(M) * D);
+  size_t chain = 0;
+  for (int64_t m : {int64_t(16), int64_t(64), int64_t(kCeSwapMax)})  // a size for all rows up to each
+    if (ce_swap_rows(few) >= m) chain = std::max(chain, ce_chain_floats(m, D));
+  s.take<float>(chain);
+  if (!grad) {
+    const int64_t part = 4 * ceil_div64(V, 128) * few;
+    s.take<float2>(M > few ? std::max(part, 2 * ceil_div64(V, 224) * M) : part);
+    s.take<float>(M);
+    s.take<double>(ceil_div64(M, 8));
+    return s.at;
+  }
+  s.take<float>(M);
+  s.take<float>(M);
+  // G of one piece, or of two
+  int64_t one = 0, two = 0;
+  for (int64_t m = few; m >= 0; --m) {
+    const int64_t cols = ce_piece(m, V);
+    const int64_t g = ce_swap_rows(m) * cols * (lists && m <= kCeTwiceRows ? 2 : 1);
+    one = std::max(one, g);
+    if (cols < V) two = std::max(two, g);
+  }
+  if (M > few) {
+    if (ce_piece(M, V) == V) {
+      one = std::max(one, M * (ceil_div64(V, 8) * 8));
+    } else {
+      const int64_t most = std::max(512 * M, kPieceBytes / 2);
+      one = std::max(one, most + 8 * M);
+      two = std::max(two, most);
+    }
+  }
+  s.take<__nv_bfloat16>(one);
+  s.take<__nv_bfloat16>(two);
+  const int64_t lone = std::max<int64_t>(
+      1, std::min(ce_most_splits(V), kCePairs / ceil_div64(D, kCeTileRows)));
+  int64_t acc = lone * ce_part_bytes(std::min<int64_t>(M, kCeTileRows), D);
+  if (M > kCeTileRows) {
+    const int64_t part = ce_part_bytes(M, D);
+    acc = std::max({acc, part, std::min(ce_most_splits(V) * part, kCePartBytes)});
+  }
+  s.take<uint8_t>(acc);
   return s.at;
 }
 
@@ -480,6 +541,18 @@ size_t distill_sections(void* base, int64_t M, int64_t V, int64_t D, int64_t K, 
   return s.at;
 }
 
+// With M rows or fewer.
+size_t distill_workspace(int64_t M, int64_t V, int64_t D, int64_t K, bool grad) {
+  Sections s{nullptr, ce_workspace(M, V, D, grad, true)};
+  const int64_t few = std::min<int64_t>(M, kCeSwapMax);
+  s.take<int2>(static_cast<size_t>(M) * (K + 1));
+  s.take<uint16_t>(M > few ? std::max(few * pick_stride(few, V), M * pick_stride(M, V))
+                           : M * pick_stride(M, V));
+  s.take<int>(M);
+  if (!grad) s.take<float>(static_cast<size_t>(M) * K);
+  return s.at;
+}
+
 gbf_status_t check_distill(const void* x, const void* w, const void* ids, const void* logits,
                            int index_type, int teacher_type, int64_t M, int64_t V, int64_t D,
                            int64_t K, float alpha, float beta) {
@@ -531,8 +604,7 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
     case GBF_OP_LINEAR_CE:
     case GBF_OP_LINEAR_CE_GRAD: {
       if (!ce_sizes_held(M, N, K)) return 0;  // as the entry points refuse them
-      CeWs w;
-      return ce_sections(nullptr, M, N, K, op == GBF_OP_LINEAR_CE_GRAD, &w);
+      return ce_workspace(M, N, K, op == GBF_OP_LINEAR_CE_GRAD, false);
     }
     default: return 0;
   }
@@ -668,8 +740,7 @@ gbf_status_t gbf_linear_ce_grad(const void* x, const void* w, const void* target
 
 size_t gbf_linear_distill_workspace_size(int64_t M, int64_t V, int64_t D, int64_t K, int grad) {
   if (M < 0 || K < 1 || K > kPickMax || !ce_sizes_held(M, V, D)) return 0;  // as refused
-  DistillWs ws;
-  return distill_sections(nullptr, M, V, D, K, grad != 0, &ws);
+  return distill_workspace(M, V, D, K, grad != 0);
 }
 
 gbf_status_t gbf_linear_distill(const void* x, const void* w, const void* ids, int index_type,

@@ -28,3 +28,17 @@ def test_mlp_grad(D):
     for F in HIDDEN:
         sizes = [gbf.gbf_workspace_size("mlp_grad", M, D, F, True) for M in rows(D + F)]
         assert sizes[0] == 0 and all(a <= b for a, b in zip(sizes, sizes[1:])), (D, F)
+
+
+VOCABULARIES = (1, 10, 1000, 32000, 50001, 131072, 2 ** 21 + 3)
+
+
+@pytest.mark.parametrize("D", (8, 64, 1000, 2056, 4096, 8192))
+@pytest.mark.parametrize("grad", [False, True])
+def test_linear_distill_and_linear_ce(D, grad):
+    for V in VOCABULARIES:
+        for K in (1, 20, 1024):
+            sizes = [gbf.linear_distill_workspace_size(M, V, D, K, grad) for M in rows(V + K)]
+            assert all(0 < a <= b for a, b in zip(sizes, sizes[1:])), (V, K)
+        sizes = [gbf.gbf_workspace_size("linear_ce_grad" if grad else "linear_ce", M, V, D, True) for M in rows(V)]
+        assert all(0 < a <= b for a, b in zip(sizes, sizes[1:])), V

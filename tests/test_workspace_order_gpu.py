@@ -3,6 +3,7 @@ in a smaller one: the results of workspaces of their own, nothing written behind
 import pytest
 import torch
 
+import test_linear_distill_gpu as distill
 from test_mlp_train_gpu import backward, forward, inputs
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,32 @@ def test_mlp_grad_without_dx(cuda_lib, M):
     only = torch.full_like(want["dw_down"], float("nan"))
     cuda_lib.mlp_grad(*args, None, None, only, M, D, F)
     assert torch.equal(only, want["dw_down"])
+
+
+@pytest.mark.parametrize("V,D,K,most", [(600, 4104, 20, 1000), (3000, 64, 5, 300), (40001, 264, 20, 700), (1000, 2056, 8, 130)])
+def test_distillation_of_fewer_rows(cuda_lib, V, D, K, most):
+    """Also of hard targets: the two losses share their passes and their workspace."""
+    ws = {g: guarded(cuda_lib.linear_distill_workspace_size(most, V, D, K, g)) for g in (False, True)}
+    hard = {g: guarded(cuda_lib.gbf_workspace_size(op, most, V, D, True)) for g, op in ((False, "linear_ce"), (True, "linear_ce_grad"))}
+    for M in sorted({1, 16, 17, 64, 65, 128, min(129, most), min(257, most), most}):
+        args = distill.inputs(M, V, D, K, seed=M, unscored=0.2)
+        loss, lse, mean = distill.forward(cuda_lib, *args)
+        want = (loss, lse, mean, *distill.backward(cuda_lib, *args, lse))
+        out = [torch.full_like(t, float("nan")) for t in want]
+        size, kinds = distill.sizes(*args)
+        cuda_lib.linear_distill(*args, *out[:3], *size, **kinds, workspace=ws[False], workspace_bytes=ws[False].numel() - 256)
+        cuda_lib.linear_distill_grad(*args, out[1], None, *out[3:], *size, **kinds, workspace=ws[True],
+                                     workspace_bytes=ws[True].numel() - 256)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), M
+        x, w, ids, _ = args
+        t = ids[:, 0].contiguous()
+        ends = [torch.full_like(v, float("nan")) for v in want]
+        for k, o in enumerate((out, ends)):  # once in a workspace of its own
+            n = [h.numel() - 256 if k else cuda_lib.gbf_workspace_size(op, M, V, D, True)
+                 for h, op in zip(hard.values(), ("linear_ce", "linear_ce_grad"))]
+            b = list(hard.values()) if k else [guarded(s) for s in n]
+            cuda_lib.linear_ce(x, w, t, *o[:3], M, V, D, workspace=b[0], workspace_bytes=n[0])
+            cuda_lib.linear_ce_grad(x, w, t, o[1], None, *o[3:], M, V, D, workspace=b[1], workspace_bytes=n[1])
+        assert all(torch.equal(a, b) for a, b in zip(out, ends)), M
+    assert all(bool((b[-256:] == 0x55).all()) for b in (*ws.values(), *hard.values()))
+    assert cuda_lib.gbf_check_device_error() == 0
