@@ -471,9 +471,10 @@ GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *o
  *   act' of GBF_ACT_RELU is 0 at 0 and at a NaN; everything else keeps a NaN (act of
  *   GBF_ACT_RELU here and in h, unlike the endings above, which make it 0).  dx [M][D], dw_gate, dw_up [F][D], dw_down
  *   [D][F] bf16; any of the four may be NULL (not computed), not all.  dh is never
- *   in memory.  Sums in fp32 on the tensor cores (whose additions cut about 1e-9 of
- *   the sum per product), rounded once.  The same bits on every run.  M == 0 gives
- *   zero weight gradients.  Workspace: gbf_workspace_size(GBF_OP_MLP_GRAD, M, D, F,
+ *   in memory.  Sums in fp32 on the tensor cores, whose additions cut up to 7e-9 of the
+ *   sum per product where all have one sign, in chains of at most 131072 products (1e-3
+ *   of such a sum) that are added in rounded fp32; rounded once.  The
+ *   same bits on every run.  M == 0 gives zero weight gradients.  Workspace: gbf_workspace_size(GBF_OP_MLP_GRAD, M, D, F,
  *   1) bytes, which do not fall with M: one for the most rows serves fewer.  Without dx
  *   2 * align256(2 * M * F) bytes do, without dx, dw_gate and dw_up none (align256: up to
  *   the next multiple of 256).

@@ -55,13 +55,26 @@ int faster_streams(MbLaunch* l, int64_t M, int64_t* cycles) {
   return two < one ? 2 : 1;
 }
 
+// The gradient of a weight: [rows][cols] over the M rows of both operands.
+void set_dw_job(MbJob* j, int64_t rows, int64_t cols, int64_t M) {
+  set_job(j, kMbStore, rows, cols, M, true, true);
+  j->splits = static_cast<int>(std::max<int64_t>(1, ceil_div64(M, kGradChain)));
+  j->m_pad = static_cast<int>(ceil_div64(rows, 32) * 32);
+}
+size_t dw_part_bytes(int64_t M, int64_t rows, int64_t cols) {  // of several parts of K
+  MbJob j;
+  set_dw_job(&j, rows, cols, M);
+  return j.splits > 1 ? align256(static_cast<size_t>(j.splits) * j.m_pad * cols * 4) : 0;
+}
+
 // Parts of K of the product for dx, each with an fp32 buffer of its own: 16 at most and
-// none shorter than 8 K blocks.
+// none shorter than 8 K blocks or longer than a chain.
+int64_t dx_least_splits(int64_t F) { return std::max<int64_t>(1, ceil_div64(2 * F, kGradChain)); }
 int64_t dx_most_splits(int64_t F) {
   return std::max<int64_t>(1, std::min<int64_t>(2 * ceil_div64(F, kBK) / 8, 16));
 }
 int64_t dx_few_splits(int64_t D, int64_t F) {  // with one row tile
-  return std::max<int64_t>(1, std::min(dx_most_splits(F), kMlpPairs / ceil_div64(D, 256)));
+  return std::max(dx_least_splits(F), std::min(dx_most_splits(F), kMlpPairs / ceil_div64(D, 256)));
 }
 // Bytes of all of them, for M rows and for any fewer: where there are several row tiles
 // no more than this are taken (a quarter of a percent of sizes would take more, and lose
@@ -73,7 +86,8 @@ int64_t dx_part_bytes(int64_t M, int64_t D, int64_t F, int64_t splits) {
 int64_t dx_part_limit(int64_t M, int64_t D, int64_t F) {
   const int64_t few = M > 0 ? dx_part_bytes(1, D, F, dx_few_splits(D, F)) : 0;
   if (M <= kMlpRows) return few;
-  return std::max(few, std::min(dx_part_bytes(M, D, F, dx_most_splits(F)), kDxPartBytes));
+  return std::max({few, dx_part_bytes(M, D, F, dx_least_splits(F)),
+                   std::min(dx_part_bytes(M, D, F, dx_most_splits(F)), kDxPartBytes)});
 }
 
 // The launch of dx and the weights' gradients: row tiles per unit, and the parts of K
@@ -90,16 +104,17 @@ MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
   int64_t best = 0;
   if (M <= kMlpRows) return {1, static_cast<int>(dx_few_splits(D, F))};
   const int64_t most = dx_most_splits(F), limit = dx_part_limit(M, D, F);
-  for (int splits = 1; splits <= most && dx_part_bytes(M, D, F, splits) <= limit; ++splits) {
+  const int least = static_cast<int>(dx_least_splits(F));
+  for (int splits = least; splits <= most && dx_part_bytes(M, D, F, splits) <= limit; ++splits) {
     MbLaunch l{};
     set_dx(&l.job[0], M, D, F, splits);
-    set_job(&l.job[1], kMbStore, F, D, M, true, true);
-    set_job(&l.job[2], kMbStore, F, D, M, true, true);
-    set_job(&l.job[3], kMbStore, D, F, M, true, true);
+    set_dw_job(&l.job[1], F, D, M);
+    set_dw_job(&l.job[2], F, D, M);
+    set_dw_job(&l.job[3], D, F, M);
     int64_t cycles;
     const int streams = faster_streams(&l, M, &cycles);
     if (splits > 1) cycles += 6000 + 8 * splits * M * D / 2500;  // bytes at about 4.8 TB/s
-    if (splits == 1 || cycles < best) {
+    if (splits == least || cycles < best) {
       best = cycles;
       p.streams = streams;
       p.dx_splits = splits;
@@ -108,23 +123,33 @@ MlpPlan plan_mlp(int64_t M, int64_t D, int64_t F) {
   return p;
 }
 
+// The bytes that a call needs: dg and du, and the parts of K of each result that has
+// several.
 struct MlpGradWs {
   __nv_bfloat16 *dg, *du;
-  float* parts;
+  float *dx, *dw_gate, *dw_up, *dw_down;
 };
-// The bytes that a call needs, dg and du (`hidden`) and the parts of dx (`splits`, 1: none).
-size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, bool hidden, int splits,
-                         MlpGradWs* w) {
-  uint8_t* p = static_cast<uint8_t*>(base);
-  const size_t act = hidden ? align256(static_cast<size_t>(M) * F * 2) : 0;
-  w->dg = reinterpret_cast<__nv_bfloat16*>(p);
-  w->du = p ? reinterpret_cast<__nv_bfloat16*>(p + act) : nullptr;
-  w->parts = p ? reinterpret_cast<float*>(p + 2 * act) : nullptr;
-  return 2 * act + align256(dx_part_bytes(M, D, F, splits));
+size_t mlp_grad_sections(void* base, int64_t M, int64_t D, int64_t F, int dx_splits, bool dx,
+                         bool dw_gate, bool dw_up, bool dw_down, MlpGradWs* w) {
+  size_t at = 0;
+  auto take = [&](size_t bytes) -> void* {
+    void* p = base && bytes ? static_cast<uint8_t*>(base) + at : nullptr;
+    at += bytes;
+    return p;
+  };
+  const size_t act = dx || dw_gate || dw_up ? align256(static_cast<size_t>(M) * F * 2) : 0;
+  w->dg = static_cast<__nv_bfloat16*>(take(act));
+  w->du = static_cast<__nv_bfloat16*>(take(act));
+  w->dx = static_cast<float*>(take(dx ? align256(dx_part_bytes(M, D, F, dx_splits)) : 0));
+  w->dw_gate = static_cast<float*>(take(dw_gate ? dw_part_bytes(M, F, D) : 0));
+  w->dw_up = static_cast<float*>(take(dw_up ? dw_part_bytes(M, F, D) : 0));
+  w->dw_down = static_cast<float*>(take(dw_down ? dw_part_bytes(M, D, F) : 0));
+  return at;
 }
 // What a call of all four gradients needs with M rows or fewer.
 size_t mlp_grad_workspace(int64_t M, int64_t D, int64_t F) {
-  return 2 * align256(static_cast<size_t>(M) * F * 2) + align256(dx_part_limit(M, D, F));
+  return 2 * align256(static_cast<size_t>(M) * F * 2) + align256(dx_part_limit(M, D, F)) +
+         2 * dw_part_bytes(M, F, D) + dw_part_bytes(M, D, F);
 }
 
 // Sizes that the kernels' 32-bit coordinates and unit counts hold.
@@ -133,7 +158,8 @@ bool mlp_sizes_held(int64_t M, int64_t D, int64_t F) {
       D > (int64_t(1) << 20) || F > (int64_t(1) << 20))
     return false;
   const int64_t m = ceil_div64(M, 256), d = ceil_div64(D, 256), f = ceil_div64(F, 128);
-  return m * f <= kMaxInt / 4 && m * d * 16 <= kMaxInt / 4 && d * f <= kMaxInt / 4;
+  return m * f <= kMaxInt / 4 && m * d * 16 <= kMaxInt / 4 &&
+         d * f * ceil_div64(std::max<int64_t>(M, 1), kGradChain) <= kMaxInt / 4;
 }
 
 gbf_status_t check_mlp(int64_t M, int64_t D, int64_t F, int act) {
@@ -174,12 +200,14 @@ bool map_parts(CUtensorMap* m, const void* p, int64_t inner, int64_t outer) {
                      CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// The gradient of a weight: out [rows][cols] = a^T b over the M rows of a and b.
-bool set_dw(MbJob* j, const void* a, const void* b, const void* out, int64_t rows, int64_t cols,
-            int64_t M) {
-  set_job(j, kMbStore, rows, cols, M, true, true);
+// The gradient of a weight: out [rows][cols] = a^T b over the M rows of a and b; parts: of
+// its K, where there are several.
+bool set_dw(MbJob* j, const void* a, const void* b, const void* out, float* parts, int64_t rows,
+            int64_t cols, int64_t M) {
+  set_dw_job(j, rows, cols, M);
   return map_mn(&j->a[0], a, rows, M) && map_mn(&j->b[0], b, cols, M) &&
-         map_out(&j->o[0], out, cols, rows, false);
+         (j->splits > 1 ? map_parts(&j->o[0], parts, cols, static_cast<int64_t>(j->splits) * j->m_pad)
+                        : map_out(&j->o[0], out, cols, rows, false));
 }
 
 gbf_status_t run_launch(MbLaunch* l, int streams, const DeviceInfo& dev, unsigned* err,
@@ -270,7 +298,7 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
   const MlpPlan plan = plan_mlp(M, D, F);
   const int splits = plan.dx_splits, streams = plan.streams;
   MlpGradWs ws;
-  const size_t need = mlp_grad_sections(workspace, M, D, F, hidden, dx ? splits : 1, &ws);
+  const size_t need = mlp_grad_sections(workspace, M, D, F, splits, dx, dw_gate, dw_up, dw_down, &ws);
   if (need && (!workspace || workspace_bytes < need)) return GBF_ERR_WORKSPACE;
   const DeviceInfo* dev;
   unsigned* err;
@@ -304,18 +332,26 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
     set_dx(&j, M, D, F, splits);
     if (!map_k(&j.a[0], ws.dg, F, M) || !map_k(&j.a[1], ws.du, F, M) ||
         !map_mn(&j.b[0], w_gate, D, F) || !map_mn(&j.b[1], w_up, D, F) ||
-        !(splits > 1 ? map_parts(&j.o[0], ws.parts, D, splits * mlp_m_pad(M))
+        !(splits > 1 ? map_parts(&j.o[0], ws.dx, D, splits * mlp_m_pad(M))
                      : map_out(&j.o[0], dx, D, M, false)))
       return GBF_ERR_CUDA;
   }
-  if ((dw_gate && !set_dw(&l.job[1], ws.dg, x, dw_gate, F, D, M)) ||
-      (dw_up && !set_dw(&l.job[2], ws.du, x, dw_up, F, D, M)) ||
-      (dw_down && !set_dw(&l.job[3], dout, h, dw_down, D, F, M)))
+  if ((dw_gate && !set_dw(&l.job[1], ws.dg, x, dw_gate, ws.dw_gate, F, D, M)) ||
+      (dw_up && !set_dw(&l.job[2], ws.du, x, dw_up, ws.dw_up, F, D, M)) ||
+      (dw_down && !set_dw(&l.job[3], dout, h, dw_down, ws.dw_down, D, F, M)))
     return GBF_ERR_CUDA;
   if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
-  if (!dx || splits == 1) return GBF_OK;
-  return cuda_status(launch_mlp_sum(ws.parts, static_cast<__nv_bfloat16*>(dx), M * D,
-                                    mlp_m_pad(M) * D, splits, dev->sms, s));
+  const float* parts[kMbJobs] = {ws.dx, ws.dw_gate, ws.dw_up, ws.dw_down};
+  void* out[kMbJobs] = {dx, dw_gate, dw_up, dw_down};
+  for (int i = 0; i < kMbJobs; ++i) {
+    const MbJob& j = l.job[i];
+    if (!out[i] || j.splits == 1) continue;
+    const int64_t cols = j.cols;
+    st = cuda_status(launch_mlp_sum(parts[i], static_cast<__nv_bfloat16*>(out[i]), j.rows * cols,
+                                    j.m_pad * cols, j.splits, dev->sms, s));
+    if (st != GBF_OK) return st;
+  }
+  return GBF_OK;
 }
 
 gbf_status_t gbf_add_rmsnorm_grad(const void* dnorm, const void* dresid, const void* resid,

@@ -297,6 +297,12 @@ struct CeLists {
 };
 cudaError_t launch_ce_lists(const CeLists& p, int sms, cudaStream_t stream);
 
+// Products of a gradient that the tensor cores add up in one chain, at most.  An addition
+// cuts the sum, up to 7e-9 of it per product where all have one sign (dWd of 64 x 64 with
+// positive values: 2^17 rows 1e-3 low, 2^20 rows 7e-3, 2^22 28e-3, several roundings to
+// bf16); longer ones are taken in parts of K, which are added in rounded fp32.
+constexpr int64_t kGradChain = 131072;
+
 // Products of a gated MLP block that is trained, and of its gradient
 // (mlp_train.cu): up to four per launch, none of which reads what another writes.
 enum MbMode { kMbNone = 0, kMbStore = 1, kMbGlu = 2, kMbGluGrad = 3 };
@@ -316,7 +322,7 @@ struct MbJob {
   int num_kb;        // 64-wide K blocks in all
   int kb_first;      // of the first pair of operands (num_kb: there is no second)
   int splits;        // parts of K, each with its own fp32 rows in o[0] (kMbStore)
-  int m_pad;         // rows between them
+  int m_pad;         // rows between them, a multiple of 32
   // by plan_mlp_launch: units, and the divisors of a unit's number
   int units, full_groups;
   MbDiv group, last, tiles, parts;
