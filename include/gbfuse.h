@@ -373,8 +373,9 @@ GBF_API gbf_status_t gbf_embedding_grad(const void *ids, int index_type, const v
  *   may be NULL (not computed), every row of the others is written.  The
  *   logits are computed again, a piece of the vocabulary at a time; G of the
  *   piece is rounded to bf16 (before f), dx and dw are summed in fp32 on the tensor
- *   cores (one chain of additions, which cut about 1e-9 of the sum per product)
- *   and rounded once.  The same bits on every run.  Workspace:
+ *   cores, whose additions cut up to 7e-9 of the sum per product where all have one
+ *   sign, in chains of at most 131072 products (1e-3 of such a sum), added in rounded
+ *   fp32, and rounded once.  The same bits on every run.  Workspace:
  *   gbf_workspace_size(GBF_OP_LINEAR_CE_GRAD, M, V, D, 1) bytes.
  */
 GBF_API gbf_status_t gbf_linear_ce(const void *x, const void *w, const void *targets,

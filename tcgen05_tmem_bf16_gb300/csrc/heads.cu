@@ -65,11 +65,12 @@ constexpr int kCePairs = 76;  // CTA pairs that run at once
 constexpr int kCeTileRows = 256;
 
 // Columns of the vocabulary per piece of the backward pass: as many whole
-// tiles as keep G of the piece within 256 MB, at least 512.
+// tiles as keep G of the piece within 256 MB, at least 512, and no more than 16 chains
+// of dx hold.
 constexpr int64_t kPieceBytes = int64_t(256) << 20;
 int64_t ce_piece(int64_t M, int64_t V) {
   const int64_t cols = std::max<int64_t>(512, kPieceBytes / 2 / std::max<int64_t>(M, 1) / 512 * 512);
-  return std::min(cols, V);
+  return std::min({cols, V, 16 * kGradChain});
 }
 
 int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -92,12 +93,13 @@ int ce_streams(int64_t M, int64_t cols, bool lists) {
 bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
 
 // Parts of K of the product for dx, each with an fp32 buffer of its own, 16 at
-// most and none shorter than 8 K blocks.  With one row tile: as many as give one
+// most and none shorter than 8 K blocks or longer than a chain.  With one row tile: as many as give one
 // round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 103
 // us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
 // beside dw).  Else: none longer than half of what a pair has to do in all, the
 // logits among it also where their launch is another (without them there are more
 // parts: 1024 x 32000 x 4096 491 us, 501; 4096 x 32000 x 8192 3.59 ms, 3.66).
+int64_t ce_least_splits(int64_t cols) { return ceil_div64(cols, kGradChain); }
 int64_t ce_most_splits(int64_t cols) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div64(cols, 64) / 8, 16));
 }
@@ -109,14 +111,21 @@ int ce_splits(int64_t M, int64_t D, int64_t cols) {
   const int64_t d = ceil_div64(D, kCeTileRows), k = ceil_div64(cols, 64);
   const int64_t most = ce_most_splits(cols);
   if (ce_streams(M) == 1)
-    return static_cast<int>(std::max<int64_t>(1, std::min(most, kCePairs / d)));
+    return static_cast<int>(std::max(ce_least_splits(cols), std::min(most, kCePairs / d)));
   const int64_t rows = 2 * kCeTileRows;
   const int64_t m = ceil_div64(M, rows), v = ceil_div64(cols, kCeTileRows);
   const int64_t all = m * d * k + m * v * ceil_div64(D, 64) +
                       ceil_div64(cols, rows) * d * ceil_div64(M, 64);
   const int64_t half = std::max<int64_t>(1, all / kCePairs / 2);
   const int64_t held = std::max<int64_t>(1, kCePartBytes / ce_part_bytes(M, D));
-  return static_cast<int>(std::min({most, ceil_div64(k, half), held}));
+  return static_cast<int>(std::max(ce_least_splits(cols), std::min({most, ceil_div64(k, half), held})));
+}
+// The same of the product for dw, whose K are the rows; rows between the parts.
+int ce_dw_splits(int64_t M) { return static_cast<int>(std::max<int64_t>(1, ceil_div64(M, kGradChain))); }
+int64_t ce_dw_pad(int64_t cols) { return ceil_div64(cols, 32) * 32; }
+size_t ce_dw_part_bytes(int64_t M, int64_t D, int64_t cols) {
+  const int64_t n = ce_dw_splits(M);
+  return n > 1 ? static_cast<size_t>(n * ce_dw_pad(cols)) * D * 4 : 0;
 }
 
 // Columns of a tile of the forward pass: 224 where the rounds of such tiles over
@@ -140,7 +149,7 @@ int64_t ce_parts(int64_t M, int64_t V, int64_t D) {
 struct CeWs {
   int *count, *rows, *tgt;
   unsigned* ticket;
-  float *lse2, *dl, *tlog, *dxacc, *chain;
+  float *lse2, *dl, *tlog, *dxacc, *dwacc, *chain;
   float2* part;
   double* sums;
   __nv_bfloat16 *xc, *g[2];
@@ -178,6 +187,7 @@ size_t ce_sections(void* base, int64_t M, int64_t V, int64_t D, bool grad, CeWs*
     w->g[0] = s.take<__nv_bfloat16>(g);
     w->g[1] = cols < V ? s.take<__nv_bfloat16>(g) : w->g[0];
     w->dxacc = s.take<float>(static_cast<size_t>(ce_splits(M, D, cols)) * m_pad * D);
+    w->dwacc = s.take<float>(ce_dw_part_bytes(M, D, cols) / 4);
   }
   return s.at;
 }
@@ -224,14 +234,17 @@ size_t ce_workspace(int64_t M, int64_t V, int64_t D, bool grad, bool lists) {
   }
   s.take<__nv_bfloat16>(one);
   s.take<__nv_bfloat16>(two);
-  const int64_t lone = std::max<int64_t>(
-      1, std::min(ce_most_splits(V), kCePairs / ceil_div64(D, kCeTileRows)));
+  const int64_t lone = std::max(ce_least_splits(ce_piece(1, V)),
+                                std::min(ce_most_splits(V), kCePairs / ceil_div64(D, kCeTileRows)));
   int64_t acc = lone * ce_part_bytes(std::min<int64_t>(M, kCeTileRows), D);
   if (M > kCeTileRows) {
     const int64_t part = ce_part_bytes(M, D);
     acc = std::max({acc, part, std::min(ce_most_splits(V) * part, kCePartBytes)});
+    for (int64_t m = kCeTileRows + 1; m <= std::min<int64_t>(M, 1024); m += 256)  // the least, in steps of 512 rows
+      acc = std::max(acc, ce_least_splits(ce_piece(m, V)) * ce_part_bytes(m, D));
   }
   s.take<uint8_t>(acc);
+  s.take<uint8_t>(ce_dw_part_bytes(M, D, ce_piece(M, V)));
   return s.at;
 }
 
@@ -424,7 +437,7 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   const int64_t rows = ce_swap_rows(M);
   const int64_t ld = few ? (twice ? 2 : 1) * rows : ceil_div64(piece, 8) * 8;
   const int64_t m_pad = ceil_div64(M, 512) * 512;
-  const int splits = ce_splits(M, D, piece);
+  const int splits = ce_splits(M, D, piece), dw_splits = ce_dw_splits(M);
   const int streams = ce_streams(M, piece, pick.list != nullptr);
   CeEnd end{};
   end.count = ws.count;
@@ -490,17 +503,34 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
         job.mode = kCeDw;
         job.cols = static_cast<int>(cols);
         job.v0 = static_cast<int>(v0);
-        job.splits = 1;
+        job.splits = dw_splits;
+        job.pad = static_cast<int>(ce_dw_pad(piece));
         job.gt = few;
         if (!(few ? ce_map_k(&job.a[0], g, rows, cols, ld) : ce_map_mn(&job.a[0], g, cols, M, ld)) ||
             (twice && !ce_map_k(&job.a[1], g + rows, rows, cols, ld)) ||
             !ce_map_mn(&job.b[0], ws.xc, D, M, D) ||
-            !ce_map_mn(&job.b[1], x, D, M, D) || !ce_map_dw(&job.o, dw, D, V, streams == 1))
+            !ce_map_mn(&job.b[1], x, D, M, D) ||
+            !(dw_splits > 1 ? ce_map_out_f32(&job.o, ws.dwacc, D, dw_splits * job.pad)
+                            : ce_map_dw(&job.o, dw, D, V, streams == 1)))
           return GBF_ERR_CUDA;
       }
     }
     if ((few || chains) && n == 0) continue;  // no G yet
     if ((st = run_ce_gemm(launch, end, M, streams, false, *dev, err, s)) != GBF_OK) return st;
+    if (n > 0 && dw && dw_splits > 1) {
+      const CeJob& job = launch.job[2];
+      CeDxOut out{};
+      out.count = ws.count;
+      out.acc = ws.dwacc;
+      out.dx = static_cast<__nv_bfloat16*>(dw) + job.v0 * D;
+      out.scale = end.scale;
+      out.mean = end.mean;
+      out.m_pad = job.pad;
+      out.splits = dw_splits;
+      out.D = p.D;
+      out.dw_rows = job.cols;
+      if ((st = cuda_status(launch_ce_dx(out, job.cols, dev->sms, s))) != GBF_OK) return st;
+    }
   }
   if (!dx) return GBF_OK;
   CeDxOut out{};

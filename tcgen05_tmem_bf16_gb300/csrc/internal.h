@@ -159,6 +159,12 @@ cudaError_t launch_clip_grad_norm(const void* const* in, void* const* out, const
                                   const int* types, int n, float max_norm, float eps, float* norm,
                                   float2* partial, int sms, cudaStream_t stream);
 
+// Products of a gradient that the tensor cores add up in one chain, at most.  An addition
+// cuts the sum, up to 7e-9 of it per product where all have one sign (dWd of 64 x 64 with
+// positive values: 2^17 rows 1e-3 low, 2^20 rows 7e-3, 2^22 28e-3, several roundings to
+// bf16); longer ones are taken in parts of K, which are added in rounded fp32.
+constexpr int64_t kGradChain = 131072;
+
 // Linear cross entropy (linear_ce.cu).  One product of the kernel with its
 // ending; the scored rows are numbered 0 .. count-1 in their order.
 enum CeMode { kCeNone = 0, kCeLse = 1, kCeGrad = 2, kCeDx = 3, kCeDw = 4 };
@@ -170,7 +176,8 @@ struct CeJob {
   int bn;      // columns of a tile: 256, or for kLse 224
   int cols;    // columns of the vocabulary: all (kCeLse) or the piece's
   int v0;      // first column of the piece
-  int splits;  // parts of K (kCeDx), each with its own fp32 buffer
+  int splits;  // parts of K (kCeDx, kCeDw), each with its own fp32 buffer
+  int pad;     // kCeDw in parts: rows between them, a multiple of 32
   int add;     // kCeDx: add to the buffer (a later piece)
   int gt;      // kCeDx, kCeDw: G is stored transposed, [cols][rows]
 };
@@ -266,11 +273,11 @@ struct CeJoin {
 };
 struct CeDxOut {
   const int* count;
-  const int* rows;
+  const int* rows;  // null: dw_rows rows of dw, as they are
   const float* acc;
   __nv_bfloat16* dx;
   float scale;
-  int mean, m_pad, splits, D;
+  int mean, m_pad, splits, D, dw_rows;
   int twice;  // the sums of G's second parts are kCeTwiceRows rows behind
 };
 // chains: one product, the logits, in units of one row tile (streams 1).
@@ -296,12 +303,6 @@ struct CeLists {
   int V, K, stride, shift;
 };
 cudaError_t launch_ce_lists(const CeLists& p, int sms, cudaStream_t stream);
-
-// Products of a gradient that the tensor cores add up in one chain, at most.  An addition
-// cuts the sum, up to 7e-9 of it per product where all have one sign (dWd of 64 x 64 with
-// positive values: 2^17 rows 1e-3 low, 2^20 rows 7e-3, 2^22 28e-3, several roundings to
-// bf16); longer ones are taken in parts of K, which are added in rounded fp32.
-constexpr int64_t kGradChain = 131072;
 
 // Products of a gated MLP block that is trained, and of its gradient
 // (mlp_train.cu): up to four per launch, none of which reads what another writes.

@@ -170,8 +170,9 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   u.split = 0;
   u.kb0 = 0;
   u.kb1 = num_kb;
-  if (u.job == 0) {  // the only product whose K is split; at most 16 parts of 2^20 blocks
-    const unsigned splits = a.job[0].splits;
+  // the products whose K is split, dx and a long dw; at most 2^25 parts x blocks
+  const unsigned splits = u.job == 0 ? a.job[0].splits : u.job == 2 ? a.job[2].splits : 1;
+  if (splits > 1) {
     const unsigned tiles = m_units * n_tiles;
     u.split = static_cast<unsigned>(t) / tiles;
     t -= u.split * tiles;
@@ -694,7 +695,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             e.part[static_cast<int64_t>(2 * u.nb + half) * e.M + t.row] = make_float2(m, sum);
         } else if (mode == kCeGrad) {
           ce_tile<kCeGrad, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
-        } else if (mode == kCeDx) {
+        } else if (mode == kCeDx || j.splits > 1) {
+          if (mode == kCeDw) {  // a part of its K
+            t.buf_row = u.split * j.pad + t.row;
+            t.count = j.cols;
+            t.add = false;
+          }
           ce_tile<kCeDx, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
         } else {
           ce_tile<kCeDw, FORM, PICK>(tb, release, t, e, flip, m, sum, cur);
@@ -1018,8 +1024,8 @@ __global__ void __launch_bounds__(kJoinThreads) ce_join_kernel(const CeJoin p) {
 
 constexpr int kOutThreads = 128;
 
-// dx of the scored rows: the splits' sums added in order, scaled, rounded once.
-// A warp per 256 columns of a row.
+// dx of the scored rows, or rows of dw: the splits' sums added in order, scaled, rounded
+// once.  A warp per 256 columns of a row.
 __global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -1028,11 +1034,11 @@ __global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
   const int segs = (p.D + 255) / 256;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kOutThreads / 32);
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * (kOutThreads / 32) + (threadIdx.x >> 5);
-       t < static_cast<int64_t>(count) * segs; t += step) {
+       t < static_cast<int64_t>(p.rows ? count : p.dw_rows) * segs; t += step) {
     const int64_t row = t / segs;
     const int col = static_cast<int>(t - row * segs) * 256 + (threadIdx.x & 31) * 8;
     if (col >= p.D) continue;
-    const int out_row = p.rows[row];
+    const int64_t out_row = p.rows ? p.rows[row] : row;
     float f[8];
     // of each part of K the sums of G's first and, where there are two, second parts
     add_parts(f, p.splits << p.twice, [&](int i) {
@@ -1041,7 +1047,7 @@ __global__ void __launch_bounds__(kOutThreads) ce_dx_kernel(const CeDxOut p) {
     });
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] *= scale;
-    st_u4(p.dx + static_cast<int64_t>(out_row) * p.D + col, pack8(f));
+    st_u4(p.dx + out_row * p.D + col, pack8(f));
   }
 }
 
