@@ -48,6 +48,13 @@ GBF_API gbf_status_t gbf_debug_force_splits(int splits);
  * of rounding. */
 GBF_API gbf_status_t gbf_debug_force_path(int path);
 
+/* The kernel that gbf_mlp_train takes for its gate/up product (grad == 0), or
+ * gbf_mlp_grad for dh: 1 the persistent one, 2 the swapped one, 8 that of CTA
+ * pairs with one row tile per unit of work, 9 with two; -1 where the sizes are
+ * refused or M == 0.  *units (may be NULL): units over the 76 pairs, 0 for the
+ * other kernels.  Needs no GPU. */
+GBF_API int gbf_debug_mlp_path(int64_t M, int64_t D, int64_t F, int grad, int64_t *units);
+
 #ifdef __cplusplus
 }
 #endif

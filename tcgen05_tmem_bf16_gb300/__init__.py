@@ -53,6 +53,8 @@ STATUS = {0: "GBF_OK", 1: "GBF_ERR_INVALID_ARG", 2: "GBF_ERR_MISALIGNED",
 PATH = {0: "none", 1: "persistent", 2: "swap_splitk", 3: "w4a16", 4: "pair",
         5: "persistent_splitk", 6: "pair_1stream", 7: "pair_splitk"}
 
+MLP_PATH = {1: "persistent", 2: "swap_splitk", 8: "pair_1tile", 9: "pair_2tiles"}
+
 EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unfused",
            "swiglu_dual_gemm_unfused", "w4a16_gemm_unfused", "gbf_workspace_size",
            "gbf_check_device_error", "gbf_status_string", "gbf_set_wait_timeout_ns",
@@ -63,7 +65,7 @@ EXPORTS = ("gemm_epilogue", "swiglu_dual_gemm", "w4a16_gemm", "gemm_epilogue_unf
            "w4a16_nvfp4_gemm", "w4a16_nvfp4_gemm_unfused", "gbf_embedding_lookup",
            "gbf_embedding_grad", "gbf_clip_grad_norm", "gbf_linear_ce", "gbf_linear_ce_grad",
            "gbf_mlp_train", "gbf_mlp_grad", "gbf_add_rmsnorm_grad", "gbf_linear_distill",
-           "gbf_linear_distill_grad", "gbf_linear_distill_workspace_size")
+           "gbf_linear_distill_grad", "gbf_linear_distill_workspace_size", "gbf_debug_mlp_path")
 
 _lock = threading.Lock()
 _lib = None
@@ -156,6 +158,8 @@ def load(path: str | None = None):
         lib.gbf_set_wait_timeout_ns.restype = I
         lib.gbf_debug_inject_timeout.argtypes = [I]
         lib.gbf_debug_inject_timeout.restype = I
+        lib.gbf_debug_mlp_path.argtypes = [I64, I64, I64, I, ctypes.POINTER(I64)]
+        lib.gbf_debug_mlp_path.restype = I
         lib.gbf_debug_set_profile.argtypes = [V, SZ]
         lib.gbf_debug_set_profile.restype = I
         lib.gbf_debug_force_splits.argtypes = [I]
@@ -496,6 +500,14 @@ def gbf_debug_force_path(path) -> int:
     code = {None: 0, "auto": 0, "persistent": 1, "pair": 4,
             "persistent_splitk": 5, "pair_1stream": 6, "pair_splitk": 7}.get(path, path)
     return int(load().gbf_debug_force_path(int(code)))
+
+
+def gbf_debug_mlp_path(M, D, F, grad=False):
+    """(kernel's name, units of work over the CTA pairs) of the gate/up product of ``mlp_train``,
+    or of dh in ``mlp_grad``."""
+    units = ctypes.c_int64(0)
+    code = load().gbf_debug_mlp_path(M, D, F, int(bool(grad)), ctypes.byref(units))
+    return MLP_PATH.get(code, "rejected"), units.value
 
 
 def gbf_kernel_path(op, M, N, K, b_layout="nk"):

@@ -11,6 +11,7 @@
 #include <initializer_list>
 
 #include "../../include/gbfuse.h"
+#include "../../include/gbfuse_debug.h"
 #include "internal.h"
 
 namespace gbf {
@@ -210,6 +211,32 @@ bool set_dw(MbJob* j, const void* a, const void* b, const void* out, float* part
                         : map_out(&j->o[0], out, cols, rows, false));
 }
 
+// The kernel of the gate/up product, or of dh, and its launch where that is the CTA
+// pairs'; M > 0.
+enum MlpPath { kMlpOneSm = 1, kMlpSwap = 2, kMlpPairOne = 8, kMlpPairTwo = 9 };
+MlpPath forward_path(int64_t M, int64_t D, int64_t F, int act, MbLaunch* l) {
+  set_job(&l->job[1], kMbGlu, M, F, D, false, false);
+  l->act = act;
+  int64_t cycles;
+  const int streams = faster_streams(l, M, &cycles);
+  // Few rows or tiles: the weights' bytes or the latency count, and the swapped kernel
+  // splits K over clusters (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
+  // rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs 56; 257 x 2048 x 5632
+  // 21, 28; 256 x 4096 x 14336 64, 56).
+  if (lib_glu_swap(M, F, D, true)) return kMlpSwap;
+  const int64_t tiles = ceil_div64(M, 128) * ceil_div64(F, 128);
+  if (ceil_div64(tiles, kMaxSms) * ceil_div64(D, kBK) * 680 + 9000 < cycles) return kMlpOneSm;
+  return streams == 2 ? kMlpPairTwo : kMlpPairOne;
+}
+MlpPath dh_path(int64_t M, int64_t D, int64_t F, int act, MbLaunch* l) {
+  // few rows or tiles, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
+  // rows 32)
+  if (lib_glu_swap(M, F, D, false)) return kMlpSwap;
+  set_job(&l->job[0], kMbGluGrad, M, F, D, false, true);
+  l->act = act;
+  return faster_streams(l, M, nullptr) == 2 ? kMlpPairTwo : kMlpPairOne;
+}
+
 gbf_status_t run_launch(MbLaunch* l, int streams, const DeviceInfo& dev, unsigned* err,
                         cudaStream_t s) {
   plan_mlp_launch(l, streams, dev.pairs);
@@ -256,24 +283,15 @@ gbf_status_t gbf_mlp_train(const void* x, const void* w_gate, const void* w_up,
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   MbLaunch l{};
   MbJob& j = l.job[1];
-  set_job(&j, kMbGlu, M, F, D, false, false);
-  l.act = act;
-  int64_t cycles;
-  const int streams = faster_streams(&l, M, &cycles);
-  // Few rows or tiles: the weights' bytes or the latency count, and the swapped kernel
-  // splits K over clusters (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
-  // rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs 56; 257 x 2048 x 5632
-  // 21, 28; 256 x 4096 x 14336 64, 56).
-  const int64_t tiles = ceil_div64(M, 128) * ceil_div64(F, 128);
-  if (lib_glu_swap(M, F, D, true) ||
-      ceil_div64(tiles, kMaxSms) * ceil_div64(D, kBK) * 680 + 9000 < cycles) {
+  const MlpPath path = forward_path(M, D, F, act, &l);
+  if (path == kMlpSwap || path == kMlpOneSm) {
     if ((st = lib_glu_keep(x, w_gate, w_up, h, g, u, M, F, D, act, s)) != GBF_OK) return st;
   } else {
     if (!map_k(&j.a[0], x, D, M) || !map_k(&j.b[0], w_gate, D, F) || !map_k(&j.b[1], w_up, D, F) ||
         !map_out(&j.o[0], h, F, M, false) || !map_out(&j.o[1], g, F, M, false) ||
         !map_out(&j.o[2], u, F, M, false))
       return GBF_ERR_CUDA;
-    if ((st = run_launch(&l, streams, *dev, err, s)) != GBF_OK) return st;
+    if ((st = run_launch(&l, path == kMlpPairTwo ? 2 : 1, *dev, err, s)) != GBF_OK) return st;
   }
   return lib_mlp_down(h, w_down, residual, out, M, D, F, s);
 }
@@ -311,20 +329,20 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
         return st;
     return GBF_OK;
   }
-  if (hidden && lib_glu_swap(M, F, D, false)) {
-    // few rows or tiles, as in gbf_mlp_train (16 x 4096 x 14336, dh alone: 21 us, units of 256
-    // rows 32)
-    if ((st = lib_glu_grad(dout, w_down, g, u, ws.dg, ws.du, M, F, D, act, s)) != GBF_OK) return st;
-  } else if (hidden) {
+  if (hidden) {
     MbLaunch l{};
     MbJob& j = l.job[0];
-    set_job(&j, kMbGluGrad, M, F, D, false, true);
-    l.act = act;
-    if (!map_k(&j.a[0], dout, D, M) || !map_mn(&j.b[0], w_down, F, D) ||
-        !map_out(&j.a[1], g, F, M, true) || !map_out(&j.b[1], u, F, M, true) ||
-        !map_out(&j.o[0], ws.dg, F, M, true) || !map_out(&j.o[1], ws.du, F, M, true))
-      return GBF_ERR_CUDA;
-    if ((st = run_launch(&l, faster_streams(&l, M, nullptr), *dev, err, s)) != GBF_OK) return st;
+    const MlpPath path = dh_path(M, D, F, act, &l);
+    if (path == kMlpSwap) {
+      st = static_cast<gbf_status_t>(lib_glu_grad(dout, w_down, g, u, ws.dg, ws.du, M, F, D, act, s));
+    } else {
+      if (!map_k(&j.a[0], dout, D, M) || !map_mn(&j.b[0], w_down, F, D) ||
+          !map_out(&j.a[1], g, F, M, true) || !map_out(&j.b[1], u, F, M, true) ||
+          !map_out(&j.o[0], ws.dg, F, M, true) || !map_out(&j.o[1], ws.du, F, M, true))
+        return GBF_ERR_CUDA;
+      st = run_launch(&l, path == kMlpPairTwo ? 2 : 1, *dev, err, s);
+    }
+    if (st != GBF_OK) return st;
   }
   MbLaunch l{};
   if (dx) {
@@ -352,6 +370,18 @@ gbf_status_t gbf_mlp_grad(const void* dout, const void* x, const void* g, const 
     if (st != GBF_OK) return st;
   }
   return GBF_OK;
+}
+
+int gbf_debug_mlp_path(int64_t M, int64_t D, int64_t F, int grad, int64_t* units) {
+  if (units) *units = 0;
+  if (M == 0 || check_mlp(M, D, F, GBF_ACT_SILU) != GBF_OK) return -1;
+  MbLaunch l{};
+  const MlpPath path = grad ? dh_path(M, D, F, GBF_ACT_SILU, &l) : forward_path(M, D, F, GBF_ACT_SILU, &l);
+  if (path == kMlpPairOne || path == kMlpPairTwo) {
+    plan_mlp_launch(&l, path == kMlpPairTwo ? 2 : 1, kMlpPairs);
+    if (units) *units = l.job[0].units + l.shorts;
+  }
+  return path;
 }
 
 gbf_status_t gbf_add_rmsnorm_grad(const void* dnorm, const void* dresid, const void* resid,

@@ -8,7 +8,7 @@ from test_mlp_train_gpu import ACTS, backward, forward, inputs
 pytestmark = pytest.mark.gpu
 
 # the swapped kernel, the one-SM kernel, CTA pairs with one and with two row tiles per unit
-FORWARD = [(16, 264, 520), (1300, 72, 4104), (513, 136, 1032), (2100, 1032, 4104)]
+FORWARD = [(16, 264, 520), (1300, 72, 4104), (513, 136, 1032), (1800, 1032, 4104)]
 BACKWARD = [(1, 64, 136), (40, 136, 264), (700, 520, 2056), (2500, 136, 2056)]
 
 
