@@ -423,7 +423,6 @@ gbf_status_t ce_backward(const CeCall& call, const float* lse, const float* dlos
   p.tgt = ws.tgt;
   p.lse2 = ws.lse2;
   p.dl = ws.dl;
-  p.soft = pick.list != nullptr;
   p.M = static_cast<int>(M);
   p.V = static_cast<int>(V);
   p.D = static_cast<int>(D);

@@ -199,7 +199,7 @@ struct CePick {
 };
 struct CeEnd {
   const int* count;   // scored rows
-  const int* tgt;     // [count] targets
+  const int* tgt;     // [count] targets (not read with a pick)
   const float* lse2;  // [count] lse / ln 2
   const float* dl;    // [count] gradient of each loss
   float2* part;       // [2 per column tile][M] (maximum, sum), powers of two
@@ -255,7 +255,6 @@ struct CePrep {
   unsigned* ticket;
   float *lse2, *dl;
   int M, V, D, rows_per;
-  int soft;               // targets only say which rows are scored: tgt is -1
 };
 struct CeJoin {
   const int* count;

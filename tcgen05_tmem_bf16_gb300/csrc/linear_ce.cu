@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(kPrepThreads)
       if (scored) {
         const int at = slot + __popc(mask & ((1u << lane) - 1u));
         p.rows[at] = static_cast<int>(r);
-        p.tgt[at] = p.soft ? -1 : static_cast<int>(t);
+        p.tgt[at] = static_cast<int>(t);
         if (p.lse2) {
           p.lse2[at] = p.lse_in[r] * kLog2e;
           p.dl[at] = p.dloss ? p.dloss[r] : 1.0f;
