@@ -143,7 +143,10 @@ __device__ __forceinline__ CeWork ce_work(const CeLaunch& a, int count, int stre
   return w;
 }
 
-// The n-th unit of a pair; false after its last.
+// The n-th unit of a pair; false after its last.  SPLITS: there are products whose K is
+// split, dx and a long dw, into at most 2^25 parts x blocks (where there are none the choice
+// costs the logits in chains half a percent).
+template <bool SPLITS>
 __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int pair, int n,
                                         CeUnit& u) {
   const int mine = w.longs / w.npairs + (pair < w.extra ? 1 : 0);
@@ -170,8 +173,10 @@ __device__ __forceinline__ bool ce_unit(const CeWork& w, const CeLaunch& a, int 
   u.split = 0;
   u.kb0 = 0;
   u.kb1 = num_kb;
-  // the products whose K is split, dx and a long dw; at most 2^25 parts x blocks
-  const unsigned splits = u.job == 0 ? a.job[0].splits : u.job == 2 ? a.job[2].splits : 1;
+  const unsigned splits = !SPLITS      ? 1
+                          : u.job == 0 ? a.job[0].splits
+                          : u.job == 2 ? a.job[2].splits
+                                       : 1;
   if (splits > 1) {
     const unsigned tiles = m_units * n_tiles;
     u.split = static_cast<unsigned>(t) / tiles;
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       uint32_t ph = 0;
       bool ok = true;
       CeUnit u;
-      for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+      for (int n = 0; ok && ce_unit<FORM != kCeChains>(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
         // A is read along its columns: G for dw, its transpose for dx
         const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
@@ -537,7 +542,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
       int use0 = 0, use1 = 0;  // of the accumulators
       int turn = 0;
       CeUnit u;
-      for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+      for (int n = 0; ok && ce_unit<FORM != kCeChains>(work, a, pair, n, u); ++n) {
         const CeJob& j = a.job[u.job];
         const bool a_mn = (j.mode == kCeDw && !j.gt) || (j.mode == kCeDx && j.gt);
         const bool b_mn = j.mode == kCeDw || j.mode == kCeDx;
@@ -612,7 +617,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     int turn = 0;
     bool ok = true;
     CeUnit u;
-    for (int n = 0; ok && ce_unit(work, a, pair, n, u); ++n) {
+    for (int n = 0; ok && ce_unit<FORM != kCeChains>(work, a, pair, n, u); ++n) {
       const CeJob& j = a.job[u.job];
       const int mode = j.mode;
       CeTileArgs t;
