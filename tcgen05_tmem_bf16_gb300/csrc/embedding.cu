@@ -688,6 +688,16 @@ int embed_piece(int64_t M, int D) {
   return piece;
 }
 
+int64_t embed_most_pieces(int64_t M, int D) {
+  const int segs = std::max(1, (D + kSegCols - 1) / kSegCols);
+  int64_t most = (M + kMaxPiece - 1) / kMaxPiece;
+  // a shorter piece is taken while those of twice its length are fewer than this
+  const int64_t fewer = 2 * ((152 * 8 - 1) / segs);
+  for (int piece = 4; piece < kMaxPiece; piece *= 2)
+    most = std::max(most, std::min((M + piece - 1) / piece, fewer));
+  return most;
+}
+
 cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat16* dout,
                                   __nv_bfloat16* dtable, int M, int V, int D, float scale,
                                   bool accumulate, const EmbedGradWs& ws, int sms,

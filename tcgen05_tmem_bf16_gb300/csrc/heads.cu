@@ -59,6 +59,16 @@ size_t embed_grad_sections(void* base, int64_t M, int64_t D, EmbedGradWs* ws) {
   return s.at;
 }
 
+// What that comes to with M positions or fewer, which may be cut into shorter pieces.
+size_t embed_grad_workspace(int64_t M, int64_t D) {
+  Sections s{nullptr};
+  for (int i = 0; i < 4; ++i) s.take<int>(M);
+  const size_t parts = static_cast<size_t>(embed_most_pieces(M, static_cast<int>(D))) * D;
+  s.take<float>(parts);
+  s.take<float>(parts);
+  return s.at;
+}
+
 // ---- linear cross entropy
 
 constexpr int kCePairs = 76;  // CTA pairs that run at once
@@ -623,8 +633,7 @@ size_t heads_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
   switch (op) {
     case GBF_OP_EMBEDDING_GRAD: {
       if (M > kMaxSorted || N > kMaxInt || K > kMaxInt) return 0;
-      EmbedGradWs ws;
-      return embed_grad_sections(nullptr, M, K, &ws);
+      return embed_grad_workspace(M, K);
     }
     case GBF_OP_CLIP_GRAD_NORM:
       if (M > kMaxInt) return 0;

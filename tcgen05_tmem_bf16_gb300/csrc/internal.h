@@ -146,6 +146,7 @@ struct EmbedGradWs {
   float *head, *tail;              // [pieces][D]: parts of runs over several pieces
 };
 int embed_piece(int64_t M, int D);  // sorted positions per piece
+int64_t embed_most_pieces(int64_t M, int D);  // of M positions or fewer
 cudaError_t launch_embedding_grad(const void* ids, bool ids64, const __nv_bfloat16* dout,
                                   __nv_bfloat16* dtable, int M, int V, int D, float scale,
                                   bool accumulate, const EmbedGradWs& ws, int sms,

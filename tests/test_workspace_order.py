@@ -42,3 +42,10 @@ def test_linear_distill_and_linear_ce(D, grad):
             assert all(0 < a <= b for a, b in zip(sizes, sizes[1:])), (V, K)
         sizes = [gbf.gbf_workspace_size("linear_ce_grad" if grad else "linear_ce", M, V, D, True) for M in rows(V)]
         assert all(0 < a <= b for a, b in zip(sizes, sizes[1:])), V
+
+
+@pytest.mark.parametrize("D", (8, 256, 1024, 1032, 2048, 4096, 8192, 2 ** 21))
+def test_embedding_grad(D):
+    many = sorted({*rows(D), 2432, 2433, 4864, 4865, 9728, 9729})
+    sizes = [gbf.gbf_workspace_size("embedding_grad", M, 32000, D, True) for M in many]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))

@@ -76,3 +76,18 @@ def test_distillation_of_fewer_rows(cuda_lib, V, D, K, most):
         assert all(torch.equal(a, b) for a, b in zip(out, ends)), M
     assert all(bool((b[-256:] == 0x55).all()) for b in (*ws.values(), *hard.values()))
     assert cuda_lib.gbf_check_device_error() == 0
+
+
+@pytest.mark.parametrize("V,D,most", [(3000, 4096, 5000), (3000, 1024, 20000)])
+def test_embedding_grad_of_fewer_positions(cuda_lib, V, D, most):
+    n = cuda_lib.gbf_workspace_size("embedding_grad", most, V, D, True)
+    for M in (1, 1024, 1025, most // 2 - 60, most // 2, most):
+        gen = torch.Generator(device="cuda").manual_seed(M)
+        ids = torch.randint(0, V, (M,), generator=gen, device="cuda")
+        dout = torch.randn(M, D, generator=gen, device="cuda").bfloat16()
+        out = [torch.full((V, D), float("nan"), device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+        for o, b in zip(out, (n, cuda_lib.gbf_workspace_size("embedding_grad", M, V, D, True))):
+            ws = guarded(b)
+            cuda_lib.embedding_grad(ids, dout, o, M, V, D, workspace=ws, workspace_bytes=b)
+            assert bool((ws[b:] == 0x55).all())
+        assert torch.equal(*out)
