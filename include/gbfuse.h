@@ -404,8 +404,10 @@ GBF_API gbf_status_t gbf_linear_ce_grad(const void *x, const void *w, const void
  *   holds; entries may be in any order, and the same id may come twice.  A row without a
  *   valid entry is not scored: its loss and lse are 0, it costs no products (above 128
  *   rows), and whatever its row of x holds reaches no result.
- *   K in 1 .. 1024; beta > 0 and finite; other arguments, sizes, alignments and
- *   accuracies as gbf_linear_ce (a loss is never below zero).  Workspace:
+ *   K in 1 .. 1024; beta > 0 and finite; other arguments, sizes, alignments and lse's
+ *   accuracy as gbf_linear_ce.  A loss is a sum of differences: off by up to about 5e-7 of
+ *   the magnitudes of lse, l and log q, however small it is itself; never below zero.
+ *   Workspace:
  *   gbf_linear_distill_workspace_size(M, V, D, K, 0) bytes, which do not fall with M.
  * gbf_linear_distill_grad -- its gradients, from the lse that gbf_linear_distill wrote:
  *     G[m][v] = dloss[m] * (exp(l[m][v] - lse[m]) - q[m][v])
@@ -470,15 +472,16 @@ GBF_API gbf_status_t gbf_clip_grad_norm(const void *const *grads, void *const *o
  *     dh = dout*Wd;   dg = dh * u * act'(g),  du = dh * act(g)    (rounded to bf16)
  *     dx = dg*Wg + du*Wu,   dw_gate = dg^T*x,  dw_up = du^T*x,  dw_down = dout^T*h
  *   act' of GBF_ACT_RELU is 0 at 0 and at a NaN; everything else keeps a NaN (act of
- *   GBF_ACT_RELU here and in h, unlike the endings above, which make it 0).  dx [M][D], dw_gate, dw_up [F][D], dw_down
- *   [D][F] bf16; any of the four may be NULL (not computed), not all.  dh is never
- *   in memory.  Sums in fp32 on the tensor cores, whose additions cut up to 7e-9 of the
- *   sum per product where all have one sign, in chains of at most 131072 products (1e-3
- *   of such a sum) that are added in rounded fp32; rounded once.  The
- *   same bits on every run.  M == 0 gives zero weight gradients.  Workspace: gbf_workspace_size(GBF_OP_MLP_GRAD, M, D, F,
- *   1) bytes, which do not fall with M: one for the most rows serves fewer.  Without dx
- *   2 * align256(2 * M * F) bytes do, without dx, dw_gate and dw_up none (align256: up to
- *   the next multiple of 256).
+ *   GBF_ACT_RELU here and in h, unlike the endings above, which make it 0).  dx
+ *   [M][D], dw_gate, dw_up [F][D], dw_down [D][F] bf16; any of the four may be NULL
+ *   (not computed), not all.  dh is never in memory.  Sums in fp32 on the tensor
+ *   cores, whose additions cut up to 7e-9 of the sum per product where all have one
+ *   sign (gbf_mlp_train's too); dx's and the weights' in chains of at most 131072
+ *   products (1e-3 of such a sum), added in rounded fp32; rounded once.  The same bits on every run.
+ *   M == 0 gives zero weight gradients.  Workspace: gbf_workspace_size(
+ *   GBF_OP_MLP_GRAD, M, D, F, 1) bytes, which do not fall with M: one for the most
+ *   rows serves fewer.  Up to 131072 rows 2 * align256(2 * M * F) bytes do without
+ *   dx, none without dx, dw_gate and dw_up (align256: up to the next multiple of 256).
  */
 GBF_API gbf_status_t gbf_mlp_train(const void *x, const void *w_gate, const void *w_up,
                                    const void *w_down, const void *residual, void *out, void *g,

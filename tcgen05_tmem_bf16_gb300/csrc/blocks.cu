@@ -93,10 +93,10 @@ int64_t dx_part_limit(int64_t M, int64_t D, int64_t F) {
 
 // The launch of dx and the weights' gradients: row tiles per unit, and the parts of K
 // of the product for dx.  With one row tile as many as give one round of units over
-// the pairs (16 x 4096 x 14336, all of the launch: 3 parts 111 us, 4, one round, 104, 5
-// 116, 9 107).  Else as the whole launch is fastest by the estimate; adding the parts
-// costs a launch and their traffic (1021 x 1000 x 2728: none 40 us, 2 or 3 parts 30.2,
-// 4 33.6).
+// the pairs (all of the gradient of 16 x 4096 x 14336: 3 parts 142 us, 4, one round, 122, 5
+// 137, 9 121).  Else as the whole launch is fastest by the estimate; adding the parts
+// costs a launch and their traffic (all of the gradient of 1021 x 1000 x 2728: none 58 us,
+// 2 or 3 parts 49, 4 52.5).
 struct MlpPlan {
   int streams, dx_splits;
 };
