@@ -158,10 +158,10 @@ __device__ __forceinline__ void glu_grad_pack(const uint32_t (&dh)[16], const ui
 // a time, on their way ahead of the arithmetic: one lane asks the TMA engine for the
 // next chunk of the next units, into a slot whose dg and du have been stored.
 //
-// dh of 4096 x 4096 x 14336 takes 245 us without g and u.  Read by the lanes themselves
-// they cost the products their shared memory, which is the same as L1 (16 bytes of 32
-// rows at a time 450 us, 64 of 8 rows 362); by the TMA engine its requests count, one
-// per row of a box: 330 us with rows of 64 bytes, 301 with 128.
+// dh of 4096 x 4096 x 14336 takes 275 us without g and u, 245 without an ending.  Read by
+// the lanes themselves they cost the products their shared memory, which is the same as L1
+// (16 bytes of 32 rows at a time 450 us, 64 of 8 rows 362); by the TMA engine its requests
+// count, one per row of a box: 330 us with rows of 64 bytes, 314 with 128.
 template <int STREAMS, int SLOTS>
 struct GradLoads {
   MbUnit u;   // of the next chunk
