@@ -220,9 +220,9 @@ MlpPath forward_path(int64_t M, int64_t D, int64_t F, int act, MbLaunch* l) {
   int64_t cycles;
   const int streams = faster_streams(l, M, &cycles);
   // Few rows or tiles: the weights' bytes or the latency count, and the swapped kernel
-  // splits K over clusters (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel where its tiles of 128
-  // rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs 56; 257 x 2048 x 5632
-  // 21, 28; 256 x 4096 x 14336 64, 56).
+  // splits K over clusters (16 x 4096 x 14336: 38 us, pairs 54).  Else the one-SM kernel
+  // where its tiles of 128 rows fill their rounds better (64 x 4096 x 14336: 47 us, pairs
+  // 56; 257 x 2048 x 5632 21, 28; 256 x 4096 x 14336 64, 56).
   if (lib_glu_swap(M, F, D, true)) return kMlpSwap;
   const int64_t tiles = ceil_div64(M, 128) * ceil_div64(F, 128);
   if (ceil_div64(tiles, kMaxSms) * ceil_div64(D, kBK) * 680 + 9000 < cycles) return kMlpOneSm;

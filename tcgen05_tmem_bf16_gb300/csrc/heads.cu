@@ -103,9 +103,9 @@ int ce_streams(int64_t M, int64_t cols, bool lists) {
 bool ce_chained(int64_t D) { return ceil_div64(D, kBK) > kCeChain; }
 
 // Parts of K of the product for dx, each with an fp32 buffer of its own, 16 at
-// most and none shorter than 8 K blocks or longer than a chain.  With one row tile: as many as give one
-// round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4 parts 103
-// us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
+// most and none shorter than 8 K blocks or longer than a chain.  With one row tile: as
+// many as give one round of units over the pairs (64 rows, 32000 x 4096, dx alone: 4
+// parts 103 us, 5 parts, a second round for four of 80 units, 129, 14 parts 108 and more
 // beside dw).  Else: none longer than half of what a pair has to do in all, the
 // logits among it also where their launch is another (without them there are more
 // parts: 1024 x 32000 x 4096 491 us, 501; 4096 x 32000 x 8192 3.59 ms, 3.66).
