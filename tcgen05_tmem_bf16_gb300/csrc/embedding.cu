@@ -378,11 +378,12 @@ __global__ void __launch_bounds__(kSumThreads)
 #pragma unroll
   for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
   constexpr int kAhead = 8;
+  // (plain loads: the kernel before may still have been writing dout when this one began)
   for (int i0 = 0; i0 < n; i0 += kAhead) {
     uint4 v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (i0 + u < n) v[u] = ldg_u4(a.dout + static_cast<int64_t>(same[i0 + u]) * a.D + col);
+      if (i0 + u < n) v[u] = ld_u4(a.dout + static_cast<int64_t>(same[i0 + u]) * a.D + col);
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (i0 + u >= n) break;
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const SumArgs a)
     for (int u = 0; u < kAhead; ++u) {
       if (i0 + u < n && skey[i0 + u + 1] < a.V) {
         const int key = skey[i0 + u + 1];
-        v[u] = ldg_u4(a.dout + static_cast<int64_t>(sidx[i0 + u]) * a.D + col);
+        v[u] = ld_u4(a.dout + static_cast<int64_t>(sidx[i0 + u]) * a.D + col);
         if (a.accumulate && skey[i0 + u + 2] != key)
           old[u] = ld_u4(a.dtable + static_cast<int64_t>(key) * a.D + col);
       }

@@ -750,12 +750,13 @@ __device__ __forceinline__ int2 block_sum2(int a, int b) {
 }
 
 // One row by one warp, four 16-byte vectors per lane in flight; zeros without src.
+// (Plain loads: the kernel before may still have been writing x when this one began.)
 __device__ __forceinline__ void copy_row(__nv_bfloat16* dst, const __nv_bfloat16* src, int D) {
   for (int c0 = (threadIdx.x & 31) * 8; c0 < D; c0 += 4 * 256) {
     uint4 v[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      v[k] = src && c0 + k * 256 < D ? ldg_u4(src + c0 + k * 256) : make_uint4(0u, 0u, 0u, 0u);
+      v[k] = src && c0 + k * 256 < D ? ld_u4(src + c0 + k * 256) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (c0 + k * 256 < D) st_u4(dst + c0 + k * 256, v[k]);
